@@ -29,6 +29,8 @@ EXPORTS = (
 )
 # include/qstate_ceiling.h: bandwidth-ceiling kernels (measurement support)
 CEILING_EXPORTS = ("qstate_ceiling_copy", "qstate_ceiling_rmw")
+# include/qstate_scan.h: the recurrences over whole sequences and their gradients
+SCAN_EXPORTS = ("qstate_scan_workspace", "qstate_scan", "qstate_scan_backward")
 
 
 class QStateConfig(ctypes.Structure):
@@ -41,6 +43,13 @@ class QStateConfig(ctypes.Structure):
         ("channel_bits", ctypes.POINTER(ctypes.c_uint8)), ("window", ctypes.c_int32),
         ("window_merge", ctypes.c_int32), ("lrb_threshold", ctypes.c_float),
     ]
+
+
+class ScanConfigC(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("batch", "heads", "heads_qk", "dk", "dv", "mixer",
+                                               "dtype", "pad")]
+                + [(n, ctypes.c_int64) for n in ("tokens", "q_stride", "k_stride", "v_stride",
+                                                 "o_stride")])
 
 
 _lib = None
@@ -75,6 +84,9 @@ def lib() -> ctypes.CDLL:
                                          ctypes.c_uint8, P]),
         "qstate_ceiling_copy": (c_int, [P, P, sz, c_int, P]),
         "qstate_ceiling_rmw": (c_int, [P, sz, ctypes.c_uint32, c_int, P]),
+        "qstate_scan_workspace": (c_int, [ctypes.POINTER(ScanConfigC), c_int, ctypes.POINTER(sz)]),
+        "qstate_scan": (c_int, [ctypes.POINTER(ScanConfigC)] + [P] * 10 + [sz, P]),
+        "qstate_scan_backward": (c_int, [ctypes.POINTER(ScanConfigC)] + [P] * 16 + [sz, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(L, name)

@@ -1,0 +1,222 @@
+// scan_api.cpp — the C ABI declared in include/qstate_scan.h: argument checks,
+// the workspace's layout and the launches.  Host code only.
+
+#include "qstate_scan.h"
+
+#include <hip/hip_runtime_api.h>
+
+#include <cstring>
+
+#include "qstate.h"
+#include "scan_launch.h"
+
+namespace {
+
+using qscan::kChunk;
+using qscan::kTerms;
+using qscan::Params;
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+bool vector_gate(int mixer) { return mixer == QSTATE_GLA || mixer == QSTATE_KDA; }
+bool delta_rule(int mixer) { return mixer == QSTATE_GDN || mixer == QSTATE_KDA; }
+
+int check_config(const qstate_scan_config* c) {
+  if (!c) return QSTATE_E_INVALID;
+  if (c->batch < 1 || c->heads < 1 || c->heads_qk < 1 || c->dk < 1 || c->dv < 1)
+    return QSTATE_E_INVALID;
+  if (c->mixer < QSTATE_GDN || c->mixer > QSTATE_KDA) return QSTATE_E_INVALID;
+  if (c->dtype < QSTATE_FP32 || c->dtype > QSTATE_FP16) return QSTATE_E_INVALID;
+  if (c->heads % c->heads_qk != 0 || c->pad != 0) return QSTATE_E_INVALID;
+  if (c->tokens < 0) return QSTATE_E_INVALID;
+  const int64_t qk = (int64_t)c->heads_qk * c->dk, hv = (int64_t)c->heads * c->dv;
+  if ((c->q_stride && c->q_stride < qk) || (c->k_stride && c->k_stride < qk) ||
+      (c->v_stride && c->v_stride < hv) || (c->o_stride && c->o_stride < hv))
+    return QSTATE_E_INVALID;
+  if (c->dk != 64 && c->dk != 128 && c->dk != 256) return QSTATE_E_UNSUPPORTED;
+  if (c->heads > 256 || c->dv > 4096 || c->tokens > 2147483647) return QSTATE_E_UNSUPPORTED;
+  const int64_t far = (int64_t)1 << 40;
+  if (c->q_stride > far || c->k_stride > far || c->v_stride > far || c->o_stride > far)
+    return QSTATE_E_UNSUPPORTED;
+  // the grids: chunks of all sequences, and a workgroup per head and column block
+  if (c->tokens / kChunk + c->batch > 2147483647 ||
+      (int64_t)c->batch * c->heads * ((c->dv + 31) / 32) > 2000000000)
+    return QSTATE_E_UNSUPPORTED;
+  return QSTATE_OK;
+}
+
+// Hands out the workspace's regions; with a null base it only counts.
+struct Area {
+  char* base;
+  size_t used;
+  template <class T>
+  void take(T*& p, uint64_t n, bool want) {
+    p = nullptr;
+    if (!want) return;
+    if (base) p = reinterpret_cast<T*>(base + used);
+    used += ((size_t)n * sizeof(T) + 255) / 256 * 256;
+  }
+};
+
+size_t layout(const qstate_scan_config* c, bool backward, void* workspace, Params& p) {
+  const bool vec = vector_gate(c->mixer), delta = delta_rule(c->mixer), bf16 = c->dtype == QSTATE_BF16;
+  std::memset(&p, 0, sizeof(p));
+  p.batch = c->batch;
+  p.heads = c->heads;
+  p.heads_qk = c->heads_qk;
+  p.dk = c->dk;
+  p.dv = c->dv;
+  p.mixer = c->mixer;
+  p.dtype = c->dtype;
+  p.tokens = c->tokens;
+  p.qs = c->q_stride ? c->q_stride : (int64_t)c->heads_qk * c->dk;
+  p.ks = c->k_stride ? c->k_stride : (int64_t)c->heads_qk * c->dk;
+  p.vs = c->v_stride ? c->v_stride : (int64_t)c->heads * c->dv;
+  p.os = c->o_stride ? c->o_stride : (int64_t)c->heads * c->dv;
+  // bfloat16 rows enter the products as they are where 16-byte loads reach them
+  p.direct = !vec && bf16 && p.qs % 8 == 0 && p.ks % 8 == 0;
+  p.terms = p.direct ? 1 : kTerms;
+  p.nslots = (int)(c->tokens / kChunk + c->batch);
+  p.vblock = 32;
+  p.dvp = (c->dv + p.vblock - 1) / p.vblock * p.vblock;
+  p.nvb = p.dvp / p.vblock;
+  p.dop_terms = bf16 ? 1 : kTerms;
+
+  Area w = {static_cast<char*>(workspace), 0};
+  const uint64_t sh = (uint64_t)p.nslots * p.heads, sq = (uint64_t)p.nslots * p.heads_qk;
+  const uint64_t tile = (uint64_t)kChunk * p.dk, ops = (vec ? sh : sq) * p.terms * tile;
+  const uint64_t square = sh * kTerms * kChunk * kChunk;
+  w.take(p.rows, sh * 5 * kChunk, true);
+  w.take(p.decay, sh * p.dk, vec);
+  w.take(p.qrow, ops, !p.direct && (!vec || !backward));
+  w.take(p.krow, ops, !p.direct && (!vec || delta));
+  w.take(p.kt, ops, true);
+  w.take(p.a, square, !backward);
+  w.take(p.t, square, delta);
+  if (backward) {
+    const uint64_t raw = sq * (bf16 ? 1 : kTerms) * tile;
+    w.take(p.korow, ops, vec);
+    w.take(p.qt, ops, true);
+    w.take(p.ket, ops, vec && delta);
+    w.take(p.kt_raw, raw, vec);
+    w.take(p.qt_raw, raw, vec);
+    w.take(p.pfx, sh * tile, vec);
+    w.take(p.sfx, sh * tile, vec);
+    w.take(p.at, square, true);
+    w.take(p.t2t, square, delta);
+    // d_o's rows serve as they are where they are bfloat16 and fill whole blocks
+    w.take(p.dop, sh * p.dop_terms * kChunk * p.dvp, !(bf16 && c->dv % p.vblock == 0));
+    w.take(p.u, sh * kTerms * kChunk * p.dvp, true);
+    w.take(p.y, sh * kTerms * kChunk * p.dvp, delta);
+    w.take(p.sc, sh * p.dk * p.dvp, true);
+    w.take(p.xc, sh * p.dk * p.dvp, true);
+    w.take(p.dbpart, (uint64_t)p.nvb * sh * kChunk, c->mixer != QSTATE_GLA);
+    w.take(p.dqpart, sh * tile, p.heads != p.heads_qk);
+    w.take(p.dkpart, sh * tile, p.heads != p.heads_qk);
+  }
+  return w.used;
+}
+
+// The arrays that both directions read.
+int check_inputs(const qstate_scan_config* c, const void* q, const void* k, const void* v,
+                 const float* log_alpha, const float* beta, const int64_t* offsets,
+                 const float* initial_state) {
+  const size_t e = c->dtype == QSTATE_FP32 ? 4 : 2;
+  const bool beta_needed = c->mixer != QSTATE_GLA;
+  if (c->tokens > 0 && (!q || !k || !v || !log_alpha || (beta_needed && !beta)))
+    return QSTATE_E_INVALID;
+  if (!offsets && c->tokens % c->batch != 0) return QSTATE_E_INVALID;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, e) || !aligned(log_alpha, 16) ||
+      !aligned(beta, 16) || !aligned(offsets, 8) || !aligned(initial_state, 16))
+    return QSTATE_E_INVALID;
+  return QSTATE_OK;
+}
+
+void set_inputs(Params& p, const void* q, const void* k, const void* v, const float* log_alpha,
+                const float* beta, const int64_t* offsets, const float* initial_state) {
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.g = log_alpha;
+  p.beta = p.mixer == QSTATE_GLA ? nullptr : beta;
+  p.offsets = offsets;
+  p.s0 = initial_state;
+}
+
+int status(hipError_t e) { return e == hipSuccess ? QSTATE_OK : QSTATE_E_LAUNCH; }
+
+}  // namespace
+
+extern "C" {
+
+int qstate_scan_workspace(const qstate_scan_config* cfg, int backward, size_t* bytes) {
+  const int rc = check_config(cfg);
+  if (rc != QSTATE_OK) return rc;
+  if (!bytes || (backward != 0 && backward != 1)) return QSTATE_E_INVALID;
+  Params p;
+  *bytes = layout(cfg, backward == 1, nullptr, p);
+  return QSTATE_OK;
+}
+
+int qstate_scan(const qstate_scan_config* cfg, const void* q, const void* k, const void* v,
+                const float* log_alpha, const float* beta, const int64_t* offsets,
+                const float* initial_state, void* o, float* final_state, void* workspace,
+                size_t workspace_bytes, void* stream) {
+  int rc = check_config(cfg);
+  if (rc == QSTATE_OK) rc = check_inputs(cfg, q, k, v, log_alpha, beta, offsets, initial_state);
+  if (rc != QSTATE_OK) return rc;
+  if (!o && !final_state) return QSTATE_E_INVALID;
+  if (!aligned(o, cfg->dtype == QSTATE_FP32 ? 4 : 2) || !aligned(final_state, 16))
+    return QSTATE_E_INVALID;
+  Params p;
+  if (!workspace || !aligned(workspace, 256) || layout(cfg, false, workspace, p) > workspace_bytes)
+    return QSTATE_E_INVALID;
+  set_inputs(p, q, k, v, log_alpha, beta, offsets, initial_state);
+  p.o = o;
+  p.s1 = final_state;
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  switch (cfg->dk) {
+    case 64: return status(qscan::forward_dk64(p, s));
+    case 128: return status(qscan::forward_dk128(p, s));
+    default: return status(qscan::forward_dk256(p, s));
+  }
+}
+
+int qstate_scan_backward(const qstate_scan_config* cfg, const void* q, const void* k,
+                         const void* v, const float* log_alpha, const float* beta,
+                         const int64_t* offsets, const float* initial_state, const void* d_o,
+                         const float* d_final_state, void* dq, void* dk, void* dv,
+                         float* dlog_alpha, float* dbeta, float* d_initial_state,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_config(cfg);
+  if (rc == QSTATE_OK) rc = check_inputs(cfg, q, k, v, log_alpha, beta, offsets, initial_state);
+  if (rc != QSTATE_OK) return rc;
+  const size_t e = cfg->dtype == QSTATE_FP32 ? 4 : 2;
+  const bool beta_needed = cfg->mixer != QSTATE_GLA;
+  if (cfg->tokens > 0 && (!d_o || !dq || !dk || !dv || !dlog_alpha || (beta_needed && !dbeta)))
+    return QSTATE_E_INVALID;
+  if (!aligned(d_o, 16) || !aligned(d_final_state, 16) || !aligned(dq, e) || !aligned(dk, e) ||
+      !aligned(dv, e) || !aligned(dlog_alpha, 4) || !aligned(dbeta, 4) ||
+      !aligned(d_initial_state, 16))
+    return QSTATE_E_INVALID;
+  Params p;
+  if (!workspace || !aligned(workspace, 256) || layout(cfg, true, workspace, p) > workspace_bytes)
+    return QSTATE_E_INVALID;
+  set_inputs(p, q, k, v, log_alpha, beta, offsets, initial_state);
+  p.dO = d_o;
+  p.ds1 = d_final_state;
+  p.dq = dq;
+  p.dkk = dk;
+  p.dv_out = dv;
+  p.dg = dlog_alpha;
+  p.dbeta = beta_needed ? dbeta : nullptr;
+  p.ds0 = d_initial_state;
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  switch (cfg->dk) {
+    case 64: return status(qscan::backward_dk64(p, s));
+    case 128: return status(qscan::backward_dk128(p, s));
+    default: return status(qscan::backward_dk256(p, s));
+  }
+}
+
+}  // extern "C"

@@ -1,0 +1,219 @@
+// scan_device.h — what the scan's kernels share: chunk lookup, element access
+// by type, splitting FP32 values into bfloat16 terms, and the matrix product of
+// split operands.
+
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "scan_launch.h"
+
+namespace qscan {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int C = kChunk;
+constexpr int P = kTerms;
+constexpr int CP = C + 8;  // LDS row of kChunk terms; 36 words: 16 rows start in 16 banks
+
+enum { GDN = 0, GLA = 1, SCALAR = 2, KDA = 3 };
+
+// One chunk of a sequence.
+struct Chunk {
+  int n;        // sequence
+  int ci;       // chunk of the sequence
+  int len;      // tokens in the chunk
+  int64_t row;  // first row
+};
+
+__device__ __forceinline__ int64_t offset_of(const Params& p, int n) {
+  if (!p.offsets) return p.tokens / p.batch * n;
+  const int64_t o = p.offsets[n];
+  return o < 0 ? 0 : o > p.tokens ? p.tokens : o;
+}
+
+// Which chunk a slot is: sequence n starts at slot offset / C + n, which
+// leaves room for its ceil(len / C) chunks and needs no sums over sequences.
+// All lanes of a wave search together, 64 probes a step.
+__device__ __forceinline__ bool find_chunk(const Params& p, int slot, Chunk& c) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = p.batch;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 63) / 64;
+    const int64_t at = lo + (int64_t)lane * step;
+    const bool le = at < hi && offset_of(p, (int)at) / C + at <= slot;
+    const int count = __popcll(__ballot(le));
+    if (count == 0) return false;
+    lo += (count - 1) * step;
+    hi = hi < lo + step ? hi : lo + step;
+  }
+  const int64_t o0 = offset_of(p, lo), o1 = offset_of(p, lo + 1);
+  const int64_t ci = slot - (o0 / C + lo);
+  const int64_t left = o1 - o0 - ci * C;
+  if (ci < 0 || left <= 0) return false;
+  c.n = lo;
+  c.ci = (int)ci;
+  c.len = left < C ? (int)left : C;
+  c.row = o0 + ci * C;
+  return true;
+}
+
+// ---- elements of the caller's arrays -------------------------------------------------------
+
+__device__ __forceinline__ float bf16_to_f(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+
+__device__ __forceinline__ float load_elem(const void* p, int64_t i, int dtype) {
+  if (dtype == 1) return bf16_to_f(static_cast<const uint16_t*>(p)[i]);
+  if (dtype == 2) return (float)static_cast<const _Float16*>(p)[i];
+  return static_cast<const float*>(p)[i];
+}
+
+// Two floats to packed bfloat16, to nearest, ties to even.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const f32x2 f = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
+}
+
+// Outputs are rounded here, once, to the caller's type.
+__device__ __forceinline__ void store_elem(void* p, int64_t i, int dtype, float x) {
+  if (dtype == 1)
+    static_cast<uint16_t*>(p)[i] = (uint16_t)pack_bf16(x, 0.0f);
+  else if (dtype == 2)
+    static_cast<_Float16*>(p)[i] = (_Float16)x;
+  else
+    static_cast<float*>(p)[i] = x;
+}
+
+// Log decays below -87 count as -87; a NaN stays.
+__device__ __forceinline__ float gate(float g) { return g < -87.0f ? -87.0f : g; }
+
+// ---- FP32 as a sum of bfloat16 terms --------------------------------------------------------
+// x = t0 + t1 + ..., each term the rest rounded to bfloat16: N terms hold x to
+// 2^(-8 N) of itself, so three hold an FP32 value (24 bits).
+
+template <int N>
+__device__ __forceinline__ void split4(const float (&x)[4], u32x2 (&t)[N]) {
+  float r[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    t[n].x = pack_bf16(r[0], r[1]);
+    t[n].y = pack_bf16(r[2], r[3]);
+    if (n + 1 < N) {
+      r[0] -= __uint_as_float(t[n].x << 16);
+      r[1] -= __uint_as_float(t[n].x & 0xFFFF0000u);
+      r[2] -= __uint_as_float(t[n].y << 16);
+      r[3] -= __uint_as_float(t[n].y & 0xFFFF0000u);
+    }
+  }
+}
+
+template <int N>
+struct Frag {  // one operand of a 16 x 16 x 32 product: row lane & 15, columns (lane >> 4) * 8 ..
+  u32x4 t[N];
+};
+
+template <int N>
+__device__ __forceinline__ Frag<N> split8(const float (&x)[8]) {
+  Frag<N> f;
+  const float a[4] = {x[0], x[1], x[2], x[3]}, b[4] = {x[4], x[5], x[6], x[7]};
+  u32x2 ta[N], tb[N];
+  split4<N>(a, ta);
+  split4<N>(b, tb);
+#pragma unroll
+  for (int n = 0; n < N; ++n) f.t[n] = u32x4{ta[n].x, ta[n].y, tb[n].x, tb[n].y};
+  return f;
+}
+
+template <int N>
+__device__ __forceinline__ Frag<N> load_frag(const uint16_t* p, int64_t plane) {
+  Frag<N> f;
+#pragma unroll
+  for (int n = 0; n < N; ++n) f.t[n] = *reinterpret_cast<const u32x4*>(p + n * plane);
+  return f;
+}
+
+template <int N>
+__device__ __forceinline__ Frag<N> load_frag_if(bool ok, const uint16_t* p, int64_t plane) {
+  if (ok) return load_frag<N>(p, plane);
+  Frag<N> f;
+#pragma unroll
+  for (int n = 0; n < N; ++n) f.t[n] = u32x4{0, 0, 0, 0};
+  return f;
+}
+
+// acc += A B^T over 32 columns.  Of the products of terms i and j those with
+// i + j below the number of terms are taken, the smallest first: what is left
+// out is below what the terms themselves leave out.  Result: column lane & 15,
+// rows (lane >> 4) * 4 + r.
+template <int NA, int NB>
+__device__ __forceinline__ void mma(f32x4& acc, const Frag<NA>& a, const Frag<NB>& b) {
+  constexpr int M = NA > NB ? NA : NB;
+#pragma unroll
+  for (int s = M - 1; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      const int j = s - i;
+      if (j >= 0 && j < NB)
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a.t[i]),
+                                                      __builtin_bit_cast(bf16x8, b.t[j]), acc, 0,
+                                                      0, 0);
+    }
+}
+
+// Four consecutive values of one row into the planes of an LDS array.
+template <int N>
+__device__ __forceinline__ void put4(uint16_t* dst, int plane, const float (&x)[4]) {
+  u32x2 t[N];
+  split4<N>(x, t);
+#pragma unroll
+  for (int n = 0; n < N; ++n) *reinterpret_cast<u32x2*>(dst + n * plane) = t[n];
+}
+
+// A row-major operand: the caller's bfloat16 rows, or planes in the workspace.
+struct Rows {
+  const uint16_t* p;
+  int64_t row, plane;
+  int len;  // rows that exist; the others count as zero
+};
+
+template <int DK>
+__device__ __forceinline__ Rows rows_of(const Params& p, const void* user, const uint16_t* ws,
+                                        int64_t stride, bool per_head, int slot, int h,
+                                        const Chunk& c) {
+  const int group = p.heads / p.heads_qk;
+  Rows r;
+  if (p.direct) {
+    r.p = static_cast<const uint16_t*>(user) + c.row * stride + (int64_t)(h / group) * DK;
+    r.row = stride;
+    r.plane = 0;
+    r.len = c.len;
+  } else {
+    const int64_t sh = per_head ? (int64_t)slot * p.heads + h
+                                : (int64_t)slot * p.heads_qk + h / group;
+    r.p = ws + sh * p.terms * C * DK;
+    r.row = DK;
+    r.plane = C * DK;
+    r.len = C;
+  }
+  return r;
+}
+
+__device__ __forceinline__ float* rows_at(const Params& p, int slot, int h) {
+  return p.rows + ((int64_t)slot * p.heads + h) * (5 * C);
+}
+
+// Sum over the 16 lanes that hold one row of a product.
+__device__ __forceinline__ float sum16(float x) {
+  x += __shfl_xor(x, 1);
+  x += __shfl_xor(x, 2);
+  x += __shfl_xor(x, 4);
+  x += __shfl_xor(x, 8);
+  return x;
+}
+
+}  // namespace qscan

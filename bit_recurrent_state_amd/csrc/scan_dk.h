@@ -1,0 +1,83 @@
+// scan_dk.h — launches of the scan's kernels for one dk (one translation unit
+// each).
+
+#pragma once
+
+#include "scan_chain.h"
+#include "scan_grads.h"
+#include "scan_prep.h"
+
+namespace qscan {
+
+inline dim3 chain_grid(const Params& p) {
+  const int64_t heads = ((int64_t)p.batch * p.heads + 7) / 8 * 8;
+  return dim3((unsigned)(heads * p.nvb));
+}
+
+template <int DK, int NT, int NPQ, bool VEC, bool DELTA>
+hipError_t forward_tail(const Params& p, hipStream_t s) {
+  const dim3 slots(p.nslots, p.heads);
+  if (VEC) {
+    operands_vector_kernel<DK, DELTA, false><<<slots, DK, 0, s>>>(p);
+    chunk_vector_kernel<DK, DELTA, false><<<slots, 256, 0, s>>>(p);
+  } else {
+    operands_kernel<DK><<<dim3(p.nslots, p.heads_qk), 256, 0, s>>>(p, 0);
+    chunk_scalar_kernel<DK, NPQ, DELTA, false><<<slots, 256, 0, s>>>(p);
+  }
+  states_kernel<DK, NT, NPQ, VEC, DELTA, false><<<chain_grid(p), 256, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+template <int DK, int NT, int NPQ, int NPO, bool VEC, bool DELTA>
+hipError_t backward_tail(const Params& p, hipStream_t s) {
+  const dim3 slots(p.nslots, p.heads);
+  if (p.nslots > 0) {
+    operands_kernel<DK><<<dim3(p.nslots, p.heads_qk), 256, 0, s>>>(p, 1);
+    if (VEC) {
+      operands_vector_kernel<DK, DELTA, true><<<slots, DK, 0, s>>>(p);
+      chunk_vector_kernel<DK, DELTA, true><<<slots, 256, 0, s>>>(p);
+    } else {
+      chunk_scalar_kernel<DK, NPQ, DELTA, true><<<slots, 256, 0, s>>>(p);
+    }
+  }
+  states_kernel<DK, NT, NPQ, VEC, DELTA, true><<<chain_grid(p), 256, 0, s>>>(p);
+  state_grads_kernel<DK, NT, NPQ, NPO, VEC, DELTA><<<chain_grid(p), 256, 0, s>>>(p);
+  if (VEC)
+    grads_vector_kernel<DK, NPO, NPO, DELTA><<<slots, 256, 0, s>>>(p);
+  else
+    grads_scalar_kernel<DK, NPQ, NPO, DELTA><<<slots, 256, 0, s>>>(p);
+  if (p.heads != p.heads_qk) share_kernel<DK><<<dim3(p.nslots, p.heads_qk), 256, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+// Operand kinds: the caller's bfloat16 rows (one term); rows split into terms
+// (FP32, FP16, unaligned bfloat16); rows scaled per channel (always split).
+template <int DK, int NT>
+hipError_t forward(const Params& p, hipStream_t s) {
+  switch (p.mixer) {
+    case GDN: return p.direct ? forward_tail<DK, NT, 1, false, true>(p, s)
+                              : forward_tail<DK, NT, P, false, true>(p, s);
+    case SCALAR: return p.direct ? forward_tail<DK, NT, 1, false, false>(p, s)
+                                 : forward_tail<DK, NT, P, false, false>(p, s);
+    case GLA: return forward_tail<DK, NT, P, true, false>(p, s);
+    case KDA: return forward_tail<DK, NT, P, true, true>(p, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+template <int DK, int NT>
+hipError_t backward(const Params& p, hipStream_t s) {
+  switch (p.mixer) {
+    case GDN: return p.direct ? backward_tail<DK, NT, 1, 1, false, true>(p, s)
+                              : backward_tail<DK, NT, P, P, false, true>(p, s);
+    case SCALAR: return p.direct ? backward_tail<DK, NT, 1, 1, false, false>(p, s)
+                                 : backward_tail<DK, NT, P, P, false, false>(p, s);
+    case GLA: return p.dtype == 1 ? backward_tail<DK, NT, P, 1, true, false>(p, s)
+                                  : backward_tail<DK, NT, P, P, true, false>(p, s);
+    case KDA: return p.dtype == 1 ? backward_tail<DK, NT, P, 1, true, true>(p, s)
+                                  : backward_tail<DK, NT, P, P, true, true>(p, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace qscan

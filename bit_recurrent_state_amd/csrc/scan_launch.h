@@ -1,0 +1,60 @@
+// scan_launch.h — what the host side (scan_api.cpp) hands to the scan's
+// kernels: one parameter block with the caller's arrays and the workspace's
+// regions, and one launcher per dk.
+
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+
+#include <cstdint>
+
+namespace qscan {
+
+constexpr int kChunk = 64;  // tokens of a chunk
+constexpr int kTerms = 3;   // bfloat16 terms of an FP32 operand
+
+// Workspace arrays hold bfloat16 terms as planes: [...][term][row][col].
+// "slot" is a chunk of a sequence: sequence n owns the slots from
+// offsets[n] / kChunk + n on, so slots need no prefix sums and never overlap.
+struct Params {
+  int batch, heads, heads_qk, dk, dv, mixer, dtype, direct;
+  int terms;     // planes of q and k: 1 (direct bfloat16) or kTerms
+  int nslots;    // upper bound of the slots in use
+  int nvb;       // blocks of dv columns of one head
+  int vblock;    // dv columns of a block
+  int64_t tokens;
+  int64_t qs, ks, vs, os;  // row strides in elements
+  const void *q, *k, *v, *dO;
+  const float *g, *beta;
+  const int64_t* offsets;
+  const float *s0, *ds1;
+  void *o, *dq, *dkk, *dv_out;
+  float *s1, *dg, *dbeta, *ds0;
+  // workspace
+  float* rows;               // [slot][head][5][kChunk]: exp(c), exp(c_end - c), beta, c (double)
+  float* decay;              // [slot][head][dk] exp(c_end) (per-channel gates)
+  uint16_t *qrow, *krow;     // [slot][head|head_qk][term][kChunk][dk]
+  uint16_t *korow;           // per-channel gates, backward: k exp(c_end - c)
+  uint16_t *kt, *qt, *ket;   // [slot][head|head_qk][term][dk][kChunk]
+  uint16_t *kt_raw, *qt_raw; // per-channel gates, backward: unscaled, per q/k head
+  float *sfx, *pfx;          // per-channel gates, backward: [slot][head][dk][kChunk], decays
+                             // from the token to its block of 16's end, and from its start
+  uint16_t *a, *t;           // [slot][head][kTerms][kChunk][kChunk]
+  uint16_t *at, *t2t;        // backward: transposed A, transposed (I + beta L)^-1
+  uint16_t* dop;             // [slot][head][term][kChunk][dvp] d_o as planes
+  uint16_t *u, *y;           // [slot][head][kTerms][kChunk][dvp]
+  float *sc, *xc;            // [slot][head][dk][dvp]: states / state gradients
+  float* dbpart;             // [nvb][slot][head][kChunk]
+  float *dqpart, *dkpart;    // [slot][head][kChunk][dk] when heads share q and k
+  int dvp;                   // dv rounded up to 32
+  int dop_terms;
+};
+
+hipError_t forward_dk64(const Params& p, hipStream_t s);
+hipError_t forward_dk128(const Params& p, hipStream_t s);
+hipError_t forward_dk256(const Params& p, hipStream_t s);
+hipError_t backward_dk64(const Params& p, hipStream_t s);
+hipError_t backward_dk128(const Params& p, hipStream_t s);
+hipError_t backward_dk256(const Params& p, hipStream_t s);
+
+}  // namespace qscan

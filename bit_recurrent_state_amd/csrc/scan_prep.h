@@ -1,0 +1,487 @@
+// scan_prep.h — the parts of the scan that every chunk computes for itself:
+// the operands' transposes and terms, the decays, A and (I + L beta)^-1.
+
+#pragma once
+
+#include "scan_device.h"
+
+namespace qscan {
+
+// ---- transposes and terms of q and k --------------------------------------------------------
+// One workgroup per (slot, q/k head).  Threads run over channels, so the
+// caller's rows are read whole; each thread turns 8 tokens of its channel into
+// 16 bytes of the transposed planes.
+template <int DK>
+__global__ void __launch_bounds__(256) operands_kernel(Params p, int backward) {
+  const int slot = blockIdx.x, hq = blockIdx.y;
+  Chunk c;
+  if (!find_chunk(p, slot, c)) return;
+  const bool vec = p.mixer == GLA || p.mixer == KDA;
+  const int terms = vec ? (p.dtype == 1 ? 1 : P) : p.terms;
+  const int64_t sh = (int64_t)slot * p.heads_qk + hq;
+  for (int which = 0; which < 2; ++which) {
+    if (which == 1 && !backward && p.direct) break;
+    const void* src = which ? p.q : p.k;
+    const int64_t stride = which ? p.qs : p.ks;
+    uint16_t* tr = vec ? (which ? p.qt_raw : p.kt_raw) : (which ? p.qt : p.kt);
+    uint16_t* rw = which ? p.qrow : p.krow;
+    const bool transpose = which == 0 || backward;
+    for (int u = threadIdx.x; u < DK * (C / 8); u += 256) {
+      const int ch = u % DK, t0 = u / DK * 8;
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        x[i] = t0 + i < c.len
+                   ? load_elem(src, (c.row + t0 + i) * stride + (int64_t)hq * DK + ch, p.dtype)
+                   : 0.0f;
+      const Frag<P> f = split8<P>(x);
+      for (int n = 0; n < terms; ++n) {
+        const u32x4 t = n == 0 ? f.t[0] : n == 1 ? f.t[1] : f.t[2];
+        if (transpose)
+          *reinterpret_cast<u32x4*>(tr + ((sh * terms + n) * DK + ch) * C + t0) = t;
+        if (!p.direct && !vec) {
+          const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            rw[((sh * terms + n) * C + t0 + i) * DK + ch] =
+                (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+        }
+      }
+    }
+  }
+}
+
+// ---- (I + M)^-1 of a strictly lower triangular M --------------------------------------------
+// Forward substitution, one wave, a column per lane: row i of the inverse is
+// e_i - sum_{m<i} M_im x_m, with M's rows read from LDS as broadcasts.
+__device__ __forceinline__ void invert64(const float (*M)[C + 4], float (&x)[C], int lane) {
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int m = 0; m < i; m += 4) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(&M[i][m]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (m + j < i) s[j] = fmaf(v[j], x[m + j], s[j]);
+    }
+    x[i] = (lane == i ? 1.0f : 0.0f) - ((s[0] + s[1]) + (s[2] + s[3]));
+  }
+}
+
+__device__ __forceinline__ void store_term_rows(uint16_t* dst, int col, const float (&x)[C]) {
+  // x: one column of [C][C]; lanes are the columns
+#pragma unroll
+  for (int i = 0; i < C; i += 4) {
+    const float v[4] = {x[i], x[i + 1], x[i + 2], x[i + 3]};
+    u32x2 t[P];
+    split4<P>(v, t);
+#pragma unroll
+    for (int n = 0; n < P; ++n) {
+      uint16_t* d = dst + (n * C + i) * C + col;
+      d[0] = (uint16_t)t[n].x;
+      d[C] = (uint16_t)(t[n].x >> 16);
+      d[2 * C] = (uint16_t)t[n].y;
+      d[3 * C] = (uint16_t)(t[n].y >> 16);
+    }
+  }
+}
+
+__device__ __forceinline__ void store_term_cols(uint16_t* dst, int row, const float (&x)[C]) {
+  // x as a row of [C][C]; lanes are the rows
+#pragma unroll
+  for (int i = 0; i < C; i += 8) {
+    const float v[8] = {x[i], x[i + 1], x[i + 2], x[i + 3], x[i + 4], x[i + 5], x[i + 6], x[i + 7]};
+    const Frag<P> f = split8<P>(v);
+#pragma unroll
+    for (int n = 0; n < P; ++n)
+      *reinterpret_cast<u32x4*>(dst + (n * C + row) * C + i) = f.t[n];
+  }
+}
+
+// What follows once M (scaled) lies in LDS: wave 0 inverts I + L diag(beta),
+// wave 1 (backward) I + diag(beta) L and stores it transposed.
+template <bool BWD>
+__device__ __forceinline__ void store_inverses(const Params& p, float (*M)[C + 4],
+                                               float (*M2)[C + 4], int64_t sh) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  if (wave == 0) {
+    float x[C];
+    invert64(M, x, lane);
+    store_term_rows(p.t + sh * P * C * C, lane, x);
+  }
+  if (BWD && wave == 1) {
+    float x[C];
+    invert64(M2, x, lane);
+    store_term_cols(p.t2t + sh * P * C * C, lane, x);
+  }
+}
+
+// d_o as planes of rows, where the backward kernels cannot take the caller's.
+__device__ __forceinline__ void store_dop(const Params& p, const Chunk& c, int64_t sh, int h) {
+  if (!p.dop) return;
+  for (int u = threadIdx.x; u < C * (p.dvp / 8); u += blockDim.x) {
+    const int t = u / (p.dvp / 8), v0 = u % (p.dvp / 8) * 8;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[i] = t < c.len && v0 + i < p.dv
+                 ? load_elem(p.dO, ((c.row + t) * p.heads + h) * p.dv + v0 + i, p.dtype)
+                 : 0.0f;
+    const Frag<P> f = split8<P>(x);
+    for (int n = 0; n < p.dop_terms; ++n)
+      *reinterpret_cast<u32x4*>(p.dop + ((sh * p.dop_terms + n) * C + t) * p.dvp + v0) =
+          n == 0 ? f.t[0] : n == 1 ? f.t[1] : f.t[2];
+  }
+}
+
+// ---- one gate per token ---------------------------------------------------------------------
+// One workgroup per (slot, head).  Sums of log decays are kept in 64 bits:
+// the differences c_i - c_j of a chunk that decays far are then still exact.
+// Forward: A; backward: its transpose (and both inverses).
+template <int DK, int NPQ, bool DELTA, bool BWD>
+__global__ void __launch_bounds__(256) chunk_scalar_kernel(Params p) {
+  __shared__ double cs[C];
+  __shared__ float bs[C];
+  __shared__ float M[DELTA ? C : 1][C + 4];
+  __shared__ float M2[DELTA && BWD ? C : 1][C + 4];
+  const int slot = blockIdx.x, h = blockIdx.y;
+  Chunk c;
+  if (!find_chunk(p, slot, c)) return;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t sh = (int64_t)slot * p.heads + h;
+  if (wave == 0) {
+    const bool in = lane < c.len;
+    const int64_t at = (c.row + lane) * p.heads + h;
+    double s = in ? (double)gate(p.g[at]) : 0.0;
+    const float beta = in ? p.beta[at] : 0.0f;
+    for (int d = 1; d < 64; d *= 2) {
+      const double o = __shfl_up(s, d);
+      if (lane >= d) s += o;
+    }
+    const double end = __shfl(s, 63);
+    cs[lane] = s;
+    bs[lane] = beta;
+    float* r = rows_at(p, slot, h);
+    r[lane] = expf((float)s);
+    r[C + lane] = expf((float)(end - s));
+    r[2 * C + lane] = beta;
+    reinterpret_cast<double*>(r + 3 * C)[lane] = s;
+  }
+  __syncthreads();
+  const Rows q = rows_of<DK>(p, p.q, p.qrow, p.qs, false, slot, h, c);
+  const Rows k = rows_of<DK>(p, p.k, p.krow, p.ks, false, slot, h, c);
+  const int fr = lane & 15, fc = (lane >> 4) * 8;
+  const int own = wave * 16 + fr;  // forward: token i; backward: token j
+  const Rows& mine = BWD ? k : q;
+  Frag<NPQ> fm[DK / 32], fk[DK / 32];
+#pragma unroll
+  for (int s = 0; s < DK / 32; ++s) {
+    fm[s] = load_frag_if<NPQ>(own < mine.len, mine.p + own * mine.row + s * 32 + fc, mine.plane);
+    if (DELTA) fk[s] = load_frag_if<NPQ>(own < k.len, k.p + own * k.row + s * 32 + fc, k.plane);
+  }
+  // tile (wave, b): columns own (i forward, j backward), rows of block b
+  for (int b = 0; b < 4; ++b) {
+    f32x4 acc = {0, 0, 0, 0}, acl = {0, 0, 0, 0};
+    const int other = b * 16 + fr;
+    const bool need = BWD ? b >= wave : b <= wave;
+    if (need) {
+      const Rows& his = BWD ? q : k;
+#pragma unroll
+      for (int s = 0; s < DK / 32; ++s) {
+        const Frag<NPQ> f =
+            load_frag_if<NPQ>(other < his.len, his.p + other * his.row + s * 32 + fc, his.plane);
+        mma(acc, f, fm[s]);
+        if (DELTA) {
+          const Frag<NPQ> g =
+              BWD ? load_frag_if<NPQ>(other < k.len, k.p + other * k.row + s * 32 + fc, k.plane)
+                  : f;
+          mma(acl, g, fk[s]);
+        }
+      }
+    }
+    float a[4];
+    const int r0 = b * 16 + (lane >> 4) * 4;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int i = BWD ? r0 + r : own, j = BWD ? own : r0 + r;
+      const float e = i >= j ? expf((float)(cs[i] - cs[j])) : 0.0f;
+      a[r] = i >= j ? acc[r] * e : 0.0f;
+      if (DELTA) {
+        const float l = i > j ? acl[r] * e : 0.0f;
+        M[i][j] = i > j ? l * bs[j] : 0.0f;
+        if (BWD) M2[i][j] = i > j ? bs[i] * l : 0.0f;
+      }
+    }
+    uint16_t* dst = (BWD ? p.at : p.a) + sh * P * C * C;
+    put4<P>(dst + own * C + r0, C * C, a);
+  }
+  if (DELTA) {
+    __syncthreads();
+    store_inverses<BWD>(p, M, M2, sh);
+  }
+  if (BWD) store_dop(p, c, sh, h);
+}
+
+// ---- a gate per key channel -----------------------------------------------------------------
+// Decays between tokens are products of factors of at most 1 and never
+// quotients: inside blocks of 16 tokens prefix sums (first token of the block
+// .. i) and suffix sums (j + 1 .. last), between them whole blocks.  Nothing
+// overflows, and nothing is lost where gates are strong.
+//
+// One workgroup per (slot, head), a thread per channel: the scaled operands
+// q e^c, k e^c and k e^(c_end - c) as rows and as columns.
+template <int DK, bool DELTA, bool BWD>
+__global__ void __launch_bounds__(DK) operands_vector_kernel(Params p) {
+  const int slot = blockIdx.x, h = blockIdx.y, ch = threadIdx.x;
+  Chunk c;
+  if (!find_chunk(p, slot, c)) return;
+  const int64_t sh = (int64_t)slot * p.heads + h;
+  const int hq = h / (p.heads / p.heads_qk);
+  float total[4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int t = b * 16 + i;
+      if (t < c.len) s += gate(p.g[((c.row + t) * p.heads + h) * DK + ch]);
+    }
+    total[b] = s;
+  }
+  p.decay[sh * DK + ch] = expf((total[0] + total[1]) + (total[2] + total[3]));
+  if (ch < C && threadIdx.x < C) {
+    float* r = rows_at(p, slot, h);
+    r[2 * C + ch] = ch < c.len ? (p.beta ? p.beta[(c.row + ch) * p.heads + h] : 1.0f) : 0.0f;
+  }
+  float before = 0.0f;
+#pragma unroll 1
+  for (int b = 0; b < 4; ++b) {
+    float g[16], sfx[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int t = b * 16 + i;
+      g[i] = t < c.len ? gate(p.g[((c.row + t) * p.heads + h) * DK + ch]) : 0.0f;
+    }
+    float after = 0.0f;
+    for (int m = 3; m > b; --m) after += m == 1 ? total[1] : m == 2 ? total[2] : total[3];
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 15; i >= 0; --i) {
+      sfx[i] = s;
+      s += g[i];
+    }
+    float pfx = 0.0f;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float qe[8], ke[8], ko[8], ps[8], ss[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int t = b * 16 + half * 8 + i;
+        pfx += g[half * 8 + i];
+        ps[i] = expf(pfx);
+        ss[i] = expf(sfx[half * 8 + i]);
+        const bool in = t < c.len;
+        const float q = in ? load_elem(p.q, (c.row + t) * p.qs + (int64_t)hq * DK + ch, p.dtype) : 0.0f;
+        const float k = in ? load_elem(p.k, (c.row + t) * p.ks + (int64_t)hq * DK + ch, p.dtype) : 0.0f;
+        const float e = expf(pfx + before);
+        qe[i] = q * e;
+        ke[i] = k * e;
+        ko[i] = k * expf(sfx[half * 8 + i] + after);
+      }
+      const int t0 = b * 16 + half * 8;
+      const Frag<P> fq = split8<P>(qe), fk = split8<P>(ke), fo = split8<P>(ko);
+#pragma unroll
+      for (int n = 0; n < P; ++n) {
+        const uint32_t wq[4] = {fq.t[n].x, fq.t[n].y, fq.t[n].z, fq.t[n].w};
+        const uint32_t wk[4] = {fk.t[n].x, fk.t[n].y, fk.t[n].z, fk.t[n].w};
+        const uint32_t wo[4] = {fo.t[n].x, fo.t[n].y, fo.t[n].z, fo.t[n].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int64_t at = ((sh * P + n) * C + t0 + i) * DK + ch;
+          const int sft = 16 * (i & 1);
+          if (!BWD) p.qrow[at] = (uint16_t)(wq[i / 2] >> sft);
+          if (DELTA) p.krow[at] = (uint16_t)(wk[i / 2] >> sft);
+          if (BWD) p.korow[at] = (uint16_t)(wo[i / 2] >> sft);
+        }
+        const int64_t tt = ((sh * P + n) * DK + ch) * C + t0;
+        *reinterpret_cast<u32x4*>(p.kt + tt) = fo.t[n];
+        if (BWD) *reinterpret_cast<u32x4*>(p.qt + tt) = fq.t[n];
+        if (BWD && DELTA) *reinterpret_cast<u32x4*>(p.ket + tt) = fk.t[n];
+      }
+      if (BWD) {
+        float* dp = p.pfx + (sh * DK + ch) * C + t0;
+        float* ds = p.sfx + (sh * DK + ch) * C + t0;
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          *reinterpret_cast<f32x4*>(dp + i) = f32x4{ps[i], ps[i + 1], ps[i + 2], ps[i + 3]};
+          *reinterpret_cast<f32x4*>(ds + i) = f32x4{ss[i], ss[i + 1], ss[i + 2], ss[i + 3]};
+        }
+      }
+    }
+    before += b == 0 ? total[0] : b == 1 ? total[1] : b == 2 ? total[2] : total[3];
+  }
+}
+
+// A (or its transpose) and the inverses with a gate per channel.  Channels go
+// by slabs of 64.  Blocks of 16 tokens below the diagonal are matrix products
+// of operands scaled towards the boundary between them; the four blocks on the
+// diagonal are summed directly, wave b block b: a lane holds one key's 16
+// channels, multiplies the decay of each later token into them and takes the
+// dot products with that token's q and k.
+template <int DK, bool DELTA, bool BWD>
+__global__ void __launch_bounds__(256) chunk_vector_kernel(Params p) {
+  constexpr int SL = 64, LP = SL + 4;
+  __shared__ float qs[C][LP], ks[C][LP], al[C][LP], px[C][LP], sx[C][LP];
+  __shared__ float tot[4][SL];
+  __shared__ float bs[C];
+  const int slot = blockIdx.x, h = blockIdx.y;
+  Chunk c;
+  if (!find_chunk(p, slot, c)) return;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t sh = (int64_t)slot * p.heads + h;
+  const int hq = h / (p.heads / p.heads_qk);
+  const int fr = lane & 15, cg = lane >> 4;
+  if (threadIdx.x < C)
+    bs[threadIdx.x] = threadIdx.x < c.len
+                          ? (p.beta ? p.beta[(c.row + threadIdx.x) * p.heads + h] : 1.0f)
+                          : 0.0f;
+  f32x4 accA[4], accL[4];
+  float dA[16], dL[16];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) accA[b] = accL[b] = f32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) dA[i] = dL[i] = 0.0f;
+  for (int c0 = 0; c0 < DK; c0 += SL) {
+    __syncthreads();
+    {
+      const int ch = threadIdx.x & 63, b = threadIdx.x >> 6;
+      float g[16], s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int t = b * 16 + i;
+        const bool in = t < c.len;
+        g[i] = in ? gate(p.g[((c.row + t) * p.heads + h) * DK + c0 + ch]) : 0.0f;
+        qs[t][ch] = in ? load_elem(p.q, (c.row + t) * p.qs + (int64_t)hq * DK + c0 + ch, p.dtype) : 0.0f;
+        ks[t][ch] = in ? load_elem(p.k, (c.row + t) * p.ks + (int64_t)hq * DK + c0 + ch, p.dtype) : 0.0f;
+        al[t][ch] = expf(g[i]);
+        s += g[i];
+        px[t][ch] = expf(s);
+      }
+      tot[b][ch] = s;
+      s = 0.0f;
+#pragma unroll
+      for (int i = 15; i >= 0; --i) {
+        sx[b * 16 + i][ch] = expf(s);
+        s += g[i];
+      }
+    }
+    __syncthreads();
+    // below the diagonal: forward wave = block of i, backward = block of j
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const bool need = BWD ? b > wave : b < wave;
+      if (!need) continue;
+      const int I = BWD ? b : wave, J = BWD ? wave : b;
+#pragma unroll
+      for (int s = 0; s < SL / 32; ++s) {
+        const int k0 = s * 32 + cg * 8;
+        float xq[8], xi[8], xj[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float mid = 0.0f;
+          for (int m = J + 1; m < I; ++m) mid += tot[m][k0 + e];
+          const float pi = px[I * 16 + fr][k0 + e];
+          xq[e] = qs[I * 16 + fr][k0 + e] * pi;
+          xi[e] = ks[I * 16 + fr][k0 + e] * pi;
+          xj[e] = ks[J * 16 + fr][k0 + e] * (sx[J * 16 + fr][k0 + e] * expf(mid));
+        }
+        const Frag<P> fq = split8<P>(xq), fj = split8<P>(xj);
+        if (BWD)
+          mma(accA[b], fq, fj);
+        else
+          mma(accA[b], fj, fq);
+        if (DELTA) {
+          const Frag<P> fi = split8<P>(xi);
+          if (BWD)
+            mma(accL[b], fi, fj);
+          else
+            mma(accL[b], fj, fi);
+        }
+      }
+    }
+    // on the diagonal
+    const int t0 = wave * 16;
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      const int k0 = cg * 16 + part * 8;
+      float kj[8], kd[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        kj[e] = ks[t0 + fr][k0 + e];
+        kd[e] = 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const bool first = i == fr;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          kd[e] = first ? kj[e] : kd[e] * al[t0 + i][k0 + e];
+          dA[i] = fmaf(qs[t0 + i][k0 + e], kd[e], dA[i]);
+          if (DELTA) dL[i] = fmaf(ks[t0 + i][k0 + e], kd[e], dL[i]);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  // the slabs' arrays are free now: M over qs, M2 over ks, A over al
+  float(*M)[LP] = qs;
+  float(*M2)[LP] = ks;
+  float(*A)[LP] = al;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    dA[i] += __shfl_xor(dA[i], 16);
+    dA[i] += __shfl_xor(dA[i], 32);
+    if (DELTA) {
+      dL[i] += __shfl_xor(dL[i], 16);
+      dL[i] += __shfl_xor(dL[i], 32);
+    }
+    if (cg == 0) {
+      const int gi = wave * 16 + i, gj = wave * 16 + fr;
+      A[gi][gj] = i >= fr ? dA[i] : 0.0f;
+      if (DELTA) {
+        const float l = i > fr ? dL[i] : 0.0f;
+        M[gi][gj] = i > fr ? l * bs[gj] : 0.0f;
+        if (BWD) M2[gi][gj] = i > fr ? bs[gi] * l : 0.0f;
+      }
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    if (b == wave) continue;
+    const bool need = BWD ? b > wave : b < wave;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = b * 16 + cg * 4 + r, col = wave * 16 + fr;
+      const int i = BWD ? row : col, j = BWD ? col : row;
+      A[i][j] = need ? accA[b][r] : 0.0f;
+      if (DELTA) {
+        M[i][j] = need ? accL[b][r] * bs[j] : 0.0f;
+        if (BWD) M2[i][j] = need ? bs[i] * accL[b][r] : 0.0f;
+      }
+    }
+  }
+  __syncthreads();
+  uint16_t* dst = (BWD ? p.at : p.a) + sh * P * C * C;
+  for (int u = threadIdx.x; u < C * C / 4; u += 256) {
+    const int r = u / (C / 4), q0 = u % (C / 4) * 4;
+    float x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = BWD ? A[q0 + e][r] : A[r][q0 + e];
+    put4<P>(dst + r * C + q0, C * C, x);
+  }
+  if (DELTA) store_inverses<BWD>(p, M, M2, sh);
+  if (BWD) store_dop(p, c, sh, h);
+}
+
+}  // namespace qscan
