@@ -32,6 +32,9 @@ CEILING_EXPORTS = ("qstate_ceiling_copy", "qstate_ceiling_rmw")
 # include/qstate_scan.h: the recurrences over whole sequences and their gradients
 SCAN_EXPORTS = ("qstate_scan_workspace", "qstate_scan", "qstate_scan_backward")
 
+# include/qstate_norm.h: the norms around the mixer block and their gradients
+NORM_EXPORTS = ("qstate_norm", "qstate_norm_workspace", "qstate_norm_backward")
+
 
 class QStateConfig(ctypes.Structure):
     _fields_ = [
@@ -50,6 +53,14 @@ class ScanConfigC(ctypes.Structure):
                                                "dtype", "pad")]
                 + [(n, ctypes.c_int64) for n in ("tokens", "q_stride", "k_stride", "v_stride",
                                                  "o_stride")])
+
+
+class NormConfigC(ctypes.Structure):
+    _fields_ = ([("tokens", ctypes.c_int64)]
+                + [(n, ctypes.c_int32) for n in ("groups", "width", "dtype", "act",
+                                                 "weight_groups")]
+                + [("eps", ctypes.c_float)]
+                + [(n, ctypes.c_int64) for n in ("x_stride", "gate_stride", "residual_stride")])
 
 
 _lib = None
@@ -86,6 +97,10 @@ def lib() -> ctypes.CDLL:
         "qstate_ceiling_rmw": (c_int, [P, sz, ctypes.c_uint32, c_int, P]),
         "qstate_scan_workspace": (c_int, [ctypes.POINTER(ScanConfigC), c_int, ctypes.POINTER(sz)]),
         "qstate_scan": (c_int, [ctypes.POINTER(ScanConfigC)] + [P] * 10 + [sz, P]),
+        "qstate_norm": (c_int, [ctypes.POINTER(NormConfigC)] + [P] * 9),
+        "qstate_norm_workspace": (c_int, [ctypes.POINTER(NormConfigC), ctypes.POINTER(sz)]),
+        "qstate_norm_backward": (c_int, [ctypes.POINTER(NormConfigC)] + [P] * 6 + [c_int]
+                                 + [P] * 9 + [sz, P]),
         "qstate_scan_backward": (c_int, [ctypes.POINTER(ScanConfigC)] + [P] * 16 + [sz, P]),
     }
     for name, (res, args) in sigs.items():

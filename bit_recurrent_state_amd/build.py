@@ -22,14 +22,16 @@ SOURCES = ([os.path.join(CSRC, f"qstate_window_dk{dk}_w{w}.hip")
            + [os.path.join(CSRC, f"qstate_{kind}_dk{dk}.hip")
               for kind in ("value", "key") for dk in (64, 128, 256)]
            + [os.path.join(CSRC, f"scan_dk{dk}.hip") for dk in (256, 128, 64)]
-           + [os.path.join(CSRC, "qstate_ceiling.hip"), os.path.join(CSRC, "scan_api.cpp")]
+           + [os.path.join(CSRC, "qstate_ceiling.hip"), os.path.join(CSRC, "scan_api.cpp"),
+              os.path.join(CSRC, "norm.hip"), os.path.join(CSRC, "norm_api.cpp")]
            + [os.path.join(CSRC, "qstate_dispatch.cpp"), os.path.join(CSRC, "qstate_api.cpp")])
 HEADERS = [os.path.join(ROOT, "include", h) for h in ("qstate.h", "qstate_ceiling.h",
-                                                         "qstate_scan.h")] + [
+                                                         "qstate_scan.h", "qstate_norm.h")] + [
     os.path.join(CSRC, h) for h in ("qstate_launch.h", "qstate_device.h", "qstate_value.h",
                                     "qstate_key.h", "qstate_window.h",
                                     "qstate_persist.h", "scan_launch.h", "scan_device.h",
-                                    "scan_prep.h", "scan_chain.h", "scan_grads.h", "scan_dk.h")]
+                                    "scan_prep.h", "scan_chain.h", "scan_grads.h", "scan_dk.h",
+                                    "norm_launch.h")]
 BUILD = os.path.join(ROOT, "_build")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

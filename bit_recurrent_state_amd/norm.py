@@ -1,0 +1,216 @@
+"""Binding of include/qstate_norm.h: the norms around the mixer block (the
+readout's norm with its gate, the residual with its scale, the next block's
+norm) and their gradients.
+
+`qstate_norm` and `qstate_norm_backward` marshal arguments like the functions
+in qstate.py; `block_norm` is the differentiable operator on top of them."""
+
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from ._lib import NormConfigC, check, lib
+from .scan import DTYPES, _array, _on_device, _stream, _workspace
+
+__all__ = ["SILU", "SIGMOID", "NormConfig", "qstate_norm", "qstate_norm_workspace",
+           "qstate_norm_backward", "block_norm"]
+
+SILU, SIGMOID = 0, 1
+
+
+@dataclass
+class NormConfig:
+    tokens: int
+    groups: int
+    width: int
+    dtype: torch.dtype = torch.float32
+    act: int = SILU
+    weight_groups: bool = False  # weight is [groups][width]
+    eps: float = 1e-6
+    x_stride: int = 0  # elements between two tokens; 0: packed
+    gate_stride: int = 0
+    residual_stride: int = 0
+
+    def to_c(self) -> NormConfigC:
+        if self.dtype not in DTYPES:
+            raise ValueError(f"dtype must be float32, bfloat16 or float16, got {self.dtype}")
+        return NormConfigC(self.tokens, self.groups, self.width, DTYPES[self.dtype], self.act,
+                           int(self.weight_groups), self.eps, self.x_stride, self.gate_stride,
+                           self.residual_stride)
+
+
+def _rows(t, name, cfg: NormConfig, stride, device, optional=True):
+    """Pointer of [tokens][groups][width] rows, tokens `stride` elements apart."""
+    if t is None:
+        if optional:
+            return None
+        raise TypeError(f"{name} is missing")
+    _on_device(t, name, device)
+    want = (cfg.tokens, cfg.groups, cfg.width)
+    if t.dtype != cfg.dtype or tuple(t.shape) != want:
+        raise ValueError(f"{name}: expected {cfg.dtype} {want}, got {t.dtype} {tuple(t.shape)}")
+    ok = ((cfg.width == 1 or t.stride(2) == 1)
+          and (cfg.groups == 1 or t.stride(1) == cfg.width)
+          and (cfg.tokens <= 1 or t.stride(0) == (stride or cfg.groups * cfg.width)))
+    if t.numel() and not ok:
+        raise ValueError(f"{name}: strides {t.stride()} are not "
+                         f"{stride or cfg.groups * cfg.width} elements between tokens with packed "
+                         "rows")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _inputs(cfg: NormConfig, x, weight, gate, residual, scale, next_weight):
+    _on_device(x, "x", None)
+    dev, f32 = x.device, torch.float32
+    nw = cfg.width * (cfg.groups if cfg.weight_groups else 1)
+    return (
+        _rows(x, "x", cfg, cfg.x_stride, dev, optional=False),
+        _array(weight, "weight", f32, nw, dev, optional=True),
+        _rows(gate, "gate", cfg, cfg.gate_stride, dev),
+        _rows(residual, "residual", cfg, cfg.residual_stride, dev),
+        _array(scale, "scale", f32, cfg.width, dev, optional=True),
+        _array(next_weight, "next_weight", f32, cfg.width, dev, optional=True),
+    )
+
+
+def qstate_norm(cfg: NormConfig, x, weight=None, gate=None, residual=None, scale=None,
+                next_weight=None, r=None, h=None, stream=None) -> None:
+    """r = residual + scale * act(gate) * rms(x) weight into `r`, rms(r) next_weight into `h`."""
+    args = _inputs(cfg, x, weight, gate, residual, scale, next_weight)
+    dev = x.device
+    out = _rows(r, "r", cfg, 0, dev), _rows(h, "h", cfg, 0, dev)
+    with torch.cuda.device(dev):
+        c = cfg.to_c()
+        check("qstate_norm", lib().qstate_norm(ctypes.byref(c), *args, *out, _stream(stream, dev)))
+
+
+def qstate_norm_workspace(cfg: NormConfig) -> int:
+    n = ctypes.c_size_t()
+    c = cfg.to_c()
+    check("qstate_norm_workspace", lib().qstate_norm_workspace(ctypes.byref(c), ctypes.byref(n)))
+    return n.value
+
+
+def qstate_norm_backward(cfg: NormConfig, x, weight=None, gate=None, residual=None, scale=None,
+                         next_weight=None, has_h=False, dr=None, dh=None, dx=None, dgate=None,
+                         dresidual=None, dweight=None, dscale=None, dnext_weight=None,
+                         workspace=None, stream=None) -> None:
+    """Gradients from `dr` and `dh`; outputs that are None are not wanted."""
+    args = _inputs(cfg, x, weight, gate, residual, scale, next_weight)
+    dev, f32 = x.device, torch.float32
+    nw = cfg.width * (cfg.groups if cfg.weight_groups else 1)
+    more = [_rows(t, n, cfg, 0, dev) for t, n in
+            ((dr, "dr"), (dh, "dh"), (dx, "dx"), (dgate, "dgate"), (dresidual, "dresidual"))]
+    more += [_array(dweight, "dweight", f32, nw, dev, optional=True),
+             _array(dscale, "dscale", f32, cfg.width, dev, optional=True),
+             _array(dnext_weight, "dnext_weight", f32, cfg.width, dev, optional=True)]
+    with torch.cuda.device(dev):
+        if workspace is None and any(t is not None for t in (dweight, dscale, dnext_weight)):
+            workspace = torch.empty(max(qstate_norm_workspace(cfg), 1), dtype=torch.uint8,
+                                    device=dev)
+        pw, nb = (None, 0) if workspace is None else _workspace(workspace, dev)
+        c = cfg.to_c()
+        check("qstate_norm_backward", lib().qstate_norm_backward(
+            ctypes.byref(c), *args, int(has_h), *more, pw, nb, _stream(stream, dev)))
+
+
+def _token_rows(t, groups, width):
+    """[.., width] as [tokens][groups][width]; a copy only where tokens do not lie at one distance
+    with packed rows in them."""
+    if t is None:
+        return None, 0
+    try:
+        r = t.view(-1, groups, width)
+    except RuntimeError:
+        r = t.reshape(-1, groups, width)
+    packed = (width == 1 or r.stride(2) == 1) and (groups == 1 or r.stride(1) == width)
+    if not packed or (r.shape[0] > 1 and r.stride(0) < groups * width):
+        r = r.clone(memory_format=torch.contiguous_format)
+    return r, 0 if r.shape[0] <= 1 or r.stride(0) == groups * width else r.stride(0)
+
+
+class _BlockNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, gate, residual, scale, next_weight, eps, act):
+        width = x.shape[-1]
+        each = weight is not None and weight.dim() == 2
+        # a weight per group: the group is the last but one dimension; else every row is alike,
+        # and [tokens][groups] only says how x's rows lie
+        groups = x.shape[-2] if x.dim() >= 2 and (each or x.dim() > 2) else 1
+        if each:
+            groups = weight.shape[0]
+        rows = [_token_rows(t, groups, width) for t in (x, gate, residual)]
+        x3, gate3, res3 = (t for t, _ in rows)
+        par = [None if t is None else t.contiguous() for t in (weight, scale, next_weight)]
+        cfg = NormConfig(x3.shape[0], groups, width, x.dtype, act, each, eps,
+                         *(s for _, s in rows))
+        r = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        h = torch.empty_like(r) if next_weight is not None else None
+        qstate_norm(cfg, x3, par[0], gate3, res3, par[1], par[2], r.view(x3.shape),
+                    None if h is None else h.view(x3.shape))
+        ctx.cfg, ctx.shape = cfg, x.shape
+        ctx.save_for_backward(x3, par[0], gate3, res3, par[1], par[2])
+        ctx.set_materialize_grads(False)
+        return r if h is None else (r, h)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dr, dh=None):
+        x, weight, gate, residual, scale, next_weight = ctx.saved_tensors
+        cfg = ctx.cfg
+        if dr is None and dh is None:
+            return (None,) * 8
+        need = ctx.needs_input_grad
+
+        def like_x(wanted):
+            return torch.empty(x.shape, dtype=x.dtype, device=x.device) if wanted else None
+
+        def like(t, wanted):
+            return torch.empty_like(t) if wanted else None
+
+        dr, dh = (None if t is None else t.contiguous().view(x.shape) for t in (dr, dh))
+        dx, dgate, dres = like_x(need[0]), like_x(need[2]), like_x(need[3])
+        dw, ds, dnw = like(weight, need[1]), like(scale, need[4]), like(next_weight, need[5])
+        qstate_norm_backward(cfg, x, weight, gate, residual, scale, next_weight,
+                             next_weight is not None, dr, dh, dx, dgate, dres, dw, ds, dnw)
+        dx, dgate, dres = (None if t is None else t.view(ctx.shape) for t in (dx, dgate, dres))
+        return dx, dw, dgate, dres, ds, dnw, None, None
+
+
+def block_norm(x, *, weight=None, gate=None, residual=None, scale=None, next_weight=None,
+               eps: float = 1e-6, act: int = SILU):
+    """The end of a mixer block in one pass over its rows, over the last dimension of x:
+
+        r = residual + scale * act(gate) * (x * rsqrt(mean(x^2) + eps) * weight)
+        h = r * rsqrt(mean(r^2) + eps) * next_weight
+
+    Parts that are None are left out; returns r, or (r, h) with next_weight.  x, gate and residual
+    have one shape [.., width] and one dtype (float32, bfloat16, float16); weight is float32
+    [width], or [heads, width] for x [.., heads, width]; scale and next_weight float32 [width].
+    FP32 between inputs and outputs.  Differentiable once in every tensor."""
+    _on_device(x, "x", None)
+    if x.dtype not in DTYPES or x.dim() < 1:
+        raise ValueError(f"x: one of float32, bfloat16, float16 [.., width], got {x.dtype} "
+                         f"{tuple(x.shape)}")
+    if act not in (SILU, SIGMOID):
+        raise ValueError(f"act: {act}")
+    for t, name in ((gate, "gate"), (residual, "residual")):
+        if t is not None:
+            _on_device(t, name, x.device)
+            if t.shape != x.shape or t.dtype != x.dtype:
+                raise ValueError(f"{name}: expected {x.dtype} {tuple(x.shape)}, got {t.dtype} "
+                                 f"{tuple(t.shape)}")
+    width = x.shape[-1]
+    for t, name in ((weight, "weight"), (scale, "scale"), (next_weight, "next_weight")):
+        if t is None:
+            continue
+        _on_device(t, name, x.device)
+        each = name == "weight" and t.dim() == 2
+        want = (x.shape[-2] if x.dim() > 1 else -1, width) if each else (width,)
+        if tuple(t.shape) != want or t.dtype != torch.float32:
+            raise ValueError(f"{name}: expected float32 {want}, got {t.dtype} {tuple(t.shape)}")
+    return _BlockNorm.apply(x, weight, gate, residual, scale, next_weight, eps, act)
