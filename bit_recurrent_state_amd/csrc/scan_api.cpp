@@ -40,7 +40,7 @@ int check_config(const qstate_scan_config* c) {
     return QSTATE_E_UNSUPPORTED;
   // the grids: chunks of all sequences, and a workgroup per head and column block
   if (c->tokens / kChunk + c->batch > 2147483647 ||
-      (int64_t)c->batch * c->heads * ((c->dv + 31) / 32) > 2000000000)
+      (int64_t)c->batch * c->heads * ((c->dv + 31) / 32) > 1000000000)
     return QSTATE_E_UNSUPPORTED;
   return QSTATE_OK;
 }
@@ -77,8 +77,8 @@ size_t layout(const qstate_scan_config* c, bool backward, void* workspace, Param
   p.direct = !vec && bf16 && p.qs % 8 == 0 && p.ks % 8 == 0;
   p.terms = p.direct ? 1 : kTerms;
   p.nslots = (int)(c->tokens / kChunk + c->batch);
-  p.vblock = 32;
-  p.dvp = (c->dv + p.vblock - 1) / p.vblock * p.vblock;
+  p.dvp = (c->dv + 31) / 32 * 32;
+  p.vblock = (int64_t)c->batch * c->heads * (p.dvp / 32) < 256 ? 16 : 32;
   p.nvb = p.dvp / p.vblock;
   p.dop_terms = bf16 ? 1 : kTerms;
 
@@ -88,7 +88,9 @@ size_t layout(const qstate_scan_config* c, bool backward, void* workspace, Param
   const uint64_t square = sh * kTerms * kChunk * kChunk;
   w.take(p.rows, sh * 5 * kChunk, true);
   w.take(p.decay, sh * p.dk, vec);
-  w.take(p.qrow, ops, !p.direct && (!vec || !backward));
+  w.take(p.far, sh, vec);
+  w.take(p.knrow, ops, vec);
+  w.take(p.qrow, ops, !p.direct);
   w.take(p.krow, ops, !p.direct && (!vec || delta));
   w.take(p.kt, ops, true);
   w.take(p.a, square, !backward);
@@ -98,6 +100,7 @@ size_t layout(const qstate_scan_config* c, bool backward, void* workspace, Param
     w.take(p.korow, ops, vec);
     w.take(p.qt, ops, true);
     w.take(p.ket, ops, vec && delta);
+    w.take(p.knt, ops, vec);
     w.take(p.kt_raw, raw, vec);
     w.take(p.qt_raw, raw, vec);
     w.take(p.pfx, sh * tile, vec);
@@ -105,7 +108,7 @@ size_t layout(const qstate_scan_config* c, bool backward, void* workspace, Param
     w.take(p.at, square, true);
     w.take(p.t2t, square, delta);
     // d_o's rows serve as they are where they are bfloat16 and fill whole blocks
-    w.take(p.dop, sh * p.dop_terms * kChunk * p.dvp, !(bf16 && c->dv % p.vblock == 0));
+    w.take(p.dop, sh * p.dop_terms * kChunk * p.dvp, !(bf16 && c->dv % 32 == 0));
     w.take(p.u, sh * kTerms * kChunk * p.dvp, true);
     w.take(p.y, sh * kTerms * kChunk * p.dvp, delta);
     w.take(p.sc, sh * p.dk * p.dvp, true);

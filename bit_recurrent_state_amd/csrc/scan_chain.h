@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(256) states_kernel(Params p) {
   constexpr int BV = 16 * NT, KS = DK / 32, MT = DK / 64, SP = DK + 8;
   __shared__ __align__(16) uint16_t Sl[P][BV][SP];
   __shared__ __align__(16) uint16_t Rt[DELTA ? P : 1][DELTA ? BV : 1][CP];
-  __shared__ __align__(16) uint16_t Wt[SAVE ? 1 : P][SAVE ? 1 : BV][CP];
+  __shared__ __align__(16) uint16_t Wt[SAVE || VEC ? 1 : P][SAVE || VEC ? 1 : BV][CP];
   __shared__ __align__(16) uint16_t Wb[P][BV][CP];  // e^(c_end - c) W (one gate), else W
   int n, h, vb;
   if (!chain_block(p, n, h, vb)) return;
@@ -74,15 +74,91 @@ __global__ void __launch_bounds__(256) states_kernel(Params p) {
   if (DELTA || !SAVE) put_state();
   __syncthreads();
 
-  for (int ci = 0; ci < nch; ++ci) {
-    const int slot = base + ci;
+  // Rows behind a sequence's end repeat its last row: beta is zero there, so
+  // what they compute reaches neither the state nor an output.
+  // A chunk's operands, each loaded again for the next chunk right after its
+  // last use: the loads have most of a chunk's time to arrive and need no
+  // second set of registers.
+  constexpr bool KQ = DELTA || !SAVE;
+  Frag<NPQ> fq[SAVE ? 1 : KS], fk[DELTA ? KS : 1], ft[MT][2];
+  Frag<P> fT[DELTA ? 2 : 1], fA[SAVE ? 1 : 2];
+  uint32_t v[NT][4];
+  f32x4 beta, ec = {1, 1, 1, 1}, eo = {1, 1, 1, 1}, dec[MT];
+  const int own = wave * 16 + fr;
+  auto chunk = [&](int ci) {
     Chunk c;
     c.n = n;
     c.ci = ci;
     c.row = o0 + (int64_t)ci * C;
     c.len = len - (int64_t)ci * C < C ? (int)(len - (int64_t)ci * C) : C;
+    return c;
+  };
+  auto load_kq = [&](int ci) {
+    const Chunk c = chunk(ci);
+    if (DELTA) {
+      const Rows kr = rows_of<DK>(p, p.k, p.krow, p.ks, VEC, base + ci, h, c);
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+        fk[s] = load_frag<NPQ>(kr.p + min(own, kr.len - 1) * kr.row + s * 32 + fg * 8, kr.plane);
+    }
+    if (!SAVE) {
+      const Rows qr = rows_of<DK>(p, p.q, p.qrow, p.qs, VEC, base + ci, h, c);
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+        fq[s] = load_frag<NPQ>(qr.p + min(own, qr.len - 1) * qr.row + s * 32 + fg * 8, qr.plane);
+    }
+  };
+  auto load_v = [&](int ci) {
+    const Chunk c = chunk(ci);
+    const float* rows = rows_at(p, base + ci, h);
+    beta = *reinterpret_cast<const f32x4*>(rows + 2 * C + tok);
+    if (!VEC) {
+      ec = *reinterpret_cast<const f32x4*>(rows + tok);
+      eo = *reinterpret_cast<const f32x4*>(rows + C + tok);
+    }
+    // places outside the sequence or the head read a valid neighbour and count as zero later
+    int64_t at[4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        at[r] = (c.row + min(tok + r, c.len - 1)) * p.vs + (int64_t)h * p.dv + min(vcol[t], p.dv - 1);
+      load_raw<4>(p.v, at, p.dtype, v[t]);
+    }
+  };
+  auto load_square = [&](const uint16_t* m, int ci, Frag<P>* f) {
+    const uint16_t* at = m + ((int64_t)(base + ci) * p.heads + h) * P * C * C + own * C + fg * 8;
+    f[0] = load_frag<P>(at, C * C);
+    f[1] = load_frag<P>(at + 32, C * C);
+  };
+  auto load_t = [&](int ci) {
+    const int slot = base + ci;
     const int64_t sh = (int64_t)slot * p.heads + h;
-    const float* rows = rows_at(p, slot, h);
+    const int64_t th = VEC ? sh : (int64_t)slot * p.heads_qk + h / (p.heads / p.heads_qk);
+    const uint16_t* kt = p.kt + th * NPQ * DK * C;
+    const float end = VEC ? 1.0f : rows_at(p, slot, h)[C - 1];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        ft[m][s] = load_frag<NPQ>(
+            kt + (int64_t)(wave * (DK / 4) + 16 * m + fr) * C + s * 32 + fg * 8, DK * C);
+      dec[m] = VEC ? *reinterpret_cast<const f32x4*>(p.decay + sh * DK + d0 + 16 * m)
+                   : f32x4{end, end, end, end};
+    }
+  };
+  if (nch > 0) {
+    load_kq(0);
+    load_v(0);
+    if (DELTA) load_square(p.t, 0, fT);
+    if (!SAVE) load_square(p.a, 0, fA);
+    load_t(0);
+  }
+
+  for (int ci = 0; ci < nch; ++ci) {
+    const Chunk c = chunk(ci);
+    const int64_t sh = (int64_t)(base + ci) * p.heads + h;
+    const int next = min(ci + 1, nch - 1);  // loads without a branch: the last chunk's again
     if (SAVE) {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
@@ -96,16 +172,7 @@ __global__ void __launch_bounds__(256) states_kernel(Params p) {
     f32x4 kS[NT], qS[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) kS[t] = qS[t] = f32x4{0, 0, 0, 0};
-    if (DELTA || !SAVE) {
-      const Rows qr = rows_of<DK>(p, p.q, p.qrow, p.qs, VEC, slot, h, c);
-      const Rows kr = rows_of<DK>(p, p.k, p.krow, p.ks, VEC, slot, h, c);
-      const int own = wave * 16 + fr;
-      Frag<NPQ> fq[KS], fk[KS];
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        if (DELTA) fk[s] = load_frag_if<NPQ>(own < kr.len, kr.p + own * kr.row + s * 32 + fg * 8, kr.plane);
-        if (!SAVE) fq[s] = load_frag_if<NPQ>(own < qr.len, qr.p + own * qr.row + s * 32 + fg * 8, qr.plane);
-      }
+    if (KQ) {
 #pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -114,38 +181,35 @@ __global__ void __launch_bounds__(256) states_kernel(Params p) {
           if (DELTA) mma(kS[t], fk[s], f);
           if (!SAVE) mma(qS[t], fq[s], f);
         }
+      load_kq(next);
     }
-    const f32x4 beta = *reinterpret_cast<const f32x4*>(rows + 2 * C + tok);
-    f32x4 ec = {1, 1, 1, 1}, eo = {1, 1, 1, 1};
-    if (!VEC) {
-      ec = *reinterpret_cast<const f32x4*>(rows + tok);
-      eo = *reinterpret_cast<const f32x4*>(rows + C + tok);
-    }
-    f32x4 U[NT];
+    f32x4 U[NT], ecur = ec;
+    float vf[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        U[t][r] = tok + r < c.len && vcol[t] < p.dv
-                      ? load_elem(p.v, (c.row + tok + r) * p.vs + (int64_t)h * p.dv + vcol[t], p.dtype)
-                      : 0.0f;
+        vf[t][r] = tok + r < c.len && vcol[t] < p.dv ? from_raw(v[t][r], p.dtype) : 0.0f;
     if (DELTA) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         float x[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = fmaf(-ec[r], kS[t][r], U[t][r]);
+        for (int r = 0; r < 4; ++r) x[r] = fmaf(-ec[r], kS[t][r], vf[t][r]);
         put4<P>(&Rt[0][t * 16 + fr][tok], BV * CP, x);
         U[t] = f32x4{0, 0, 0, 0};
       }
       __syncthreads();
-      const uint16_t* T = p.t + sh * P * C * C + (wave * 16 + fr) * C + fg * 8;
-      for (int s = 0; s <= wave / 2; ++s) {
-        const Frag<P> f = load_frag<P>(T + s * 32, C * C);
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-          mma(U[t], f, load_frag<P>(&Rt[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
-      }
+      for (int s = 0; s < 2; ++s)
+        if (s <= wave / 2)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            mma(U[t], fT[s], load_frag<P>(&Rt[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
+      load_square(p.t, next, fT);
+    } else {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) U[t] = f32x4{vf[t][0], vf[t][1], vf[t][2], vf[t][3]};
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -171,51 +235,50 @@ __global__ void __launch_bounds__(256) states_kernel(Params p) {
         }
       }
     }
+    load_v(next);
     __syncthreads();
-    if (!SAVE && p.o) {
-      const uint16_t* A = p.a + sh * P * C * C + (wave * 16 + fr) * C + fg * 8;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) qS[t][r] *= ec[r];
-      for (int s = 0; s <= wave / 2; ++s) {
-        const Frag<P> f = load_frag<P>(A + s * 32, C * C);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          mma(qS[t], f,
-              load_frag<P>(VEC ? &Wb[0][t * 16 + fr][s * 32 + fg * 8]
-                               : &Wt[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
-      }
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (tok + r < c.len && vcol[t] < p.dv)
-            store_elem(p.o, (c.row + tok + r) * p.os + (int64_t)h * p.dv + vcol[t], p.dtype, qS[t][r]);
-    }
     // the state at the chunk's end
-    {
-      const float end = VEC ? 1.0f : rows[C - 1];
-      const int64_t th = VEC ? sh : (int64_t)slot * p.heads_qk + h / (p.heads / p.heads_qk);
-      const uint16_t* kt = p.kt + th * NPQ * DK * C;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int row = wave * (DK / 4) + 16 * m;
-        f32x4 dec = {end, end, end, end};
-        if (VEC) dec = *reinterpret_cast<const f32x4*>(p.decay + sh * DK + d0 + 16 * m);
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[m][t][r] *= dec[m][r];
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
+          mma(S[m][t], ft[m][s], load_frag<P>(&Wb[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
+    }
+    load_t(next);
+    if (KQ) put_state();
+    if (!SAVE) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) S[m][t][r] *= dec[r];
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const Frag<NPQ> f = load_frag<NPQ>(kt + (int64_t)(row + fr) * C + s * 32 + fg * 8, DK * C);
+        for (int r = 0; r < 4; ++r) qS[t][r] *= ecur[r];
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (s <= wave / 2)
 #pragma unroll
           for (int t = 0; t < NT; ++t)
-            mma(S[m][t], f, load_frag<P>(&Wb[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
+            mma(qS[t], fA[s],
+                load_frag<P>(VEC ? &Wb[0][t * 16 + fr][s * 32 + fg * 8]
+                                 : &Wt[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
+      load_square(p.a, next, fA);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        int64_t at[4];
+        bool ok[4];
+        float x[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          at[r] = (c.row + tok + r) * p.os + (int64_t)h * p.dv + vcol[t];
+          ok[r] = p.o && tok + r < c.len && vcol[t] < p.dv;
+          x[r] = qS[t][r];
         }
+        store_elems<4>(p.o, at, ok, p.dtype, x);
       }
-      if (DELTA || !SAVE) put_state();
     }
     __syncthreads();
   }
@@ -276,15 +339,87 @@ __global__ void __launch_bounds__(256) state_grads_kernel(Params p) {
   put_state();
   __syncthreads();
 
-  for (int ci = nch - 1; ci >= 0; --ci) {
-    const int slot = base + ci;
+  // operands are reloaded after their last use, as in states_kernel
+  Frag<NPQ> fk[KS], fq[MT][2], ft[DELTA ? MT : 1][2];
+  Frag<P> fA[2], fT[DELTA ? 2 : 1];
+  uint32_t x[NT][4], u[NT][4][P];
+  f32x4 beta, ec = {1, 1, 1, 1}, eo = {1, 1, 1, 1}, dec[MT];
+  const int own = wave * 16 + fr;
+  auto chunk = [&](int ci) {
     Chunk c;
     c.n = n;
     c.ci = ci;
     c.row = o0 + (int64_t)ci * C;
     c.len = len - (int64_t)ci * C < C ? (int)(len - (int64_t)ci * C) : C;
+    return c;
+  };
+  auto load_do = [&](int ci) {
+    const Chunk c = chunk(ci);
+    const int64_t sh = (int64_t)(base + ci) * p.heads + h;
+    const float* rows = rows_at(p, base + ci, h);
+    beta = *reinterpret_cast<const f32x4*>(rows + 2 * C + tok);
+    if (!VEC) {
+      ec = *reinterpret_cast<const f32x4*>(rows + tok);
+      eo = *reinterpret_cast<const f32x4*>(rows + C + tok);
+    }
+    int64_t at[4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        at[r] = ((c.row + min(tok + r, c.len - 1)) * p.heads + h) * p.dv + min(vcol[t], p.dv - 1);
+      load_raw<4>(p.dO, at, p.dtype, x[t]);
+      if (p.dbeta) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int q = 0; q < P; ++q)
+            u[t][r][q] = p.u[((sh * P + q) * C + tok + r) * p.dvp + vcol[t]];
+      }
+    }
+  };
+  auto load_k = [&](int ci) {
+    const Rows kr = rows_of<DK>(p, p.k, VEC ? p.korow : p.krow, p.ks, VEC, base + ci, h, chunk(ci));
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+      fk[s] = load_frag<NPQ>(kr.p + min(own, kr.len - 1) * kr.row + s * 32 + fg * 8, kr.plane);
+  };
+  auto load_square = [&](const uint16_t* m, int ci, Frag<P>* f) {
+    const uint16_t* at = m + ((int64_t)(base + ci) * p.heads + h) * P * C * C + own * C + fg * 8;
+    f[0] = load_frag<P>(at, C * C);
+    f[1] = load_frag<P>(at + 32, C * C);
+  };
+  auto load_t = [&](int ci) {
+    const int slot = base + ci;
     const int64_t sh = (int64_t)slot * p.heads + h;
-    const float* rows = rows_at(p, slot, h);
+    const int64_t th = VEC ? sh : (int64_t)slot * p.heads_qk + h / (p.heads / p.heads_qk);
+    const uint16_t* qt = p.qt + th * NPQ * DK * C;
+    const uint16_t* kt = (VEC ? p.ket : p.kt) + th * NPQ * DK * C;
+    const float end = VEC ? 1.0f : rows_at(p, slot, h)[C - 1];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int64_t at = (int64_t)(wave * (DK / 4) + 16 * m + fr) * C + s * 32 + fg * 8;
+        fq[m][s] = load_frag<NPQ>(qt + at, DK * C);
+        if (DELTA) ft[m][s] = load_frag<NPQ>(kt + at, DK * C);
+      }
+      dec[m] = VEC ? *reinterpret_cast<const f32x4*>(p.decay + sh * DK + d0 + 16 * m)
+                   : f32x4{end, end, end, end};
+    }
+  };
+  if (nch > 0) {
+    load_do(nch - 1);
+    load_k(nch - 1);
+    load_square(p.at, nch - 1, fA);
+    if (DELTA) load_square(p.t2t, nch - 1, fT);
+    load_t(nch - 1);
+  }
+
+  for (int ci = nch - 1; ci >= 0; --ci) {
+    const Chunk c = chunk(ci);
+    const int64_t sh = (int64_t)(base + ci) * p.heads + h;
+    const int next = max(ci - 1, 0);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -292,68 +427,61 @@ __global__ void __launch_bounds__(256) state_grads_kernel(Params p) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           p.xc[(sh * DK + d0 + 16 * m + r) * p.dvp + vcol[t]] = X[m][t][r];
-    const f32x4 beta = *reinterpret_cast<const f32x4*>(rows + 2 * C + tok);
-    f32x4 ec = {1, 1, 1, 1}, eo = {1, 1, 1, 1};
-    if (!VEC) {
-      ec = *reinterpret_cast<const f32x4*>(rows + tok);
-      eo = *reinterpret_cast<const f32x4*>(rows + C + tok);
-    }
+    const f32x4 bc = beta, ecc = ec, eoc = eo;
+    float uc[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float x[4], xe[4];
+      float xo[4], xe[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        x[r] = tok + r < c.len && vcol[t] < p.dv
-                   ? load_elem(p.dO, ((c.row + tok + r) * p.heads + h) * p.dv + vcol[t], p.dtype)
-                   : 0.0f;
-        xe[r] = x[r] * ec[r];
+        xo[r] = tok + r < c.len && vcol[t] < p.dv ? from_raw(x[t][r], p.dtype) : 0.0f;
+        xe[r] = xo[r] * ec[r];
+        uc[t][r] = 0.0f;
+        if (p.dbeta) {
+#pragma unroll
+          for (int q = P - 1; q >= 0; --q) uc[t][r] += bf16_to_f((uint16_t)u[t][r][q]);
+        }
       }
-      put4<NPO>(&Ot[0][t * 16 + fr][tok], BV * CP, x);
+      put4<NPO>(&Ot[0][t * 16 + fr][tok], BV * CP, xo);
       if (!VEC) put4<P>(&Oe[0][t * 16 + fr][tok], BV * CP, xe);
     }
+    load_do(next);
     f32x4 W[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) W[t] = f32x4{0, 0, 0, 0};
-    {
-      const Rows kr = rows_of<DK>(p, p.k, VEC ? p.korow : p.krow, p.ks, VEC, slot, h, c);
-      const int own = wave * 16 + fr;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const Frag<NPQ> fk = load_frag_if<NPQ>(own < kr.len, kr.p + own * kr.row + s * 32 + fg * 8, kr.plane);
+    for (int s = 0; s < KS; ++s)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-          mma(W[t], fk, load_frag<P>(&Xl[0][t * 16 + fr][s * 32 + fg * 8], BV * SP));
-      }
-    }
+      for (int t = 0; t < NT; ++t)
+        mma(W[t], fk[s], load_frag<P>(&Xl[0][t * 16 + fr][s * 32 + fg * 8], BV * SP));
+    load_k(next);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) W[t][r] *= eo[r];
+      for (int r = 0; r < 4; ++r) W[t][r] *= eoc[r];
     __syncthreads();
-    {
-      const uint16_t* A = p.at + sh * P * C * C + (wave * 16 + fr) * C + fg * 8;
-      for (int s = wave / 2; s < 2; ++s) {
-        const Frag<P> f = load_frag<P>(A + s * 32, C * C);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      if (s >= wave / 2)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-          mma(W[t], f, load_frag<NPO>(&Ot[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
-      }
-    }
+          mma(W[t], fA[s], load_frag<NPO>(&Ot[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
+    load_square(p.at, next, fA);
     if (DELTA) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const float x[4] = {W[t][0], W[t][1], W[t][2], W[t][3]};
-        put4<P>(&Dt[0][t * 16 + fr][tok], BV * CP, x);
+        const float w[4] = {W[t][0], W[t][1], W[t][2], W[t][3]};
+        put4<P>(&Dt[0][t * 16 + fr][tok], BV * CP, w);
         W[t] = f32x4{0, 0, 0, 0};
       }
       __syncthreads();
-      const uint16_t* T = p.t2t + sh * P * C * C + (wave * 16 + fr) * C + fg * 8;
-      for (int s = wave / 2; s < 2; ++s) {
-        const Frag<P> f = load_frag<P>(T + s * 32, C * C);
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-          mma(W[t], f, load_frag<P>(&Dt[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
-      }
+      for (int s = 0; s < 2; ++s)
+        if (s >= wave / 2)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            mma(W[t], fT[s], load_frag<P>(&Dt[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
+      load_square(p.t2t, next, fT);
     }
     // W holds Z
     float db[4] = {0, 0, 0, 0};
@@ -362,20 +490,20 @@ __global__ void __launch_bounds__(256) state_grads_kernel(Params p) {
       float y[4], ye[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        y[r] = beta[r] * W[t][r];
-        ye[r] = -ec[r] * y[r];
-        const bool in = tok + r < c.len && vcol[t] < p.dv;
-        if (in) store_elem(p.dv_out, ((c.row + tok + r) * p.heads + h) * p.dv + vcol[t], p.dtype, y[r]);
-        if (p.dbeta) {
-          float u = 0.0f;
-#pragma unroll
-          for (int q = P - 1; q >= 0; --q)
-            u += bf16_to_f(p.u[((sh * P + q) * C + tok + r) * p.dvp + vcol[t]]);
-          db[r] = fmaf(u, W[t][r], db[r]);
-        }
+        y[r] = bc[r] * W[t][r];
+        ye[r] = -ecc[r] * y[r];
+        if (p.dbeta) db[r] = fmaf(uc[t][r], W[t][r], db[r]);
       }
+      if (DELTA) put4<P>(&Yt[0][t * 16 + fr][tok], BV * CP, ye);
+      int64_t at[4];
+      bool ok[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        at[r] = ((c.row + tok + r) * p.heads + h) * p.dv + vcol[t];
+        ok[r] = tok + r < c.len && vcol[t] < p.dv;
+      }
+      store_elems<4>(p.dv_out, at, ok, p.dtype, y);
       if (DELTA) {
-        put4<P>(&Yt[0][t * 16 + fr][tok], BV * CP, ye);
         u32x2 yy[P];
         split4<P>(y, yy);
 #pragma unroll
@@ -396,38 +524,26 @@ __global__ void __launch_bounds__(256) state_grads_kernel(Params p) {
             p.dbpart + ((int64_t)vb * p.nslots * p.heads + sh) * C + tok) = f32x4{db[0], db[1], db[2], db[3]};
     }
     if (DELTA) __syncthreads();
-    {
-      const float end = VEC ? 1.0f : rows[C - 1];
-      const int64_t th = VEC ? sh : (int64_t)slot * p.heads_qk + h / (p.heads / p.heads_qk);
-      const uint16_t* qt = p.qt + th * NPQ * DK * C;
-      const uint16_t* kt = (VEC ? p.ket : p.kt) + th * NPQ * DK * C;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int row = wave * (DK / 4) + 16 * m;
-        f32x4 dec = {end, end, end, end};
-        if (VEC) dec = *reinterpret_cast<const f32x4*>(p.decay + sh * DK + d0 + 16 * m);
+    for (int m = 0; m < MT; ++m) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) X[m][t][r] *= dec[r];
+        for (int r = 0; r < 4; ++r) X[m][t][r] *= dec[m][r];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int64_t at = (int64_t)(row + fr) * C + s * 32 + fg * 8;
-          const Frag<NPQ> f = load_frag<NPQ>(qt + at, DK * C);
-          Frag<NPQ> g;
-          if (DELTA) g = load_frag<NPQ>(kt + at, DK * C);
+      for (int s = 0; s < 2; ++s)
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            if (VEC)
-              mma(X[m][t], f, load_frag<NPO>(&Ot[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
-            else
-              mma(X[m][t], f, load_frag<P>(&Oe[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
-            if (DELTA) mma(X[m][t], g, load_frag<P>(&Yt[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
-          }
+        for (int t = 0; t < NT; ++t) {
+          if (VEC)
+            mma(X[m][t], fq[m][s], load_frag<NPO>(&Ot[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
+          else
+            mma(X[m][t], fq[m][s], load_frag<P>(&Oe[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
+          if (DELTA)
+            mma(X[m][t], ft[m][s], load_frag<P>(&Yt[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
         }
-      }
-      put_state();
     }
+    load_t(next);
+    put_state();
     __syncthreads();
   }
   if (p.ds0) {

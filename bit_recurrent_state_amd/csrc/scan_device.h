@@ -73,6 +73,28 @@ __device__ __forceinline__ float load_elem(const void* p, int64_t i, int dtype) 
   return static_cast<const float*>(p)[i];
 }
 
+// The same in two steps, for many elements at once: load_elem branches on the
+// type and converts, so that each load would be waited for before the next.
+template <int N>
+__device__ __forceinline__ void load_raw(const void* p, const int64_t (&at)[N], int dtype,
+                                         uint32_t (&raw)[N]) {
+  if (dtype == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) raw[i] = static_cast<const uint32_t*>(p)[at[i]];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) raw[i] = static_cast<const uint16_t*>(p)[at[i]];
+  }
+}
+
+// Without branches: the type is the same for all, but a branch per element
+// would cut the code around it into pieces.
+__device__ __forceinline__ float from_raw(uint32_t raw, int dtype) {
+  const uint32_t half = dtype == 2 ? ~0u : 0u;
+  const uint32_t h = __float_as_uint((float)__builtin_bit_cast(_Float16, (uint16_t)raw));
+  return __uint_as_float((h & half) | ((raw << (dtype == 1 ? 16 : 0)) & ~half));
+}
+
 // Two floats to packed bfloat16, to nearest, ties to even.
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const f32x2 f = {a, b};
@@ -87,6 +109,25 @@ __device__ __forceinline__ void store_elem(void* p, int64_t i, int dtype, float 
     static_cast<_Float16*>(p)[i] = (_Float16)x;
   else
     static_cast<float*>(p)[i] = x;
+}
+
+// N outputs, those with `ok`.
+template <int N>
+__device__ __forceinline__ void store_elems(void* p, const int64_t (&at)[N], const bool (&ok)[N],
+                                            int dtype, const float (&x)[N]) {
+  if (dtype == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (ok[i]) static_cast<float*>(p)[at[i]] = x[i];
+  } else {
+    const uint32_t half = dtype == 2 ? ~0u : 0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t h = __builtin_bit_cast(uint16_t, (_Float16)x[i]);
+      if (ok[i])
+        static_cast<uint16_t*>(p)[at[i]] = (uint16_t)((h & half) | (pack_bf16(x[i], 0.0f) & ~half));
+    }
+  }
 }
 
 // Log decays below -87 count as -87; a NaN stays.

@@ -19,10 +19,11 @@ hipError_t forward_tail(const Params& p, hipStream_t s) {
   const dim3 slots(p.nslots, p.heads);
   if (VEC) {
     operands_vector_kernel<DK, DELTA, false><<<slots, DK, 0, s>>>(p);
+    chunk_kernel<DK, P, true, DELTA, false><<<slots, 256, 0, s>>>(p);
     chunk_vector_kernel<DK, DELTA, false><<<slots, 256, 0, s>>>(p);
   } else {
     operands_kernel<DK><<<dim3(p.nslots, p.heads_qk), 256, 0, s>>>(p, 0);
-    chunk_scalar_kernel<DK, NPQ, DELTA, false><<<slots, 256, 0, s>>>(p);
+    chunk_kernel<DK, NPQ, false, DELTA, false><<<slots, 256, 0, s>>>(p);
   }
   states_kernel<DK, NT, NPQ, VEC, DELTA, false><<<chain_grid(p), 256, 0, s>>>(p);
   return hipGetLastError();
@@ -31,22 +32,22 @@ hipError_t forward_tail(const Params& p, hipStream_t s) {
 template <int DK, int NT, int NPQ, int NPO, bool VEC, bool DELTA>
 hipError_t backward_tail(const Params& p, hipStream_t s) {
   const dim3 slots(p.nslots, p.heads);
-  if (p.nslots > 0) {
-    operands_kernel<DK><<<dim3(p.nslots, p.heads_qk), 256, 0, s>>>(p, 1);
+  operands_kernel<DK><<<dim3(p.nslots, p.heads_qk), 256, 0, s>>>(p, 1);
+  {
     if (VEC) {
       operands_vector_kernel<DK, DELTA, true><<<slots, DK, 0, s>>>(p);
+      chunk_kernel<DK, P, true, DELTA, true><<<slots, 256, 0, s>>>(p);
       chunk_vector_kernel<DK, DELTA, true><<<slots, 256, 0, s>>>(p);
     } else {
-      chunk_scalar_kernel<DK, NPQ, DELTA, true><<<slots, 256, 0, s>>>(p);
+      chunk_kernel<DK, NPQ, false, DELTA, true><<<slots, 256, 0, s>>>(p);
     }
   }
   states_kernel<DK, NT, NPQ, VEC, DELTA, true><<<chain_grid(p), 256, 0, s>>>(p);
   state_grads_kernel<DK, NT, NPQ, NPO, VEC, DELTA><<<chain_grid(p), 256, 0, s>>>(p);
-  if (VEC)
-    grads_vector_kernel<DK, NPO, NPO, DELTA><<<slots, 256, 0, s>>>(p);
-  else
-    grads_scalar_kernel<DK, NPQ, NPO, DELTA><<<slots, 256, 0, s>>>(p);
-  if (p.heads != p.heads_qk) share_kernel<DK><<<dim3(p.nslots, p.heads_qk), 256, 0, s>>>(p);
+  grads_kernel<DK, NPQ, VEC ? NPO : NPQ, NPO, VEC, DELTA><<<slots, 256, 0, s>>>(p);
+  if (VEC) grads_vector_kernel<DK, NPO, NPO, DELTA><<<slots, 256, 0, s>>>(p);
+  if (p.heads != p.heads_qk)
+    share_kernel<DK><<<dim3(p.nslots, p.heads_qk, kChunk * DK / 1024), 256, 0, s>>>(p);
   return hipGetLastError();
 }
 

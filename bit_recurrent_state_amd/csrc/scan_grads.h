@@ -59,17 +59,26 @@ __device__ __forceinline__ Frag<P> state_frag(const float* s, float (&x)[8]) {
   return split8<P>(x);
 }
 
+// dq and dk of 4 tokens of a channel.
 template <int DK>
 __device__ __forceinline__ void store_qk(const Params& p, const Chunk& c, int64_t sh, int h, int t,
-                                         int ch, float dq, float dk) {
-  if (t >= c.len) return;
+                                         int ch, const float (&dq)[4], const float (&dk)[4]) {
   if (p.heads == p.heads_qk) {
-    const int64_t at = ((c.row + t) * p.heads + h) * DK + ch;
-    store_elem(p.dq, at, p.dtype, dq);
-    store_elem(p.dkk, at, p.dtype, dk);
+    int64_t at[4];
+    bool ok[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      at[r] = ((c.row + t + r) * p.heads + h) * DK + ch;
+      ok[r] = t + r < c.len;
+    }
+    store_elems<4>(p.dq, at, ok, p.dtype, dq);
+    store_elems<4>(p.dkk, at, ok, p.dtype, dk);
   } else {
-    p.dqpart[(sh * C + t) * DK + ch] = dq;
-    p.dkpart[(sh * C + t) * DK + ch] = dk;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      p.dqpart[(sh * C + t + r) * DK + ch] = dq[r];
+      p.dkpart[(sh * C + t + r) * DK + ch] = dk[r];
+    }
   }
 }
 
@@ -82,140 +91,327 @@ __device__ __forceinline__ void store_dbeta(const Params& p, const Chunk& c, int
   p.dbeta[(c.row + threadIdx.x) * p.heads + h] = s;
 }
 
-// ---- one gate per token ----------------------------------------------------------------------
-template <int DK, int NPQ, int NPO, bool DELTA>
-__global__ void __launch_bounds__(256) grads_scalar_kernel(Params p) {
-  constexpr int CT = DK / 64, PL = C * CP;
-  __shared__ __align__(16) uint16_t E[P][C][CP], Et[P][C][CP];
-  __shared__ __align__(16) uint16_t F[DELTA ? P : 1][DELTA ? C : 1][CP];
-  __shared__ __align__(16) uint16_t Ft[DELTA ? P : 1][DELTA ? C : 1][CP];
+// ---- the states' and the chunk's products ----------------------------------------------------
+// The value columns pass through LDS in slabs of 64: rows of d_o, U and Y, which
+// all waves need.  A wave's own channels of the states come straight from
+// memory and are split in its registers.  E and F then take the slabs' place,
+// one after the other, as rows and as columns.
+//
+// One gate per token: E and F carry the decay G.  VEC (chunks that do not decay
+// far): G_ij = e^c_i e^-c_j per channel, so sum_j E_ij (k_j e^-c_j) is scaled by
+// e^c_i, and sum_i E_ij (q_i e^c_i) by e^-c_j.  NPR: terms of the unscaled q and
+// k (VEC).
+template <int DK, int NPQ, int NPR, int NPO, bool VEC, bool DELTA>
+__global__ void __launch_bounds__(256) grads_kernel(Params p) {
+  constexpr int CT = DK / 64, VS = 64, VP = VS + 8, NP = NPO + (DELTA ? 2 : 1) * P;
+  constexpr int PL = C * CP;
+  constexpr int kWords = (NP * C * VP > 2 * P * C * CP ? NP * C * VP : 2 * P * C * CP);
+  __shared__ __align__(16) uint16_t lds[kWords];
   __shared__ float red[2][4][C];
   __shared__ float redx[4];
+  uint16_t* const Ol = lds;
+  uint16_t* const Ul = lds + NPO * C * VP;
+  uint16_t* const Yl = Ul + P * C * VP;
+  uint16_t* const El = lds;           // [P][C][CP]
+  uint16_t* const Et = lds + P * PL;  // transposed
   const int slot = blockIdx.x, h = blockIdx.y;
   Chunk c;
   if (!find_chunk(p, slot, c)) return;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int fr = lane & 15, fg = lane >> 4;
   const int64_t sh = (int64_t)slot * p.heads + h;
+  if (VEC && p.far[sh]) return;
   const int hq = h / (p.heads / p.heads_qk);
   const float* rows = rows_at(p, slot, h);
-  const double* cs = reinterpret_cast<const double*>(rows + 3 * C);
   const ValueRows dO = dout_rows(p, sh, h, c);
-  const ValueRows U = {p.u + sh * P * C * p.dvp, p.dvp, (int64_t)C * p.dvp, C};
-  const ValueRows Y = {p.y + sh * P * C * p.dvp, p.dvp, (int64_t)C * p.dvp, C};
-  const int nvs = p.dvp / 32;
+  const int ch0 = wave * (DK / 4) + fr;
 
-  for (int b = 0; b < 4; ++b) {  // rows of block `wave`, columns of block b
-    f32x4 e = {0, 0, 0, 0}, f = {0, 0, 0, 0};
-    if (b <= wave)
-      for (int s = 0; s < nvs; ++s) {
-        const Frag<P> u = value_frag<P>(U, b * 16 + fr, s * 32 + fg * 8);
-        mma(e, value_frag<NPO>(dO, wave * 16 + fr, s * 32 + fg * 8), u);
-        if (DELTA) mma(f, value_frag<P>(Y, wave * 16 + fr, s * 32 + fg * 8), u);
+  f32x4 e[4], f[4], aq[CT][4], ap[DELTA ? CT : 1][4], am[CT][4];
+  float xs[CT];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    e[m] = f[m] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      aq[ct][m] = am[ct][m] = f32x4{0, 0, 0, 0};
+      if (DELTA) ap[ct][m] = f32x4{0, 0, 0, 0};
+    }
+  }
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) xs[ct] = 0.0f;
+
+  for (int v0 = 0; v0 < p.dvp; v0 += VS) {
+    const int ns = p.dvp - v0 >= VS ? 2 : 1;
+    // rows into LDS: 8 vectors of 8 a row, 2 rows of every plane a thread
+    {
+      const int col = threadIdx.x & 7;
+      u32x4 st[NP][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = i * 32 + (threadIdx.x >> 3);
+        // columns behind dvp repeat the last ones and are not used
+        const int64_t vc = v0 + min(col * 8, p.dvp - v0 - 8);
+        const int64_t ro = (int64_t)min(r, dO.len - 1) * dO.row + vc;
+#pragma unroll
+        for (int n = 0; n < NPO; ++n)
+          st[n][i] = *reinterpret_cast<const u32x4*>(dO.p + n * dO.plane + ro);
+#pragma unroll
+        for (int n = 0; n < P; ++n) {
+          const int64_t at = ((sh * P + n) * C + r) * p.dvp + vc;
+          st[NPO + n][i] = *reinterpret_cast<const u32x4*>(p.u + at);
+          if (DELTA) st[NPO + P + n][i] = *reinterpret_cast<const u32x4*>(p.y + at);
+        }
+        if (r >= c.len) {
+#pragma unroll
+          for (int n = 0; n < NPO; ++n) st[n][i] = u32x4{0, 0, 0, 0};
+        }
       }
-    const int j = b * 16 + fr, i0 = wave * 16 + fg * 4;
-    const float beta = rows[2 * C + j];
-    float xe[4], xf[4];
+      __syncthreads();  // the last slab has been read
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int i = i0 + r;
-      const float g = i >= j ? beta * expf((float)(cs[i] - cs[j])) : 0.0f;
-      xe[r] = i >= j ? e[r] * g : 0.0f;
-      xf[r] = i > j ? -f[r] * g : 0.0f;
+      for (int n = 0; n < NP; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<u32x4*>(lds + (n * C + i * 32 + (threadIdx.x >> 3)) * VP + col * 8) = st[n][i];
     }
-    u32x2 t[P];
-    split4<P>(xe, t);
+    f32x4 sv[CT][2][2], xv[CT][2][2];
 #pragma unroll
-    for (int q = 0; q < P; ++q) {
-      *reinterpret_cast<u32x2*>(&Et[q][j][i0]) = t[q];
-      E[q][i0][j] = (uint16_t)t[q].x;
-      E[q][i0 + 1][j] = (uint16_t)(t[q].x >> 16);
-      E[q][i0 + 2][j] = (uint16_t)t[q].y;
-      E[q][i0 + 3][j] = (uint16_t)(t[q].y >> 16);
-    }
-    if (DELTA) {
-      split4<P>(xf, t);
+    for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int q = 0; q < P; ++q) {
-        *reinterpret_cast<u32x2*>(&Ft[q][j][i0]) = t[q];
-        F[q][i0][j] = (uint16_t)t[q].x;
-        F[q][i0 + 1][j] = (uint16_t)(t[q].x >> 16);
-        F[q][i0 + 2][j] = (uint16_t)t[q].y;
-        F[q][i0 + 3][j] = (uint16_t)(t[q].y >> 16);
+      for (int s = 0; s < 2; ++s) {
+        const int64_t at = (sh * DK + ch0 + ct * 16) * p.dvp + v0 + min(s, ns - 1) * 32 + fg * 8;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          sv[ct][s][q] = *reinterpret_cast<const f32x4*>(p.sc + at + q * 4);
+          xv[ct][s][q] = *reinterpret_cast<const f32x4*>(p.xc + at + q * 4);
+        }
+      }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (s >= ns) break;
+      const int at = fr * VP + s * 32 + fg * 8;
+      const Frag<NPO> fo = load_frag<NPO>(Ol + wave * 16 * VP + at, C * VP);
+      Frag<P> fy;
+      if (DELTA) fy = load_frag<P>(Yl + wave * 16 * VP + at, C * VP);
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (b <= wave) {
+          const Frag<P> fu = load_frag<P>(Ul + b * 16 * VP + at, C * VP);
+          mma(e[b], fo, fu);
+          if (DELTA) mma(f[b], fy, fu);
+        }
+      Frag<P> fs[CT], fx[CT];
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        float x0[8], x1[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x0[i] = sv[ct][s][i / 4][i % 4];
+          x1[i] = xv[ct][s][i / 4][i % 4];
+          xs[ct] = fmaf(x0[i], x1[i], xs[ct]);
+        }
+        fs[ct] = split8<P>(x0);
+        fx[ct] = split8<P>(x1);
+      }
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const Frag<NPO> go = load_frag<NPO>(Ol + m * 16 * VP + at, C * VP);
+        const Frag<P> gu = load_frag<P>(Ul + m * 16 * VP + at, C * VP);
+        Frag<P> gy;
+        if (DELTA) gy = load_frag<P>(Yl + m * 16 * VP + at, C * VP);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          mma(aq[ct][m], go, fs[ct]);
+          if (DELTA) mma(ap[ct][m], gy, fs[ct]);
+          mma(am[ct][m], gu, fx[ct]);
+        }
       }
     }
   }
-  __syncthreads();
 
-  float sS[4][4], sD[4][4], xs = 0.0f;
+  // E (then F) as planes in LDS: rows i of block `wave`, columns j of block b
+  const double* cs = reinterpret_cast<const double*>(rows + 3 * C);
+  auto put_square = [&](f32x4(&x)[4], bool strict, float sign) {
+    __syncthreads();
 #pragma unroll
-  for (int m = 0; m < 4; ++m)
+    for (int b = 0; b < 4; ++b) {
+      const int j = b * 16 + fr, i0 = wave * 16 + fg * 4;
+      const float beta = sign * rows[2 * C + j];
+      float v[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) sS[m][r] = sD[m][r] = 0.0f;
-  const int64_t tq = (int64_t)slot * p.heads_qk + hq;
-#pragma unroll 1
-  for (int ct = 0; ct < CT; ++ct) {
-    const int ch = wave * (DK / 4) + ct * 16 + fr;
-    f32x4 aq[4], ap[4], am[4], ai[4];
+      for (int r = 0; r < 4; ++r) {
+        const int i = i0 + r;
+        const bool in = strict ? i > j : i >= j;
+        float g = beta;
+        if (!VEC) g *= expf(in ? (float)(cs[i] - cs[j]) : 0.0f);
+        v[r] = in ? x[b][r] * g : 0.0f;
+      }
+      u32x2 t[P];
+      split4<P>(v, t);
 #pragma unroll
-    for (int m = 0; m < 4; ++m) aq[m] = ap[m] = am[m] = ai[m] = f32x4{0, 0, 0, 0};
-    for (int s = 0; s < nvs; ++s) {
-      const int64_t at = (sh * DK + ch) * p.dvp + s * 32 + fg * 8;
-      float x0[8], x1[8];
-      const Frag<P> fs = state_frag(p.sc + at, x0), fx = state_frag(p.xc + at, x1);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) xs = fmaf(x0[e], x1[e], xs);
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        mma(aq[m], value_frag<NPO>(dO, m * 16 + fr, s * 32 + fg * 8), fs);
-        if (DELTA) mma(ap[m], value_frag<P>(Y, m * 16 + fr, s * 32 + fg * 8), fs);
-        mma(am[m], value_frag<P>(U, m * 16 + fr, s * 32 + fg * 8), fx);
+      for (int q = 0; q < P; ++q) {
+        *reinterpret_cast<u32x2*>(Et + q * PL + j * CP + i0) = t[q];
+        uint16_t* d = El + q * PL + i0 * CP + j;
+        d[0] = (uint16_t)t[q].x;
+        d[CP] = (uint16_t)(t[q].x >> 16);
+        d[2 * CP] = (uint16_t)t[q].y;
+        d[3 * CP] = (uint16_t)(t[q].y >> 16);
       }
     }
-    float kx[4][4], qx[4][4];
+    __syncthreads();
+  };
+  const int64_t tq = VEC ? sh : (int64_t)slot * p.heads_qk + hq;
+  const uint16_t* const kn = (VEC ? p.knt : p.kt) + tq * NPQ * DK * C;  // right operand of E, F
+  const uint16_t* const qe = p.qt + tq * NPQ * DK * C;                  // of E transposed
+  const uint16_t* const ke = (VEC ? p.ket : p.kt) + tq * NPQ * DK * C;  // of F transposed
+  put_square(e, false, 1.0f);
+  f32x4 ai[CT][4];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    const int ch = ch0 + ct * 16;
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       const int t0 = m * 16 + fg * 4;
-      const f32x4 ec = *reinterpret_cast<const f32x4*>(rows + t0);
-      const f32x4 eo = *reinterpret_cast<const f32x4*>(rows + C + t0);
       const f32x4 be = *reinterpret_cast<const f32x4*>(rows + 2 * C + t0);
+      f32x4 ec, eo;
+      if (VEC) {
+        ec = *reinterpret_cast<const f32x4*>(p.pfx + (sh * DK + ch) * C + t0);
+        eo = *reinterpret_cast<const f32x4*>(p.sfx + (sh * DK + ch) * C + t0);
+      } else {
+        ec = *reinterpret_cast<const f32x4*>(rows + t0);
+        eo = *reinterpret_cast<const f32x4*>(rows + C + t0);
+      }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const bool in = t0 + r < c.len;
-        kx[m][r] = in ? load_elem(p.k, (c.row + t0 + r) * p.ks + (int64_t)hq * DK + ch, p.dtype) : 0.0f;
-        qx[m][r] = in ? load_elem(p.q, (c.row + t0 + r) * p.qs + (int64_t)hq * DK + ch, p.dtype) : 0.0f;
-        aq[m][r] *= ec[r];
-        ap[m][r] *= -ec[r];
-        am[m][r] *= eo[r] * be[r];
-        sS[m][r] = fmaf(kx[m][r], am[m][r], sS[m][r]);
+        if (!VEC) {  // VEC: scaled below, together with the chunk's own part
+          aq[ct][m][r] *= ec[r];
+          if (DELTA) ap[ct][m][r] *= -ec[r];
+        } else if (DELTA) {
+          ap[ct][m][r] = -ap[ct][m][r];
+        }
+        am[ct][m][r] *= eo[r] * be[r];
       }
+      ai[ct][m] = f32x4{0, 0, 0, 0};
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const int64_t at = (tq * NPQ * DK + ch) * C + s * 32 + fg * 8;
-      const Frag<NPQ> fk = load_frag<NPQ>(p.kt + at, DK * C);
-      const Frag<NPQ> fq = load_frag<NPQ>(p.qt + at, DK * C);
+      const int64_t at = (int64_t)ch * C + s * 32 + fg * 8;
+      const Frag<NPQ> fk = load_frag<NPQ>(kn + at, DK * C);
+      const Frag<NPQ> fq = load_frag<NPQ>(qe + at, DK * C);
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const int row = m * 16 + fr, col = s * 32 + fg * 8;
-        if (s <= m / 2) {
-          mma(aq[m], load_frag<P>(&E[0][row][col], PL), fk);
-          if (DELTA) mma(ap[m], load_frag<P>(&F[0][row][col], PL), fk);
+        const int o = (m * 16 + fr) * CP + s * 32 + fg * 8;
+        if (s <= m / 2) mma(aq[ct][m], load_frag<P>(El + o, PL), fk);
+        if (s >= m / 2) mma(ai[ct][m], load_frag<P>(Et + o, PL), fq);
+      }
+    }
+  }
+  if (DELTA) {
+    put_square(f, true, -1.0f);
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int64_t at = (int64_t)(ch0 + ct * 16) * C + s * 32 + fg * 8;
+        const Frag<NPQ> fk = load_frag<NPQ>(kn + at, DK * C);
+        const Frag<NPQ> fe = load_frag<NPQ>(ke + at, DK * C);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const int o = (m * 16 + fr) * CP + s * 32 + fg * 8;
+          if (s <= m / 2) mma(ap[ct][m], load_frag<P>(El + o, PL), fk);
+          if (s >= m / 2) mma(ai[ct][m], load_frag<P>(Et + o, PL), fe);
         }
-        if (s >= m / 2) {
-          mma(ai[m], load_frag<P>(&Et[0][row][col], PL), fq);
-          if (DELTA) mma(ai[m], load_frag<P>(&Ft[0][row][col], PL), fk);
+      }
+  }
+
+  // the outputs, and the sums for the gates
+  const uint16_t* const kr = (VEC ? p.kt_raw : p.kt) + ((int64_t)slot * p.heads_qk + hq) * NPR * DK * C;
+  const uint16_t* const qr = (VEC ? p.qt_raw : p.qt) + ((int64_t)slot * p.heads_qk + hq) * NPR * DK * C;
+  auto raw4 = [&](const uint16_t* src, int ch, int t0, float(&x)[4]) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] = 0.0f;
+#pragma unroll
+    for (int n = NPR - 1; n >= 0; --n) {
+      const u32x2 w = *reinterpret_cast<const u32x2*>(src + ((int64_t)n * DK + ch) * C + t0);
+      x[0] += __uint_as_float(w.x << 16);
+      x[1] += __uint_as_float(w.x & 0xFFFF0000u);
+      x[2] += __uint_as_float(w.y << 16);
+      x[3] += __uint_as_float(w.y & 0xFFFF0000u);
+    }
+  };
+  float sS[4][4], sD[4][4];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    const int ch = ch0 + ct * 16;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int t0 = m * 16 + fg * 4;
+      float k[4], q[4], dq[4], dk[4];
+      raw4(kr, ch, t0, k);
+      raw4(qr, ch, t0, q);
+      f32x4 ec = {1, 1, 1, 1};
+      if (VEC) ec = *reinterpret_cast<const f32x4*>(p.pfx + (sh * DK + ch) * C + t0);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float a = aq[ct][m][r], b = DELTA ? ap[ct][m][r] : 0.0f, i = ai[ct][m][r];
+        if (VEC) {
+          a *= ec[r];
+          b *= ec[r];
+          i /= ec[r];
+        }
+        dq[r] = a;
+        dk[r] = b + am[ct][m][r] + i;
+        const float s = k[r] * am[ct][m][r], d = q[r] * a + k[r] * (b - i);
+        sS[m][r] = VEC || ct == 0 ? s : sS[m][r] + s;
+        sD[m][r] = VEC || ct == 0 ? d : sD[m][r] + d;
+      }
+      store_qk<DK>(p, c, sh, h, t0, ch, dq, dk);
+    }
+    if (VEC) {
+      // dlog_alpha of the channel: sums over the tokens before and behind
+      float x = xs[ct];
+      x += __shfl_xor(x, 16);
+      x += __shfl_xor(x, 32);
+      float before[4], after[4], base = p.decay[sh * DK + ch] * x, tail = 0.0f;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const float a = (sS[m][0] + sS[m][1]) + (sS[m][2] + sS[m][3]);
+        before[m] = base;
+#pragma unroll
+        for (int o = 0; o < 4; ++o) {
+          const float y = __shfl(a, fr + 16 * o);
+          base += y;
+          if (o < fg) before[m] += y;
+        }
+      }
+#pragma unroll
+      for (int m = 3; m >= 0; --m) {
+        const float a = (sD[m][0] + sD[m][1]) + (sD[m][2] + sD[m][3]);
+        after[m] = tail;
+#pragma unroll
+        for (int o = 3; o >= 0; --o) {
+          const float y = __shfl(a, fr + 16 * o);
+          tail += y;
+          if (o > fg) after[m] += y;
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        float b = before[m], a[4], s = after[m];
+#pragma unroll
+        for (int r = 3; r >= 0; --r) a[r] = s += sD[m][r];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = m * 16 + fg * 4 + r;
+          if (t < c.len) p.dg[((c.row + t) * p.heads + h) * DK + ch] = b + a[r];
+          b += sS[m][r];
         }
       }
     }
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        sD[m][r] += qx[m][r] * aq[m][r] + kx[m][r] * (ap[m][r] - ai[m][r]);
-        store_qk<DK>(p, c, sh, h, m * 16 + fg * 4 + r, ch, aq[m][r],
-                     ap[m][r] + am[m][r] + ai[m][r]);
-      }
+  }
+  if (VEC) {
+    if (wave == 0) store_dbeta(p, c, sh, h);
+    return;
   }
 #pragma unroll
   for (int m = 0; m < 4; ++m)
@@ -227,18 +423,21 @@ __global__ void __launch_bounds__(256) grads_scalar_kernel(Params p) {
         red[1][wave][m * 16 + fg * 4 + r] = b;
       }
     }
-  xs = sum16(xs);
-  xs += __shfl_xor(xs, 16);
-  xs += __shfl_xor(xs, 32);
-  if (lane == 0) redx[wave] = xs;
+  float x = xs[0];
+#pragma unroll
+  for (int ct = 1; ct < CT; ++ct) x += xs[ct];
+  x = sum16(x);
+  x += __shfl_xor(x, 16);
+  x += __shfl_xor(x, 32);
+  if (lane == 0) redx[wave] = x;
   __syncthreads();
   if (wave == 0) {
-    double s = 0.0, d = 0.0, x = 0.0;
+    double s = 0.0, d = 0.0, sx = 0.0;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       s += red[0][w][lane];
       d += red[1][w][lane];
-      x += redx[w];
+      sx += redx[w];
     }
     double before = s, after = d;
     for (int o = 1; o < 64; o *= 2) {
@@ -247,12 +446,12 @@ __global__ void __launch_bounds__(256) grads_scalar_kernel(Params p) {
       if (lane + o < 64) after += b;
     }
     if (lane < c.len)
-      p.dg[(c.row + lane) * p.heads + h] = (float)(rows[C - 1] * x + (before - s) + after);
+      p.dg[(c.row + lane) * p.heads + h] = (float)(rows[C - 1] * sx + (before - s) + after);
     store_dbeta(p, c, sh, h);
   }
 }
 
-// ---- a gate per key channel ------------------------------------------------------------------
+// ---- a gate per key channel, chunks that decay far -------------------------------------------
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
@@ -277,6 +476,7 @@ __global__ void __launch_bounds__(256) grads_vector_kernel(Params p) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int fr = lane & 15, fg = lane >> 4;
   const int64_t sh = (int64_t)slot * p.heads + h;
+  if (!p.far[sh]) return;
   const int hq = h / (p.heads / p.heads_qk);
   const float* rows = rows_at(p, slot, h);
   const ValueRows dO = dout_rows(p, sh, h, c);
@@ -469,7 +669,7 @@ __global__ void __launch_bounds__(256) grads_vector_kernel(Params p) {
         }
       }
 #pragma unroll
-      for (int i = 15; i >= 0; --i) {
+      for (int i = 15; i >= 0; --i) {  // token i's decay is taken on as i is passed
         y[i] = fmaf(Ed[fg][i][i], q[i], y[i]);
 #pragma unroll
         for (int j = 0; j < i; ++j) {
@@ -479,8 +679,6 @@ __global__ void __launch_bounds__(256) grads_vector_kernel(Params p) {
         }
       }
     }
-    // y_j so far holds the decay of token j too where later tokens reach it: see above, the
-    // factor of token i is taken on when i is passed, so y_j ends with the decays of j+1 .. i.
     auto exchange = [&](const float(&v)[16], f32x4(&out)[4]) {
       wave_sync();
 #pragma unroll
@@ -506,7 +704,8 @@ __global__ void __launch_bounds__(256) grads_vector_kernel(Params p) {
     // gates: token sums per channel, 16 tokens per lane
     f32x4 dc[4];
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
+    for (int m = 0; m < 4; ++m) {
+      float dq[4], dk[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int t = m * 16 + fg * 4 + r;
@@ -514,8 +713,11 @@ __global__ void __launch_bounds__(256) grads_vector_kernel(Params p) {
         const float q = in ? load_elem(p.q, (c.row + t) * p.qs + (int64_t)hq * DK + ch, p.dtype) : 0.0f;
         const float k = in ? load_elem(p.k, (c.row + t) * p.ks + (int64_t)hq * DK + ch, p.dtype) : 0.0f;
         dc[m][r] = q * aq[m][r] + k * (ap[m][r] - ai[m][r]);
-        store_qk<DK>(p, c, sh, h, t, ch, aq[m][r], ap[m][r] + am[m][r] + ai[m][r]);
+        dq[r] = aq[m][r];
+        dk[r] = ap[m][r] + am[m][r] + ai[m][r];
       }
+      store_qk<DK>(p, c, sh, h, m * 16 + fg * 4, ch, dq, dk);
+    }
     auto gather = [&](const f32x4(&v)[4], float(&out)[16]) {
       wave_sync();
 #pragma unroll
@@ -563,24 +765,29 @@ __global__ void __launch_bounds__(256) grads_vector_kernel(Params p) {
   if (wave == 0) store_dbeta(p, c, sh, h);
 }
 
-// dq and dk of heads that share them: summed in the order of the heads.
+// dq and dk of heads that share them: summed in the order of the heads, four
+// channels a thread.
 template <int DK>
 __global__ void __launch_bounds__(256) share_kernel(Params p) {
   const int slot = blockIdx.x, hq = blockIdx.y;
   Chunk c;
   if (!find_chunk(p, slot, c)) return;
   const int group = p.heads / p.heads_qk;
-  for (int u = threadIdx.x; u < c.len * DK; u += 256) {
-    float a = 0.0f, b = 0.0f;
-    for (int g = 0; g < group; ++g) {
-      const int64_t at = ((int64_t)slot * p.heads + hq * group + g) * C * DK + u;
-      a += p.dqpart[at];
-      b += p.dkpart[at];
-    }
-    const int64_t to = ((c.row + u / DK) * p.heads_qk + hq) * DK + u % DK;
-    store_elem(p.dq, to, p.dtype, a);
-    store_elem(p.dkk, to, p.dtype, b);
+  const int u = (blockIdx.z * 256 + threadIdx.x) * 4;
+  if (u >= c.len * DK) return;
+  f32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+  const int64_t from = ((int64_t)slot * p.heads + hq * group) * C * DK + u;
+#pragma unroll 4
+  for (int g = 0; g < group; ++g) {
+    a += *reinterpret_cast<const f32x4*>(p.dqpart + from + (int64_t)g * C * DK);
+    b += *reinterpret_cast<const f32x4*>(p.dkpart + from + (int64_t)g * C * DK);
   }
+  const int64_t to = ((c.row + u / DK) * p.heads_qk + hq) * DK + u % DK;
+  const int64_t at[4] = {to, to + 1, to + 2, to + 3};
+  const bool ok[4] = {true, true, true, true};
+  const float x[4] = {a[0], a[1], a[2], a[3]}, y[4] = {b[0], b[1], b[2], b[3]};
+  store_elems<4>(p.dq, at, ok, p.dtype, x);
+  store_elems<4>(p.dkk, at, ok, p.dtype, y);
 }
 
 }  // namespace qscan

@@ -12,6 +12,7 @@ namespace qscan {
 
 constexpr int kChunk = 64;  // tokens of a chunk
 constexpr int kTerms = 3;   // bfloat16 terms of an FP32 operand
+constexpr float kFarDecay = 8.0f;  // largest decay of a chunk, as a logarithm, that is divided out
 
 // Workspace arrays hold bfloat16 terms as planes: [...][term][row][col].
 // "slot" is a chunk of a sequence: sequence n owns the slots from
@@ -34,11 +35,14 @@ struct Params {
   float* rows;               // [slot][head][5][kChunk]: exp(c), exp(c_end - c), beta, c (double)
   float* decay;              // [slot][head][dk] exp(c_end) (per-channel gates)
   uint16_t *qrow, *krow;     // [slot][head|head_qk][term][kChunk][dk]
+  uint16_t *knrow;           // per-channel gates: k exp(-c)
+  uint32_t* far;             // [slot][head] per-channel gates: a channel decays beyond kFarDecay
   uint16_t *korow;           // per-channel gates, backward: k exp(c_end - c)
-  uint16_t *kt, *qt, *ket;   // [slot][head|head_qk][term][dk][kChunk]
+  uint16_t *kt, *qt, *ket, *knt;  // [slot][head|head_qk][term][dk][kChunk]
   uint16_t *kt_raw, *qt_raw; // per-channel gates, backward: unscaled, per q/k head
   float *sfx, *pfx;          // per-channel gates, backward: [slot][head][dk][kChunk], decays
-                             // from the token to its block of 16's end, and from its start
+                             // from the token to the chunk's end, and from its start (of its
+                             // block of 16, where the chunk decays far)
   uint16_t *a, *t;           // [slot][head][kTerms][kChunk][kChunk]
   uint16_t *at, *t2t;        // backward: transposed A, transposed (I + beta L)^-1
   uint16_t* dop;             // [slot][head][term][kChunk][dvp] d_o as planes

@@ -19,6 +19,42 @@ __global__ void __launch_bounds__(256) operands_kernel(Params p, int backward) {
   const bool vec = p.mixer == GLA || p.mixer == KDA;
   const int terms = vec ? (p.dtype == 1 ? 1 : P) : p.terms;
   const int64_t sh = (int64_t)slot * p.heads_qk + hq;
+  if (p.dtype == 1 && terms == 1) {
+    // bfloat16 is moved as it is: 8 tokens of 2 channels per thread
+    for (int which = 0; which <= backward; ++which) {
+      const uint16_t* src = static_cast<const uint16_t*>(which ? p.q : p.k);
+      const int64_t stride = which ? p.qs : p.ks;
+      uint16_t* tr = vec ? (which ? p.qt_raw : p.kt_raw) : (which ? p.qt : p.kt);
+      for (int u = threadIdx.x; u < DK / 2 * (C / 8); u += 256) {
+        const int ch = u % (DK / 2) * 2, t0 = u / (DK / 2) * 8;
+        uint32_t x[8];
+        const uint16_t* at = src + (int64_t)hq * DK + ch;
+        if (stride % 2 == 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            x[i] = *reinterpret_cast<const uint32_t*>(at + (c.row + min(t0 + i, c.len - 1)) * stride);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint16_t* r = at + (c.row + min(t0 + i, c.len - 1)) * stride;
+            x[i] = r[0] | (uint32_t)r[1] << 16;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (t0 + i >= c.len) x[i] = 0;
+        u32x4 lo, hi;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          lo[i] = (x[2 * i] & 0xFFFFu) | (x[2 * i + 1] << 16);
+          hi[i] = (x[2 * i] >> 16) | (x[2 * i + 1] & 0xFFFF0000u);
+        }
+        *reinterpret_cast<u32x4*>(tr + (sh * DK + ch) * C + t0) = lo;
+        *reinterpret_cast<u32x4*>(tr + (sh * DK + ch + 1) * C + t0) = hi;
+      }
+    }
+    return;
+  }
   for (int which = 0; which < 2; ++which) {
     if (which == 1 && !backward && p.direct) break;
     const void* src = which ? p.q : p.k;
@@ -29,11 +65,14 @@ __global__ void __launch_bounds__(256) operands_kernel(Params p, int backward) {
     for (int u = threadIdx.x; u < DK * (C / 8); u += 256) {
       const int ch = u % DK, t0 = u / DK * 8;
       float x[8];
+      int64_t at[8];
+      uint32_t raw[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        x[i] = t0 + i < c.len
-                   ? load_elem(src, (c.row + t0 + i) * stride + (int64_t)hq * DK + ch, p.dtype)
-                   : 0.0f;
+        at[i] = (c.row + min(t0 + i, c.len - 1)) * stride + (int64_t)hq * DK + ch;
+      load_raw<8>(src, at, p.dtype, raw);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = t0 + i < c.len ? from_raw(raw[i], p.dtype) : 0.0f;
       const Frag<P> f = split8<P>(x);
       for (int n = 0; n < terms; ++n) {
         const u32x4 t = n == 0 ? f.t[0] : n == 1 ? f.t[1] : f.t[2];
@@ -52,68 +91,124 @@ __global__ void __launch_bounds__(256) operands_kernel(Params p, int backward) {
 }
 
 // ---- (I + M)^-1 of a strictly lower triangular M --------------------------------------------
-// Forward substitution, one wave, a column per lane: row i of the inverse is
-// e_i - sum_{m<i} M_im x_m, with M's rows read from LDS as broadcasts.
-__device__ __forceinline__ void invert64(const float (*M)[C + 4], float (&x)[C], int lane) {
+// In LDS, in FP32, stable as forward substitution is: the four diagonal blocks
+// of 16 by substitution (a lane per column, a wave per block), then blocks of
+// 32 and 64 by X21 = -X22 (M21 X11) on FP32 matrix instructions.  One product's
+// result is the next one's right operand without leaving its registers: step r
+// of a product takes the columns k = 4 (lane >> 4) + r, as results hold rows.
+// 64 steps of substitution by one wave took 20 us a workgroup, this 2.
+typedef float Square[C + 4];
+
+// D += A B for one 16 x 16 block: A from LDS rows, B given as four results.
+__device__ __forceinline__ f32x4 block_mma(const Square* A, int ra, int ca, const f32x4& b,
+                                           f32x4 acc) {
+  const int lane = threadIdx.x & 63;
+  const f32x4 a = *reinterpret_cast<const f32x4*>(&A[ra * 16 + (lane & 15)][ca * 16 + (lane >> 4) * 4]);
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int m = 0; m < i; m += 4) {
-      const f32x4 v = *reinterpret_cast<const f32x4*>(&M[i][m]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (m + j < i) s[j] = fmaf(v[j], x[m + j], s[j]);
-    }
-    x[i] = (lane == i ? 1.0f : 0.0f) - ((s[0] + s[1]) + (s[2] + s[3]));
-  }
+  for (int r = 0; r < 4; ++r) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], b[r], acc, 0, 0, 0);
+  return acc;
 }
 
-__device__ __forceinline__ void store_term_rows(uint16_t* dst, int col, const float (&x)[C]) {
-  // x: one column of [C][C]; lanes are the columns
+__device__ __forceinline__ f32x4 block_load(const Square* X, int rb, int cb) {
+  const int lane = threadIdx.x & 63;
+  f32x4 b;
 #pragma unroll
-  for (int i = 0; i < C; i += 4) {
-    const float v[4] = {x[i], x[i + 1], x[i + 2], x[i + 3]};
-    u32x2 t[P];
-    split4<P>(v, t);
-#pragma unroll
-    for (int n = 0; n < P; ++n) {
-      uint16_t* d = dst + (n * C + i) * C + col;
-      d[0] = (uint16_t)t[n].x;
-      d[C] = (uint16_t)(t[n].x >> 16);
-      d[2 * C] = (uint16_t)t[n].y;
-      d[3 * C] = (uint16_t)(t[n].y >> 16);
-    }
-  }
+  for (int r = 0; r < 4; ++r) b[r] = X[rb * 16 + (lane >> 4) * 4 + r][cb * 16 + (lane & 15)];
+  return b;
 }
 
-__device__ __forceinline__ void store_term_cols(uint16_t* dst, int row, const float (&x)[C]) {
-  // x as a row of [C][C]; lanes are the rows
+__device__ __forceinline__ void block_store(Square* X, int rb, int cb, const f32x4& b, float sign) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int i = 0; i < C; i += 8) {
-    const float v[8] = {x[i], x[i + 1], x[i + 2], x[i + 3], x[i + 4], x[i + 5], x[i + 6], x[i + 7]};
-    const Frag<P> f = split8<P>(v);
-#pragma unroll
-    for (int n = 0; n < P; ++n)
-      *reinterpret_cast<u32x4*>(dst + (n * C + row) * C + i) = f.t[n];
-  }
+  for (int r = 0; r < 4; ++r)
+    X[rb * 16 + (lane >> 4) * 4 + r][cb * 16 + (lane & 15)] = sign * b[r];
 }
 
-// What follows once M (scaled) lies in LDS: wave 0 inverts I + L diag(beta),
-// wave 1 (backward) I + diag(beta) L and stores it transposed.
-template <bool BWD>
-__device__ __forceinline__ void store_inverses(const Params& p, float (*M)[C + 4],
-                                               float (*M2)[C + 4], int64_t sh) {
+// N matrices M (their strict lower triangles set, the rest zero), overwritten
+// by the inverses.  All four waves call this, with M complete in LDS.
+template <int N>
+__device__ __forceinline__ void invert(Square* M0, Square* M1) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  if (wave == 0) {
-    float x[C];
-    invert64(M, x, lane);
-    store_term_rows(p.t + sh * P * C * C, lane, x);
+  const int col = lane & 15, g = lane >> 4;
+  {
+    const Square* M = N == 2 && (g & 1) ? M1 : M0;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+      for (int m = 0; m < i; m += 4) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(&M[wave * 16 + i][wave * 16 + m]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (m + j < i) {
+            if (j & 1)
+              s1 = fmaf(v[j], x[m + j], s1);
+            else
+              s0 = fmaf(v[j], x[m + j], s0);
+          }
+      }
+      x[i] = (col == i ? 1.0f : 0.0f) - (s0 + s1);
+    }
+    __syncthreads();
+    if (g < N) {
+      Square* X = g ? M1 : M0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) X[wave * 16 + i][wave * 16 + col] = x[i];
+    }
   }
-  if (BWD && wave == 1) {
-    float x[C];
-    invert64(M2, x, lane);
-    store_term_cols(p.t2t + sh * P * C * C, lane, x);
+  __syncthreads();
+  const f32x4 zero = {0, 0, 0, 0};
+  if (wave < 2 * N) {  // blocks (1, 0) and (3, 2)
+    Square* X = wave < 2 ? M0 : M1;
+    const int b = (wave & 1) * 2;
+    const f32x4 d = block_mma(X, b + 1, b, block_load(X, b, b), zero);
+    block_store(X, b + 1, b, block_mma(X, b + 1, b + 1, d, zero), -1.0f);
+  }
+  __syncthreads();
+  f32x4 y2 = zero, y3 = zero;
+  Square* X = wave < 2 ? M0 : M1;
+  const int b = wave & 1;
+  if (wave < 2 * N) {  // column block b of the lower left quarter
+    f32x4 d2 = zero, d3 = zero;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (c >= b) {
+        const f32x4 x = block_load(X, c, b);
+        d2 = block_mma(X, 2, c, x, d2);
+        d3 = block_mma(X, 3, c, x, d3);
+      }
+    y2 = block_mma(X, 2, 2, d2, zero);
+    y3 = block_mma(X, 3, 3, d3, block_mma(X, 3, 2, d2, zero));
+  }
+  __syncthreads();
+  if (wave < 2 * N) {
+    block_store(X, 2, b, y2, -1.0f);
+    block_store(X, 3, b, y3, -1.0f);
+  }
+  __syncthreads();
+}
+
+// What follows once M = L diag(beta) (and, backward, M2 = diag(beta) L) lies in
+// LDS: the inverses, the second transposed.
+template <bool BWD>
+__device__ __forceinline__ void store_inverses(const Params& p, Square* M, Square* M2, int64_t sh) {
+  __syncthreads();
+  invert<BWD ? 2 : 1>(M, M2);
+  uint16_t* t1 = p.t + sh * P * C * C;
+  for (int u = threadIdx.x; u < C * C / 4; u += 256) {
+    const int r = u / (C / 4), q0 = u % (C / 4) * 4;
+    const f32x4 v = *reinterpret_cast<const f32x4*>(&M[r][q0]);
+    const float x[4] = {v[0], v[1], v[2], v[3]};
+    put4<P>(t1 + r * C + q0, C * C, x);
+  }
+  if (BWD) {
+    uint16_t* t2 = p.t2t + sh * P * C * C;
+    for (int u = threadIdx.x; u < C * C / 4; u += 256) {
+      const int r = u % C, q0 = u / C * 4;  // rows by lane: LDS columns are then read without conflicts
+      const float x[4] = {M2[q0][r], M2[q0 + 1][r], M2[q0 + 2][r], M2[q0 + 3][r]};
+      put4<P>(t2 + r * C + q0, C * C, x);
+    }
   }
 }
 
@@ -139,18 +234,27 @@ __device__ __forceinline__ void store_dop(const Params& p, const Chunk& c, int64
 // One workgroup per (slot, head).  Sums of log decays are kept in 64 bits:
 // the differences c_i - c_j of a chunk that decays far are then still exact.
 // Forward: A; backward: its transpose (and both inverses).
-template <int DK, int NPQ, bool DELTA, bool BWD>
-__global__ void __launch_bounds__(256) chunk_scalar_kernel(Params p) {
+//
+// VEC: a gate per key channel, for chunks over which no channel decays by more
+// than e^kFarDecay: A = (q e^c)(k e^-c)^T and L = (k e^c)(k e^-c)^T are then
+// plain products.  Their exponents are rounded to 2^-24 of kFarDecay at most, so
+// the quotients they stand for hold to FP32.  Other chunks go to
+// chunk_vector_kernel.
+template <int DK, int NPQ, bool VEC, bool DELTA, bool BWD>
+__global__ void __launch_bounds__(256) chunk_kernel(Params p) {
   __shared__ double cs[C];
   __shared__ float bs[C];
-  __shared__ float M[DELTA ? C : 1][C + 4];
-  __shared__ float M2[DELTA && BWD ? C : 1][C + 4];
+  __shared__ __align__(16) float M[DELTA ? C : 1][C + 4];
+  __shared__ __align__(16) float M2[DELTA && BWD ? C : 1][C + 4];
   const int slot = blockIdx.x, h = blockIdx.y;
   Chunk c;
   if (!find_chunk(p, slot, c)) return;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t sh = (int64_t)slot * p.heads + h;
-  if (wave == 0) {
+  if (BWD) store_dop(p, c, sh, h);
+  if (VEC && p.far[sh]) return;
+  if (VEC && wave == 0) bs[lane] = rows_at(p, slot, h)[2 * C + lane];
+  if (!VEC && wave == 0) {
     const bool in = lane < c.len;
     const int64_t at = (c.row + lane) * p.heads + h;
     double s = in ? (double)gate(p.g[at]) : 0.0;
@@ -169,8 +273,9 @@ __global__ void __launch_bounds__(256) chunk_scalar_kernel(Params p) {
     reinterpret_cast<double*>(r + 3 * C)[lane] = s;
   }
   __syncthreads();
-  const Rows q = rows_of<DK>(p, p.q, p.qrow, p.qs, false, slot, h, c);
-  const Rows k = rows_of<DK>(p, p.k, p.krow, p.ks, false, slot, h, c);
+  const Rows q = rows_of<DK>(p, p.q, p.qrow, p.qs, VEC, slot, h, c);
+  const Rows k = rows_of<DK>(p, p.k, VEC ? p.knrow : p.krow, p.ks, VEC, slot, h, c);
+  const Rows ki = rows_of<DK>(p, p.k, p.krow, p.ks, VEC, slot, h, c);  // the reading key of L
   const int fr = lane & 15, fc = (lane >> 4) * 8;
   const int own = wave * 16 + fr;  // forward: token i; backward: token j
   const Rows& mine = BWD ? k : q;
@@ -178,7 +283,8 @@ __global__ void __launch_bounds__(256) chunk_scalar_kernel(Params p) {
 #pragma unroll
   for (int s = 0; s < DK / 32; ++s) {
     fm[s] = load_frag_if<NPQ>(own < mine.len, mine.p + own * mine.row + s * 32 + fc, mine.plane);
-    if (DELTA) fk[s] = load_frag_if<NPQ>(own < k.len, k.p + own * k.row + s * 32 + fc, k.plane);
+    const Rows& l = BWD ? k : ki;
+    if (DELTA) fk[s] = load_frag_if<NPQ>(own < l.len, l.p + own * l.row + s * 32 + fc, l.plane);
   }
   // tile (wave, b): columns own (i forward, j backward), rows of block b
   for (int b = 0; b < 4; ++b) {
@@ -194,7 +300,7 @@ __global__ void __launch_bounds__(256) chunk_scalar_kernel(Params p) {
         mma(acc, f, fm[s]);
         if (DELTA) {
           const Frag<NPQ> g =
-              BWD ? load_frag_if<NPQ>(other < k.len, k.p + other * k.row + s * 32 + fc, k.plane)
+              BWD ? load_frag_if<NPQ>(other < ki.len, ki.p + other * ki.row + s * 32 + fc, ki.plane)
                   : f;
           mma(acl, g, fk[s]);
         }
@@ -205,7 +311,7 @@ __global__ void __launch_bounds__(256) chunk_scalar_kernel(Params p) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int i = BWD ? r0 + r : own, j = BWD ? own : r0 + r;
-      const float e = i >= j ? expf((float)(cs[i] - cs[j])) : 0.0f;
+      const float e = VEC ? 1.0f : i >= j ? expf((float)(cs[i] - cs[j])) : 0.0f;
       a[r] = i >= j ? acc[r] * e : 0.0f;
       if (DELTA) {
         const float l = i > j ? acl[r] * e : 0.0f;
@@ -216,11 +322,7 @@ __global__ void __launch_bounds__(256) chunk_scalar_kernel(Params p) {
     uint16_t* dst = (BWD ? p.at : p.a) + sh * P * C * C;
     put4<P>(dst + own * C + r0, C * C, a);
   }
-  if (DELTA) {
-    __syncthreads();
-    store_inverses<BWD>(p, M, M2, sh);
-  }
-  if (BWD) store_dop(p, c, sh, h);
+  if (DELTA) store_inverses<BWD>(p, M, M2, sh);
 }
 
 // ---- a gate per key channel -----------------------------------------------------------------
@@ -230,7 +332,8 @@ __global__ void __launch_bounds__(256) chunk_scalar_kernel(Params p) {
 // overflows, and nothing is lost where gates are strong.
 //
 // One workgroup per (slot, head), a thread per channel: the scaled operands
-// q e^c, k e^c and k e^(c_end - c) as rows and as columns.
+// q e^c, k e^c, k e^(c_end - c) and, unless the chunk decays too far, k e^-c as
+// rows and as columns.
 template <int DK, bool DELTA, bool BWD>
 __global__ void __launch_bounds__(DK) operands_vector_kernel(Params p) {
   const int slot = blockIdx.x, h = blockIdx.y, ch = threadIdx.x;
@@ -245,11 +348,15 @@ __global__ void __launch_bounds__(DK) operands_vector_kernel(Params p) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int t = b * 16 + i;
-      if (t < c.len) s += gate(p.g[((c.row + t) * p.heads + h) * DK + ch]);
+      const float g = gate(p.g[((c.row + min(t, c.len - 1)) * p.heads + h) * DK + ch]);
+      s += t < c.len ? g : 0.0f;
     }
     total[b] = s;
   }
-  p.decay[sh * DK + ch] = expf((total[0] + total[1]) + (total[2] + total[3]));
+  const float all = (total[0] + total[1]) + (total[2] + total[3]);
+  p.decay[sh * DK + ch] = expf(all);
+  const bool far = __syncthreads_or(!(all >= -kFarDecay));
+  if (threadIdx.x == 0) p.far[sh] = far;
   if (ch < C && threadIdx.x < C) {
     float* r = rows_at(p, slot, h);
     r[2 * C + ch] = ch < c.len ? (p.beta ? p.beta[(c.row + ch) * p.heads + h] : 1.0f) : 0.0f;
@@ -261,7 +368,8 @@ __global__ void __launch_bounds__(DK) operands_vector_kernel(Params p) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int t = b * 16 + i;
-      g[i] = t < c.len ? gate(p.g[((c.row + t) * p.heads + h) * DK + ch]) : 0.0f;
+      const float x = gate(p.g[((c.row + min(t, c.len - 1)) * p.heads + h) * DK + ch]);
+      g[i] = t < c.len ? x : 0.0f;
     }
     float after = 0.0f;
     for (int m = 3; m > b; --m) after += m == 1 ? total[1] : m == 2 ? total[2] : total[3];
@@ -274,39 +382,56 @@ __global__ void __launch_bounds__(DK) operands_vector_kernel(Params p) {
     float pfx = 0.0f;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      float qe[8], ke[8], ko[8], ps[8], ss[8];
+      float qe[8], ke[8], ko[8], kn[8], ps[8], ss[8];
+      int64_t aq[8], ak[8];
+      uint32_t rq[8], rk[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t row = c.row + min(b * 16 + half * 8 + i, c.len - 1);
+        aq[i] = row * p.qs + (int64_t)hq * DK + ch;
+        ak[i] = row * p.ks + (int64_t)hq * DK + ch;
+      }
+      load_raw<8>(p.q, aq, p.dtype, rq);
+      load_raw<8>(p.k, ak, p.dtype, rk);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int t = b * 16 + half * 8 + i;
         pfx += g[half * 8 + i];
-        ps[i] = expf(pfx);
-        ss[i] = expf(sfx[half * 8 + i]);
         const bool in = t < c.len;
-        const float q = in ? load_elem(p.q, (c.row + t) * p.qs + (int64_t)hq * DK + ch, p.dtype) : 0.0f;
-        const float k = in ? load_elem(p.k, (c.row + t) * p.ks + (int64_t)hq * DK + ch, p.dtype) : 0.0f;
+        const float q = in ? from_raw(rq[i], p.dtype) : 0.0f;
+        const float k = in ? from_raw(rk[i], p.dtype) : 0.0f;
         const float e = expf(pfx + before);
         qe[i] = q * e;
         ke[i] = k * e;
-        ko[i] = k * expf(sfx[half * 8 + i] + after);
+        const float eo = expf(sfx[half * 8 + i] + after);
+        ko[i] = k * eo;
+        kn[i] = far ? 0.0f : k * expf(-(pfx + before));
+        if (BWD) {
+          ps[i] = far ? expf(pfx) : e;
+          ss[i] = far ? expf(sfx[half * 8 + i]) : eo;
+        }
       }
       const int t0 = b * 16 + half * 8;
-      const Frag<P> fq = split8<P>(qe), fk = split8<P>(ke), fo = split8<P>(ko);
+      const Frag<P> fq = split8<P>(qe), fk = split8<P>(ke), fo = split8<P>(ko), fn = split8<P>(kn);
 #pragma unroll
       for (int n = 0; n < P; ++n) {
         const uint32_t wq[4] = {fq.t[n].x, fq.t[n].y, fq.t[n].z, fq.t[n].w};
         const uint32_t wk[4] = {fk.t[n].x, fk.t[n].y, fk.t[n].z, fk.t[n].w};
         const uint32_t wo[4] = {fo.t[n].x, fo.t[n].y, fo.t[n].z, fo.t[n].w};
+        const uint32_t wn[4] = {fn.t[n].x, fn.t[n].y, fn.t[n].z, fn.t[n].w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int64_t at = ((sh * P + n) * C + t0 + i) * DK + ch;
           const int sft = 16 * (i & 1);
-          if (!BWD) p.qrow[at] = (uint16_t)(wq[i / 2] >> sft);
+          p.qrow[at] = (uint16_t)(wq[i / 2] >> sft);
+          p.knrow[at] = (uint16_t)(wn[i / 2] >> sft);
           if (DELTA) p.krow[at] = (uint16_t)(wk[i / 2] >> sft);
           if (BWD) p.korow[at] = (uint16_t)(wo[i / 2] >> sft);
         }
         const int64_t tt = ((sh * P + n) * DK + ch) * C + t0;
         *reinterpret_cast<u32x4*>(p.kt + tt) = fo.t[n];
         if (BWD) *reinterpret_cast<u32x4*>(p.qt + tt) = fq.t[n];
+        if (BWD) *reinterpret_cast<u32x4*>(p.knt + tt) = fn.t[n];
         if (BWD && DELTA) *reinterpret_cast<u32x4*>(p.ket + tt) = fk.t[n];
       }
       if (BWD) {
@@ -323,7 +448,8 @@ __global__ void __launch_bounds__(DK) operands_vector_kernel(Params p) {
   }
 }
 
-// A (or its transpose) and the inverses with a gate per channel.  Channels go
+// A (or its transpose) and the inverses with a gate per channel, for chunks
+// that decay far.  Channels go
 // by slabs of 64.  Blocks of 16 tokens below the diagonal are matrix products
 // of operands scaled towards the boundary between them; the four blocks on the
 // diagonal are summed directly, wave b block b: a lane holds one key's 16
@@ -332,7 +458,7 @@ __global__ void __launch_bounds__(DK) operands_vector_kernel(Params p) {
 template <int DK, bool DELTA, bool BWD>
 __global__ void __launch_bounds__(256) chunk_vector_kernel(Params p) {
   constexpr int SL = 64, LP = SL + 4;
-  __shared__ float qs[C][LP], ks[C][LP], al[C][LP], px[C][LP], sx[C][LP];
+  __shared__ __align__(16) float qs[C][LP], ks[C][LP], al[C][LP], px[C][LP], sx[C][LP];
   __shared__ float tot[4][SL];
   __shared__ float bs[C];
   const int slot = blockIdx.x, h = blockIdx.y;
@@ -340,6 +466,7 @@ __global__ void __launch_bounds__(256) chunk_vector_kernel(Params p) {
   if (!find_chunk(p, slot, c)) return;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t sh = (int64_t)slot * p.heads + h;
+  if (!p.far[sh]) return;
   const int hq = h / (p.heads / p.heads_qk);
   const int fr = lane & 15, cg = lane >> 4;
   if (threadIdx.x < C)
@@ -481,7 +608,6 @@ __global__ void __launch_bounds__(256) chunk_vector_kernel(Params p) {
     put4<P>(dst + r * C + q0, C * C, x);
   }
   if (DELTA) store_inverses<BWD>(p, M, M2, sh);
-  if (BWD) store_dop(p, c, sh, h);
 }
 
 }  // namespace qscan
