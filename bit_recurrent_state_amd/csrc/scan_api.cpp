@@ -109,8 +109,8 @@ size_t layout(const qstate_scan_config* c, bool backward, void* workspace, Param
     w.take(p.t2t, square, delta);
     // d_o's rows serve as they are where they are bfloat16 and fill whole blocks
     w.take(p.dop, sh * p.dop_terms * kChunk * p.dvp, !(bf16 && c->dv % 32 == 0));
-    w.take(p.u, sh * kTerms * kChunk * p.dvp, true);
-    w.take(p.y, sh * kTerms * kChunk * p.dvp, delta);
+    w.take(p.u, sh * kChunk * p.dvp, true);
+    w.take(p.y, sh * kChunk * p.dvp, delta);
     w.take(p.sc, sh * p.dk * p.dvp, true);
     w.take(p.xc, sh * p.dk * p.dvp, true);
     w.take(p.dbpart, (uint64_t)p.nvb * sh * kChunk, c->mixer != QSTATE_GLA);

@@ -1,7 +1,7 @@
 // scan_chain.h — the parts of the scan that go from chunk to chunk: the states
 // forward and their gradients backward.
 //
-// One workgroup of four waves per (sequence, head, block of BV value columns).
+// One workgroup per (sequence, head, block of BV value columns).
 // The state block stays in FP32 matrix accumulators, transposed: wave w holds
 // key channels [w dk/4, (w+1) dk/4) x BV columns.  Its terms are written to LDS
 // once a chunk for the products that contract over dk.  The operands that only
@@ -29,30 +29,118 @@ __device__ __forceinline__ bool chain_block(const Params& p, int& n, int& h, int
 // Forward.  Per chunk: R = V - e^c K S^T (delta rule), U = T R, W = beta U,
 // O = e^c Q S^T + A W, S = e^c_end S + (e^(c_end - c) W)^T K.  Row scales are
 // applied to results and to W, so that with one gate per token q and k enter
-// the products unrounded.  SAVE (for the backward pass): the states at the
-// chunks' starts and U are stored, and no output.
-template <int DK, int NT, int NPQ, bool VEC, bool DELTA, bool SAVE>
-__global__ void __launch_bounds__(256) states_kernel(Params p) {
+// the products unrounded.
+//
+// What bounds it is the chain from one state to the next, so it has waves of
+// its own: waves 0..3 compute R, U and S, waves 4..7 beside them O, which
+// nothing waits for.  (All in four waves: 6400 cycles a chunk, O's part 1900.)
+// Outputs of 16 bits take PO = 2 terms of q, A, S and W, which hold them to
+// 2^-16; everything that reaches the state takes all three.
+//
+// SAVE (for the backward pass): four waves, no output; the states at the
+// chunks' starts and U are stored.
+template <int DK, int NT, int NPQ, int PO, bool VEC, bool DELTA, bool SAVE>
+__global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
   constexpr int BV = 16 * NT, KS = DK / 32, MT = DK / 64, SP = DK + 8;
+  constexpr int NQ = NPQ < PO ? NPQ : PO;
+  constexpr bool D = NPQ == 1;
   __shared__ __align__(16) uint16_t Sl[P][BV][SP];
   __shared__ __align__(16) uint16_t Rt[DELTA ? P : 1][DELTA ? BV : 1][CP];
-  __shared__ __align__(16) uint16_t Wt[SAVE || VEC ? 1 : P][SAVE || VEC ? 1 : BV][CP];
+  __shared__ __align__(16) uint16_t Wt[SAVE || VEC ? 1 : PO][SAVE || VEC ? 1 : BV][CP];
   __shared__ __align__(16) uint16_t Wb[P][BV][CP];  // e^(c_end - c) W (one gate), else W
   int n, h, vb;
   if (!chain_block(p, n, h, vb)) return;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = (threadIdx.x >> 6) & 3, lane = threadIdx.x & 63;
+  const bool reader = !SAVE && threadIdx.x >= 256;
   const int fr = lane & 15, fg = lane >> 4;
   const int64_t o0 = offset_of(p, n), o1 = offset_of(p, n + 1);
   const int64_t len = o1 > o0 ? o1 - o0 : 0;
   const int nch = (int)((len + C - 1) / C);
   const int base = (int)(o0 / C) + n;
-  const int d0 = wave * (DK / 4) + fg * 4;  // + 16 m: first of the lane's 4 channels
-  const int tok = wave * 16 + fg * 4;       // first of the lane's 4 tokens
-  const int64_t nh = (int64_t)n * p.heads + h;
+  const int tok = wave * 16 + fg * 4;  // first of the lane's 4 tokens
   int vcol[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) vcol[t] = vb * BV + t * 16 + fr;
+  // Operands are loaded again for the next chunk right after their last use:
+  // the loads have most of a chunk's time to arrive and need no second set of
+  // registers.  No branch goes around them (the last chunk loads itself again),
+  // so that each use waits for its own loads only.
+  auto chunk = [&](int ci) {
+    Chunk c;
+    c.n = n;
+    c.ci = ci;
+    c.row = o0 + (int64_t)ci * C;
+    c.len = len - (int64_t)ci * C < C ? (int)(len - (int64_t)ci * C) : C;
+    return c;
+  };
+  auto head_of = [&](int ci) { return (int64_t)(base + ci) * p.heads + h; };
 
+  if (reader) {
+    Frag<NQ> fq[KS];
+    Frag<PO> fA[2];
+    f32x4 ec = {1, 1, 1, 1};
+    auto load_q = [&](int ci) {
+      const auto q = rows_of<DK, D>(p, p.q, p.qrow, p.qs, VEC, base + ci, h, chunk(ci));
+#pragma unroll
+      for (int s = 0; s < KS; ++s) fq[s] = q.template frag<NQ>(wave, s);
+      if (!VEC) ec = *reinterpret_cast<const f32x4*>(rows_at(p, base + ci, h) + tok);
+    };
+    auto load_a = [&](int ci) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) fA[s] = tile_frag<PO, C>(p.a + head_of(ci) * P * C * C, wave, s, C * C);
+    };
+    if (nch > 0) {
+      load_q(0);
+      load_a(0);
+    }
+    __syncthreads();
+    for (int ci = 0; ci < nch; ++ci) {
+      const Chunk c = chunk(ci);
+      const int next = min(ci + 1, nch - 1);
+      f32x4 O[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) O[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          mma(O[t], fq[s], load_frag<PO>(&Sl[0][t * 16 + fr][s * 32 + fg * 8], BV * SP));
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) O[t][r] *= ec[r];
+      load_q(next);
+      if (DELTA) __syncthreads();
+      __syncthreads();
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (s <= wave / 2)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            mma(O[t], fA[s],
+                load_frag<PO>(VEC ? &Wb[0][t * 16 + fr][s * 32 + fg * 8]
+                                  : &Wt[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
+      load_a(next);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        int64_t at[4];
+        bool ok[4];
+        float x[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          at[r] = (c.row + tok + r) * p.os + (int64_t)h * p.dv + vcol[t];
+          ok[r] = p.o && tok + r < c.len && vcol[t] < p.dv;
+          x[r] = O[t][r];
+        }
+        store_elems<4>(p.o, at, ok, p.dtype, x);
+      }
+      __syncthreads();
+    }
+    return;
+  }
+
+  const int d0 = wave * (DK / 4) + fg * 4;  // + 16 m: first of the lane's 4 channels
+  const int64_t nh = (int64_t)n * p.heads + h;
   f32x4 S[MT][NT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
@@ -71,42 +159,14 @@ __global__ void __launch_bounds__(256) states_kernel(Params p) {
         put4<P>(&Sl[0][t * 16 + fr][d0 + 16 * m], BV * SP, x);
       }
   };
-  if (DELTA || !SAVE) put_state();
-  __syncthreads();
-
-  // Rows behind a sequence's end repeat its last row: beta is zero there, so
-  // what they compute reaches neither the state nor an output.
-  // A chunk's operands, each loaded again for the next chunk right after its
-  // last use: the loads have most of a chunk's time to arrive and need no
-  // second set of registers.
-  constexpr bool KQ = DELTA || !SAVE;
-  Frag<NPQ> fq[SAVE ? 1 : KS], fk[DELTA ? KS : 1], ft[MT][2];
-  Frag<P> fT[DELTA ? 2 : 1], fA[SAVE ? 1 : 2];
+  Frag<NPQ> fk[DELTA ? KS : 1], ft[MT][2];
+  Frag<P> fT[DELTA ? 2 : 1];
   uint32_t v[NT][4];
   f32x4 beta, ec = {1, 1, 1, 1}, eo = {1, 1, 1, 1}, dec[MT];
-  const int own = wave * 16 + fr;
-  auto chunk = [&](int ci) {
-    Chunk c;
-    c.n = n;
-    c.ci = ci;
-    c.row = o0 + (int64_t)ci * C;
-    c.len = len - (int64_t)ci * C < C ? (int)(len - (int64_t)ci * C) : C;
-    return c;
-  };
-  auto load_kq = [&](int ci) {
-    const Chunk c = chunk(ci);
-    if (DELTA) {
-      const Rows kr = rows_of<DK>(p, p.k, p.krow, p.ks, VEC, base + ci, h, c);
+  auto load_k = [&](int ci) {
+    const auto k = rows_of<DK, D>(p, p.k, p.krow, p.ks, VEC, base + ci, h, chunk(ci));
 #pragma unroll
-      for (int s = 0; s < KS; ++s)
-        fk[s] = load_frag<NPQ>(kr.p + min(own, kr.len - 1) * kr.row + s * 32 + fg * 8, kr.plane);
-    }
-    if (!SAVE) {
-      const Rows qr = rows_of<DK>(p, p.q, p.qrow, p.qs, VEC, base + ci, h, c);
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-        fq[s] = load_frag<NPQ>(qr.p + min(own, qr.len - 1) * qr.row + s * 32 + fg * 8, qr.plane);
-    }
+    for (int s = 0; s < KS; ++s) fk[s] = k.template frag<NPQ>(wave, s);
   };
   auto load_v = [&](int ci) {
     const Chunk c = chunk(ci);
@@ -126,64 +186,37 @@ __global__ void __launch_bounds__(256) states_kernel(Params p) {
       load_raw<4>(p.v, at, p.dtype, v[t]);
     }
   };
-  auto load_square = [&](const uint16_t* m, int ci, Frag<P>* f) {
-    const uint16_t* at = m + ((int64_t)(base + ci) * p.heads + h) * P * C * C + own * C + fg * 8;
-    f[0] = load_frag<P>(at, C * C);
-    f[1] = load_frag<P>(at + 32, C * C);
+  auto load_T = [&](int ci) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) fT[s] = tile_frag<P, C>(p.t + head_of(ci) * P * C * C, wave, s, C * C);
   };
-  auto load_t = [&](int ci) {
+  auto load_kt = [&](int ci) {
     const int slot = base + ci;
-    const int64_t sh = (int64_t)slot * p.heads + h;
-    const int64_t th = VEC ? sh : (int64_t)slot * p.heads_qk + h / (p.heads / p.heads_qk);
+    const int64_t th = VEC ? head_of(ci) : (int64_t)slot * p.heads_qk + h / (p.heads / p.heads_qk);
     const uint16_t* kt = p.kt + th * NPQ * DK * C;
     const float end = VEC ? 1.0f : rows_at(p, slot, h)[C - 1];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-        ft[m][s] = load_frag<NPQ>(
-            kt + (int64_t)(wave * (DK / 4) + 16 * m + fr) * C + s * 32 + fg * 8, DK * C);
-      dec[m] = VEC ? *reinterpret_cast<const f32x4*>(p.decay + sh * DK + d0 + 16 * m)
+      for (int s = 0; s < 2; ++s) ft[m][s] = tile_frag<NPQ, C>(kt, wave * MT + m, s, DK * C);
+      dec[m] = VEC ? *reinterpret_cast<const f32x4*>(p.decay + head_of(ci) * DK + d0 + 16 * m)
                    : f32x4{end, end, end, end};
     }
   };
   if (nch > 0) {
-    load_kq(0);
+    if (DELTA) load_k(0);
     load_v(0);
-    if (DELTA) load_square(p.t, 0, fT);
-    if (!SAVE) load_square(p.a, 0, fA);
-    load_t(0);
+    if (DELTA) load_T(0);
+    load_kt(0);
   }
+  if (DELTA || !SAVE) put_state();
+  __syncthreads();
 
   for (int ci = 0; ci < nch; ++ci) {
     const Chunk c = chunk(ci);
-    const int64_t sh = (int64_t)(base + ci) * p.heads + h;
-    const int next = min(ci + 1, nch - 1);  // loads without a branch: the last chunk's again
-    if (SAVE) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            p.sc[(sh * DK + d0 + 16 * m + r) * p.dvp + vcol[t]] = S[m][t][r];
-    }
-    // K S^T and Q S^T for the wave's 16 tokens
-    f32x4 kS[NT], qS[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) kS[t] = qS[t] = f32x4{0, 0, 0, 0};
-    if (KQ) {
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const Frag<P> f = load_frag<P>(&Sl[0][t * 16 + fr][s * 32 + fg * 8], BV * SP);
-          if (DELTA) mma(kS[t], fk[s], f);
-          if (!SAVE) mma(qS[t], fq[s], f);
-        }
-      load_kq(next);
-    }
-    f32x4 U[NT], ecur = ec;
+    const int64_t sh = head_of(ci);
+    const int next = min(ci + 1, nch - 1);
+    f32x4 U[NT];
     float vf[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -191,6 +224,15 @@ __global__ void __launch_bounds__(256) states_kernel(Params p) {
       for (int r = 0; r < 4; ++r)
         vf[t][r] = tok + r < c.len && vcol[t] < p.dv ? from_raw(v[t][r], p.dtype) : 0.0f;
     if (DELTA) {
+      f32x4 kS[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) kS[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          mma(kS[t], fk[s], load_frag<P>(&Sl[0][t * 16 + fr][s * 32 + fg * 8], BV * SP));
+      load_k(next);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         float x[4];
@@ -206,7 +248,7 @@ __global__ void __launch_bounds__(256) states_kernel(Params p) {
 #pragma unroll
           for (int t = 0; t < NT; ++t)
             mma(U[t], fT[s], load_frag<P>(&Rt[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
-      load_square(p.t, next, fT);
+      load_T(next);
     } else {
 #pragma unroll
       for (int t = 0; t < NT; ++t) U[t] = f32x4{vf[t][0], vf[t][1], vf[t][2], vf[t][3]};
@@ -219,24 +261,24 @@ __global__ void __launch_bounds__(256) states_kernel(Params p) {
         w[r] = beta[r] * U[t][r];
         wb[r] = VEC ? w[r] : w[r] * eo[r];
       }
-      if (!SAVE && !VEC) put4<P>(&Wt[0][t * 16 + fr][tok], BV * CP, w);
       put4<P>(&Wb[0][t * 16 + fr][tok], BV * CP, wb);
-      if (SAVE) {
-        u32x2 uu[P];
-        const float x[4] = {U[t][0], U[t][1], U[t][2], U[t][3]};
-        split4<P>(x, uu);
-#pragma unroll
-        for (int q = 0; q < P; ++q) {
-          uint16_t* d = p.u + ((sh * P + q) * C + tok) * p.dvp + vcol[t];
-          d[0] = (uint16_t)uu[q].x;
-          d[p.dvp] = (uint16_t)(uu[q].x >> 16);
-          d[2 * p.dvp] = (uint16_t)uu[q].y;
-          d[3 * p.dvp] = (uint16_t)(uu[q].y >> 16);
-        }
-      }
+      if (!SAVE && !VEC) put4<PO>(&Wt[0][t * 16 + fr][tok], BV * CP, w);
     }
     load_v(next);
     __syncthreads();
+    if (SAVE) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) p.u[(sh * C + tok + r) * p.dvp + vcol[t]] = U[t][r];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            p.sc[(sh * DK + d0 + 16 * m + r) * p.dvp + vcol[t]] = S[m][t][r];
+    }
     // the state at the chunk's end
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -250,36 +292,8 @@ __global__ void __launch_bounds__(256) states_kernel(Params p) {
         for (int t = 0; t < NT; ++t)
           mma(S[m][t], ft[m][s], load_frag<P>(&Wb[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
     }
-    load_t(next);
-    if (KQ) put_state();
-    if (!SAVE) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) qS[t][r] *= ecur[r];
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (s <= wave / 2)
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-            mma(qS[t], fA[s],
-                load_frag<P>(VEC ? &Wb[0][t * 16 + fr][s * 32 + fg * 8]
-                                 : &Wt[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
-      load_square(p.a, next, fA);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        int64_t at[4];
-        bool ok[4];
-        float x[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          at[r] = (c.row + tok + r) * p.os + (int64_t)h * p.dv + vcol[t];
-          ok[r] = p.o && tok + r < c.len && vcol[t] < p.dv;
-          x[r] = qS[t][r];
-        }
-        store_elems<4>(p.o, at, ok, p.dtype, x);
-      }
-    }
+    load_kt(next);
+    if (DELTA || !SAVE) put_state();
     __syncthreads();
   }
   if (p.s1) {
@@ -342,9 +356,9 @@ __global__ void __launch_bounds__(256) state_grads_kernel(Params p) {
   // operands are reloaded after their last use, as in states_kernel
   Frag<NPQ> fk[KS], fq[MT][2], ft[DELTA ? MT : 1][2];
   Frag<P> fA[2], fT[DELTA ? 2 : 1];
-  uint32_t x[NT][4], u[NT][4][P];
+  uint32_t x[NT][4];
+  float u[NT][4];
   f32x4 beta, ec = {1, 1, 1, 1}, eo = {1, 1, 1, 1}, dec[MT];
-  const int own = wave * 16 + fr;
   auto chunk = [&](int ci) {
     Chunk c;
     c.n = n;
@@ -371,23 +385,19 @@ __global__ void __launch_bounds__(256) state_grads_kernel(Params p) {
       load_raw<4>(p.dO, at, p.dtype, x[t]);
       if (p.dbeta) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int q = 0; q < P; ++q)
-            u[t][r][q] = p.u[((sh * P + q) * C + tok + r) * p.dvp + vcol[t]];
+        for (int r = 0; r < 4; ++r) u[t][r] = p.u[(sh * C + tok + r) * p.dvp + vcol[t]];
       }
     }
   };
   auto load_k = [&](int ci) {
-    const Rows kr = rows_of<DK>(p, p.k, VEC ? p.korow : p.krow, p.ks, VEC, base + ci, h, chunk(ci));
+    const auto k = rows_of<DK, NPQ == 1>(p, p.k, VEC ? p.korow : p.krow, p.ks, VEC, base + ci, h, chunk(ci));
 #pragma unroll
-    for (int s = 0; s < KS; ++s)
-      fk[s] = load_frag<NPQ>(kr.p + min(own, kr.len - 1) * kr.row + s * 32 + fg * 8, kr.plane);
+    for (int s = 0; s < KS; ++s) fk[s] = k.template frag<NPQ>(wave, s);
   };
   auto load_square = [&](const uint16_t* m, int ci, Frag<P>* f) {
-    const uint16_t* at = m + ((int64_t)(base + ci) * p.heads + h) * P * C * C + own * C + fg * 8;
-    f[0] = load_frag<P>(at, C * C);
-    f[1] = load_frag<P>(at + 32, C * C);
+    const uint16_t* at = m + ((int64_t)(base + ci) * p.heads + h) * P * C * C;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) f[s] = tile_frag<P, C>(at, wave, s, C * C);
   };
   auto load_t = [&](int ci) {
     const int slot = base + ci;
@@ -400,9 +410,8 @@ __global__ void __launch_bounds__(256) state_grads_kernel(Params p) {
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const int64_t at = (int64_t)(wave * (DK / 4) + 16 * m + fr) * C + s * 32 + fg * 8;
-        fq[m][s] = load_frag<NPQ>(qt + at, DK * C);
-        if (DELTA) ft[m][s] = load_frag<NPQ>(kt + at, DK * C);
+        fq[m][s] = tile_frag<NPQ, C>(qt, wave * MT + m, s, DK * C);
+        if (DELTA) ft[m][s] = tile_frag<NPQ, C>(kt, wave * MT + m, s, DK * C);
       }
       dec[m] = VEC ? *reinterpret_cast<const f32x4*>(p.decay + sh * DK + d0 + 16 * m)
                    : f32x4{end, end, end, end};
@@ -436,11 +445,7 @@ __global__ void __launch_bounds__(256) state_grads_kernel(Params p) {
       for (int r = 0; r < 4; ++r) {
         xo[r] = tok + r < c.len && vcol[t] < p.dv ? from_raw(x[t][r], p.dtype) : 0.0f;
         xe[r] = xo[r] * ec[r];
-        uc[t][r] = 0.0f;
-        if (p.dbeta) {
-#pragma unroll
-          for (int q = P - 1; q >= 0; --q) uc[t][r] += bf16_to_f((uint16_t)u[t][r][q]);
-        }
+        uc[t][r] = p.dbeta ? u[t][r] : 0.0f;
       }
       put4<NPO>(&Ot[0][t * 16 + fr][tok], BV * CP, xo);
       if (!VEC) put4<P>(&Oe[0][t * 16 + fr][tok], BV * CP, xe);
@@ -504,16 +509,8 @@ __global__ void __launch_bounds__(256) state_grads_kernel(Params p) {
       }
       store_elems<4>(p.dv_out, at, ok, p.dtype, y);
       if (DELTA) {
-        u32x2 yy[P];
-        split4<P>(y, yy);
 #pragma unroll
-        for (int q = 0; q < P; ++q) {
-          uint16_t* d = p.y + ((sh * P + q) * C + tok) * p.dvp + vcol[t];
-          d[0] = (uint16_t)yy[q].x;
-          d[p.dvp] = (uint16_t)(yy[q].x >> 16);
-          d[2 * p.dvp] = (uint16_t)yy[q].y;
-          d[3 * p.dvp] = (uint16_t)(yy[q].y >> 16);
-        }
+        for (int r = 0; r < 4; ++r) p.y[(sh * C + tok + r) * p.dvp + vcol[t]] = y[r];
       }
     }
     if (p.dbeta) {

@@ -178,15 +178,6 @@ __device__ __forceinline__ Frag<N> load_frag(const uint16_t* p, int64_t plane) {
   return f;
 }
 
-template <int N>
-__device__ __forceinline__ Frag<N> load_frag_if(bool ok, const uint16_t* p, int64_t plane) {
-  if (ok) return load_frag<N>(p, plane);
-  Frag<N> f;
-#pragma unroll
-  for (int n = 0; n < N; ++n) f.t[n] = u32x4{0, 0, 0, 0};
-  return f;
-}
-
 // acc += A B^T over 32 columns.  Of the products of terms i and j those with
 // i + j below the number of terms are taken, the smallest first: what is left
 // out is below what the terms themselves leave out.  Result: column lane & 15,
@@ -215,31 +206,64 @@ __device__ __forceinline__ void put4(uint16_t* dst, int plane, const float (&x)[
   for (int n = 0; n < N; ++n) *reinterpret_cast<u32x2*>(dst + n * plane) = t[n];
 }
 
-// A row-major operand: the caller's bfloat16 rows, or planes in the workspace.
+// Operands in the workspace lie in the order in which waves load them: tiles of
+// 16 rows x 32 columns, one kilobyte of 64 lanes' 16 bytes, so that a fragment
+// load reads eight whole cache lines.  (Rows of 2 DK bytes took 200 cycles a
+// load, bound by the lines in flight.)
+template <int COLS>
+__device__ __forceinline__ int tiled(int row, int col) {
+  return ((row >> 4) * (COLS / 32) + (col >> 5)) * 512 + ((row & 15) + ((col & 31) >> 3) * 16) * 8 +
+         (col & 7);
+}
+
+// Fragment s of row block rb.
+template <int N, int COLS>
+__device__ __forceinline__ Frag<N> tile_frag(const uint16_t* p, int rb, int s, int64_t plane) {
+  return load_frag<N>(p + (rb * (COLS / 32) + s) * 512 + (threadIdx.x & 63) * 8, plane);
+}
+
+// The first N terms.
+template <int N, int M>
+__device__ __forceinline__ Frag<N> head(const Frag<M>& f) {
+  Frag<N> h;
+#pragma unroll
+  for (int n = 0; n < N; ++n) h.t[n] = f.t[n];
+  return h;
+}
+
+// q or k of a chunk as the left operand: the caller's bfloat16 rows, or tiles
+// in the workspace.  Rows behind the sequence's end repeat its last row: beta is
+// zero there, so what they compute reaches neither a state nor an output.
+template <int DK, bool DIRECT>
 struct Rows {
   const uint16_t* p;
-  int64_t row, plane;
-  int len;  // rows that exist; the others count as zero
+  int64_t stride;
+  int last;
+
+  template <int N>
+  __device__ __forceinline__ Frag<N> frag(int rb, int s) const {
+    const int lane = threadIdx.x & 63;
+    if (DIRECT)
+      return load_frag<N>(p + min(rb * 16 + (lane & 15), last) * stride + s * 32 + (lane >> 4) * 8, 0);
+    return tile_frag<N, DK>(p, rb, s, C * DK);
+  }
 };
 
-template <int DK>
-__device__ __forceinline__ Rows rows_of(const Params& p, const void* user, const uint16_t* ws,
-                                        int64_t stride, bool per_head, int slot, int h,
-                                        const Chunk& c) {
+template <int DK, bool DIRECT>
+__device__ __forceinline__ Rows<DK, DIRECT> rows_of(const Params& p, const void* user,
+                                                    const uint16_t* ws, int64_t stride,
+                                                    bool per_head, int slot, int h,
+                                                    const Chunk& c) {
   const int group = p.heads / p.heads_qk;
-  Rows r;
-  if (p.direct) {
+  Rows<DK, DIRECT> r;
+  if (DIRECT) {
     r.p = static_cast<const uint16_t*>(user) + c.row * stride + (int64_t)(h / group) * DK;
-    r.row = stride;
-    r.plane = 0;
-    r.len = c.len;
+    r.stride = stride;
+    r.last = c.len - 1;
   } else {
     const int64_t sh = per_head ? (int64_t)slot * p.heads + h
                                 : (int64_t)slot * p.heads_qk + h / group;
-    r.p = ws + sh * p.terms * C * DK;
-    r.row = DK;
-    r.plane = C * DK;
-    r.len = C;
+    r.p = ws + sh * P * C * DK;
   }
   return r;
 }

@@ -21,7 +21,7 @@
 
 namespace qscan {
 
-struct ValueRows {  // [kChunk][dvp] rows of d_o, U or Y
+struct ValueRows {  // [kChunk][dvp] rows of d_o
   const uint16_t* p;
   int64_t row, plane;
   int len;
@@ -43,9 +43,15 @@ __device__ __forceinline__ ValueRows dout_rows(const Params& p, int64_t sh, int 
   return r;
 }
 
+// Rows behind the end repeat the last one (of dO they are set to zero where that matters).
 template <int N>
 __device__ __forceinline__ Frag<N> value_frag(const ValueRows& v, int row, int col) {
-  return load_frag_if<N>(row < v.len, v.p + row * v.row + col, v.plane);
+  Frag<N> f = load_frag<N>(v.p + min(row, v.len - 1) * v.row + col, v.plane);
+  if (row >= v.len) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) f.t[n] = u32x4{0, 0, 0, 0};
+  }
+  return f;
 }
 
 // Eight FP32 values, and their terms.
@@ -142,36 +148,46 @@ __global__ void __launch_bounds__(256) grads_kernel(Params p) {
 
   for (int v0 = 0; v0 < p.dvp; v0 += VS) {
     const int ns = p.dvp - v0 >= VS ? 2 : 1;
-    // rows into LDS: 8 vectors of 8 a row, 2 rows of every plane a thread
+    // rows into LDS: 8 vectors of 8 a row, 2 rows of every array a thread
     {
-      const int col = threadIdx.x & 7;
-      u32x4 st[NP][2];
+      constexpr int A = DELTA ? 2 : 1;  // U, Y
+      const int col = threadIdx.x & 7, row = threadIdx.x >> 3;
+      u32x4 so[NPO][2];
+      f32x4 sf[A][2][2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = i * 32 + (threadIdx.x >> 3);
+        const int r = i * 32 + row;
         // columns behind dvp repeat the last ones and are not used
         const int64_t vc = v0 + min(col * 8, p.dvp - v0 - 8);
         const int64_t ro = (int64_t)min(r, dO.len - 1) * dO.row + vc;
 #pragma unroll
-        for (int n = 0; n < NPO; ++n)
-          st[n][i] = *reinterpret_cast<const u32x4*>(dO.p + n * dO.plane + ro);
-#pragma unroll
-        for (int n = 0; n < P; ++n) {
-          const int64_t at = ((sh * P + n) * C + r) * p.dvp + vc;
-          st[NPO + n][i] = *reinterpret_cast<const u32x4*>(p.u + at);
-          if (DELTA) st[NPO + P + n][i] = *reinterpret_cast<const u32x4*>(p.y + at);
+        for (int n = 0; n < NPO; ++n) {
+          so[n][i] = *reinterpret_cast<const u32x4*>(dO.p + n * dO.plane + ro);
+          if (r >= c.len) so[n][i] = u32x4{0, 0, 0, 0};
         }
-        if (r >= c.len) {
+        const int64_t at = (sh * C + r) * p.dvp + vc;
 #pragma unroll
-          for (int n = 0; n < NPO; ++n) st[n][i] = u32x4{0, 0, 0, 0};
+        for (int q = 0; q < 2; ++q) {
+          sf[0][i][q] = *reinterpret_cast<const f32x4*>(p.u + at + q * 4);
+          if (DELTA) sf[A - 1][i][q] = *reinterpret_cast<const f32x4*>(p.y + at + q * 4);
         }
       }
       __syncthreads();  // the last slab has been read
 #pragma unroll
-      for (int n = 0; n < NP; ++n)
+      for (int i = 0; i < 2; ++i) {
+        const int o = (i * 32 + row) * VP + col * 8;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          *reinterpret_cast<u32x4*>(lds + (n * C + i * 32 + (threadIdx.x >> 3)) * VP + col * 8) = st[n][i];
+        for (int n = 0; n < NPO; ++n) *reinterpret_cast<u32x4*>(Ol + n * C * VP + o) = so[n][i];
+#pragma unroll
+        for (int a = 0; a < A; ++a) {
+          const float x[8] = {sf[a][i][0][0], sf[a][i][0][1], sf[a][i][0][2], sf[a][i][0][3],
+                              sf[a][i][1][0], sf[a][i][1][1], sf[a][i][1][2], sf[a][i][1][3]};
+          const Frag<P> f = split8<P>(x);
+#pragma unroll
+          for (int n = 0; n < P; ++n)
+            *reinterpret_cast<u32x4*>((a ? Yl : Ul) + n * C * VP + o) = f.t[n];
+        }
+      }
     }
     f32x4 sv[CT][2][2], xv[CT][2][2];
 #pragma unroll
@@ -295,9 +311,8 @@ __global__ void __launch_bounds__(256) grads_kernel(Params p) {
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const int64_t at = (int64_t)ch * C + s * 32 + fg * 8;
-      const Frag<NPQ> fk = load_frag<NPQ>(kn + at, DK * C);
-      const Frag<NPQ> fq = load_frag<NPQ>(qe + at, DK * C);
+      const Frag<NPQ> fk = tile_frag<NPQ, C>(kn, wave * CT + ct, s, DK * C);
+      const Frag<NPQ> fq = tile_frag<NPQ, C>(qe, wave * CT + ct, s, DK * C);
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         const int o = (m * 16 + fr) * CP + s * 32 + fg * 8;
@@ -312,9 +327,8 @@ __global__ void __launch_bounds__(256) grads_kernel(Params p) {
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const int64_t at = (int64_t)(ch0 + ct * 16) * C + s * 32 + fg * 8;
-        const Frag<NPQ> fk = load_frag<NPQ>(kn + at, DK * C);
-        const Frag<NPQ> fe = load_frag<NPQ>(ke + at, DK * C);
+        const Frag<NPQ> fk = tile_frag<NPQ, C>(kn, wave * CT + ct, s, DK * C);
+        const Frag<NPQ> fe = tile_frag<NPQ, C>(ke, wave * CT + ct, s, DK * C);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const int o = (m * 16 + fr) * CP + s * 32 + fg * 8;
@@ -332,7 +346,7 @@ __global__ void __launch_bounds__(256) grads_kernel(Params p) {
     for (int r = 0; r < 4; ++r) x[r] = 0.0f;
 #pragma unroll
     for (int n = NPR - 1; n >= 0; --n) {
-      const u32x2 w = *reinterpret_cast<const u32x2*>(src + ((int64_t)n * DK + ch) * C + t0);
+      const u32x2 w = *reinterpret_cast<const u32x2*>(src + n * DK * C + tiled<C>(ch, t0));
       x[0] += __uint_as_float(w.x << 16);
       x[1] += __uint_as_float(w.x & 0xFFFF0000u);
       x[2] += __uint_as_float(w.y << 16);
@@ -480,17 +494,19 @@ __global__ void __launch_bounds__(256) grads_vector_kernel(Params p) {
   const int hq = h / (p.heads / p.heads_qk);
   const float* rows = rows_at(p, slot, h);
   const ValueRows dO = dout_rows(p, sh, h, c);
-  const ValueRows U = {p.u + sh * P * C * p.dvp, p.dvp, (int64_t)C * p.dvp, C};
-  const ValueRows Y = {p.y + sh * P * C * p.dvp, p.dvp, (int64_t)C * p.dvp, C};
+  auto uy_frag = [&](const float* src, int row, int col) {
+    float x[8];
+    return state_frag(src + (sh * C + row) * p.dvp + col, x);
+  };
   const int nvs = p.dvp / 32;
 
   for (int b = 0; b < 4; ++b) {
     f32x4 e = {0, 0, 0, 0}, f = {0, 0, 0, 0};
     if (b <= wave)
       for (int s = 0; s < nvs; ++s) {
-        const Frag<P> u = value_frag<P>(U, b * 16 + fr, s * 32 + fg * 8);
+        const Frag<P> u = uy_frag(p.u, b * 16 + fr, s * 32 + fg * 8);
         mma(e, value_frag<NPO>(dO, wave * 16 + fr, s * 32 + fg * 8), u);
-        if (DELTA) mma(f, value_frag<P>(Y, wave * 16 + fr, s * 32 + fg * 8), u);
+        if (DELTA) mma(f, uy_frag(p.y, wave * 16 + fr, s * 32 + fg * 8), u);
       }
     const int j = b * 16 + fr, i0 = wave * 16 + fg * 4;
     const float beta = rows[2 * C + j];
@@ -549,8 +565,8 @@ __global__ void __launch_bounds__(256) grads_vector_kernel(Params p) {
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         mma(aq[m], value_frag<NPO>(dO, m * 16 + fr, s * 32 + fg * 8), fs);
-        if (DELTA) mma(ap[m], value_frag<P>(Y, m * 16 + fr, s * 32 + fg * 8), fs);
-        mma(am[m], value_frag<P>(U, m * 16 + fr, s * 32 + fg * 8), fx);
+        if (DELTA) mma(ap[m], uy_frag(p.y, m * 16 + fr, s * 32 + fg * 8), fs);
+        mma(am[m], uy_frag(p.u, m * 16 + fr, s * 32 + fg * 8), fx);
       }
     }
     xs += __shfl_xor(xs, 16);
@@ -583,7 +599,7 @@ __global__ void __launch_bounds__(256) grads_vector_kernel(Params p) {
     for (int s = 0; s < 2; ++s) {
       const int t0 = s * 32 + fg * 8, blk = t0 / 16;  // the lane's 8 tokens and their block
       float k[8], q[8], ks[8], qs[8], kp[8];
-      const int64_t at = (tq * NPR * DK + ch) * C + t0;
+      const int64_t at = tq * NPR * DK * C + tiled<C>(ch, t0);
 #pragma unroll
       for (int e = 0; e < 8; ++e) k[e] = q[e] = 0.0f;
 #pragma unroll

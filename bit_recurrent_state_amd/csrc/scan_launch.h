@@ -14,7 +14,8 @@ constexpr int kChunk = 64;  // tokens of a chunk
 constexpr int kTerms = 3;   // bfloat16 terms of an FP32 operand
 constexpr float kFarDecay = 8.0f;  // largest decay of a chunk, as a logarithm, that is divided out
 
-// Workspace arrays hold bfloat16 terms as planes: [...][term][row][col].
+// Workspace operands are bfloat16 terms, a plane per term, in tiles of 16 rows
+// x 32 columns (scan_device.h); the sizes below are rows x columns.
 // "slot" is a chunk of a sequence: sequence n owns the slots from
 // offsets[n] / kChunk + n on, so slots need no prefix sums and never overlap.
 struct Params {
@@ -45,8 +46,8 @@ struct Params {
                              // block of 16, where the chunk decays far)
   uint16_t *a, *t;           // [slot][head][kTerms][kChunk][kChunk]
   uint16_t *at, *t2t;        // backward: transposed A, transposed (I + beta L)^-1
-  uint16_t* dop;             // [slot][head][term][kChunk][dvp] d_o as planes
-  uint16_t *u, *y;           // [slot][head][kTerms][kChunk][dvp]
+  uint16_t* dop;             // [slot][head][term][kChunk][dvp] d_o as planes of plain rows
+  float *u, *y;              // [slot][head][kChunk][dvp]
   float *sc, *xc;            // [slot][head][dk][dvp]: states / state gradients
   float* dbpart;             // [nvb][slot][head][kChunk]
   float *dqpart, *dkpart;    // [slot][head][kChunk][dk] when heads share q and k

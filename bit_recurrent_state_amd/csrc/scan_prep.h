@@ -49,8 +49,8 @@ __global__ void __launch_bounds__(256) operands_kernel(Params p, int backward) {
           lo[i] = (x[2 * i] & 0xFFFFu) | (x[2 * i + 1] << 16);
           hi[i] = (x[2 * i] >> 16) | (x[2 * i + 1] & 0xFFFF0000u);
         }
-        *reinterpret_cast<u32x4*>(tr + (sh * DK + ch) * C + t0) = lo;
-        *reinterpret_cast<u32x4*>(tr + (sh * DK + ch + 1) * C + t0) = hi;
+        *reinterpret_cast<u32x4*>(tr + sh * DK * C + tiled<C>(ch, t0)) = lo;
+        *reinterpret_cast<u32x4*>(tr + sh * DK * C + tiled<C>(ch + 1, t0)) = hi;
       }
     }
     return;
@@ -73,19 +73,28 @@ __global__ void __launch_bounds__(256) operands_kernel(Params p, int backward) {
       load_raw<8>(src, at, p.dtype, raw);
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = t0 + i < c.len ? from_raw(raw[i], p.dtype) : 0.0f;
+      if (!transpose) continue;
       const Frag<P> f = split8<P>(x);
-      for (int n = 0; n < terms; ++n) {
-        const u32x4 t = n == 0 ? f.t[0] : n == 1 ? f.t[1] : f.t[2];
-        if (transpose)
-          *reinterpret_cast<u32x4*>(tr + ((sh * terms + n) * DK + ch) * C + t0) = t;
-        if (!p.direct && !vec) {
-          const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+      for (int n = 0; n < terms; ++n)
+        *reinterpret_cast<u32x4*>(tr + (sh * terms + n) * DK * C + tiled<C>(ch, t0)) =
+            n == 0 ? f.t[0] : n == 1 ? f.t[1] : f.t[2];
+    }
+    if (p.direct || vec) continue;
+    for (int u = threadIdx.x; u < DK / 8 * C; u += 256) {  // rows: 8 channels of a token
+      const int c0 = u % (DK / 8) * 8, tk = u / (DK / 8);
+      float x[8];
+      int64_t at[8];
+      uint32_t raw[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            rw[((sh * terms + n) * C + t0 + i) * DK + ch] =
-                (uint16_t)(w[i / 2] >> (16 * (i & 1)));
-        }
-      }
+      for (int i = 0; i < 8; ++i)
+        at[i] = (c.row + min(tk, c.len - 1)) * stride + (int64_t)hq * DK + c0 + i;
+      load_raw<8>(src, at, p.dtype, raw);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = tk < c.len ? from_raw(raw[i], p.dtype) : 0.0f;
+      const Frag<P> f = split8<P>(x);
+#pragma unroll
+      for (int n = 0; n < P; ++n)
+        *reinterpret_cast<u32x4*>(rw + (sh * P + n) * DK * C + tiled<DK>(tk, c0)) = f.t[n];
     }
   }
 }
@@ -200,14 +209,14 @@ __device__ __forceinline__ void store_inverses(const Params& p, Square* M, Squar
     const int r = u / (C / 4), q0 = u % (C / 4) * 4;
     const f32x4 v = *reinterpret_cast<const f32x4*>(&M[r][q0]);
     const float x[4] = {v[0], v[1], v[2], v[3]};
-    put4<P>(t1 + r * C + q0, C * C, x);
+    put4<P>(t1 + tiled<C>(r, q0), C * C, x);
   }
   if (BWD) {
     uint16_t* t2 = p.t2t + sh * P * C * C;
     for (int u = threadIdx.x; u < C * C / 4; u += 256) {
       const int r = u % C, q0 = u / C * 4;  // rows by lane: LDS columns are then read without conflicts
       const float x[4] = {M2[q0][r], M2[q0 + 1][r], M2[q0 + 2][r], M2[q0 + 3][r]};
-      put4<P>(t2 + r * C + q0, C * C, x);
+      put4<P>(t2 + tiled<C>(r, q0), C * C, x);
     }
   }
 }
@@ -273,37 +282,28 @@ __global__ void __launch_bounds__(256) chunk_kernel(Params p) {
     reinterpret_cast<double*>(r + 3 * C)[lane] = s;
   }
   __syncthreads();
-  const Rows q = rows_of<DK>(p, p.q, p.qrow, p.qs, VEC, slot, h, c);
-  const Rows k = rows_of<DK>(p, p.k, VEC ? p.knrow : p.krow, p.ks, VEC, slot, h, c);
-  const Rows ki = rows_of<DK>(p, p.k, p.krow, p.ks, VEC, slot, h, c);  // the reading key of L
-  const int fr = lane & 15, fc = (lane >> 4) * 8;
+  constexpr bool D = NPQ == 1;
+  const auto q = rows_of<DK, D>(p, p.q, p.qrow, p.qs, VEC, slot, h, c);
+  const auto k = rows_of<DK, D>(p, p.k, VEC ? p.knrow : p.krow, p.ks, VEC, slot, h, c);
+  const auto ki = rows_of<DK, D>(p, p.k, p.krow, p.ks, VEC, slot, h, c);  // the reading key of L
+  const int fr = lane & 15;
   const int own = wave * 16 + fr;  // forward: token i; backward: token j
-  const Rows& mine = BWD ? k : q;
   Frag<NPQ> fm[DK / 32], fk[DK / 32];
 #pragma unroll
   for (int s = 0; s < DK / 32; ++s) {
-    fm[s] = load_frag_if<NPQ>(own < mine.len, mine.p + own * mine.row + s * 32 + fc, mine.plane);
-    const Rows& l = BWD ? k : ki;
-    if (DELTA) fk[s] = load_frag_if<NPQ>(own < l.len, l.p + own * l.row + s * 32 + fc, l.plane);
+    fm[s] = BWD ? k.template frag<NPQ>(wave, s) : q.template frag<NPQ>(wave, s);
+    if (DELTA) fk[s] = BWD ? fm[s] : ki.template frag<NPQ>(wave, s);
   }
   // tile (wave, b): columns own (i forward, j backward), rows of block b
   for (int b = 0; b < 4; ++b) {
     f32x4 acc = {0, 0, 0, 0}, acl = {0, 0, 0, 0};
-    const int other = b * 16 + fr;
     const bool need = BWD ? b >= wave : b <= wave;
     if (need) {
-      const Rows& his = BWD ? q : k;
 #pragma unroll
       for (int s = 0; s < DK / 32; ++s) {
-        const Frag<NPQ> f =
-            load_frag_if<NPQ>(other < his.len, his.p + other * his.row + s * 32 + fc, his.plane);
+        const Frag<NPQ> f = BWD ? q.template frag<NPQ>(b, s) : k.template frag<NPQ>(b, s);
         mma(acc, f, fm[s]);
-        if (DELTA) {
-          const Frag<NPQ> g =
-              BWD ? load_frag_if<NPQ>(other < ki.len, ki.p + other * ki.row + s * 32 + fc, ki.plane)
-                  : f;
-          mma(acl, g, fk[s]);
-        }
+        if (DELTA) mma(acl, BWD ? ki.template frag<NPQ>(b, s) : f, fk[s]);
       }
     }
     float a[4];
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(256) chunk_kernel(Params p) {
       }
     }
     uint16_t* dst = (BWD ? p.at : p.a) + sh * P * C * C;
-    put4<P>(dst + own * C + r0, C * C, a);
+    put4<P>(dst + tiled<C>(own, r0), C * C, a);
   }
   if (DELTA) store_inverses<BWD>(p, M, M2, sh);
 }
@@ -421,14 +421,14 @@ __global__ void __launch_bounds__(DK) operands_vector_kernel(Params p) {
         const uint32_t wn[4] = {fn.t[n].x, fn.t[n].y, fn.t[n].z, fn.t[n].w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int64_t at = ((sh * P + n) * C + t0 + i) * DK + ch;
+          const int64_t at = (sh * P + n) * C * DK + tiled<DK>(t0 + i, ch);
           const int sft = 16 * (i & 1);
           p.qrow[at] = (uint16_t)(wq[i / 2] >> sft);
           p.knrow[at] = (uint16_t)(wn[i / 2] >> sft);
           if (DELTA) p.krow[at] = (uint16_t)(wk[i / 2] >> sft);
           if (BWD) p.korow[at] = (uint16_t)(wo[i / 2] >> sft);
         }
-        const int64_t tt = ((sh * P + n) * DK + ch) * C + t0;
+        const int64_t tt = (sh * P + n) * C * DK + tiled<C>(ch, t0);
         *reinterpret_cast<u32x4*>(p.kt + tt) = fo.t[n];
         if (BWD) *reinterpret_cast<u32x4*>(p.qt + tt) = fq.t[n];
         if (BWD) *reinterpret_cast<u32x4*>(p.knt + tt) = fn.t[n];
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(256) chunk_vector_kernel(Params p) {
     float x[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = BWD ? A[q0 + e][r] : A[r][q0 + e];
-    put4<P>(dst + r * C + q0, C * C, x);
+    put4<P>(dst + tiled<C>(r, q0), C * C, x);
   }
   if (DELTA) store_inverses<BWD>(p, M, M2, sh);
 }
