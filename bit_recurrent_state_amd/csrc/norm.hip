@@ -21,13 +21,6 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 template <int DT>
-__device__ __forceinline__ float widen(const void* p, int64_t i) {
-  if (DT == 1) return __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
-  if (DT == 2) return (float)static_cast<const _Float16*>(p)[i];
-  return static_cast<const float*>(p)[i];
-}
-
-template <int DT>
 __device__ __forceinline__ uint32_t narrow2(float a, float b) {
   const f32x2 f = {a, b};
   if (DT == 1) return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
@@ -41,47 +34,58 @@ __device__ __forceinline__ int column(int v, int e, int t, int team) {
   return VEC ? (v * team + t) * 8 + e : (v * 8 + e) * team + t;
 }
 
+// A thread's values of a row as they lie in memory, so that the next row's can
+// be on their way while this one is worked on.
+template <int DT, int V>
+struct Raw {
+  u32x4 w[V][DT == 0 ? 2 : 1];
+};
+
 template <int DT, int V, bool VEC>
-__device__ __forceinline__ void load_row(const void* p, int64_t at, int t, int team, int width,
-                                         float (&x)[V * 8]) {
+__device__ __forceinline__ void load_raw(const void* p, int64_t at, int t, int team, int width,
+                                         Raw<DT, V>& x) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if (VEC) {
-      const int c = column<true>(v, 0, t, team);
-      if (c >= width) {
+      // columns behind the width repeat the last ones and count as zero later
+      const int c = min(column<true>(v, 0, t, team), width - 8);
+      const char* s = static_cast<const char*>(p) + (at + c) * (DT == 0 ? 4 : 2);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[v * 8 + e] = 0.0f;
-      } else if (DT == 0) {
-        const f32x4* s = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + at + c);
-        const f32x4 a = s[0], b = s[1];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[v * 8 + e] = a[e];
-          x[v * 8 + 4 + e] = b[e];
-        }
-      } else {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + at + c);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (DT == 1) {
-            x[v * 8 + 2 * e] = __uint_as_float(w[e] << 16);
-            x[v * 8 + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-          } else {
-            const uint32_t two = w[e];  // bit casts take whole values, not vector elements
-            const f16x2 h = __builtin_bit_cast(f16x2, two);
-            x[v * 8 + 2 * e] = (float)h.x;
-            x[v * 8 + 2 * e + 1] = (float)h.y;
-          }
-        }
-      }
+      for (int i = 0; i < (DT == 0 ? 2 : 1); ++i) x.w[v][i] = reinterpret_cast<const u32x4*>(s)[i];
     } else {
+      uint32_t e[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = column<false>(v, e, t, team);
-        x[v * 8 + e] = c < width ? widen<DT>(p, at + c) : 0.0f;
+      for (int i = 0; i < 8; ++i) {
+        const int64_t c = at + min(column<false>(v, i, t, team), width - 1);
+        e[i] = DT == 0 ? static_cast<const uint32_t*>(p)[c] : static_cast<const uint16_t*>(p)[c];
+      }
+      if (DT == 0) {
+        x.w[v][0] = u32x4{e[0], e[1], e[2], e[3]};
+        x.w[v][DT == 0] = u32x4{e[4], e[5], e[6], e[7]};
+      } else {
+        x.w[v][0] = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
       }
     }
   }
+}
+
+template <int DT, int V, bool VEC>
+__device__ __forceinline__ void widen(const Raw<DT, V>& r, int t, int team, int width,
+                                      float (&x)[V * 8]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t w = DT == 0 ? r.w[v][DT == 0 ? i / 4 : 0][i % 4] : r.w[v][0][i / 2];
+      float f;
+      if (DT == 0)
+        f = __uint_as_float(w);
+      else if (DT == 1)
+        f = __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+      else
+        f = (float)__builtin_bit_cast(_Float16, (uint16_t)(i & 1 ? w >> 16 : w));
+      x[v * 8 + i] = column<VEC>(v, i, t, team) < width ? f : 0.0f;
+    }
 }
 
 template <int DT, int V, bool VEC>
@@ -158,21 +162,33 @@ __device__ __forceinline__ void team_sum(float& a, float& b, int team, float (*l
   }
 }
 
-// act(z) and, for the gradient, its derivative.
+// act(z) and, for the gradient, its derivative.  exp(-z) is 2^t (1 + r ln 2) with
+// t + r = -z log2 e in two parts, the reciprocal is refined once: both hold to
+// an ulp or two at a third of the library functions' instructions, which bound
+// the backward kernel otherwise.
 __device__ __forceinline__ float activate(float z, int act, float& slope) {
-  const float s = 1.0f / (1.0f + expf(-z));
-  slope = act == 0 ? s * (1.0f + z * (1.0f - s)) : s * (1.0f - s);
+  const float hi = -1.44269502f, lo = -1.92596303e-8f;
+  const float c = z > 87.0f ? 87.0f : z < -87.0f ? -87.0f : z;  // e stays a normal number; NaN stays
+  const float t = c * hi;
+  const float r = fmaf(c, lo, fmaf(c, hi, -t));
+  float e = __builtin_amdgcn_exp2f(t);
+  e = fmaf(e, r * 0.693147182f, e);
+  const float d = 1.0f + e;
+  float s = __builtin_amdgcn_rcpf(d);
+  s = fmaf(fmaf(-d, s, 1.0f), s, s);
+  const float q = s * e;  // 1 - s without cancellation
+  slope = act == 0 ? s * fmaf(z, q, 1.0f) : s * q;
   return act == 0 ? z * s : s;
 }
 
 struct Place {
-  int64_t x, gate, residual, out;
+  int64_t x, gate, residual;
 };
 
 __device__ __forceinline__ Place place(const Params& p, int64_t row) {
-  if (p.groups == 1) return {row * p.xs, row * p.gs, row * p.rs, row * p.width};
+  if (p.groups == 1) return {row * p.xs, row * p.gs, row * p.rs};
   const int64_t tok = row / p.groups, in = (row - tok * p.groups) * p.width;
-  return {tok * p.xs + in, tok * p.gs + in, tok * p.rs + in, row * p.width};
+  return {tok * p.xs + in, tok * p.gs + in, tok * p.rs + in};
 }
 
 template <int DT, int V, bool WIDE, bool VEC, int BLOCK>
@@ -187,35 +203,44 @@ __global__ void __launch_bounds__(BLOCK) forward_kernel(Params p) {
   load_weight<V, VEC>(p.scale, 0, t, team, width, sc);
   if (p.h) load_weight<V, VEC>(p.next_weight, 0, t, team, width, w2);
   // WIDE teams are whole workgroups, the others stay inside a wave: no barrier is passed by a part
-  for (int64_t row = first < p.teams ? first : p.rows; row < p.rows; row += p.teams) {
-    const Place at = place(p, row);
+  int64_t row = first < p.teams ? first : p.rows;
+  if (row >= p.rows) return;
+  Raw<DT, V> rx, rz, ry;
+  auto load = [&](int64_t r) {
+    const Place at = place(p, r);
+    load_raw<DT, V, VEC>(p.x, at.x, t, team, width, rx);
+    if (p.gate) load_raw<DT, V, VEC>(p.gate, at.gate, t, team, width, rz);
+    if (p.residual) load_raw<DT, V, VEC>(p.residual, at.residual, t, team, width, ry);
+  };
+  load(row);
+  for (; row < p.rows; row += p.teams) {
+    const int64_t out = row * width;
     float x[N], z[N], y[N];
-    load_row<DT, V, VEC>(p.x, at.x, t, team, width, x);
-    if (p.gate) load_row<DT, V, VEC>(p.gate, at.gate, t, team, width, z);
-    if (p.residual) load_row<DT, V, VEC>(p.residual, at.residual, t, team, width, y);
+    widen<DT, V, VEC>(rx, t, team, width, x);
+    if (p.gate) widen<DT, V, VEC>(rz, t, team, width, z);
+    if (p.residual) widen<DT, V, VEC>(ry, t, team, width, y);
+    if (row + p.teams < p.rows) load(row + p.teams);
     float s = 0.0f, unused = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) s = fmaf(x[i], x[i], s);
     team_sum<WIDE>(s, unused, team, lds);
     const float rs = 1.0f / sqrtf(s / (float)width + p.eps);
+    s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < N; ++i) {  // columns behind the width hold zeros
       float n = x[i] * rs * w[i], slope;
       if (p.gate) n *= activate(z[i], p.act, slope);
       n *= sc[i];
       x[i] = p.residual ? y[i] + n : n;
-    }
-    if (p.r) store_row<DT, V, VEC>(p.r, at.out, t, team, width, x);
-    if (!p.h) continue;
-    s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i)  // columns behind the width hold zeros
       s = fmaf(x[i], x[i], s);
+    }
+    if (p.r) store_row<DT, V, VEC>(p.r, out, t, team, width, x);
+    if (!p.h) continue;
     team_sum<WIDE>(s, unused, team, lds);
     const float rs2 = 1.0f / sqrtf(s / (float)width + p.eps);
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = x[i] * rs2 * w2[i];
-    store_row<DT, V, VEC>(p.h, at.out, t, team, width, x);
+    store_row<DT, V, VEC>(p.h, out, t, team, width, x);
   }
 }
 
@@ -233,20 +258,42 @@ __global__ void __launch_bounds__(BLOCK) backward_kernel(Params p) {
   if (p.has_h) load_weight<V, VEC>(p.next_weight, 0, t, team, width, w2);
 #pragma unroll
   for (int i = 0; i < N; ++i) dw[i] = ds[i] = dw2[i] = 0.0f;
-  for (int64_t row = first < p.teams ? first : p.rows; row < p.rows; row += p.teams) {
-    const Place at = place(p, row);
-    float x[N], z[N], y[N], d[N], m[N];
-    load_row<DT, V, VEC>(p.x, at.x, t, team, width, x);
-    if (p.gate) load_row<DT, V, VEC>(p.gate, at.gate, t, team, width, z);
-    const bool use_h = p.has_h && p.dh;
-    if (p.residual && use_h) load_row<DT, V, VEC>(p.residual, at.residual, t, team, width, y);
-    if (p.dr)
-      load_row<DT, V, VEC>(p.dr, at.out, t, team, width, d);
-    else {
+  const bool use_h = p.has_h && p.dh;
+  Raw<DT, V> rx, rz, ry, rd, rm;
+  auto load = [&](int64_t r) {
+    const Place at = place(p, r);
+    load_raw<DT, V, VEC>(p.x, at.x, t, team, width, rx);
+    if (p.gate) load_raw<DT, V, VEC>(p.gate, at.gate, t, team, width, rz);
+    if (p.residual && use_h) load_raw<DT, V, VEC>(p.residual, at.residual, t, team, width, ry);
+    if (p.dr) load_raw<DT, V, VEC>(p.dr, r * width, t, team, width, rd);
+    if (use_h) load_raw<DT, V, VEC>(p.dh, r * width, t, team, width, rm);
+  };
+  int64_t row = first < p.teams ? first : p.rows;
+  if (row < p.rows) load(row);
+  for (; row < p.rows; row += p.teams) {
+    const int64_t out = row * width;
+    float x[N], z[N], y[N], d[N], m[N], act[N], slope[N];
+    widen<DT, V, VEC>(rx, t, team, width, x);
+    if (p.gate) {
+      widen<DT, V, VEC>(rz, t, team, width, z);
+#pragma unroll
+      for (int i = 0; i < N; ++i) act[i] = activate(z[i], p.act, slope[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        act[i] = 1.0f;
+        slope[i] = 0.0f;
+      }
+    }
+    if (p.residual && use_h) widen<DT, V, VEC>(ry, t, team, width, y);
+    if (p.dr) {
+      widen<DT, V, VEC>(rd, t, team, width, d);
+    } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) d[i] = 0.0f;
     }
-    if (use_h) load_row<DT, V, VEC>(p.dh, at.out, t, team, width, m);
+    if (use_h) widen<DT, V, VEC>(rm, t, team, width, m);
+    if (row + p.teams < p.rows) load(row + p.teams);
     float s = 0.0f, q = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) s = fmaf(x[i], x[i], s);
@@ -259,9 +306,7 @@ __global__ void __launch_bounds__(BLOCK) backward_kernel(Params p) {
       float ss = 0.0f, mr = 0.0f;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        float n = x[i] * w[i], slope;
-        if (p.gate) n *= activate(z[i], p.act, slope);
-        n *= sc[i];
+        const float n = x[i] * w[i] * act[i] * sc[i];
         y[i] = p.residual ? y[i] + n : n;
         ss = fmaf(y[i], y[i], ss);
         mr = fmaf(m[i] * w2[i], y[i], mr);
@@ -275,27 +320,25 @@ __global__ void __launch_bounds__(BLOCK) backward_kernel(Params p) {
         dw2[i] = fmaf(m[i], y[i] * rs2, dw2[i]);
       }
     }
-    if (p.dresidual) store_row<DT, V, VEC>(p.dresidual, at.out, t, team, width, d);
+    if (p.dresidual) store_row<DT, V, VEC>(p.dresidual, out, t, team, width, d);
     float dn = 0.0f;
     q = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      float slope = 0.0f, a = 1.0f;
-      if (p.gate) a = activate(z[i], p.act, slope);
-      ds[i] = fmaf(d[i], x[i] * w[i] * a, ds[i]);
-      const float dy = d[i] * sc[i];
-      z[i] = dy * x[i] * w[i] * slope;
+      const float a = act[i], xw = x[i] * w[i], dy = d[i] * sc[i];
+      ds[i] = fmaf(d[i], xw * a, ds[i]);
+      z[i] = dy * xw * slope[i];
       dw[i] = fmaf(dy * a, x[i], dw[i]);
       d[i] = dy * a * w[i];
       dn = fmaf(d[i], x[i], dn);
     }
-    if (p.dgate) store_row<DT, V, VEC>(p.dgate, at.out, t, team, width, z);
+    if (p.dgate) store_row<DT, V, VEC>(p.dgate, out, t, team, width, z);
     if (p.dx) {
       team_sum<WIDE>(dn, q, team, lds);
       dn *= inv;
 #pragma unroll
       for (int i = 0; i < N; ++i) d[i] = rs * (d[i] - x[i] * dn);
-      store_row<DT, V, VEC>(p.dx, at.out, t, team, width, d);
+      store_row<DT, V, VEC>(p.dx, out, t, team, width, d);
     }
   }
   if (!p.part) return;
@@ -369,9 +412,12 @@ hipError_t run(const Params& p, bool back, hipStream_t s) {
 template <int DT>
 hipError_t pick(const Params& p, bool back, hipStream_t s) {
   if (!p.wide) return run<DT, 1, false, 256>(p, back, s);
-  if (p.block == 256) return p.vectors == 1 ? run<DT, 1, true, 256>(p, back, s) : run<DT, 2, true, 256>(p, back, s);
-  if (p.block == 512) return run<DT, 2, true, 512>(p, back, s);
-  return run<DT, 2, true, 1024>(p, back, s);
+  switch (p.block) {
+    case 128: return run<DT, 1, true, 128>(p, back, s);
+    case 256: return run<DT, 1, true, 256>(p, back, s);
+    case 512: return run<DT, 1, true, 512>(p, back, s);
+    default: return p.vectors == 1 ? run<DT, 1, true, 1024>(p, back, s) : run<DT, 2, true, 1024>(p, back, s);
+  }
 }
 
 static hipError_t by_type(const Params& p, int dtype, bool back, hipStream_t s) {

@@ -37,13 +37,13 @@ int check_config(const qstate_norm_config* c) {
   return QSTATE_OK;
 }
 
-// Teams: up to 512 values a wave's part takes a row, 8 values a lane; above
-// that a workgroup with 8 or 16 values a thread.  As many teams as fill the
-// card twice (256 CUs, 8 waves each, where a row of 4096 values keeps 5 x 16
-// bytes per lane in flight), or one per row if there are fewer rows.  With a
+// Teams: rows of up to 512 values take 1 .. 64 lanes of a wave, 8 values a
+// lane; wider ones a workgroup, 8 values a thread (16 above 8192).  As many
+// teams as fill the card (256 CUs, 16 waves each forward, 8 backward, as the
+// registers allow), or one per row if there are fewer rows.  With a
 // weight for each group their number is a multiple of the groups, so that a
 // team meets one group only.
-void plan(const qstate_norm_config* c, Params& p) {
+void plan(const qstate_norm_config* c, bool backward, Params& p) {
   std::memset(&p, 0, sizeof(p));
   p.rows = c->tokens * c->groups;
   p.groups = c->groups;
@@ -56,16 +56,17 @@ void plan(const qstate_norm_config* c, Params& p) {
   p.gs = c->gate_stride ? c->gate_stride : row;
   p.rs = c->residual_stride ? c->residual_stride : row;
   p.wide = c->width > 512;
-  p.vectors = c->width > 2048 ? 2 : 1;
+  p.vectors = c->width > 8192 ? 2 : 1;
   if (p.wide) {
-    p.block = c->width > 8192 ? 1024 : c->width > 4096 ? 512 : 256;
+    p.block = 128;
+    while (p.block * 8 < c->width && p.block < 1024) p.block *= 2;
     p.team = p.block;
   } else {
     p.block = 256;
     p.team = 1;
     while (p.team * 8 < c->width) p.team *= 2;
   }
-  int64_t teams = (int64_t)256 * 512 / p.team;
+  int64_t teams = (int64_t)256 * (backward ? 512 : 1024) / p.team;
   if (teams > p.rows) teams = p.rows;
   if (p.each) teams = (teams + p.groups - 1) / p.groups * p.groups;
   p.teams = teams;
@@ -93,7 +94,7 @@ int qstate_norm(const qstate_norm_config* cfg, const void* x, const float* weigh
       !aligned(h, e) || !aligned(weight, 4) || !aligned(scale, 4) || !aligned(next_weight, 4))
     return QSTATE_E_INVALID;
   Params p;
-  plan(cfg, p);
+  plan(cfg, false, p);
   if (p.rows == 0) return QSTATE_OK;
   p.x = x;
   p.weight = weight;
@@ -116,7 +117,7 @@ int qstate_norm_workspace(const qstate_norm_config* cfg, size_t* bytes) {
   if (rc != QSTATE_OK) return rc;
   if (!bytes) return QSTATE_E_INVALID;
   Params p;
-  plan(cfg, p);
+  plan(cfg, true, p);
   *bytes = (size_t)p.partials * p.width * 3 * sizeof(float);
   return QSTATE_OK;
 }
@@ -144,7 +145,7 @@ int qstate_norm_backward(const qstate_norm_config* cfg, const void* x, const flo
   for (const void* q : floats)
     if (!aligned(q, 4)) return QSTATE_E_INVALID;
   Params p;
-  plan(cfg, p);
+  plan(cfg, true, p);
   p.x = x;
   p.weight = weight;
   p.gate = gate;

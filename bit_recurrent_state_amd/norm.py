@@ -14,7 +14,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from ._lib import NormConfigC, check, lib
-from .scan import DTYPES, _array, _on_device, _stream, _workspace
+from .scan import DTYPES, _array, _call, _on_device, _ptr, _stream, _workspace
 
 __all__ = ["SILU", "SIGMOID", "NormConfig", "qstate_norm", "qstate_norm_workspace",
            "qstate_norm_backward", "block_norm"]
@@ -60,7 +60,7 @@ def _rows(t, name, cfg: NormConfig, stride, device, optional=True):
         raise ValueError(f"{name}: strides {t.stride()} are not "
                          f"{stride or cfg.groups * cfg.width} elements between tokens with packed "
                          "rows")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _inputs(cfg: NormConfig, x, weight, gate, residual, scale, next_weight):
@@ -83,16 +83,34 @@ def qstate_norm(cfg: NormConfig, x, weight=None, gate=None, residual=None, scale
     args = _inputs(cfg, x, weight, gate, residual, scale, next_weight)
     dev = x.device
     out = _rows(r, "r", cfg, 0, dev), _rows(h, "h", cfg, 0, dev)
-    with torch.cuda.device(dev):
-        c = cfg.to_c()
-        check("qstate_norm", lib().qstate_norm(ctypes.byref(c), *args, *out, _stream(stream, dev)))
+    _launch(cfg.to_c(), dev, args, out, stream)
+
+
+def _launch(c, dev, inputs, out, stream):
+    check("qstate_norm", _call(dev, lib().qstate_norm, c, *inputs, *out, _stream(stream, dev)))
+
+
+def _launch_backward(c, dev, inputs, has_h, more, workspace, stream):
+    check("qstate_norm_backward", _call(dev, lib().qstate_norm_backward, c, *inputs, has_h, *more,
+                                        *workspace, _stream(stream, dev)))
 
 
 def qstate_norm_workspace(cfg: NormConfig) -> int:
+    return _workspace_bytes(cfg.to_c())
+
+
+def _workspace_bytes(c: NormConfigC) -> int:
     n = ctypes.c_size_t()
-    c = cfg.to_c()
-    check("qstate_norm_workspace", lib().qstate_norm_workspace(ctypes.byref(c), ctypes.byref(n)))
+    check("qstate_norm_workspace", lib().qstate_norm_workspace(c, n))
     return n.value
+
+
+def _own_workspace(c, wanted, dev):
+    """A workspace of this call where sums over rows are wanted: the tensor, (pointer, bytes)."""
+    if not wanted:
+        return None, (None, 0)
+    w = torch.empty(max(_workspace_bytes(c), 1), dtype=torch.uint8, device=dev)
+    return w, (w.data_ptr(), w.numel())
 
 
 def qstate_norm_backward(cfg: NormConfig, x, weight=None, gate=None, residual=None, scale=None,
@@ -108,14 +126,13 @@ def qstate_norm_backward(cfg: NormConfig, x, weight=None, gate=None, residual=No
     more += [_array(dweight, "dweight", f32, nw, dev, optional=True),
              _array(dscale, "dscale", f32, cfg.width, dev, optional=True),
              _array(dnext_weight, "dnext_weight", f32, cfg.width, dev, optional=True)]
-    with torch.cuda.device(dev):
-        if workspace is None and any(t is not None for t in (dweight, dscale, dnext_weight)):
-            workspace = torch.empty(max(qstate_norm_workspace(cfg), 1), dtype=torch.uint8,
-                                    device=dev)
-        pw, nb = (None, 0) if workspace is None else _workspace(workspace, dev)
-        c = cfg.to_c()
-        check("qstate_norm_backward", lib().qstate_norm_backward(
-            ctypes.byref(c), *args, int(has_h), *more, pw, nb, _stream(stream, dev)))
+    c = cfg.to_c()
+    if workspace is not None:
+        keep, w = None, _workspace(workspace, dev)
+    else:
+        keep, w = _own_workspace(c, any(t is not None for t in (dweight, dscale, dnext_weight)),
+                                 dev)
+    _launch_backward(c, dev, args, int(has_h), more, w, stream)
 
 
 def _token_rows(t, groups, width):
@@ -133,52 +150,50 @@ def _token_rows(t, groups, width):
     return r, 0 if r.shape[0] <= 1 or r.stride(0) == groups * width else r.stride(0)
 
 
+def _forward(x, weight, gate, residual, scale, next_weight, eps, act):
+    """The checked call: r, h, and what backward needs."""
+    width = x.shape[-1]
+    each = weight is not None and weight.dim() == 2
+    # [tokens][groups]: a weight per group needs it, for the others it says how the rows lie
+    groups = x.shape[-2] if x.dim() > 2 or each else 1
+    (x3, xs), (gate3, gs), (res3, rs) = (_token_rows(t, groups, width) for t in (x, gate, residual))
+    weight, scale, next_weight = (None if t is None else t.contiguous()
+                                  for t in (weight, scale, next_weight))
+    c = NormConfigC(x3.shape[0], groups, width, DTYPES[x.dtype], act, int(each), eps, xs, gs, rs)
+    r = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    h = torch.empty_like(r) if next_weight is not None else None
+    saved = (x3, weight, gate3, res3, scale, next_weight)
+    _launch(c, x.device, [_ptr(t) for t in saved], (r.data_ptr(), _ptr(h)), None)
+    return r, h, c, saved
+
+
 class _BlockNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, gate, residual, scale, next_weight, eps, act):
-        width = x.shape[-1]
-        each = weight is not None and weight.dim() == 2
-        # a weight per group: the group is the last but one dimension; else every row is alike,
-        # and [tokens][groups] only says how x's rows lie
-        groups = x.shape[-2] if x.dim() >= 2 and (each or x.dim() > 2) else 1
-        if each:
-            groups = weight.shape[0]
-        rows = [_token_rows(t, groups, width) for t in (x, gate, residual)]
-        x3, gate3, res3 = (t for t, _ in rows)
-        par = [None if t is None else t.contiguous() for t in (weight, scale, next_weight)]
-        cfg = NormConfig(x3.shape[0], groups, width, x.dtype, act, each, eps,
-                         *(s for _, s in rows))
-        r = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        h = torch.empty_like(r) if next_weight is not None else None
-        qstate_norm(cfg, x3, par[0], gate3, res3, par[1], par[2], r.view(x3.shape),
-                    None if h is None else h.view(x3.shape))
-        ctx.cfg, ctx.shape = cfg, x.shape
-        ctx.save_for_backward(x3, par[0], gate3, res3, par[1], par[2])
+        r, h, ctx.cfg, saved = _forward(x, weight, gate, residual, scale, next_weight, eps, act)
+        ctx.shape = x.shape
+        ctx.save_for_backward(*saved)
         ctx.set_materialize_grads(False)
         return r if h is None else (r, h)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dr, dh=None):
-        x, weight, gate, residual, scale, next_weight = ctx.saved_tensors
-        cfg = ctx.cfg
         if dr is None and dh is None:
             return (None,) * 8
+        saved = ctx.saved_tensors
+        x, weight, gate, residual, scale, next_weight = saved
         need = ctx.needs_input_grad
-
-        def like_x(wanted):
-            return torch.empty(x.shape, dtype=x.dtype, device=x.device) if wanted else None
-
-        def like(t, wanted):
-            return torch.empty_like(t) if wanted else None
-
-        dr, dh = (None if t is None else t.contiguous().view(x.shape) for t in (dr, dh))
-        dx, dgate, dres = like_x(need[0]), like_x(need[2]), like_x(need[3])
-        dw, ds, dnw = like(weight, need[1]), like(scale, need[4]), like(next_weight, need[5])
-        qstate_norm_backward(cfg, x, weight, gate, residual, scale, next_weight,
-                             next_weight is not None, dr, dh, dx, dgate, dres, dw, ds, dnw)
-        dx, dgate, dres = (None if t is None else t.view(ctx.shape) for t in (dx, dgate, dres))
-        return dx, dw, dgate, dres, ds, dnw, None, None
+        dev = x.device
+        dr, dh = (None if t is None else t.contiguous() for t in (dr, dh))
+        dx, dgate, dres = (torch.empty(ctx.shape, dtype=x.dtype, device=dev) if need[i] else None
+                           for i in (0, 2, 3))
+        sums = [torch.empty_like(t) if need[i] else None
+                for t, i in ((weight, 1), (scale, 4), (next_weight, 5))]
+        keep, w = _own_workspace(ctx.cfg, any(t is not None for t in sums), dev)
+        _launch_backward(ctx.cfg, dev, [_ptr(t) for t in saved], int(next_weight is not None),
+                         [_ptr(t) for t in (dr, dh, dx, dgate, dres, *sums)], w, None)
+        return dx, sums[0], dgate, dres, sums[1], sums[2], None, None
 
 
 def block_norm(x, *, weight=None, gate=None, residual=None, scale=None, next_weight=None,
@@ -213,4 +228,8 @@ def block_norm(x, *, weight=None, gate=None, residual=None, scale=None, next_wei
         want = (x.shape[-2] if x.dim() > 1 else -1, width) if each else (width,)
         if tuple(t.shape) != want or t.dtype != torch.float32:
             raise ValueError(f"{name}: expected float32 {want}, got {t.dtype} {tuple(t.shape)}")
-    return _BlockNorm.apply(x, weight, gate, residual, scale, next_weight, eps, act)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in
+                                       (x, weight, gate, residual, scale, next_weight)):
+        return _BlockNorm.apply(x, weight, gate, residual, scale, next_weight, eps, act)
+    r, h = _forward(x, weight, gate, residual, scale, next_weight, eps, act)[:2]
+    return r if h is None else (r, h)

@@ -49,12 +49,25 @@ class ScanConfig:
         return self.mixer in (GLA, KDA)
 
 
-def _stream(stream, device) -> ctypes.c_void_p:
+def _stream(stream, device) -> int:
+    """The handle of `stream`, or of the current stream of the device."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        return torch._C._cuda_getCurrentRawStream(device.index)
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
+
+
+def _call(device, fn, *args):
+    """fn(*args) with the tensors' device as the current one."""
+    if torch.cuda.current_device() == device.index:
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _on_device(t, name, device):
@@ -74,7 +87,7 @@ def _array(t: Optional[torch.Tensor], name: str, dtype, numel: int, device, opti
     if t.dtype != dtype or not t.is_contiguous() or t.numel() != numel:
         raise ValueError(f"{name}: expected contiguous {dtype} with {numel} elements, got "
                          f"{t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _rows(t: Optional[torch.Tensor], name: str, cfg: ScanConfig, heads: int, width: int,
@@ -91,15 +104,33 @@ def _rows(t: Optional[torch.Tensor], name: str, cfg: ScanConfig, heads: int, wid
     if t.numel() and not ok:
         raise ValueError(f"{name}: strides {t.stride()} are not {stride or heads * width} elements "
                          "between tokens with packed heads")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def qstate_scan_workspace(cfg: ScanConfig, backward: bool = False) -> int:
+    return _workspace_bytes(cfg.to_c(), backward)
+
+
+def _workspace_bytes(c: ScanConfigC, backward: bool) -> int:
     n = ctypes.c_size_t()
-    c = cfg.to_c()
-    check("qstate_scan_workspace", lib().qstate_scan_workspace(ctypes.byref(c), int(backward),
-                                                               ctypes.byref(n)))
+    check("qstate_scan_workspace", lib().qstate_scan_workspace(c, int(backward), n))
     return n.value
+
+
+def _launch_scan(c, dev, inputs, o, final_state, workspace, stream):
+    check("qstate_scan", _call(dev, lib().qstate_scan, c, *inputs, o, final_state, *workspace,
+                               _stream(stream, dev)))
+
+
+def _launch_backward(c, dev, inputs, more, workspace, stream):
+    check("qstate_scan_backward", _call(dev, lib().qstate_scan_backward, c, *inputs, *more,
+                                        *workspace, _stream(stream, dev)))
+
+
+def _own_workspace(c, backward, dev):
+    """A workspace of this call: the tensor, and (pointer, bytes)."""
+    w = torch.empty(_workspace_bytes(c, backward), dtype=torch.uint8, device=dev)
+    return w, (w.data_ptr(), w.numel())
 
 
 def _inputs(cfg: ScanConfig, q, k, v, log_alpha, beta, offsets, initial_state):
@@ -124,7 +155,7 @@ def _workspace(workspace, dev):
     _on_device(workspace, "workspace", dev)
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous uint8 tensor")
-    return ctypes.c_void_p(workspace.data_ptr()), workspace.numel()
+    return workspace.data_ptr(), workspace.numel()
 
 
 def qstate_scan(cfg: ScanConfig, q, k, v, log_alpha, beta=None, offsets=None, initial_state=None,
@@ -135,13 +166,10 @@ def qstate_scan(cfg: ScanConfig, q, k, v, log_alpha, beta=None, offsets=None, in
     po = _rows(o, "o", cfg, cfg.heads, cfg.dv, cfg.o_stride, dev, optional=True)
     ps = _array(final_state, "final_state", torch.float32,
                 cfg.batch * cfg.heads * cfg.dv * cfg.dk, dev, optional=True)
-    with torch.cuda.device(dev):
-        if workspace is None:
-            workspace = torch.empty(qstate_scan_workspace(cfg), dtype=torch.uint8, device=dev)
-        pw, nw = _workspace(workspace, dev)
-        c = cfg.to_c()
-        check("qstate_scan", lib().qstate_scan(ctypes.byref(c), *args, po, ps, pw, nw,
-                                               _stream(stream, dev)))
+    c = cfg.to_c()
+    keep, w = (None, _workspace(workspace, dev)) if workspace is not None else \
+        _own_workspace(c, False, dev)
+    _launch_scan(c, dev, args, po, ps, w, stream)
 
 
 def qstate_scan_backward(cfg: ScanConfig, q, k, v, log_alpha, beta, offsets, initial_state, d_o,
@@ -164,13 +192,10 @@ def qstate_scan_backward(cfg: ScanConfig, q, k, v, log_alpha, beta, offsets, ini
         None if cfg.mixer == GLA else _array(dbeta, "dbeta", f32, gates, dev),
         _array(d_initial_state, "d_initial_state", f32, state, dev, optional=True),
     )
-    with torch.cuda.device(dev):
-        if workspace is None:
-            workspace = torch.empty(qstate_scan_workspace(cfg, True), dtype=torch.uint8, device=dev)
-        pw, nw = _workspace(workspace, dev)
-        c = cfg.to_c()
-        check("qstate_scan_backward", lib().qstate_scan_backward(
-            ctypes.byref(c), *args, *more, pw, nw, _stream(stream, dev)))
+    c = cfg.to_c()
+    keep, w = (None, _workspace(workspace, dev)) if workspace is not None else \
+        _own_workspace(c, True, dev)
+    _launch_backward(c, dev, args, more, w, stream)
 
 
 def _token_rows(t: torch.Tensor) -> torch.Tensor:
@@ -198,36 +223,55 @@ def _aligned(t: torch.Tensor) -> torch.Tensor:
     return t.clone() if t.data_ptr() % 16 else t
 
 
+def _forward(q, k, v, log_alpha, beta, initial_state, offsets, mixer, batch):
+    """The checked call: outputs, and what backward needs."""
+    q3, k3, v3 = _token_rows(q), _token_rows(k), _token_rows(v)
+    g = _aligned(log_alpha)
+    b = None if beta is None else _aligned(beta)
+    s0 = None if initial_state is None else _aligned(initial_state)
+    tokens, heads, dv = v3.shape
+    heads_qk, dk = q3.shape[1:]
+    dev = v.device
+    c = ScanConfigC(batch, heads, heads_qk, dk, dv, mixer, DTYPES[v.dtype], 0, tokens,
+                    _row_stride(q3), _row_stride(k3), _row_stride(v3), 0)
+    # rows of no sequence are left alone by the kernels
+    new = torch.empty if offsets is None else torch.zeros
+    o = new(v.shape, dtype=v.dtype, device=dev)
+    final = torch.empty((batch, heads, dv, dk), dtype=torch.float32, device=dev)
+    keep, w = _own_workspace(c, False, dev)
+    saved = (q3, k3, v3, g, b, s0, offsets)
+    _launch_scan(c, dev, [_ptr(t) for t in (q3, k3, v3, g, b, offsets, s0)], o.data_ptr(),
+                 final.data_ptr(), w, None)
+    return o, final, c, saved
+
+
 class _Scan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, log_alpha, beta, initial_state, offsets, mixer, batch):
-        q3, k3, v3 = _token_rows(q), _token_rows(k), _token_rows(v)
-        g = _aligned(log_alpha)
-        b = None if beta is None else _aligned(beta)
-        s0 = None if initial_state is None else _aligned(initial_state)
-        cfg = ScanConfig(batch, v3.shape[1], q3.shape[2], v3.shape[2], v3.shape[0], q3.shape[1],
-                         mixer, v.dtype, _row_stride(q3), _row_stride(k3), _row_stride(v3))
-        # rows of no sequence are left alone by the kernels
-        o = (torch.empty if offsets is None else torch.zeros)(v.shape, dtype=v.dtype, device=v.device)
-        final = torch.empty((batch, cfg.heads, cfg.dv, cfg.dk), dtype=torch.float32, device=v.device)
-        qstate_scan(cfg, q3, k3, v3, g, b, offsets, s0, o.view(v3.shape), final)
-        ctx.cfg = cfg
-        ctx.shapes = q.shape, k.shape, v.shape
-        ctx.save_for_backward(q3, k3, v3, g, b, s0, offsets)
+        o, final, ctx.cfg, saved = _forward(q, k, v, log_alpha, beta, initial_state, offsets,
+                                            mixer, batch)
+        ctx.shapes = q.shape, v.shape
+        ctx.save_for_backward(*saved)
+        ctx.set_materialize_grads(False)
         return o, final
 
     @staticmethod
     @once_differentiable
     def backward(ctx, d_o, d_final):
         q, k, v, g, b, s0, offsets = ctx.saved_tensors
-        cfg = ctx.cfg
+        dev = v.device
+        qk, vo = ctx.shapes
         new = torch.empty if offsets is None else torch.zeros
-        dq, dk, dv = (new(s, dtype=v.dtype, device=v.device) for s in ctx.shapes)
-        dg = new(g.shape, dtype=torch.float32, device=v.device)
-        db = None if b is None else new(b.shape, dtype=torch.float32, device=v.device)
-        ds = None if s0 is None or not ctx.needs_input_grad[5] else torch.empty_like(s0)
-        qstate_scan_backward(cfg, q, k, v, g, b, offsets, s0, _aligned(d_o), _aligned(d_final),
-                             dq, dk, dv, dg, db, ds)
+        d_o = torch.zeros(vo, dtype=v.dtype, device=dev) if d_o is None else _aligned(d_o)
+        d_final = None if d_final is None else _aligned(d_final)
+        dq, dk = new(qk, dtype=v.dtype, device=dev), new(qk, dtype=v.dtype, device=dev)
+        dv = new(vo, dtype=v.dtype, device=dev)
+        dg = new(g.shape, dtype=torch.float32, device=dev)
+        db = None if b is None else new(b.shape, dtype=torch.float32, device=dev)
+        ds = torch.empty_like(s0) if s0 is not None and ctx.needs_input_grad[5] else None
+        keep, w = _own_workspace(ctx.cfg, True, dev)
+        _launch_backward(ctx.cfg, dev, [_ptr(t) for t in (q, k, v, g, b, offsets, s0)],
+                         [_ptr(t) for t in (d_o, d_final, dq, dk, dv, dg, db, ds)], w, None)
         return dq, dk, dv, dg, db, ds, None, None, None
 
 
@@ -286,4 +330,7 @@ def scan(q, k, v, log_alpha, beta=None, *, mixer: int = GDN, initial_state=None,
                 or initial_state.dtype != torch.float32):
             raise ValueError(f"initial_state: expected float32 {(batch, heads, dv, dk)}, got "
                              f"{initial_state.dtype} {tuple(initial_state.shape)}")
-    return _Scan.apply(q, k, v, log_alpha, beta, initial_state, offsets, mixer, batch)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in
+                                       (q, k, v, log_alpha, beta, initial_state)):
+        return _Scan.apply(q, k, v, log_alpha, beta, initial_state, offsets, mixer, batch)
+    return _forward(q, k, v, log_alpha, beta, initial_state, offsets, mixer, batch)[:2]
