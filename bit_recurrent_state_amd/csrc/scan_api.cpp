@@ -35,7 +35,7 @@ int check_config(const qstate_scan_config* c) {
     return QSTATE_E_INVALID;
   if (c->dk != 64 && c->dk != 128 && c->dk != 256) return QSTATE_E_UNSUPPORTED;
   if (c->heads > 256 || c->dv > 4096 || c->tokens > 2147483647) return QSTATE_E_UNSUPPORTED;
-  const int64_t far = (int64_t)1 << 40;
+  const int64_t far = (int64_t)1 << 22;  // offsets inside a chunk take 32 bits
   if (c->q_stride > far || c->k_stride > far || c->v_stride > far || c->o_stride > far)
     return QSTATE_E_UNSUPPORTED;
   // the grids: chunks of all sequences, and a workgroup per head and column block
@@ -177,6 +177,11 @@ int qstate_scan(const qstate_scan_config* cfg, const void* q, const void* k, con
   set_inputs(p, q, k, v, log_alpha, beta, offsets, initial_state);
   p.o = o;
   p.s1 = final_state;
+  // The lengths are on the device.  Without offsets they are known here.
+  const int64_t most = offsets ? cfg->tokens : cfg->tokens / cfg->batch;
+  p.short_len = qscan::kShort;
+  p.some_short = offsets || most <= qscan::kShort;
+  p.some_long = most > qscan::kShort;
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   switch (cfg->dk) {
     case 64: return status(qscan::forward_dk64(p, s));

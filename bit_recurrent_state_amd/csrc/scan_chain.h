@@ -55,6 +55,7 @@ __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
   const int fr = lane & 15, fg = lane >> 4;
   const int64_t o0 = offset_of(p, n), o1 = offset_of(p, n + 1);
   const int64_t len = o1 > o0 ? o1 - o0 : 0;
+  if (!SAVE && len <= p.short_len) return;
   const int nch = (int)((len + C - 1) / C);
   const int base = (int)(o0 / C) + n;
   const int tok = wave * 16 + fg * 4;  // first of the lane's 4 tokens
@@ -93,25 +94,48 @@ __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
       load_q(0);
       load_a(0);
     }
+    f32x4 O[NT];
+    // A chunk's outputs are stored behind the next chunk's first product, while
+    // the other waves compute U: right after A W they would hold up the barrier.
+    auto store = [&](int ci, const f32x4(&x)[NT]) {
+      const Chunk c = chunk(ci);
+      const int64_t at = c.row * p.os + (int64_t)h * p.dv;
+      char* o = static_cast<char*>(p.o) + at * (p.dtype == 0 ? 4 : 2);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        uint32_t off[4];
+        bool ok[4];
+        float y[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          off[r] = (uint32_t)(tok + r) * (uint32_t)p.os + vcol[t];
+          ok[r] = p.o && tok + r < c.len && vcol[t] < p.dv;
+          y[r] = x[t][r];
+        }
+        store_elems<4>(o, off, ok, p.dtype, y);
+      }
+    };
     __syncthreads();
     for (int ci = 0; ci < nch; ++ci) {
-      const Chunk c = chunk(ci);
       const int next = min(ci + 1, nch - 1);
-      f32x4 O[NT];
+      f32x4 Q[NT];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) O[t] = f32x4{0, 0, 0, 0};
+      for (int t = 0; t < NT; ++t) Q[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-          mma(O[t], fq[s], load_frag<PO>(&Sl[0][t * 16 + fr][s * 32 + fg * 8], BV * SP));
+          mma(Q[t], fq[s], load_frag<PO>(&Sl[0][t * 16 + fr][s * 32 + fg * 8], BV * SP));
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) O[t][r] *= ec[r];
+        for (int r = 0; r < 4; ++r) Q[t][r] *= ec[r];
       load_q(next);
       if (DELTA) __syncthreads();
+      if (ci > 0) store(ci - 1, O);
       __syncthreads();
+#pragma unroll
+      for (int t = 0; t < NT; ++t) O[t] = Q[t];
 #pragma unroll
       for (int s = 0; s < 2; ++s)
         if (s <= wave / 2)
@@ -121,21 +145,9 @@ __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
                 load_frag<PO>(VEC ? &Wb[0][t * 16 + fr][s * 32 + fg * 8]
                                   : &Wt[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
       load_a(next);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        int64_t at[4];
-        bool ok[4];
-        float x[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          at[r] = (c.row + tok + r) * p.os + (int64_t)h * p.dv + vcol[t];
-          ok[r] = p.o && tok + r < c.len && vcol[t] < p.dv;
-          x[r] = O[t][r];
-        }
-        store_elems<4>(p.o, at, ok, p.dtype, x);
-      }
       __syncthreads();
     }
+    store(nch - 1, O);
     return;
   }
 
@@ -177,13 +189,16 @@ __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
       eo = *reinterpret_cast<const f32x4*>(rows + C + tok);
     }
     // places outside the sequence or the head read a valid neighbour and count as zero later
-    int64_t at[4];
+    const char* src = static_cast<const char*>(p.v) +
+                      (c.row * p.vs + (int64_t)h * p.dv) * (p.dtype == 0 ? 4 : 2);
+    uint32_t at[4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        at[r] = (c.row + min(tok + r, c.len - 1)) * p.vs + (int64_t)h * p.dv + min(vcol[t], p.dv - 1);
-      load_raw<4>(p.v, at, p.dtype, v[t]);
+        at[r] = min((uint32_t)(tok + r) * (uint32_t)p.vs, (uint32_t)(c.len - 1) * (uint32_t)p.vs) +
+                min(vcol[t], p.dv - 1);
+      load_raw<4>(src, at, p.dtype, v[t]);
     }
   };
   auto load_T = [&](int ci) {
@@ -224,14 +239,17 @@ __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
       for (int r = 0; r < 4; ++r)
         vf[t][r] = tok + r < c.len && vcol[t] < p.dv ? from_raw(v[t][r], p.dtype) : 0.0f;
     if (DELTA) {
-      f32x4 kS[NT];
+      f32x4 kS[NT], kS2[NT];  // two chains of dependent products
 #pragma unroll
-      for (int t = 0; t < NT; ++t) kS[t] = f32x4{0, 0, 0, 0};
+      for (int t = 0; t < NT; ++t) kS[t] = kS2[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-          mma(kS[t], fk[s], load_frag<P>(&Sl[0][t * 16 + fr][s * 32 + fg * 8], BV * SP));
+          mma(s & 1 ? kS2[t] : kS[t], fk[s],
+              load_frag<P>(&Sl[0][t * 16 + fr][s * 32 + fg * 8], BV * SP));
+#pragma unroll
+      for (int t = 0; t < NT; ++t) kS[t] += kS2[t];
       load_k(next);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -376,13 +394,16 @@ __global__ void __launch_bounds__(256) state_grads_kernel(Params p) {
       ec = *reinterpret_cast<const f32x4*>(rows + tok);
       eo = *reinterpret_cast<const f32x4*>(rows + C + tok);
     }
-    int64_t at[4];
+    const uint32_t stride = (uint32_t)p.heads * p.dv;
+    const char* src = static_cast<const char*>(p.dO) +
+                      (c.row * p.heads + h) * p.dv * (p.dtype == 0 ? 4 : 2);
+    uint32_t at[4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        at[r] = ((c.row + min(tok + r, c.len - 1)) * p.heads + h) * p.dv + min(vcol[t], p.dv - 1);
-      load_raw<4>(p.dO, at, p.dtype, x[t]);
+        at[r] = min((uint32_t)(tok + r) * stride, (uint32_t)(c.len - 1) * stride) + min(vcol[t], p.dv - 1);
+      load_raw<4>(src, at, p.dtype, x[t]);
       if (p.dbeta) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) u[t][r] = p.u[(sh * C + tok + r) * p.dvp + vcol[t]];
@@ -500,14 +521,16 @@ __global__ void __launch_bounds__(256) state_grads_kernel(Params p) {
         if (p.dbeta) db[r] = fmaf(uc[t][r], W[t][r], db[r]);
       }
       if (DELTA) put4<P>(&Yt[0][t * 16 + fr][tok], BV * CP, ye);
-      int64_t at[4];
+      char* dst = static_cast<char*>(p.dv_out) +
+                  (c.row * p.heads + h) * p.dv * (p.dtype == 0 ? 4 : 2);
+      uint32_t at[4];
       bool ok[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        at[r] = ((c.row + tok + r) * p.heads + h) * p.dv + vcol[t];
+        at[r] = (uint32_t)(tok + r) * (uint32_t)p.heads * p.dv + vcol[t];
         ok[r] = tok + r < c.len && vcol[t] < p.dv;
       }
-      store_elems<4>(p.dv_out, at, ok, p.dtype, y);
+      store_elems<4>(dst, at, ok, p.dtype, y);
       if (DELTA) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) p.y[(sh * C + tok + r) * p.dvp + vcol[t]] = y[r];

@@ -55,7 +55,7 @@ __device__ __forceinline__ bool find_chunk(const Params& p, int slot, Chunk& c) 
   const int64_t o0 = offset_of(p, lo), o1 = offset_of(p, lo + 1);
   const int64_t ci = slot - (o0 / C + lo);
   const int64_t left = o1 - o0 - ci * C;
-  if (ci < 0 || left <= 0) return false;
+  if (ci < 0 || left <= 0 || o1 - o0 <= p.short_len) return false;
   c.n = lo;
   c.ci = (int)ci;
   c.len = left < C ? (int)left : C;
@@ -75,8 +75,8 @@ __device__ __forceinline__ float load_elem(const void* p, int64_t i, int dtype) 
 
 // The same in two steps, for many elements at once: load_elem branches on the
 // type and converts, so that each load would be waited for before the next.
-template <int N>
-__device__ __forceinline__ void load_raw(const void* p, const int64_t (&at)[N], int dtype,
+template <int N, class I>
+__device__ __forceinline__ void load_raw(const void* p, const I (&at)[N], int dtype,
                                          uint32_t (&raw)[N]) {
   if (dtype == 0) {
 #pragma unroll
@@ -112,8 +112,8 @@ __device__ __forceinline__ void store_elem(void* p, int64_t i, int dtype, float 
 }
 
 // N outputs, those with `ok`.
-template <int N>
-__device__ __forceinline__ void store_elems(void* p, const int64_t (&at)[N], const bool (&ok)[N],
+template <int N, class I>
+__device__ __forceinline__ void store_elems(void* p, const I (&at)[N], const bool (&ok)[N],
                                             int dtype, const float (&x)[N]) {
   if (dtype == 0) {
 #pragma unroll
@@ -128,6 +128,46 @@ __device__ __forceinline__ void store_elems(void* p, const int64_t (&at)[N], con
         static_cast<uint16_t*>(p)[at[i]] = (uint16_t)((h & half) | (pack_bf16(x[i], 0.0f) & ~half));
     }
   }
+}
+
+// e^x to an ulp or two for x <= 88 (0 far below): 2^t (1 + r ln 2), x log2 e = t + r.
+__device__ __forceinline__ float fast_exp(float x) {
+  const float hi = 1.44269502f, lo = 1.92596303e-8f;
+  const float t = x * hi;
+  const float r = fmaf(x, lo, fmaf(x, hi, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return fmaf(e, r * 0.693147182f, e);
+}
+
+// Four neighbouring elements; `even`: they are aligned to four.
+__device__ __forceinline__ void load4(const void* p, int64_t at, int dtype, bool even,
+                                      float (&x)[4]) {
+  uint32_t w[4];
+  if (dtype == 0) {
+    const uint32_t* s = static_cast<const uint32_t*>(p) + at;
+    if (even) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(s);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = s[i];
+    }
+  } else {
+    const uint16_t* s = static_cast<const uint16_t*>(p) + at;
+    if (even) {
+      const u32x2 v = *reinterpret_cast<const u32x2*>(s);
+      w[0] = v.x & 0xFFFFu;
+      w[1] = v.x >> 16;
+      w[2] = v.y & 0xFFFFu;
+      w[3] = v.y >> 16;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = s[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = from_raw(w[i], dtype);
 }
 
 // Log decays below -87 count as -87; a NaN stays.

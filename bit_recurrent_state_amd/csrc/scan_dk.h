@@ -6,6 +6,7 @@
 #include "scan_chain.h"
 #include "scan_grads.h"
 #include "scan_prep.h"
+#include "scan_tokens.h"
 
 namespace qscan {
 
@@ -17,8 +18,13 @@ inline dim3 chain_grid(const Params& p) {
 template <int DK, int NT, int NPQ, int PO, bool VEC, bool DELTA>
 hipError_t forward_tail(const Params& p, hipStream_t s) {
   const dim3 slots(p.nslots, p.heads);
+  if (p.some_short) {
+    const dim3 rows((unsigned)((int64_t)p.batch * p.heads * ((p.dv + 31) / 32)));
+    tokens_kernel<DK, VEC, DELTA><<<rows, 256, 0, s>>>(p);
+    if (!p.some_long) return hipGetLastError();
+  }
   if (VEC) {
-    operands_vector_kernel<DK, DELTA, false><<<slots, DK, 0, s>>>(p);
+    operands_vector_kernel<DK, DELTA, false><<<slots, 256, 0, s>>>(p);
     chunk_kernel<DK, P, true, DELTA, false><<<slots, 256, 0, s>>>(p);
     chunk_vector_kernel<DK, DELTA, false><<<slots, 256, 0, s>>>(p);
   } else {
@@ -35,7 +41,7 @@ hipError_t backward_tail(const Params& p, hipStream_t s) {
   operands_kernel<DK><<<dim3(p.nslots, p.heads_qk), 256, 0, s>>>(p, 1);
   {
     if (VEC) {
-      operands_vector_kernel<DK, DELTA, true><<<slots, DK, 0, s>>>(p);
+      operands_vector_kernel<DK, DELTA, true><<<slots, 256, 0, s>>>(p);
       chunk_kernel<DK, P, true, DELTA, true><<<slots, 256, 0, s>>>(p);
       chunk_vector_kernel<DK, DELTA, true><<<slots, 256, 0, s>>>(p);
     } else {

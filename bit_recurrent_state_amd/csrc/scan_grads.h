@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(256) grads_kernel(Params p) {
         const int i = i0 + r;
         const bool in = strict ? i > j : i >= j;
         float g = beta;
-        if (!VEC) g *= expf(in ? (float)(cs[i] - cs[j]) : 0.0f);
+        if (!VEC) g *= fast_exp(in ? (float)(cs[i] - cs[j]) : 0.0f);
         v[r] = in ? x[b][r] * g : 0.0f;
       }
       u32x2 t[P];

@@ -12,6 +12,7 @@ namespace qscan {
 
 constexpr int kChunk = 64;  // tokens of a chunk
 constexpr int kTerms = 3;   // bfloat16 terms of an FP32 operand
+constexpr int kShort = 8;   // longest sequence that is taken token by token
 constexpr float kFarDecay = 8.0f;  // largest decay of a chunk, as a logarithm, that is divided out
 
 // Workspace operands are bfloat16 terms, a plane per term, in tiles of 16 rows
@@ -21,6 +22,8 @@ constexpr float kFarDecay = 8.0f;  // largest decay of a chunk, as a logarithm, 
 struct Params {
   int batch, heads, heads_qk, dk, dv, mixer, dtype, direct;
   int terms;     // planes of q and k: 1 (direct bfloat16) or kTerms
+  int short_len; // sequences up to this length go to tokens_kernel (forward)
+  int some_short, some_long;  // whether there may be sequences up to that length, and beyond
   int nslots;    // upper bound of the slots in use
   int nvb;       // blocks of dv columns of one head
   int vblock;    // dv columns of a block

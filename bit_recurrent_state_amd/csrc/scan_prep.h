@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(256) chunk_kernel(Params p) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int i = BWD ? r0 + r : own, j = BWD ? own : r0 + r;
-      const float e = VEC ? 1.0f : i >= j ? expf((float)(cs[i] - cs[j])) : 0.0f;
+      const float e = VEC ? 1.0f : i >= j ? fast_exp((float)(cs[i] - cs[j])) : 0.0f;
       a[r] = i >= j ? acc[r] * e : 0.0f;
       if (DELTA) {
         const float l = i > j ? acl[r] * e : 0.0f;
@@ -331,120 +331,149 @@ __global__ void __launch_bounds__(256) chunk_kernel(Params p) {
 // .. i) and suffix sums (j + 1 .. last), between them whole blocks.  Nothing
 // overflows, and nothing is lost where gates are strong.
 //
-// One workgroup per (slot, head), a thread per channel: the scaled operands
-// q e^c, k e^c, k e^(c_end - c) and, unless the chunk decays too far, k e^-c as
-// rows and as columns.
+// One workgroup per (slot, head): the scaled operands q e^c, k e^c,
+// k e^(c_end - c) and, unless the chunk decays too far, k e^-c as rows and as
+// columns.  A wave writes a whole tile at a time.
 template <int DK, bool DELTA, bool BWD>
-__global__ void __launch_bounds__(DK) operands_vector_kernel(Params p) {
-  const int slot = blockIdx.x, h = blockIdx.y, ch = threadIdx.x;
+__global__ void __launch_bounds__(256) operands_vector_kernel(Params p) {
+  constexpr int LP = DK + 4;
+  __shared__ __align__(16) float pre[C][LP], suf[C][LP];  // sums of log decays inside blocks of 16
+  __shared__ __align__(16) float tot[4][DK];
+  const int slot = blockIdx.x, h = blockIdx.y;
   Chunk c;
   if (!find_chunk(p, slot, c)) return;
   const int64_t sh = (int64_t)slot * p.heads + h;
   const int hq = h / (p.heads / p.heads_qk);
-  float total[4];
+  const bool qeven = p.qs % 4 == 0, keven = p.ks % 4 == 0;
+  for (int u = threadIdx.x; u < DK * 4; u += 256) {
+    const int ch = u % DK, t0 = u / DK * 16;
+    float g[16], s = 0.0f;
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int t = b * 16 + i;
-      const float g = gate(p.g[((c.row + min(t, c.len - 1)) * p.heads + h) * DK + ch]);
-      s += t < c.len ? g : 0.0f;
-    }
-    total[b] = s;
-  }
-  const float all = (total[0] + total[1]) + (total[2] + total[3]);
-  p.decay[sh * DK + ch] = expf(all);
-  const bool far = __syncthreads_or(!(all >= -kFarDecay));
-  if (threadIdx.x == 0) p.far[sh] = far;
-  if (ch < C && threadIdx.x < C) {
-    float* r = rows_at(p, slot, h);
-    r[2 * C + ch] = ch < c.len ? (p.beta ? p.beta[(c.row + ch) * p.heads + h] : 1.0f) : 0.0f;
-  }
-  float before = 0.0f;
-#pragma unroll 1
-  for (int b = 0; b < 4; ++b) {
-    float g[16], sfx[16];
+    for (int i = 0; i < 16; ++i)
+      g[i] = p.g[((c.row + min(t0 + i, c.len - 1)) * p.heads + h) * DK + ch];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const int t = b * 16 + i;
-      const float x = gate(p.g[((c.row + min(t, c.len - 1)) * p.heads + h) * DK + ch]);
-      g[i] = t < c.len ? x : 0.0f;
+      g[i] = t0 + i < c.len ? gate(g[i]) : 0.0f;
+      s += g[i];
+      pre[t0 + i][ch] = s;
     }
-    float after = 0.0f;
-    for (int m = 3; m > b; --m) after += m == 1 ? total[1] : m == 2 ? total[2] : total[3];
-    float s = 0.0f;
+    tot[u / DK][ch] = s;
+    s = 0.0f;
 #pragma unroll
     for (int i = 15; i >= 0; --i) {
-      sfx[i] = s;
+      suf[t0 + i][ch] = s;
       s += g[i];
     }
-    float pfx = 0.0f;
+  }
+  if (threadIdx.x < C) {
+    const int t = threadIdx.x;
+    rows_at(p, slot, h)[2 * C + t] = t < c.len ? (p.beta ? p.beta[(c.row + t) * p.heads + h] : 1.0f) : 0.0f;
+  }
+  __syncthreads();
+  bool over = false;
+  if (threadIdx.x < DK) {
+    const int ch = threadIdx.x;
+    const float all = (tot[0][ch] + tot[1][ch]) + (tot[2][ch] + tot[3][ch]);
+    p.decay[sh * DK + ch] = fast_exp(all);
+    over = !(all >= -kFarDecay);
+  }
+  const bool far = __syncthreads_or(over);
+  if (threadIdx.x == 0) p.far[sh] = far;
+
+  // rows: 8 channels of a token
+  for (int u = threadIdx.x; u < C * DK / 8; u += 256) {
+    const int tile = u >> 6, t = tile / (DK / 32) * 16 + (u & 15);
+    const int ch = tile % (DK / 32) * 32 + (u >> 4 & 3) * 8, b = t >> 4;
+    const int64_t row = c.row + min(t, c.len - 1);
+    float qe[8], ke[8], ko[8], kn[8];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float qe[8], ke[8], ko[8], kn[8], ps[8], ss[8];
-      int64_t aq[8], ak[8];
-      uint32_t rq[8], rk[8];
+    for (int q = 0; q < 2; ++q) {
+      float x[4], y[4];
+      load4(p.q, row * p.qs + (int64_t)hq * DK + ch + 4 * q, p.dtype, qeven, x);
+      load4(p.k, row * p.ks + (int64_t)hq * DK + ch + 4 * q, p.dtype, keven, y);
+      f32x4 cs = *reinterpret_cast<const f32x4*>(&pre[t][ch + 4 * q]);
+      f32x4 se = *reinterpret_cast<const f32x4*>(&suf[t][ch + 4 * q]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t row = c.row + min(b * 16 + half * 8 + i, c.len - 1);
-        aq[i] = row * p.qs + (int64_t)hq * DK + ch;
-        ak[i] = row * p.ks + (int64_t)hq * DK + ch;
+      for (int m = 0; m < 4; ++m) {
+        const f32x4 w = *reinterpret_cast<const f32x4*>(&tot[m][ch + 4 * q]);
+        if (m < b) cs += w;
+        if (m > b) se += w;
       }
-      load_raw<8>(p.q, aq, p.dtype, rq);
-      load_raw<8>(p.k, ak, p.dtype, rk);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int t = b * 16 + half * 8 + i;
-        pfx += g[half * 8 + i];
-        const bool in = t < c.len;
-        const float q = in ? from_raw(rq[i], p.dtype) : 0.0f;
-        const float k = in ? from_raw(rk[i], p.dtype) : 0.0f;
-        const float e = expf(pfx + before);
-        qe[i] = q * e;
-        ke[i] = k * e;
-        const float eo = expf(sfx[half * 8 + i] + after);
-        ko[i] = k * eo;
-        kn[i] = far ? 0.0f : k * expf(-(pfx + before));
-        if (BWD) {
-          ps[i] = far ? expf(pfx) : e;
-          ss[i] = far ? expf(sfx[half * 8 + i]) : eo;
-        }
-      }
-      const int t0 = b * 16 + half * 8;
-      const Frag<P> fq = split8<P>(qe), fk = split8<P>(ke), fo = split8<P>(ko), fn = split8<P>(kn);
-#pragma unroll
-      for (int n = 0; n < P; ++n) {
-        const uint32_t wq[4] = {fq.t[n].x, fq.t[n].y, fq.t[n].z, fq.t[n].w};
-        const uint32_t wk[4] = {fk.t[n].x, fk.t[n].y, fk.t[n].z, fk.t[n].w};
-        const uint32_t wo[4] = {fo.t[n].x, fo.t[n].y, fo.t[n].z, fo.t[n].w};
-        const uint32_t wn[4] = {fn.t[n].x, fn.t[n].y, fn.t[n].z, fn.t[n].w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int64_t at = (sh * P + n) * C * DK + tiled<DK>(t0 + i, ch);
-          const int sft = 16 * (i & 1);
-          p.qrow[at] = (uint16_t)(wq[i / 2] >> sft);
-          p.knrow[at] = (uint16_t)(wn[i / 2] >> sft);
-          if (DELTA) p.krow[at] = (uint16_t)(wk[i / 2] >> sft);
-          if (BWD) p.korow[at] = (uint16_t)(wo[i / 2] >> sft);
-        }
-        const int64_t tt = (sh * P + n) * C * DK + tiled<C>(ch, t0);
-        *reinterpret_cast<u32x4*>(p.kt + tt) = fo.t[n];
-        if (BWD) *reinterpret_cast<u32x4*>(p.qt + tt) = fq.t[n];
-        if (BWD) *reinterpret_cast<u32x4*>(p.knt + tt) = fn.t[n];
-        if (BWD && DELTA) *reinterpret_cast<u32x4*>(p.ket + tt) = fk.t[n];
-      }
-      if (BWD) {
-        float* dp = p.pfx + (sh * DK + ch) * C + t0;
-        float* ds = p.sfx + (sh * DK + ch) * C + t0;
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          *reinterpret_cast<f32x4*>(dp + i) = f32x4{ps[i], ps[i + 1], ps[i + 2], ps[i + 3]};
-          *reinterpret_cast<f32x4*>(ds + i) = f32x4{ss[i], ss[i + 1], ss[i + 2], ss[i + 3]};
-        }
+      for (int i = 0; i < 4; ++i) {
+        const float e = fast_exp(cs[i]), in = t < c.len ? 1.0f : 0.0f;
+        qe[4 * q + i] = in * x[i] * e;
+        ke[4 * q + i] = in * y[i] * e;
+        if (BWD) ko[4 * q + i] = in * y[i] * fast_exp(se[i]);
+        kn[4 * q + i] = far ? 0.0f : in * y[i] * fast_exp(-cs[i]);
       }
     }
-    before += b == 0 ? total[0] : b == 1 ? total[1] : b == 2 ? total[2] : total[3];
+    const int64_t at = sh * P * C * DK + u * 8;
+    auto put = [&](uint16_t* dst, const float(&x)[8]) {
+      const Frag<P> f = split8<P>(x);
+#pragma unroll
+      for (int n = 0; n < P; ++n) *reinterpret_cast<u32x4*>(dst + at + n * C * DK) = f.t[n];
+    };
+    put(p.qrow, qe);
+    put(p.knrow, kn);
+    if (DELTA) put(p.krow, ke);
+    if (BWD) put(p.korow, ko);
+  }
+  // columns: 8 tokens of a channel
+  for (int u = threadIdx.x; u < C * DK / 8; u += 256) {
+    const int tile = u >> 6, ch = tile / 2 * 16 + (u & 15);
+    const int t0 = tile % 2 * 32 + (u >> 4 & 3) * 8, b = t0 >> 4;
+    int64_t aq[8], ak[8];
+    uint32_t rq[8], rk[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t row = c.row + min(t0 + i, c.len - 1);
+      aq[i] = row * p.qs + (int64_t)hq * DK + ch;
+      ak[i] = row * p.ks + (int64_t)hq * DK + ch;
+    }
+    load_raw<8>(p.k, ak, p.dtype, rk);
+    if (BWD) load_raw<8>(p.q, aq, p.dtype, rq);
+    float before = 0.0f, after = 0.0f;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      if (m < b) before += tot[m][ch];
+      if (m > b) after += tot[m][ch];
+    }
+    float qe[8], ke[8], ko[8], kn[8], ps[8], ss[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float k = t0 + i < c.len ? from_raw(rk[i], p.dtype) : 0.0f;
+      const float se = suf[t0 + i][ch], eo = fast_exp(se + after);
+      ko[i] = k * eo;
+      if (BWD) {
+        const float q = t0 + i < c.len ? from_raw(rq[i], p.dtype) : 0.0f;
+        const float cs = pre[t0 + i][ch], e = fast_exp(cs + before);
+        qe[i] = q * e;
+        ke[i] = k * e;
+        kn[i] = far ? 0.0f : k * fast_exp(-(cs + before));
+        ps[i] = far ? fast_exp(cs) : e;
+        ss[i] = far ? fast_exp(se) : eo;
+      }
+    }
+    const int64_t at = sh * P * C * DK + u * 8;
+    auto put = [&](uint16_t* dst, const float(&x)[8]) {
+      const Frag<P> f = split8<P>(x);
+#pragma unroll
+      for (int n = 0; n < P; ++n) *reinterpret_cast<u32x4*>(dst + at + n * C * DK) = f.t[n];
+    };
+    put(p.kt, ko);
+    if (BWD) {
+      put(p.qt, qe);
+      put(p.knt, kn);
+      if (DELTA) put(p.ket, ke);
+      float* dp = p.pfx + (sh * DK + ch) * C + t0;
+      float* ds = p.sfx + (sh * DK + ch) * C + t0;
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        *reinterpret_cast<f32x4*>(dp + i) = f32x4{ps[i], ps[i + 1], ps[i + 2], ps[i + 3]};
+        *reinterpret_cast<f32x4*>(ds + i) = f32x4{ss[i], ss[i + 1], ss[i + 2], ss[i + 3]};
+      }
+    }
   }
 }
 

@@ -1,0 +1,86 @@
+// scan_tokens.h — short sequences, token by token: single new tokens of running
+// sequences, and sequences with none.
+//
+// What a sequence of a few tokens costs is its state, read once and written
+// once; the chunks' fixed work would be several times that.  A wave takes 8
+// value rows, 8 lanes a row, and keeps them in registers over the tokens: FP32
+// throughout, one multiply and two fused multiply-adds per element and token,
+// dot products summed over the row's lanes.
+
+#pragma once
+
+#include "scan_device.h"
+
+namespace qscan {
+
+__device__ __forceinline__ float sum8(float x) {
+  x += __shfl_xor(x, 1);
+  x += __shfl_xor(x, 2);
+  x += __shfl_xor(x, 4);
+  return x;
+}
+
+template <int DK, bool VEC, bool DELTA>
+__global__ void __launch_bounds__(256) tokens_kernel(Params p) {
+  constexpr int Q = DK / 32;  // groups of 4 channels: channel 32 q + 4 (lane & 7)
+  const int nb = (p.dv + 31) / 32;
+  const int64_t b = blockIdx.x;
+  const int64_t nh = b / nb;
+  const int n = (int)(nh / p.heads), h = (int)(nh % p.heads);
+  const int64_t o0 = offset_of(p, n), o1 = offset_of(p, n + 1);
+  const int64_t left = o1 - o0;
+  if (left > p.short_len) return;
+  const int len = left > 0 ? (int)left : 0;
+  const int lane = threadIdx.x & 63, l = lane & 7;
+  const int v = (int)(b % nb) * 32 + (threadIdx.x >> 6) * 8 + (lane >> 3);
+  const bool in = v < p.dv;
+  const int hq = h / (p.heads / p.heads_qk);
+  const bool qeven = p.qs % 4 == 0, keven = p.ks % 4 == 0;
+  const int64_t st = (nh * p.dv + (in ? v : p.dv - 1)) * DK + 4 * l;
+  f32x4 S[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+    S[q] = p.s0 ? *reinterpret_cast<const f32x4*>(p.s0 + st + 32 * q) : f32x4{0, 0, 0, 0};
+  for (int i = 0; i < len; ++i) {
+    const int64_t row = o0 + i;
+    float k[Q][4], x[Q][4];
+    f32x4 g[VEC ? Q : 1];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      load4(p.k, row * p.ks + (int64_t)hq * DK + 32 * q + 4 * l, p.dtype, keven, k[q]);
+      load4(p.q, row * p.qs + (int64_t)hq * DK + 32 * q + 4 * l, p.dtype, qeven, x[q]);
+      if (VEC)
+        g[q] = *reinterpret_cast<const f32x4*>(p.g + (row * p.heads + h) * DK + 32 * q + 4 * l);
+    }
+    const float ga = VEC ? 0.0f : p.g[row * p.heads + h];
+    const float beta = p.beta ? p.beta[row * p.heads + h] : 1.0f;
+    float w = load_elem(p.v, row * p.vs + (int64_t)h * p.dv + (in ? v : p.dv - 1), p.dtype);
+    const float a = VEC ? 0.0f : fast_exp(gate(ga));
+    float u = 0.0f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        S[q][e] *= VEC ? fast_exp(gate(g[VEC ? q : 0][e])) : a;
+        if (DELTA) u = fmaf(S[q][e], k[q][e], u);
+      }
+    if (DELTA) w -= sum8(u);
+    w *= beta;
+    float o = 0.0f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        S[q][e] = fmaf(w, k[q][e], S[q][e]);
+        o = fmaf(S[q][e], x[q][e], o);
+      }
+    o = sum8(o);
+    if (p.o && in && l == 0) store_elem(p.o, row * p.os + (int64_t)h * p.dv + v, p.dtype, o);
+  }
+  if (p.s1 && in) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) *reinterpret_cast<f32x4*>(p.s1 + st + 32 * q) = S[q];
+  }
+}
+
+}  // namespace qscan

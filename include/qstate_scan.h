@@ -28,7 +28,7 @@
  * Layout (device memory, caller-owned).  Sequences are packed behind each
  * other, rows are tokens:
  *   q, k       dtype [tokens][heads_qk][dk], rows q_stride / k_stride
- *              elements apart (0: heads_qk * dk); head h uses q/k head
+ *              elements apart (0: heads_qk * dk; at most 2^22); head h uses q/k head
  *              h / (heads / heads_qk)
  *   v, o       dtype [tokens][heads][dv], rows v_stride / o_stride apart
  *   log_alpha  float [tokens][heads] (GDN, SCALAR) or [tokens][heads][dk]
