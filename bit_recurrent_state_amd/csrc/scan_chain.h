@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
           ok[r] = p.o && tok + r < c.len && vcol[t] < p.dv;
           y[r] = x[t][r];
         }
-        store_elems<4>(o, off, ok, p.dtype, y);
+        store_always<4>(o, off, ok, p.dtype, p.sink, y);
       }
     };
     __syncthreads();
@@ -288,14 +288,15 @@ __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) p.u[(sh * C + tok + r) * p.dvp + vcol[t]] = U[t][r];
+        for (int r = 0; r < 4; ++r)
+          p.u[sh * C * p.dvp + (uint32_t)((tok + r) * p.dvp + vcol[t])] = U[t][r];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            p.sc[(sh * DK + d0 + 16 * m + r) * p.dvp + vcol[t]] = S[m][t][r];
+            p.sc[sh * DK * p.dvp + (uint32_t)((d0 + 16 * m + r) * p.dvp + vcol[t])] = S[m][t][r];
     }
     // the state at the chunk's end
 #pragma unroll
@@ -328,28 +329,147 @@ __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
 // end: dW = A^T dO + e^(c_end - c) K X^T, Z = (I + beta L)^-T dW (delta rule;
 // else dW), dV = Y = beta Z, dbeta = U . Z over the value columns, and
 // X = e^c_end X + (e^c dO)^T Q - (e^c Y)^T K (the last with the delta rule).
+//
+// As forward, the chain has waves of its own (0..3).  What does not wait for X,
+// A^T dO and (e^c dO)^T Q, waves 4..7 compute one chunk ahead and hand over in
+// LDS.
 template <int DK, int NT, int NPQ, int NPO, bool VEC, bool DELTA>
-__global__ void __launch_bounds__(256) state_grads_kernel(Params p) {
-  constexpr int BV = 16 * NT, KS = DK / 32, MT = DK / 64, SP = DK + 8;
+__global__ void __launch_bounds__(512) state_grads_kernel(Params p) {
+  constexpr bool BETA = DELTA || !VEC;  // GLA has none
+  constexpr int BV = 16 * NT, KS = DK / 32, MT = DK / 64, SP = DK + 8, FP = C + 4;
   __shared__ __align__(16) uint16_t Xl[P][BV][SP];
-  __shared__ __align__(16) uint16_t Ot[NPO][BV][CP];                            // d_o
-  __shared__ __align__(16) uint16_t Oe[VEC ? 1 : P][VEC ? 1 : BV][CP];          // e^c d_o
-  __shared__ __align__(16) uint16_t Dt[DELTA ? P : 1][DELTA ? BV : 1][CP];      // dW
-  __shared__ __align__(16) uint16_t Yt[DELTA ? P : 1][DELTA ? BV : 1][CP];      // -e^c Y
+  __shared__ __align__(16) uint16_t Ot[NPO][BV][CP];                        // d_o
+  __shared__ __align__(16) uint16_t Oe[VEC ? 1 : P][VEC ? 1 : BV][CP];      // e^c d_o
+  __shared__ __align__(16) uint16_t Dt[DELTA ? P : 1][DELTA ? BV : 1][CP];  // dW
+  __shared__ __align__(16) uint16_t Yt[DELTA ? P : 1][DELTA ? BV : 1][CP];  // -e^c Y
+  __shared__ __align__(16) float Al[BV][FP];                                // A^T dO
+  __shared__ __align__(16) float Gl[4][MT * NT][64][4];                     // (e^c dO)^T Q
   int n, h, vb;
   if (!chain_block(p, n, h, vb)) return;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = (threadIdx.x >> 6) & 3, lane = threadIdx.x & 63;
+  const bool helper = threadIdx.x >= 256;
   const int fr = lane & 15, fg = lane >> 4;
   const int64_t o0 = offset_of(p, n), o1 = offset_of(p, n + 1);
   const int64_t len = o1 > o0 ? o1 - o0 : 0;
   const int nch = (int)((len + C - 1) / C);
   const int base = (int)(o0 / C) + n;
-  const int d0 = wave * (DK / 4) + fg * 4;
   const int tok = wave * 16 + fg * 4;
-  const int64_t nh = (int64_t)n * p.heads + h;
+  const int group = p.heads / p.heads_qk;
   int vcol[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) vcol[t] = vb * BV + t * 16 + fr;
+  // operands are reloaded after their last use, without branches, as in states_kernel
+  auto chunk = [&](int ci) {
+    Chunk c;
+    c.n = n;
+    c.ci = ci;
+    c.row = o0 + (int64_t)ci * C;
+    c.len = len - (int64_t)ci * C < C ? (int)(len - (int64_t)ci * C) : C;
+    return c;
+  };
+  auto head_of = [&](int ci) { return (int64_t)(base + ci) * p.heads + h; };
+  auto qk_of = [&](int ci) { return VEC ? head_of(ci) : (int64_t)(base + ci) * p.heads_qk + h / group; };
+
+  if (helper) {
+    Frag<NPQ> fq[MT][2];
+    Frag<P> fA[2];
+    uint32_t x[NT][4];
+    f32x4 ec = {1, 1, 1, 1}, A[NT], G[MT][NT];
+    auto load_do = [&](int ci) {
+      const Chunk c = chunk(ci);
+      if (!VEC) ec = *reinterpret_cast<const f32x4*>(rows_at(p, base + ci, h) + tok);
+      const uint32_t stride = (uint32_t)p.heads * p.dv;
+      const char* src = static_cast<const char*>(p.dO) +
+                        (c.row * p.heads + h) * p.dv * (p.dtype == 0 ? 4 : 2);
+      uint32_t at[4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          at[r] = min((uint32_t)(tok + r) * stride, (uint32_t)(c.len - 1) * stride) + min(vcol[t], p.dv - 1);
+        load_raw<4>(src, at, p.dtype, x[t]);
+      }
+    };
+    auto load_mats = [&](int ci) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) fA[s] = tile_frag<P, C>(p.at + head_of(ci) * P * C * C, wave, s, C * C);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          fq[m][s] = tile_frag<NPQ, C>(p.qt + qk_of(ci) * NPQ * DK * C, wave * MT + m, s, DK * C);
+    };
+    auto stage = [&](int ci) {
+      const Chunk c = chunk(ci);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float xo[4], xe[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          xo[r] = tok + r < c.len && vcol[t] < p.dv ? from_raw(x[t][r], p.dtype) : 0.0f;
+          xe[r] = xo[r] * ec[r];
+        }
+        put4<NPO>(&Ot[0][t * 16 + fr][tok], BV * CP, xo);
+        if (!VEC) put4<P>(&Oe[0][t * 16 + fr][tok], BV * CP, xe);
+      }
+    };
+    auto products = [&]() {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        A[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          if (s >= wave / 2)
+            mma(A[t], fA[s], load_frag<NPO>(&Ot[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
+        *reinterpret_cast<f32x4*>(&Al[t * 16 + fr][tok]) = A[t];
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          G[m][t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            if (VEC)
+              mma(G[m][t], fq[m][s], load_frag<NPO>(&Ot[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
+            else
+              mma(G[m][t], fq[m][s], load_frag<P>(&Oe[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
+        }
+    };
+    auto hand_over = [&]() {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          *reinterpret_cast<f32x4*>(Gl[wave][m * NT + t][lane]) = G[m][t];
+    };
+    if (nch > 0) {
+      load_do(nch - 1);
+      load_mats(nch - 1);
+      stage(nch - 1);
+    }
+    __syncthreads();
+    if (nch > 0) {
+      load_do(max(nch - 2, 0));
+      products();
+      load_mats(max(nch - 2, 0));
+    }
+    __syncthreads();
+    for (int ci = nch - 1; ci >= 0; --ci) {  // one chunk ahead: ci - 1
+      hand_over();
+      stage(max(ci - 1, 0));
+      load_do(max(ci - 2, 0));
+      if (DELTA) __syncthreads();
+      __syncthreads();
+      products();  // the chain has read this chunk's Al, and reads Gl until the last barrier
+      load_mats(max(ci - 2, 0));
+      __syncthreads();
+    }
+    return;
+  }
+
+  const int d0 = wave * (DK / 4) + fg * 4;
+  const int64_t nh = (int64_t)n * p.heads + h;
   f32x4 X[MT][NT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
@@ -368,131 +488,75 @@ __global__ void __launch_bounds__(256) state_grads_kernel(Params p) {
         put4<P>(&Xl[0][t * 16 + fr][d0 + 16 * m], BV * SP, x);
       }
   };
-  put_state();
-  __syncthreads();
-
-  // operands are reloaded after their last use, as in states_kernel
-  Frag<NPQ> fk[KS], fq[MT][2], ft[DELTA ? MT : 1][2];
-  Frag<P> fA[2], fT[DELTA ? 2 : 1];
-  uint32_t x[NT][4];
-  float u[NT][4];
+  Frag<NPQ> fk[KS], ft[DELTA ? MT : 1][2];
+  Frag<P> fT[DELTA ? 2 : 1];
   f32x4 beta, ec = {1, 1, 1, 1}, eo = {1, 1, 1, 1}, dec[MT];
-  auto chunk = [&](int ci) {
-    Chunk c;
-    c.n = n;
-    c.ci = ci;
-    c.row = o0 + (int64_t)ci * C;
-    c.len = len - (int64_t)ci * C < C ? (int)(len - (int64_t)ci * C) : C;
-    return c;
-  };
-  auto load_do = [&](int ci) {
-    const Chunk c = chunk(ci);
-    const int64_t sh = (int64_t)(base + ci) * p.heads + h;
-    const float* rows = rows_at(p, base + ci, h);
-    beta = *reinterpret_cast<const f32x4*>(rows + 2 * C + tok);
-    if (!VEC) {
-      ec = *reinterpret_cast<const f32x4*>(rows + tok);
-      eo = *reinterpret_cast<const f32x4*>(rows + C + tok);
-    }
-    const uint32_t stride = (uint32_t)p.heads * p.dv;
-    const char* src = static_cast<const char*>(p.dO) +
-                      (c.row * p.heads + h) * p.dv * (p.dtype == 0 ? 4 : 2);
-    uint32_t at[4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        at[r] = min((uint32_t)(tok + r) * stride, (uint32_t)(c.len - 1) * stride) + min(vcol[t], p.dv - 1);
-      load_raw<4>(src, at, p.dtype, x[t]);
-      if (p.dbeta) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) u[t][r] = p.u[(sh * C + tok + r) * p.dvp + vcol[t]];
-      }
-    }
-  };
+  float u[NT][4];
   auto load_k = [&](int ci) {
     const auto k = rows_of<DK, NPQ == 1>(p, p.k, VEC ? p.korow : p.krow, p.ks, VEC, base + ci, h, chunk(ci));
 #pragma unroll
     for (int s = 0; s < KS; ++s) fk[s] = k.template frag<NPQ>(wave, s);
+    if (!VEC) eo = *reinterpret_cast<const f32x4*>(rows_at(p, base + ci, h) + C + tok);
   };
-  auto load_square = [&](const uint16_t* m, int ci, Frag<P>* f) {
-    const uint16_t* at = m + ((int64_t)(base + ci) * p.heads + h) * P * C * C;
+  auto load_T = [&](int ci) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) f[s] = tile_frag<P, C>(at, wave, s, C * C);
+    for (int s = 0; s < 2; ++s) fT[s] = tile_frag<P, C>(p.t2t + head_of(ci) * P * C * C, wave, s, C * C);
   };
-  auto load_t = [&](int ci) {
-    const int slot = base + ci;
-    const int64_t sh = (int64_t)slot * p.heads + h;
-    const int64_t th = VEC ? sh : (int64_t)slot * p.heads_qk + h / (p.heads / p.heads_qk);
-    const uint16_t* qt = p.qt + th * NPQ * DK * C;
-    const uint16_t* kt = (VEC ? p.ket : p.kt) + th * NPQ * DK * C;
-    const float end = VEC ? 1.0f : rows_at(p, slot, h)[C - 1];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        fq[m][s] = tile_frag<NPQ, C>(qt, wave * MT + m, s, DK * C);
-        if (DELTA) ft[m][s] = tile_frag<NPQ, C>(kt, wave * MT + m, s, DK * C);
-      }
-      dec[m] = VEC ? *reinterpret_cast<const f32x4*>(p.decay + sh * DK + d0 + 16 * m)
-                   : f32x4{end, end, end, end};
-    }
-  };
-  if (nch > 0) {
-    load_do(nch - 1);
-    load_k(nch - 1);
-    load_square(p.at, nch - 1, fA);
-    if (DELTA) load_square(p.t2t, nch - 1, fT);
-    load_t(nch - 1);
-  }
-
-  for (int ci = nch - 1; ci >= 0; --ci) {
-    const Chunk c = chunk(ci);
-    const int64_t sh = (int64_t)(base + ci) * p.heads + h;
-    const int next = max(ci - 1, 0);
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
+  auto load_u = [&](int ci) {
+    const float* rows = rows_at(p, base + ci, h);
+    beta = *reinterpret_cast<const f32x4*>(rows + 2 * C + tok);
+    if (!VEC) ec = *reinterpret_cast<const f32x4*>(rows + tok);
+    if (BETA) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          p.xc[(sh * DK + d0 + 16 * m + r) * p.dvp + vcol[t]] = X[m][t][r];
-    const f32x4 bc = beta, ecc = ec, eoc = eo;
-    float uc[NT][4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float xo[4], xe[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        xo[r] = tok + r < c.len && vcol[t] < p.dv ? from_raw(x[t][r], p.dtype) : 0.0f;
-        xe[r] = xo[r] * ec[r];
-        uc[t][r] = p.dbeta ? u[t][r] : 0.0f;
-      }
-      put4<NPO>(&Ot[0][t * 16 + fr][tok], BV * CP, xo);
-      if (!VEC) put4<P>(&Oe[0][t * 16 + fr][tok], BV * CP, xe);
+          u[t][r] = p.u[head_of(ci) * C * p.dvp + (uint32_t)((tok + r) * p.dvp + vcol[t])];
     }
-    load_do(next);
-    f32x4 W[NT];
+  };
+  auto load_kt = [&](int ci) {
+    const float end = VEC ? 1.0f : rows_at(p, base + ci, h)[C - 1];
+    const uint16_t* kt = (VEC ? p.ket : p.kt) + qk_of(ci) * NPQ * DK * C;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) W[t] = f32x4{0, 0, 0, 0};
+    for (int m = 0; m < MT; ++m) {
+      if (DELTA) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) ft[m][s] = tile_frag<NPQ, C>(kt, wave * MT + m, s, DK * C);
+      }
+      dec[m] = VEC ? *reinterpret_cast<const f32x4*>(p.decay + head_of(ci) * DK + d0 + 16 * m)
+                   : f32x4{end, end, end, end};
+    }
+  };
+  if (nch > 0) {
+    load_k(nch - 1);
+    if (DELTA) load_T(nch - 1);
+    load_u(nch - 1);
+    load_kt(nch - 1);
+  }
+  put_state();
+  __syncthreads();
+  __syncthreads();
+
+  for (int ci = nch - 1; ci >= 0; --ci) {
+    const Chunk c = chunk(ci);
+    const int64_t sh = head_of(ci);
+    const int next = max(ci - 1, 0);
+    f32x4 W[NT], W2[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) W[t] = W2[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int s = 0; s < KS; ++s)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
-        mma(W[t], fk[s], load_frag<P>(&Xl[0][t * 16 + fr][s * 32 + fg * 8], BV * SP));
+        mma(s & 1 ? W2[t] : W[t], fk[s],
+            load_frag<P>(&Xl[0][t * 16 + fr][s * 32 + fg * 8], BV * SP));
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const f32x4 a = *reinterpret_cast<const f32x4*>(&Al[t * 16 + fr][tok]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) W[t][r] = fmaf(W[t][r] + W2[t][r], eo[r], a[r]);
+    }
     load_k(next);
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) W[t][r] *= eoc[r];
-    __syncthreads();
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-      if (s >= wave / 2)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          mma(W[t], fA[s], load_frag<NPO>(&Ot[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
-    load_square(p.at, next, fA);
     if (DELTA) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -507,20 +571,44 @@ __global__ void __launch_bounds__(256) state_grads_kernel(Params p) {
 #pragma unroll
           for (int t = 0; t < NT; ++t)
             mma(W[t], fT[s], load_frag<P>(&Dt[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
-      load_square(p.t2t, next, fT);
+      load_T(next);
     }
     // W holds Z
-    float db[4] = {0, 0, 0, 0};
+    float y[NT][4], db[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float y[4], ye[4];
+      float ye[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        y[r] = bc[r] * W[t][r];
-        ye[r] = -ecc[r] * y[r];
-        if (p.dbeta) db[r] = fmaf(uc[t][r], W[t][r], db[r]);
+        y[t][r] = beta[r] * W[t][r];
+        ye[r] = -ec[r] * y[t][r];
+        if (BETA) db[r] = fmaf(u[t][r], W[t][r], db[r]);
       }
       if (DELTA) put4<P>(&Yt[0][t * 16 + fr][tok], BV * CP, ye);
+    }
+    load_u(next);
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const f32x4 g = *reinterpret_cast<const f32x4*>(Gl[wave][m * NT + t][lane]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          p.xc[sh * DK * p.dvp + (uint32_t)((d0 + 16 * m + r) * p.dvp + vcol[t])] = X[m][t][r];
+          X[m][t][r] = fmaf(X[m][t][r], dec[m][r], g[r]);
+        }
+        if (DELTA) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            mma(X[m][t], ft[m][s], load_frag<P>(&Yt[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
+        }
+      }
+    load_kt(next);
+    put_state();
+    // stores behind the work that others wait for
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
       char* dst = static_cast<char*>(p.dv_out) +
                   (c.row * p.heads + h) * p.dv * (p.dtype == 0 ? 4 : 2);
       uint32_t at[4];
@@ -529,41 +617,16 @@ __global__ void __launch_bounds__(256) state_grads_kernel(Params p) {
       for (int r = 0; r < 4; ++r) {
         at[r] = (uint32_t)(tok + r) * (uint32_t)p.heads * p.dv + vcol[t];
         ok[r] = tok + r < c.len && vcol[t] < p.dv;
+        if (DELTA) p.y[sh * C * p.dvp + (uint32_t)((tok + r) * p.dvp + vcol[t])] = y[t][r];
       }
-      store_elems<4>(dst, at, ok, p.dtype, y);
-      if (DELTA) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) p.y[(sh * C + tok + r) * p.dvp + vcol[t]] = y[r];
-      }
+      store_always<4>(dst, at, ok, p.dtype, p.sink, y[t]);
     }
-    if (p.dbeta) {
+    if (BETA) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) db[r] = sum16(db[r]);
-      if (fr == 0)
-        *reinterpret_cast<f32x4*>(
-            p.dbpart + ((int64_t)vb * p.nslots * p.heads + sh) * C + tok) = f32x4{db[0], db[1], db[2], db[3]};
+      *reinterpret_cast<f32x4*>(p.dbpart + ((int64_t)vb * p.nslots * p.heads + sh) * C + tok) =
+          f32x4{db[0], db[1], db[2], db[3]};  // 16 lanes, one value
     }
-    if (DELTA) __syncthreads();
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) X[m][t][r] *= dec[m][r];
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if (VEC)
-            mma(X[m][t], fq[m][s], load_frag<NPO>(&Ot[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
-          else
-            mma(X[m][t], fq[m][s], load_frag<P>(&Oe[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
-          if (DELTA)
-            mma(X[m][t], ft[m][s], load_frag<P>(&Yt[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
-        }
-    }
-    load_t(next);
-    put_state();
     __syncthreads();
   }
   if (p.ds0) {

@@ -170,6 +170,28 @@ __device__ __forceinline__ void load4(const void* p, int64_t at, int dtype, bool
   for (int i = 0; i < 4; ++i) x[i] = from_raw(w[i], dtype);
 }
 
+// The same without a branch: places that are not `ok` go to the sink.  Loads
+// and stores return in order, and a branch around a store would make every
+// later wait for a load wait for newer ones too.
+template <int N>
+__device__ __forceinline__ void store_always(char* p, const uint32_t (&at)[N], const bool (&ok)[N],
+                                             int dtype, float* sink, const float (&x)[N]) {
+  char* const s = reinterpret_cast<char*>(sink + (threadIdx.x & 63));
+  if (dtype == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      *reinterpret_cast<float*>(ok[i] ? p + (uint64_t)at[i] * 4 : s) = x[i];
+  } else {
+    const uint32_t half = dtype == 2 ? ~0u : 0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t h = __builtin_bit_cast(uint16_t, (_Float16)x[i]);
+      *reinterpret_cast<uint16_t*>(ok[i] ? p + (uint64_t)at[i] * 2 : s) =
+          (uint16_t)((h & half) | (pack_bf16(x[i], 0.0f) & ~half));
+    }
+  }
+}
+
 // Log decays below -87 count as -87; a NaN stays.
 __device__ __forceinline__ float gate(float g) { return g < -87.0f ? -87.0f : g; }
 

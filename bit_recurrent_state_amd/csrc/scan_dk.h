@@ -49,8 +49,9 @@ hipError_t backward_tail(const Params& p, hipStream_t s) {
     }
   }
   states_kernel<DK, NT, NPQ, P, VEC, DELTA, true><<<chain_grid(p), 256, 0, s>>>(p);
-  state_grads_kernel<DK, NT, NPQ, NPO, VEC, DELTA><<<chain_grid(p), 256, 0, s>>>(p);
-  grads_kernel<DK, NPQ, VEC ? NPO : NPQ, NPO, VEC, DELTA><<<slots, 256, 0, s>>>(p);
+  state_grads_kernel<DK, NT, NPQ, NPO, VEC, DELTA><<<chain_grid(p), 512, 0, s>>>(p);
+  grads_kernel<DK, NPQ, VEC ? NPO : NPQ, NPO, VEC, DELTA>
+      <<<slots, DK >= 128 ? 512 : 256, 0, s>>>(p);
   if (VEC) grads_vector_kernel<DK, NPO, NPO, DELTA><<<slots, 256, 0, s>>>(p);
   if (p.heads != p.heads_qk)
     share_kernel<DK><<<dim3(p.nslots, p.heads_qk, kChunk * DK / 1024), 256, 0, s>>>(p);

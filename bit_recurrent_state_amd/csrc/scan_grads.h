@@ -108,13 +108,13 @@ __device__ __forceinline__ void store_dbeta(const Params& p, const Chunk& c, int
 // e^c_i, and sum_i E_ij (q_i e^c_i) by e^-c_j.  NPR: terms of the unscaled q and
 // k (VEC).
 template <int DK, int NPQ, int NPR, int NPO, bool VEC, bool DELTA>
-__global__ void __launch_bounds__(256) grads_kernel(Params p) {
-  constexpr int CT = DK / 64, VS = 64, VP = VS + 8, NP = NPO + (DELTA ? 2 : 1) * P;
+__global__ void __launch_bounds__(DK >= 128 ? 512 : 256) grads_kernel(Params p) {
+  constexpr int NW = DK >= 128 ? 8 : 4, CT = DK / (16 * NW), NE = 16 / NW, VS = 64, VP = VS + 8, NP = NPO + (DELTA ? 2 : 1) * P;
   constexpr int PL = C * CP;
   constexpr int kWords = (NP * C * VP > 2 * P * C * CP ? NP * C * VP : 2 * P * C * CP);
   __shared__ __align__(16) uint16_t lds[kWords];
-  __shared__ float red[2][4][C];
-  __shared__ float redx[4];
+  __shared__ float red[2][NW][C];
+  __shared__ float redx[NW];
   uint16_t* const Ol = lds;
   uint16_t* const Ul = lds + NPO * C * VP;
   uint16_t* const Yl = Ul + P * C * VP;
@@ -130,13 +130,16 @@ __global__ void __launch_bounds__(256) grads_kernel(Params p) {
   const int hq = h / (p.heads / p.heads_qk);
   const float* rows = rows_at(p, slot, h);
   const ValueRows dO = dout_rows(p, sh, h, c);
-  const int ch0 = wave * (DK / 4) + fr;
+  const int ch0 = wave * (DK / NW) + fr;
+  // E and F: the wave's row block, and its column blocks b0, b0 + 4 / NE, ..
+  const int rb = wave * 4 / NW, b0 = wave % (NW / 4);
 
-  f32x4 e[4], f[4], aq[CT][4], ap[DELTA ? CT : 1][4], am[CT][4];
+  f32x4 e[NE], f[NE], aq[CT][4], ap[DELTA ? CT : 1][4], am[CT][4];
   float xs[CT];
 #pragma unroll
+  for (int b = 0; b < NE; ++b) e[b] = f[b] = f32x4{0, 0, 0, 0};
+#pragma unroll
   for (int m = 0; m < 4; ++m) {
-    e[m] = f[m] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
       aq[ct][m] = am[ct][m] = f32x4{0, 0, 0, 0};
@@ -148,14 +151,16 @@ __global__ void __launch_bounds__(256) grads_kernel(Params p) {
 
   for (int v0 = 0; v0 < p.dvp; v0 += VS) {
     const int ns = p.dvp - v0 >= VS ? 2 : 1;
-    // rows into LDS: 8 vectors of 8 a row, 2 rows of every array a thread
+    f32x4 sv[CT][2][2], xv[CT][2][2];
+    // rows into LDS: 8 vectors of 8 a row
     {
       constexpr int A = DELTA ? 2 : 1;  // U, Y
       const int col = threadIdx.x & 7, row = threadIdx.x >> 3;
-      u32x4 so[NPO][2];
-      f32x4 sf[A][2][2];
+      constexpr int R = 8 / NW;  // rows a thread
+      u32x4 so[NPO][R];
+      f32x4 sf[A][R][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < R; ++i) {
         const int r = i * 32 + row;
         // columns behind dvp repeat the last ones and are not used
         const int64_t vc = v0 + min(col * 8, p.dvp - v0 - 8);
@@ -172,9 +177,20 @@ __global__ void __launch_bounds__(256) grads_kernel(Params p) {
           if (DELTA) sf[A - 1][i][q] = *reinterpret_cast<const f32x4*>(p.y + at + q * 4);
         }
       }
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int64_t at = (sh * DK + ch0 + ct * 16) * p.dvp + v0 + min(s, ns - 1) * 32 + fg * 8;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            sv[ct][s][q] = *reinterpret_cast<const f32x4*>(p.sc + at + q * 4);
+            xv[ct][s][q] = *reinterpret_cast<const f32x4*>(p.xc + at + q * 4);
+          }
+        }
       __syncthreads();  // the last slab has been read
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < R; ++i) {
         const int o = (i * 32 + row) * VP + col * 8;
 #pragma unroll
         for (int n = 0; n < NPO; ++n) *reinterpret_cast<u32x4*>(Ol + n * C * VP + o) = so[n][i];
@@ -189,30 +205,18 @@ __global__ void __launch_bounds__(256) grads_kernel(Params p) {
         }
       }
     }
-    f32x4 sv[CT][2][2], xv[CT][2][2];
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int64_t at = (sh * DK + ch0 + ct * 16) * p.dvp + v0 + min(s, ns - 1) * 32 + fg * 8;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          sv[ct][s][q] = *reinterpret_cast<const f32x4*>(p.sc + at + q * 4);
-          xv[ct][s][q] = *reinterpret_cast<const f32x4*>(p.xc + at + q * 4);
-        }
-      }
     __syncthreads();
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       if (s >= ns) break;
       const int at = fr * VP + s * 32 + fg * 8;
-      const Frag<NPO> fo = load_frag<NPO>(Ol + wave * 16 * VP + at, C * VP);
+      const Frag<NPO> fo = load_frag<NPO>(Ol + rb * 16 * VP + at, C * VP);
       Frag<P> fy;
-      if (DELTA) fy = load_frag<P>(Yl + wave * 16 * VP + at, C * VP);
+      if (DELTA) fy = load_frag<P>(Yl + rb * 16 * VP + at, C * VP);
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        if (b <= wave) {
-          const Frag<P> fu = load_frag<P>(Ul + b * 16 * VP + at, C * VP);
+      for (int b = 0; b < NE; ++b)
+        if (b0 + b * (NW / 4) <= rb) {
+          const Frag<P> fu = load_frag<P>(Ul + (b0 + b * (NW / 4)) * 16 * VP + at, C * VP);
           mma(e[b], fo, fu);
           if (DELTA) mma(f[b], fy, fu);
         }
@@ -245,13 +249,13 @@ __global__ void __launch_bounds__(256) grads_kernel(Params p) {
     }
   }
 
-  // E (then F) as planes in LDS: rows i of block `wave`, columns j of block b
+  // E (then F) as planes in LDS
   const double* cs = reinterpret_cast<const double*>(rows + 3 * C);
-  auto put_square = [&](f32x4(&x)[4], bool strict, float sign) {
+  auto put_square = [&](f32x4(&x)[NE], bool strict, float sign) {
     __syncthreads();
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int j = b * 16 + fr, i0 = wave * 16 + fg * 4;
+    for (int b = 0; b < NE; ++b) {
+      const int j = (b0 + b * (NW / 4)) * 16 + fr, i0 = rb * 16 + fg * 4;
       const float beta = sign * rows[2 * C + j];
       float v[4];
 #pragma unroll
@@ -448,7 +452,7 @@ __global__ void __launch_bounds__(256) grads_kernel(Params p) {
   if (wave == 0) {
     double s = 0.0, d = 0.0, sx = 0.0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < NW; ++w) {
       s += red[0][w][lane];
       d += red[1][w][lane];
       sx += redx[w];

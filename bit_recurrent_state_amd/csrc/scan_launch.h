@@ -36,6 +36,7 @@ struct Params {
   void *o, *dq, *dkk, *dv_out;
   float *s1, *dg, *dbeta, *ds0;
   // workspace
+  float* sink;               // [64] where lanes without an output write
   float* rows;               // [slot][head][5][kChunk]: exp(c), exp(c_end - c), beta, c (double)
   float* decay;              // [slot][head][dk] exp(c_end) (per-channel gates)
   uint16_t *qrow, *krow;     // [slot][head|head_qk][term][kChunk][dk]

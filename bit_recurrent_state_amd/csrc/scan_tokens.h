@@ -41,10 +41,12 @@ __global__ void __launch_bounds__(256) tokens_kernel(Params p) {
 #pragma unroll
   for (int q = 0; q < Q; ++q)
     S[q] = p.s0 ? *reinterpret_cast<const f32x4*>(p.s0 + st + 32 * q) : f32x4{0, 0, 0, 0};
-  for (int i = 0; i < len; ++i) {
+  // a token's inputs, loaded one token ahead
+  float k[Q][4], x[Q][4], ga = 0.0f, beta = 1.0f;
+  f32x4 g[VEC ? Q : 1];
+  uint32_t vr[1];
+  auto load = [&](int i) {
     const int64_t row = o0 + i;
-    float k[Q][4], x[Q][4];
-    f32x4 g[VEC ? Q : 1];
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       load4(p.k, row * p.ks + (int64_t)hq * DK + 32 * q + 4 * l, p.dtype, keven, k[q]);
@@ -52,30 +54,46 @@ __global__ void __launch_bounds__(256) tokens_kernel(Params p) {
       if (VEC)
         g[q] = *reinterpret_cast<const f32x4*>(p.g + (row * p.heads + h) * DK + 32 * q + 4 * l);
     }
-    const float ga = VEC ? 0.0f : p.g[row * p.heads + h];
-    const float beta = p.beta ? p.beta[row * p.heads + h] : 1.0f;
-    float w = load_elem(p.v, row * p.vs + (int64_t)h * p.dv + (in ? v : p.dv - 1), p.dtype);
-    const float a = VEC ? 0.0f : fast_exp(gate(ga));
+    if (!VEC) ga = p.g[row * p.heads + h];
+    if (p.beta) beta = p.beta[row * p.heads + h];
+    const int64_t at[1] = {row * p.vs + (int64_t)h * p.dv + (in ? v : p.dv - 1)};
+    load_raw<1>(p.v, at, p.dtype, vr);
+  };
+  if (len > 0) load(0);
+  for (int i = 0; i < len; ++i) {
+    float kc[Q][4], xc[Q][4], a[VEC ? Q : 1][4];
+    const float bc = beta;
+    float w = from_raw(vr[0], p.dtype);
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        kc[q][e] = k[q][e];
+        xc[q][e] = x[q][e];
+        if (VEC) a[VEC ? q : 0][e] = fast_exp(gate(g[VEC ? q : 0][e]));
+      }
+    if (!VEC) a[0][0] = fast_exp(gate(ga));
+    if (i + 1 < len) load(i + 1);
     float u = 0.0f;
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        S[q][e] *= VEC ? fast_exp(gate(g[VEC ? q : 0][e])) : a;
-        if (DELTA) u = fmaf(S[q][e], k[q][e], u);
+        S[q][e] *= VEC ? a[VEC ? q : 0][e] : a[0][0];
+        if (DELTA) u = fmaf(S[q][e], kc[q][e], u);
       }
     if (DELTA) w -= sum8(u);
-    w *= beta;
+    w *= bc;
     float o = 0.0f;
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        S[q][e] = fmaf(w, k[q][e], S[q][e]);
-        o = fmaf(S[q][e], x[q][e], o);
+        S[q][e] = fmaf(w, kc[q][e], S[q][e]);
+        o = fmaf(S[q][e], xc[q][e], o);
       }
     o = sum8(o);
-    if (p.o && in && l == 0) store_elem(p.o, row * p.os + (int64_t)h * p.dv + v, p.dtype, o);
+    if (p.o && in && l == 0) store_elem(p.o, (o0 + i) * p.os + (int64_t)h * p.dv + v, p.dtype, o);
   }
   if (p.s1 && in) {
 #pragma unroll
