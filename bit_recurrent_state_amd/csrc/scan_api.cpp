@@ -86,6 +86,7 @@ size_t layout(const qstate_scan_config* c, bool backward, void* workspace, Param
   const uint64_t sh = (uint64_t)p.nslots * p.heads, sq = (uint64_t)p.nslots * p.heads_qk;
   const uint64_t tile = (uint64_t)kChunk * p.dk, ops = (vec ? sh : sq) * p.terms * tile;
   const uint64_t square = sh * kTerms * kChunk * kChunk;
+  w.take(p.chunks, p.nslots, true);
   w.take(p.sink, 64, true);
   w.take(p.rows, sh * 5 * kChunk, true);
   w.take(p.decay, sh * p.dk, vec);

@@ -63,6 +63,24 @@ __device__ __forceinline__ bool find_chunk(const Params& p, int slot, Chunk& c) 
   return true;
 }
 
+// The first kernel of a call searches and leaves what it found for the others:
+// one load instead of a search's two or three that wait for each other.
+__device__ __forceinline__ bool find_and_note(const Params& p, int slot, bool note, Chunk& c) {
+  const bool found = find_chunk(p, slot, c);
+  if (note && threadIdx.x == 0)
+    p.chunks[slot] = found ? make_int4(c.n, c.ci, c.len, (int)c.row) : make_int4(-1, 0, 0, 0);
+  return found;
+}
+
+__device__ __forceinline__ bool noted_chunk(const Params& p, int slot, Chunk& c) {
+  const int4 e = p.chunks[slot];
+  c.n = e.x;
+  c.ci = e.y;
+  c.len = e.z;
+  c.row = e.w;
+  return c.n >= 0;
+}
+
 // ---- elements of the caller's arrays -------------------------------------------------------
 
 __device__ __forceinline__ float bf16_to_f(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
@@ -334,12 +352,25 @@ __device__ __forceinline__ float* rows_at(const Params& p, int slot, int h) {
   return p.rows + ((int64_t)slot * p.heads + h) * (5 * C);
 }
 
-// Sum over the 16 lanes that hold one row of a product.
+// Sums over the 16 lanes that hold one row of a product, and over 8 lanes, by
+// DPP: shuffles go through LDS and were half the time of kernels with many.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+
 __device__ __forceinline__ float sum16(float x) {
-  x += __shfl_xor(x, 1);
-  x += __shfl_xor(x, 2);
-  x += __shfl_xor(x, 4);
-  x += __shfl_xor(x, 8);
+  x += dpp<0x128>(x);  // row_ror 8, 4, 2, 1
+  x += dpp<0x124>(x);
+  x += dpp<0x122>(x);
+  x += dpp<0x121>(x);
+  return x;
+}
+
+__device__ __forceinline__ float sum8(float x) {
+  x += dpp<0xB1>(x);   // quad_perm 1, 0, 3, 2
+  x += dpp<0x4E>(x);   // quad_perm 2, 3, 0, 1
+  x += dpp<0x141>(x);  // row_half_mirror: the other four of eight
   return x;
 }
 

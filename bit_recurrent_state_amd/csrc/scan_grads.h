@@ -88,13 +88,27 @@ __device__ __forceinline__ void store_qk(const Params& p, const Chunk& c, int64_
   }
 }
 
-// dbeta: the column blocks' parts.
-__device__ __forceinline__ void store_dbeta(const Params& p, const Chunk& c, int64_t sh, int h) {
-  if (!p.dbeta || (int)threadIdx.x >= c.len) return;
+// dbeta: the column blocks' parts, summed in a fixed order; a wave takes every
+// NW-th, store_dbeta (the threads of one wave, after a barrier) their sums.
+template <int NW>
+__device__ __forceinline__ void sum_dbeta(const Params& p, int64_t sh, float (*red)[C]) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   float s = 0.0f;
-  for (int b = 0; b < p.nvb; ++b)
-    s += p.dbpart[((int64_t)b * p.nslots * p.heads + sh) * C + threadIdx.x];
-  p.dbeta[(c.row + threadIdx.x) * p.heads + h] = s;
+  if (p.dbeta)
+    for (int b = wave; b < p.nvb; b += NW)
+      s += p.dbpart[((int64_t)b * p.nslots * p.heads + sh) * C + lane];
+  red[wave][lane] = s;
+}
+
+template <int NW>
+__device__ __forceinline__ void store_dbeta(const Params& p, const Chunk& c, int h,
+                                            const float (*red)[C]) {
+  const int t = threadIdx.x & 63;
+  if (!p.dbeta || t >= c.len) return;
+  float s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) s += red[w][t];
+  p.dbeta[(c.row + t) * p.heads + h] = s;
 }
 
 // ---- the states' and the chunk's products ----------------------------------------------------
@@ -113,7 +127,8 @@ __global__ void __launch_bounds__(DK >= 128 ? 512 : 256) grads_kernel(Params p) 
   constexpr int PL = C * CP;
   constexpr int kWords = (NP * C * VP > 2 * P * C * CP ? NP * C * VP : 2 * P * C * CP);
   __shared__ __align__(16) uint16_t lds[kWords];
-  __shared__ float red[2][NW][C];
+  __shared__ float red[2][NW][C], redb[NW][C];
+  __shared__ __align__(16) float rows[5 * C];
   __shared__ float redx[NW];
   uint16_t* const Ol = lds;
   uint16_t* const Ul = lds + NPO * C * VP;
@@ -122,13 +137,16 @@ __global__ void __launch_bounds__(DK >= 128 ? 512 : 256) grads_kernel(Params p) 
   uint16_t* const Et = lds + P * PL;  // transposed
   const int slot = blockIdx.x, h = blockIdx.y;
   Chunk c;
-  if (!find_chunk(p, slot, c)) return;
+  if (!noted_chunk(p, slot, c)) return;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int fr = lane & 15, fg = lane >> 4;
   const int64_t sh = (int64_t)slot * p.heads + h;
   if (VEC && p.far[sh]) return;
   const int hq = h / (p.heads / p.heads_qk);
-  const float* rows = rows_at(p, slot, h);
+  if (threadIdx.x >= 64 && threadIdx.x < 64 + 5 * C / 4)
+    reinterpret_cast<f32x4*>(rows)[threadIdx.x - 64] =
+        reinterpret_cast<const f32x4*>(rows_at(p, slot, h))[threadIdx.x - 64];
+  sum_dbeta<NW>(p, sh, redb);
   const ValueRows dO = dout_rows(p, sh, h, c);
   const int ch0 = wave * (DK / NW) + fr;
   // E and F: the wave's row block, and its column blocks b0, b0 + 4 / NE, ..
@@ -283,7 +301,15 @@ __global__ void __launch_bounds__(DK >= 128 ? 512 : 256) grads_kernel(Params p) 
   const int64_t tq = VEC ? sh : (int64_t)slot * p.heads_qk + hq;
   const uint16_t* const kn = (VEC ? p.knt : p.kt) + tq * NPQ * DK * C;  // right operand of E, F
   const uint16_t* const qe = p.qt + tq * NPQ * DK * C;                  // of E transposed
-  const uint16_t* const ke = (VEC ? p.ket : p.kt) + tq * NPQ * DK * C;  // of F transposed
+  const uint16_t* const ke = p.ket + tq * NPQ * DK * C;                 // of F transposed (VEC)
+  Frag<NPQ> fk[CT][2], fq[CT][2];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      fk[ct][s] = tile_frag<NPQ, C>(kn, wave * CT + ct, s, DK * C);
+      fq[ct][s] = tile_frag<NPQ, C>(qe, wave * CT + ct, s, DK * C);
+    }
   put_square(e, false, 1.0f);
   f32x4 ai[CT][4];
 #pragma unroll
@@ -315,46 +341,59 @@ __global__ void __launch_bounds__(DK >= 128 ? 512 : 256) grads_kernel(Params p) 
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const Frag<NPQ> fk = tile_frag<NPQ, C>(kn, wave * CT + ct, s, DK * C);
-      const Frag<NPQ> fq = tile_frag<NPQ, C>(qe, wave * CT + ct, s, DK * C);
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         const int o = (m * 16 + fr) * CP + s * 32 + fg * 8;
-        if (s <= m / 2) mma(aq[ct][m], load_frag<P>(El + o, PL), fk);
-        if (s >= m / 2) mma(ai[ct][m], load_frag<P>(Et + o, PL), fq);
+        if (s <= m / 2) mma(aq[ct][m], load_frag<P>(El + o, PL), fk[ct][s]);
+        if (s >= m / 2) mma(ai[ct][m], load_frag<P>(Et + o, PL), fq[ct][s]);
       }
     }
   }
+  // one gate per token: F's right operands are k's columns both times
+  if (DELTA && VEC) {
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) fq[ct][s] = tile_frag<NPQ, C>(ke, wave * CT + ct, s, DK * C);
+  }
+  // the unscaled k and q, for the gates
+  const uint16_t* const kr = (VEC ? p.kt_raw : p.kt) + ((int64_t)slot * p.heads_qk + hq) * NPR * DK * C;
+  const uint16_t* const qr = (VEC ? p.qt_raw : p.qt) + ((int64_t)slot * p.heads_qk + hq) * NPR * DK * C;
+  u32x2 rk[CT][4][NPR], rq[CT][4][NPR];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int n = 0; n < NPR; ++n) {
+        const int at = n * DK * C + tiled<C>(ch0 + ct * 16, m * 16 + fg * 4);
+        rk[ct][m][n] = *reinterpret_cast<const u32x2*>(kr + at);
+        rq[ct][m][n] = *reinterpret_cast<const u32x2*>(qr + at);
+      }
   if (DELTA) {
     put_square(f, true, -1.0f);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const Frag<NPQ> fk = tile_frag<NPQ, C>(kn, wave * CT + ct, s, DK * C);
-        const Frag<NPQ> fe = tile_frag<NPQ, C>(ke, wave * CT + ct, s, DK * C);
+      for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const int o = (m * 16 + fr) * CP + s * 32 + fg * 8;
-          if (s <= m / 2) mma(ap[ct][m], load_frag<P>(El + o, PL), fk);
-          if (s >= m / 2) mma(ai[ct][m], load_frag<P>(Et + o, PL), fe);
+          if (s <= m / 2) mma(ap[ct][m], load_frag<P>(El + o, PL), fk[ct][s]);
+          if (s >= m / 2) mma(ai[ct][m], load_frag<P>(Et + o, PL), VEC ? fq[ct][s] : fk[ct][s]);
         }
-      }
   }
 
   // the outputs, and the sums for the gates
-  const uint16_t* const kr = (VEC ? p.kt_raw : p.kt) + ((int64_t)slot * p.heads_qk + hq) * NPR * DK * C;
-  const uint16_t* const qr = (VEC ? p.qt_raw : p.qt) + ((int64_t)slot * p.heads_qk + hq) * NPR * DK * C;
-  auto raw4 = [&](const uint16_t* src, int ch, int t0, float(&x)[4]) {
+  auto sum4 = [&](const u32x2(&w)[NPR], float(&x)[4]) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) x[r] = 0.0f;
 #pragma unroll
     for (int n = NPR - 1; n >= 0; --n) {
-      const u32x2 w = *reinterpret_cast<const u32x2*>(src + n * DK * C + tiled<C>(ch, t0));
-      x[0] += __uint_as_float(w.x << 16);
-      x[1] += __uint_as_float(w.x & 0xFFFF0000u);
-      x[2] += __uint_as_float(w.y << 16);
-      x[3] += __uint_as_float(w.y & 0xFFFF0000u);
+      x[0] += __uint_as_float(w[n].x << 16);
+      x[1] += __uint_as_float(w[n].x & 0xFFFF0000u);
+      x[2] += __uint_as_float(w[n].y << 16);
+      x[3] += __uint_as_float(w[n].y & 0xFFFF0000u);
     }
   };
   float sS[4][4], sD[4][4];
@@ -365,8 +404,8 @@ __global__ void __launch_bounds__(DK >= 128 ? 512 : 256) grads_kernel(Params p) 
     for (int m = 0; m < 4; ++m) {
       const int t0 = m * 16 + fg * 4;
       float k[4], q[4], dq[4], dk[4];
-      raw4(kr, ch, t0, k);
-      raw4(qr, ch, t0, q);
+      sum4(rk[ct][m], k);
+      sum4(rq[ct][m], q);
       f32x4 ec = {1, 1, 1, 1};
       if (VEC) ec = *reinterpret_cast<const f32x4*>(p.pfx + (sh * DK + ch) * C + t0);
 #pragma unroll
@@ -428,7 +467,7 @@ __global__ void __launch_bounds__(DK >= 128 ? 512 : 256) grads_kernel(Params p) 
     }
   }
   if (VEC) {
-    if (wave == 0) store_dbeta(p, c, sh, h);
+    if (wave == 0) store_dbeta<NW>(p, c, h, redb);
     return;
   }
 #pragma unroll
@@ -465,7 +504,7 @@ __global__ void __launch_bounds__(DK >= 128 ? 512 : 256) grads_kernel(Params p) 
     }
     if (lane < c.len)
       p.dg[(c.row + lane) * p.heads + h] = (float)(rows[C - 1] * sx + (before - s) + after);
-    store_dbeta(p, c, sh, h);
+    store_dbeta<NW>(p, c, h, redb);
   }
 }
 
@@ -490,13 +529,15 @@ __global__ void __launch_bounds__(256) grads_vector_kernel(Params p) {
   __shared__ __align__(16) float buf[4][16][FP];
   const int slot = blockIdx.x, h = blockIdx.y;
   Chunk c;
-  if (!find_chunk(p, slot, c)) return;
+  if (!noted_chunk(p, slot, c)) return;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int fr = lane & 15, fg = lane >> 4;
   const int64_t sh = (int64_t)slot * p.heads + h;
   if (!p.far[sh]) return;
   const int hq = h / (p.heads / p.heads_qk);
   const float* rows = rows_at(p, slot, h);
+  __shared__ float redb[4][C];
+  sum_dbeta<4>(p, sh, redb);
   const ValueRows dO = dout_rows(p, sh, h, c);
   auto uy_frag = [&](const float* src, int row, int col) {
     float x[8];
@@ -782,7 +823,7 @@ __global__ void __launch_bounds__(256) grads_vector_kernel(Params p) {
       pre += x[i];
     }
   }
-  if (wave == 0) store_dbeta(p, c, sh, h);
+  if (wave == 0) store_dbeta<4>(p, c, h, redb);
 }
 
 // dq and dk of heads that share them: summed in the order of the heads, four
@@ -791,7 +832,7 @@ template <int DK>
 __global__ void __launch_bounds__(256) share_kernel(Params p) {
   const int slot = blockIdx.x, hq = blockIdx.y;
   Chunk c;
-  if (!find_chunk(p, slot, c)) return;
+  if (!noted_chunk(p, slot, c)) return;
   const int group = p.heads / p.heads_qk;
   const int u = (blockIdx.z * 256 + threadIdx.x) * 4;
   if (u >= c.len * DK) return;

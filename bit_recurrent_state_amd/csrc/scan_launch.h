@@ -5,6 +5,7 @@
 #pragma once
 
 #include <hip/hip_runtime_api.h>
+#include <hip/hip_vector_types.h>
 
 #include <cstdint>
 
@@ -36,6 +37,7 @@ struct Params {
   void *o, *dq, *dkk, *dv_out;
   float *s1, *dg, *dbeta, *ds0;
   // workspace
+  int4* chunks;              // [slot] sequence (-1: none), chunk of it, tokens, first row
   float* sink;               // [64] where lanes without an output write
   float* rows;               // [slot][head][5][kChunk]: exp(c), exp(c_end - c), beta, c (double)
   float* decay;              // [slot][head][dk] exp(c_end) (per-channel gates)

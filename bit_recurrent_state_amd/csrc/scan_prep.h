@@ -15,7 +15,7 @@ template <int DK>
 __global__ void __launch_bounds__(256) operands_kernel(Params p, int backward) {
   const int slot = blockIdx.x, hq = blockIdx.y;
   Chunk c;
-  if (!find_chunk(p, slot, c)) return;
+  if (!find_and_note(p, slot, hq == 0, c)) return;
   const bool vec = p.mixer == GLA || p.mixer == KDA;
   const int terms = vec ? (p.dtype == 1 ? 1 : P) : p.terms;
   const int64_t sh = (int64_t)slot * p.heads_qk + hq;
@@ -257,11 +257,23 @@ __global__ void __launch_bounds__(256) chunk_kernel(Params p) {
   __shared__ __align__(16) float M2[DELTA && BWD ? C : 1][C + 4];
   const int slot = blockIdx.x, h = blockIdx.y;
   Chunk c;
-  if (!find_chunk(p, slot, c)) return;
+  if (!noted_chunk(p, slot, c)) return;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t sh = (int64_t)slot * p.heads + h;
   if (BWD) store_dop(p, c, sh, h);
   if (VEC && p.far[sh]) return;
+  constexpr bool D = NPQ == 1;
+  const auto q = rows_of<DK, D>(p, p.q, p.qrow, p.qs, VEC, slot, h, c);
+  const auto k = rows_of<DK, D>(p, p.k, VEC ? p.knrow : p.krow, p.ks, VEC, slot, h, c);
+  const auto ki = rows_of<DK, D>(p, p.k, p.krow, p.ks, VEC, slot, h, c);  // the reading key of L
+  const int fr = lane & 15;
+  const int own = wave * 16 + fr;  // forward: token i; backward: token j
+  Frag<NPQ> fm[DK / 32], fk[DK / 32];
+#pragma unroll
+  for (int s = 0; s < DK / 32; ++s) {
+    fm[s] = BWD ? k.template frag<NPQ>(wave, s) : q.template frag<NPQ>(wave, s);
+    if (DELTA) fk[s] = BWD ? fm[s] : ki.template frag<NPQ>(wave, s);
+  }
   if (VEC && wave == 0) bs[lane] = rows_at(p, slot, h)[2 * C + lane];
   if (!VEC && wave == 0) {
     const bool in = lane < c.len;
@@ -282,18 +294,6 @@ __global__ void __launch_bounds__(256) chunk_kernel(Params p) {
     reinterpret_cast<double*>(r + 3 * C)[lane] = s;
   }
   __syncthreads();
-  constexpr bool D = NPQ == 1;
-  const auto q = rows_of<DK, D>(p, p.q, p.qrow, p.qs, VEC, slot, h, c);
-  const auto k = rows_of<DK, D>(p, p.k, VEC ? p.knrow : p.krow, p.ks, VEC, slot, h, c);
-  const auto ki = rows_of<DK, D>(p, p.k, p.krow, p.ks, VEC, slot, h, c);  // the reading key of L
-  const int fr = lane & 15;
-  const int own = wave * 16 + fr;  // forward: token i; backward: token j
-  Frag<NPQ> fm[DK / 32], fk[DK / 32];
-#pragma unroll
-  for (int s = 0; s < DK / 32; ++s) {
-    fm[s] = BWD ? k.template frag<NPQ>(wave, s) : q.template frag<NPQ>(wave, s);
-    if (DELTA) fk[s] = BWD ? fm[s] : ki.template frag<NPQ>(wave, s);
-  }
   // tile (wave, b): columns own (i forward, j backward), rows of block b
   for (int b = 0; b < 4; ++b) {
     f32x4 acc = {0, 0, 0, 0}, acl = {0, 0, 0, 0};
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(256) operands_vector_kernel(Params p) {
   __shared__ __align__(16) float tot[4][DK];
   const int slot = blockIdx.x, h = blockIdx.y;
   Chunk c;
-  if (!find_chunk(p, slot, c)) return;
+  if (!(BWD ? noted_chunk(p, slot, c) : find_and_note(p, slot, h == 0, c))) return;
   const int64_t sh = (int64_t)slot * p.heads + h;
   const int hq = h / (p.heads / p.heads_qk);
   const bool qeven = p.qs % 4 == 0, keven = p.ks % 4 == 0;
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(256) chunk_vector_kernel(Params p) {
   __shared__ float bs[C];
   const int slot = blockIdx.x, h = blockIdx.y;
   Chunk c;
-  if (!find_chunk(p, slot, c)) return;
+  if (!noted_chunk(p, slot, c)) return;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t sh = (int64_t)slot * p.heads + h;
   if (!p.far[sh]) return;

@@ -13,13 +13,6 @@
 
 namespace qscan {
 
-__device__ __forceinline__ float sum8(float x) {
-  x += __shfl_xor(x, 1);
-  x += __shfl_xor(x, 2);
-  x += __shfl_xor(x, 4);
-  return x;
-}
-
 template <int DK, bool VEC, bool DELTA>
 __global__ void __launch_bounds__(256) tokens_kernel(Params p) {
   constexpr int Q = DK / 32;  // groups of 4 channels: channel 32 q + 4 (lane & 7)
