@@ -89,7 +89,7 @@ int qstate_norm(const qstate_norm_config* cfg, const void* x, const float* weigh
   const int rc = check_config(cfg);
   if (rc != QSTATE_OK) return rc;
   const size_t e = elem(cfg->dtype);
-  if ((cfg->tokens > 0 && !x) || (!r && !h) || (next_weight && !h)) return QSTATE_E_INVALID;
+  if (cfg->tokens > 0 && (!x || (!r && !h) || (next_weight && !h))) return QSTATE_E_INVALID;
   if (!aligned(x, e) || !aligned(gate, e) || !aligned(residual, e) || !aligned(r, e) ||
       !aligned(h, e) || !aligned(weight, 4) || !aligned(scale, 4) || !aligned(next_weight, 4))
     return QSTATE_E_INVALID;

@@ -25,6 +25,7 @@ struct Params {
   int terms;     // planes of q and k: 1 (direct bfloat16) or kTerms
   int short_len; // sequences up to this length go to tokens_kernel (forward)
   int some_short, some_long;  // whether there may be sequences up to that length, and beyond
+  int out_terms; // terms of what only reaches an output (forward): 2 for 16-bit types
   int nslots;    // upper bound of the slots in use
   int nvb;       // blocks of dv columns of one head
   int vblock;    // dv columns of a block

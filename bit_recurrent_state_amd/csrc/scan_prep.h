@@ -207,6 +207,7 @@ __device__ __forceinline__ void store_inverses(const Params& p, Square* M, Squar
   uint16_t* t1 = p.t + sh * P * C * C;
   for (int u = threadIdx.x; u < C * C / 4; u += 256) {
     const int r = u / (C / 4), q0 = u % (C / 4) * 4;
+    if (r < 32 && q0 >= 32) continue;  // zeros that are not read
     const f32x4 v = *reinterpret_cast<const f32x4*>(&M[r][q0]);
     const float x[4] = {v[0], v[1], v[2], v[3]};
     put4<P>(t1 + tiled<C>(r, q0), C * C, x);
@@ -214,7 +215,9 @@ __device__ __forceinline__ void store_inverses(const Params& p, Square* M, Squar
   if (BWD) {
     uint16_t* t2 = p.t2t + sh * P * C * C;
     for (int u = threadIdx.x; u < C * C / 4; u += 256) {
-      const int r = u % C, q0 = u / C * 4;  // rows by lane: LDS columns are then read without conflicts
+      const int r = u % C, q0 = u / C * 4;
+      if (r >= 32 && q0 < 32) continue;
+      // rows by lane: LDS columns are then read without conflicts
       const float x[4] = {M2[q0][r], M2[q0 + 1][r], M2[q0 + 2][r], M2[q0 + 3][r]};
       put4<P>(t2 + tiled<C>(r, q0), C * C, x);
     }
@@ -319,8 +322,14 @@ __global__ void __launch_bounds__(256) chunk_kernel(Params p) {
         if (BWD) M2[i][j] = i > j ? bs[i] * l : 0.0f;
       }
     }
-    uint16_t* dst = (BWD ? p.at : p.a) + sh * P * C * C;
-    put4<P>(dst + tiled<C>(own, r0), C * C, a);
+    // tiles of 32 columns beside the diagonal that hold only zeros are not read
+    uint16_t* dst = (BWD ? p.at : p.a) + sh * P * C * C + tiled<C>(own, r0);
+    if (BWD ? (b >> 1) >= (wave >> 1) : (b >> 1) <= (wave >> 1)) {
+      if (BWD || p.out_terms == P)
+        put4<P>(dst, C * C, a);
+      else
+        put4<2>(dst, C * C, a);
+    }
   }
   if (DELTA) store_inverses<BWD>(p, M, M2, sh);
 }

@@ -15,10 +15,12 @@ import torch
 
 from ._lib import (BDR, GDN, GLA, KDA, KEY_AXIS, RTN, SCALAR, SR, VALUE_AXIS, QStateConfig, check,
                    lib)
+from .norm import SILU, NormConfig, qstate_norm
+from .scan import scan
 
 __all__ = [
     "GDN", "GLA", "SCALAR", "KDA", "RTN", "SR", "BDR", "VALUE_AXIS", "KEY_AXIS", "Config",
-    "QState",
+    "QState", "ReadoutNorm",
     "qstate_state_bytes", "qstate_create", "qstate_load_fp32", "qstate_step",
     "qstate_readout", "qstate_store_fp32", "qstate_get_step", "qstate_set_step",
     "qstate_destroy", "qstate_bits_by_decay",
@@ -174,6 +176,24 @@ def qstate_bits_by_decay(retention, mode: int, thr_or_frac: float, lo_bits: int 
     return out
 
 
+@dataclass
+class ReadoutNorm:
+    """What a layer does with the readout before its output projection:
+    o * rsqrt(mean(o^2) + eps) * weight * act(gate), over each head's dv values."""
+
+    weight: Optional[torch.Tensor] = None  # float32 [dv] or [heads, dv]
+    gate: Optional[torch.Tensor] = None    # as o
+    eps: float = 1e-6
+    act: int = SILU
+
+    def apply_(self, o: torch.Tensor, stream=None) -> None:
+        """In place on o [tokens, heads, dv]."""
+        each = self.weight is not None and self.weight.dim() == 2
+        cfg = NormConfig(o.shape[0], o.shape[1], o.shape[2], o.dtype, self.act, each, self.eps)
+        gate = None if self.gate is None else self.gate.reshape(o.shape)
+        qstate_norm(cfg, o, self.weight, gate, r=o, stream=stream)
+
+
 class QState:
     """A handle plus the torch device buffers it works on (caller-owned memory)."""
 
@@ -191,8 +211,33 @@ class QState:
     def load_fp32(self, S, stream=None):
         qstate_load_fp32(self.handle, S, self.cfg, stream)
 
-    def step(self, q, k, v, alpha, beta=None, o=None, stream=None):
+    def step(self, q, k, v, alpha, beta=None, o=None, stream=None, norm=None):
+        """One token for every sequence; with `norm` (a ReadoutNorm), o is the normed and gated
+        readout."""
         qstate_step(self.handle, self.cfg, q, k, v, alpha, beta, o, stream)
+        if norm is not None and o is not None:
+            norm.apply_(o.view(self.cfg.batch, self.cfg.heads, self.cfg.dv), stream)
+
+    def prefill(self, q, k, v, log_alpha, beta=None, offsets=None, norm=None):
+        """A prompt's or a chunk's tokens at once, for sequences that decode on with `step`: the
+        scan from the stored state, whose end is stored back (one quantization event for every
+        sequence, those without tokens too: the counter goes up by one, a window starts empty).  Arguments as `scan`'s, one sequence per batch
+        row, q and k with the handle's heads or a divisor of them; returns o."""
+        c = self.cfg
+        if offsets is not None and offsets.numel() != c.batch + 1:
+            raise ValueError(f"offsets: expected {c.batch + 1} elements, got {offsets.numel()}")
+        if v.shape[-2:] != (c.heads, c.dv) or q.shape[-1] != c.dk or (
+                offsets is None and v.shape[0] != c.batch):
+            raise ValueError(f"q {tuple(q.shape)}, v {tuple(v.shape)} do not go with the state "
+                             f"[{c.batch}][{c.heads}][{c.dv}][{c.dk}]")
+        with torch.no_grad(), torch.cuda.device(v.device):
+            S = torch.empty((c.batch, c.heads, c.dv, c.dk), dtype=torch.float32, device=v.device)
+            self.store_fp32(S)
+            o, S = scan(q, k, v, log_alpha, beta, mixer=c.mixer, initial_state=S, offsets=offsets)
+            self.load_fp32(S)
+            if norm is not None:
+                norm.apply_(o.view(-1, c.heads, c.dv))
+        return o
 
     def readout(self, q, o, stream=None):
         qstate_readout(self.handle, self.cfg, q, o, stream)

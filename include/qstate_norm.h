@@ -22,8 +22,8 @@
  *              elements apart (0: groups * width)
  *   weight     float [width], or [groups][width] with weight_groups = 1
  *   scale, next_weight  float [width]
- * r may be the residual's own array, h may be x's own, if rows are packed;
- * otherwise outputs must not overlap inputs.  weight, scale, next_weight may be
+ * r may be the residual's own array, and r or h may be x's own, if rows are
+ * packed; otherwise outputs must not overlap inputs.  weight, scale, next_weight may be
  * NULL (1).  Row pointers are aligned to their type (16-byte aligned rows are
  * read fastest).
  *
