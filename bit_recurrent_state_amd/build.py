@@ -30,7 +30,8 @@ HEADERS = [os.path.join(ROOT, "include", h) for h in ("qstate.h", "qstate_ceilin
     os.path.join(CSRC, h) for h in ("qstate_launch.h", "qstate_device.h", "qstate_value.h",
                                     "qstate_key.h", "qstate_window.h",
                                     "qstate_persist.h", "scan_launch.h", "scan_device.h",
-                                    "scan_prep.h", "scan_chain.h", "scan_grads.h", "scan_tokens.h",
+                                    "scan_prep.h", "scan_prep_vector.h",
+                                    "scan_chain.h", "scan_grads.h", "scan_tokens.h",
                                     "scan_dk.h",
                                     "norm_launch.h")]
 BUILD = os.path.join(ROOT, "_build")

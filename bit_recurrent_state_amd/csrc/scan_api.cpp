@@ -101,12 +101,14 @@ size_t layout(const qstate_scan_config* c, bool backward, void* workspace, Param
   w.take(p.rows, sh * 5 * kChunk, true);
   w.take(p.decay, sh * p.dk, vec);
   w.take(p.far, sh, vec);
-  w.take(p.knrow, ops, vec);
+  const bool fused = vec && !backward && c->dk <= 128;  // scan_prep_vector.h
+  w.take(p.knrow, ops, vec && !fused);
   w.take(p.qrow, ops, !p.direct);
   w.take(p.krow, ops, !p.direct && (!vec || delta));
   w.take(p.kt, ops, true);
   w.take(p.a, square, !backward);
   w.take(p.t, square, delta);
+  w.take(p.u, sh * kChunk * p.dvp, backward || (fused && delta));
   if (backward) {
     const uint64_t raw = sq * (bf16 ? 1 : kTerms) * tile;
     w.take(p.korow, ops, vec);
@@ -121,7 +123,6 @@ size_t layout(const qstate_scan_config* c, bool backward, void* workspace, Param
     w.take(p.t2t, square, delta);
     // d_o's rows serve as they are where they are bfloat16 and fill whole blocks
     w.take(p.dop, sh * p.dop_terms * kChunk * p.dvp, !(bf16 && c->dv % 32 == 0));
-    w.take(p.u, sh * kChunk * p.dvp, true);
     w.take(p.y, sh * kChunk * p.dvp, delta);
     w.take(p.sc, sh * p.dk * p.dvp, true);
     w.take(p.xc, sh * p.dk * p.dvp, true);

@@ -37,15 +37,18 @@ __device__ __forceinline__ bool chain_block(const Params& p, int& n, int& h, int
 // Outputs of 16 bits take PO = 2 terms of q, A, S and W, which hold them to
 // 2^-16; everything that reaches the state takes all three.
 //
+// SOLVED: U0 = T V and K^ = T K~ are given (scan_prep_vector.h), and U = U0 - K^ S^T.
+//
 // SAVE (for the backward pass): four waves, no output; the states at the
 // chunks' starts and U are stored.
-template <int DK, int NT, int NPQ, int PO, bool VEC, bool DELTA, bool SAVE>
+template <int DK, int NT, int NPQ, int PO, bool VEC, bool DELTA, bool SAVE, bool SOLVED>
 __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
   constexpr int BV = 16 * NT, KS = DK / 32, MT = DK / 64, SP = DK + 8;
   constexpr int NQ = NPQ < PO ? NPQ : PO;
   constexpr bool D = NPQ == 1;
   __shared__ __align__(16) uint16_t Sl[P][BV][SP];
-  __shared__ __align__(16) uint16_t Rt[DELTA ? P : 1][DELTA ? BV : 1][CP];
+  constexpr bool TR = DELTA && !SOLVED;  // U = T R is computed here
+  __shared__ __align__(16) uint16_t Rt[TR ? P : 1][TR ? BV : 1][CP];
   __shared__ __align__(16) uint16_t Wt[SAVE || VEC ? 1 : PO][SAVE || VEC ? 1 : BV][CP];
   __shared__ __align__(16) uint16_t Wb[P][BV][CP];  // e^(c_end - c) W (one gate), else W
   int n, h, vb;
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) Q[t][r] *= ec[r];
       load_q(next);
-      if (DELTA) __syncthreads();
+      if (TR) __syncthreads();
       if (ci > 0) store(ci - 1, O);
       __syncthreads();
 #pragma unroll
@@ -172,8 +175,8 @@ __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
       }
   };
   Frag<NPQ> fk[DELTA ? KS : 1], ft[MT][2];
-  Frag<P> fT[DELTA ? 2 : 1];
-  uint32_t v[NT][4];
+  Frag<P> fT[TR ? 2 : 1];
+  uint32_t v[NT][4];  // the values, or U0 as floats
   f32x4 beta, ec = {1, 1, 1, 1}, eo = {1, 1, 1, 1}, dec[MT];
   auto load_k = [&](int ci) {
     const auto k = rows_of<DK, D>(p, p.k, p.krow, p.ks, VEC, base + ci, h, chunk(ci));
@@ -189,6 +192,14 @@ __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
       eo = *reinterpret_cast<const f32x4*>(rows + C + tok);
     }
     // places outside the sequence or the head read a valid neighbour and count as zero later
+    if (SOLVED) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          v[t][r] = __float_as_uint(p.u[head_of(ci) * C * p.dvp + (uint32_t)((tok + r) * p.dvp + vcol[t])]);
+      return;
+    }
     const char* src = static_cast<const char*>(p.v) +
                       (c.row * p.vs + (int64_t)h * p.dv) * (p.dtype == 0 ? 4 : 2);
     uint32_t at[4];
@@ -221,7 +232,7 @@ __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
   if (nch > 0) {
     if (DELTA) load_k(0);
     load_v(0);
-    if (DELTA) load_T(0);
+    if (TR) load_T(0);
     load_kt(0);
   }
   if (DELTA || !SAVE) put_state();
@@ -237,7 +248,8 @@ __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        vf[t][r] = tok + r < c.len && vcol[t] < p.dv ? from_raw(v[t][r], p.dtype) : 0.0f;
+        vf[t][r] = SOLVED ? __uint_as_float(v[t][r])
+                   : tok + r < c.len && vcol[t] < p.dv ? from_raw(v[t][r], p.dtype) : 0.0f;
     if (DELTA) {
       f32x4 kS[NT], kS2[NT];  // two chains of dependent products
 #pragma unroll
@@ -256,9 +268,11 @@ __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
         float x[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) x[r] = fmaf(-ec[r], kS[t][r], vf[t][r]);
-        put4<P>(&Rt[0][t * 16 + fr][tok], BV * CP, x);
-        U[t] = f32x4{0, 0, 0, 0};
+        if (TR) put4<P>(&Rt[0][t * 16 + fr][tok], BV * CP, x);
+        U[t] = TR ? f32x4{0, 0, 0, 0} : f32x4{x[0], x[1], x[2], x[3]};
       }
+    }
+    if (TR) {
       __syncthreads();
 #pragma unroll
       for (int s = 0; s < 2; ++s)
@@ -267,7 +281,8 @@ __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
           for (int t = 0; t < NT; ++t)
             mma(U[t], fT[s], load_frag<P>(&Rt[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
       load_T(next);
-    } else {
+    }
+    if (!DELTA) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) U[t] = f32x4{vf[t][0], vf[t][1], vf[t][2], vf[t][3]};
     }

@@ -6,6 +6,7 @@
 #include "scan_chain.h"
 #include "scan_grads.h"
 #include "scan_prep.h"
+#include "scan_prep_vector.h"
 #include "scan_tokens.h"
 
 namespace qscan {
@@ -23,7 +24,12 @@ hipError_t forward_tail(const Params& p, hipStream_t s) {
     tokens_kernel<DK, VEC, DELTA><<<rows, 256, 0, s>>>(p);
     if (!p.some_long) return hipGetLastError();
   }
-  if (VEC) {
+  constexpr bool SOLVED = VEC && DELTA && DK <= 128;
+  if constexpr (VEC && DK <= 128) {
+    prep_vector_kernel<DK, PO, DELTA, false><<<slots, 512, 0, s>>>(p);
+    chunk_vector_kernel<DK, DELTA, false><<<slots, 256, 0, s>>>(p);
+    if (DELTA) prep_vector_kernel<DK, PO, DELTA, true><<<slots, 512, 0, s>>>(p);
+  } else if constexpr (VEC) {
     operands_vector_kernel<DK, DELTA, false><<<slots, 256, 0, s>>>(p);
     chunk_kernel<DK, P, true, DELTA, false><<<slots, 256, 0, s>>>(p);
     chunk_vector_kernel<DK, DELTA, false><<<slots, 256, 0, s>>>(p);
@@ -31,7 +37,7 @@ hipError_t forward_tail(const Params& p, hipStream_t s) {
     operands_kernel<DK><<<dim3(p.nslots, p.heads_qk), 256, 0, s>>>(p, 0);
     chunk_kernel<DK, NPQ, false, DELTA, false><<<slots, 256, 0, s>>>(p);
   }
-  states_kernel<DK, NT, NPQ, PO, VEC, DELTA, false><<<chain_grid(p), 512, 0, s>>>(p);
+  states_kernel<DK, NT, NPQ, PO, VEC, DELTA, false, SOLVED><<<chain_grid(p), 512, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -48,7 +54,7 @@ hipError_t backward_tail(const Params& p, hipStream_t s) {
       chunk_kernel<DK, NPQ, false, DELTA, true><<<slots, 256, 0, s>>>(p);
     }
   }
-  states_kernel<DK, NT, NPQ, P, VEC, DELTA, true><<<chain_grid(p), 256, 0, s>>>(p);
+  states_kernel<DK, NT, NPQ, P, VEC, DELTA, true, false><<<chain_grid(p), 256, 0, s>>>(p);
   state_grads_kernel<DK, NT, NPQ, NPO, VEC, DELTA><<<chain_grid(p), 512, 0, s>>>(p);
   grads_kernel<DK, NPQ, VEC ? NPO : NPQ, NPO, VEC, DELTA>
       <<<slots, DK >= 128 ? 512 : 256, 0, s>>>(p);

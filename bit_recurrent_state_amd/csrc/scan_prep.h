@@ -134,13 +134,14 @@ __device__ __forceinline__ void block_store(Square* X, int rb, int cb, const f32
 }
 
 // N matrices M (their strict lower triangles set, the rest zero), overwritten
-// by the inverses.  All four waves call this, with M complete in LDS.
+// by the inverses.  All waves (four or eight) call this, with M complete in LDS.
 template <int N>
 __device__ __forceinline__ void invert(Square* M0, Square* M1) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int col = lane & 15, g = lane >> 4;
   {
     const Square* M = N == 2 && (g & 1) ? M1 : M0;
+    const int wave = threadIdx.x >> 6 & 3;  // waves beyond four repeat the first four's work
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {

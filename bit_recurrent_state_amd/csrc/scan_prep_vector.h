@@ -1,0 +1,276 @@
+// scan_prep_vector.h — the forward pass's preparation with a gate per key
+// channel, dk up to 128: scaled operands, A, and for the delta rule the chunk
+// solved in advance.
+//
+// With R = V - K~ S^T and U = T R, U = U0 - K^ S^T where U0 = T V and K^ = T K~
+// do not wait for the state.  The chain then has one product and one barrier
+// less a chunk, at the same bytes: K^ takes the place of K~ = k e^c, U0 that of T.
+//
+// One workgroup of eight waves per (slot, head).  Waves 0..3 take the rows of q
+// (block `wave`) and A, waves 4..7 those of k, L and T: the rows they scale are
+// the fragments they multiply.  Only k e^-c goes through LDS.  Chunks that decay
+// far leave A and L to their own kernel (scan_prep.h) and are solved here after
+// it has run (`solve` alone).
+
+#pragma once
+
+#include "scan_prep.h"
+
+namespace qscan {
+
+// K^ and U0 from T, FP32 in LDS: a wave takes 16 channels (of K~^T, in its
+// registers) and 16 value columns at a time.  Results come with four channels or
+// columns of a token in a lane.
+template <int DK>
+__device__ __forceinline__ void solve(const Params& p, const Chunk& c, int64_t sh, int h,
+                                      const Square* T, const Frag<P> (&kt)[2]) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int fr = lane & 15, fg = lane >> 4;
+  auto t_frag = [&](int rb, int s) {
+    float x[8];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(&T[rb * 16 + fr][s * 32 + fg * 8 + 4 * q]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[4 * q + e] = v[e];
+    }
+    return split8<P>(x);
+  };
+  const int vb = p.dvp / 16;
+  for (int b = wave; b < vb; b += 8) {
+    // V^T: 8 tokens of a column
+    const int v = min(b * 16 + fr, p.dv - 1);
+    Frag<P> f[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      int64_t at[8];
+      uint32_t raw[8];
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        at[e] = (c.row + min(s * 32 + fg * 8 + e, c.len - 1)) * p.vs + (int64_t)h * p.dv + v;
+      load_raw<8>(p.v, at, p.dtype, raw);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        x[e] = s * 32 + fg * 8 + e < c.len && b * 16 + fr < p.dv ? from_raw(raw[e], p.dtype) : 0.0f;
+      f[s] = split8<P>(x);
+    }
+#pragma unroll
+    for (int rb = 0; rb < 4; ++rb) {
+      f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (s <= rb / 2) mma(acc, f[s], t_frag(rb, s));
+      *reinterpret_cast<f32x4*>(p.u + (sh * C + rb * 16 + fr) * p.dvp + b * 16 + fg * 4) = acc;
+    }
+  }
+  if (wave < DK / 16) {
+#pragma unroll
+    for (int rb = 0; rb < 4; ++rb) {
+      f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (s <= rb / 2) mma(acc, kt[s], t_frag(rb, s));
+      const float x[4] = {acc[0], acc[1], acc[2], acc[3]};
+      put4<P>(p.krow + sh * P * C * DK + tiled<DK>(rb * 16 + fr, wave * 16 + fg * 4), C * DK, x);
+    }
+  }
+}
+
+// FAR: only chunks that decay far, whose T chunk_vector_kernel has left in p.t;
+// otherwise everything, but for those chunks no A, L, T and what follows.
+template <int DK, int PO, bool DELTA, bool FAR>
+__global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
+  constexpr int LP = DK + 4, KS = DK / 32;
+  constexpr int kPre = C * LP > C * (C + 4) ? C * LP : C * (C + 4);
+  __shared__ __align__(16) float buf[kPre];  // sums of log decays in blocks of 16; then M and T
+  __shared__ __align__(16) uint16_t Kn[P][C * DK];
+  __shared__ __align__(16) float tot[4][DK];
+  __shared__ float bs[C];
+  float(*pre)[LP] = reinterpret_cast<float(*)[LP]>(buf);
+  Square* M = reinterpret_cast<Square*>(buf);
+  const int slot = blockIdx.x, h = blockIdx.y;
+  Chunk c;
+  if (!(FAR ? noted_chunk(p, slot, c) : find_and_note(p, slot, h == 0, c))) return;
+  const int64_t sh = (int64_t)slot * p.heads + h;
+  if (FAR && !p.far[sh]) return;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, rb = wave & 3;
+  const int fr = lane & 15, fg = lane >> 4;
+  const int hq = h / (p.heads / p.heads_qk);
+  const bool qeven = p.qs % 4 == 0, keven = p.ks % 4 == 0;
+  for (int u = threadIdx.x; u < DK * 4; u += 512) {
+    const int ch = u % DK, t0 = u / DK * 16;
+    float g[16], s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      g[i] = p.g[((c.row + min(t0 + i, c.len - 1)) * p.heads + h) * DK + ch];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s += t0 + i < c.len ? gate(g[i]) : 0.0f;
+      pre[t0 + i][ch] = s;
+    }
+    tot[u / DK][ch] = s;
+  }
+  if (threadIdx.x < C) {
+    const int t = threadIdx.x;
+    const float b = t < c.len ? (p.beta ? p.beta[(c.row + t) * p.heads + h] : 1.0f) : 0.0f;
+    bs[t] = b;
+    rows_at(p, slot, h)[2 * C + t] = b;
+  }
+  __syncthreads();
+  bool over = false;
+  if (!FAR && threadIdx.x < DK) {
+    const int ch = threadIdx.x;
+    const float all = (tot[0][ch] + tot[1][ch]) + (tot[2][ch] + tot[3][ch]);
+    p.decay[sh * DK + ch] = fast_exp(all);
+    over = !(all >= -kFarDecay);
+  }
+  const bool far = FAR || __syncthreads_or(over);
+  if (!FAR && threadIdx.x == 0) p.far[sh] = far;
+
+  // columns of k: a wave's 16 channels, both halves of the tokens
+  Frag<P> kt[2];
+  if (wave < DK / 16) {
+    const int ch = wave * 16 + fr;
+    const float t4[4] = {tot[0][ch], tot[1][ch], tot[2][ch], tot[3][ch]};
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int t0 = s * 32 + fg * 8, b = t0 >> 4;
+      int64_t at[8];
+      uint32_t raw[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) at[i] = (c.row + min(t0 + i, c.len - 1)) * p.ks + (int64_t)hq * DK + ch;
+      load_raw<8>(p.k, at, p.dtype, raw);
+      float before = 0.0f, after = 0.0f;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        if (m < b) before += t4[m];
+        if (m > b) after += t4[m];
+      }
+      // decays from a token to the end of its block: the block's less the token's, summed again
+      // from the gates where that would cancel
+      float sfx[8];
+      if (far) {
+        const int e0 = b * 16 + 16;
+        float s2 = 0.0f;
+        for (int i = e0 - 1; i > t0 + 7; --i)
+          s2 += i < c.len ? gate(p.g[((c.row + i) * p.heads + h) * DK + ch]) : 0.0f;
+#pragma unroll
+        for (int i = 7; i >= 0; --i) {
+          sfx[i] = s2;
+          s2 += t0 + i < c.len ? gate(p.g[((c.row + t0 + i) * p.heads + h) * DK + ch]) : 0.0f;
+        }
+      } else {
+        const float block = b == 0 ? t4[0] : b == 1 ? t4[1] : b == 2 ? t4[2] : t4[3];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sfx[i] = block - pre[t0 + i][ch];
+      }
+      float ko[8], ke[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float k = t0 + i < c.len ? from_raw(raw[i], p.dtype) : 0.0f;
+        ko[i] = k * fast_exp(sfx[i] + after);
+        if (DELTA) ke[i] = k * fast_exp(pre[t0 + i][ch] + before);
+      }
+      if (DELTA) kt[s] = split8<P>(ke);
+      if (!FAR) {
+        const Frag<P> f = split8<P>(ko);
+#pragma unroll
+        for (int n = 0; n < P; ++n)
+          *reinterpret_cast<u32x4*>(p.kt + (sh * P + n) * C * DK + (wave * 2 + s) * 512 + lane * 8) = f.t[n];
+      }
+    }
+  }
+  if (FAR) {
+    if (DELTA) {
+      __syncthreads();
+      const uint16_t* t = p.t + sh * P * C * C;
+      for (int u = threadIdx.x; u < C * C; u += 512) {
+        const int r = u / C, q = u % C;
+        float x = 0.0f;
+        if (r >= 32 || q < 32)
+#pragma unroll
+          for (int n = P - 1; n >= 0; --n) x += bf16_to_f(t[n * C * C + tiled<C>(r, q)]);
+        M[r][q] = x;
+      }
+      __syncthreads();
+      solve<DK>(p, c, sh, h, M, kt);
+    }
+    return;
+  }
+
+  // rows: block rb of q (waves 0..3) or k (4..7)
+  const bool second = wave >= 4;
+  const int t = rb * 16 + fr;
+  const int64_t row = c.row + min(t, c.len - 1);
+  const float in = t < c.len ? 1.0f : 0.0f;
+  Frag<P> own[KS];
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    const int ch = s * 32 + fg * 8;
+    float xe[8], xn[8];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      float x[4];
+      if (second)
+        load4(p.k, row * p.ks + (int64_t)hq * DK + ch + 4 * q, p.dtype, keven, x);
+      else
+        load4(p.q, row * p.qs + (int64_t)hq * DK + ch + 4 * q, p.dtype, qeven, x);
+      f32x4 cs = *reinterpret_cast<const f32x4*>(&pre[t][ch + 4 * q]);
+#pragma unroll
+      for (int m = 0; m < 3; ++m)
+        if (m < rb) cs += *reinterpret_cast<const f32x4*>(&tot[m][ch + 4 * q]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        xe[4 * q + i] = in * x[i] * fast_exp(cs[i]);
+        xn[4 * q + i] = far ? 0.0f : in * x[i] * fast_exp(-cs[i]);
+      }
+    }
+    own[s] = split8<P>(xe);
+    if (second) {
+      const Frag<P> f = split8<P>(xn);
+#pragma unroll
+      for (int n = 0; n < P; ++n)
+        *reinterpret_cast<u32x4*>(&Kn[n][(rb * KS + s) * 512 + lane * 8]) = f.t[n];
+    } else {
+#pragma unroll
+      for (int n = 0; n < PO; ++n)
+        *reinterpret_cast<u32x4*>(p.qrow + (sh * P + n) * C * DK + (rb * KS + s) * 512 + lane * 8) =
+            own[s].t[n];
+    }
+  }
+  __syncthreads();  // k e^-c is there, and the sums have been read
+  if (far) return;
+  for (int b = 0; b < 4; ++b) {
+    f32x4 acc = {0, 0, 0, 0};
+    if (b <= rb && (DELTA || !second)) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const Frag<P> f = tile_frag<P, DK>(&Kn[0][0], b, s, C * DK);
+        if (second)
+          mma(acc, f, own[s]);
+        else
+          mma(acc, head<PO>(f), head<PO>(own[s]));
+      }
+    }
+    const int i = rb * 16 + fr, j0 = b * 16 + fg * 4;
+    float x[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int j = j0 + r;
+      x[r] = second ? (i > j ? acc[r] * bs[j] : 0.0f) : (i >= j ? acc[r] : 0.0f);
+    }
+    if (second) {
+      if (DELTA) *reinterpret_cast<f32x4*>(&M[i][j0]) = f32x4{x[0], x[1], x[2], x[3]};
+    } else if ((b >> 1) <= (rb >> 1)) {
+      put4<PO>(p.a + sh * P * C * C + tiled<C>(i, j0), C * C, x);
+    }
+  }
+  if (DELTA) {
+    __syncthreads();
+    invert<1>(M, M);
+    solve<DK>(p, c, sh, h, M, kt);
+  }
+}
+
+}  // namespace qscan
