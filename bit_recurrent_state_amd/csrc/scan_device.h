@@ -43,16 +43,23 @@ __device__ __forceinline__ int64_t offset_of(const Params& p, int n) {
 __device__ __forceinline__ bool find_chunk(const Params& p, int slot, Chunk& c) {
   const int lane = threadIdx.x & 63;
   int lo = 0, hi = p.batch;
-  while (hi - lo > 1) {
+  int64_t o0, o1;
+  for (;;) {
     const int step = (hi - lo + 63) / 64;
     const int64_t at = lo + (int64_t)lane * step;
-    const bool le = at < hi && offset_of(p, (int)at) / C + at <= slot;
+    // one probe past the end: it is the last sequence's end
+    const int64_t o = offset_of(p, (int)(at < p.batch ? at : p.batch));
+    const bool le = at < hi && o / C + at <= slot;
     const int count = __popcll(__ballot(le));
     if (count == 0) return false;
     lo += (count - 1) * step;
+    if (step == 1) {
+      o0 = __shfl(o, count - 1);
+      o1 = count < 64 ? __shfl(o, count) : offset_of(p, lo + 1);
+      break;
+    }
     hi = hi < lo + step ? hi : lo + step;
   }
-  const int64_t o0 = offset_of(p, lo), o1 = offset_of(p, lo + 1);
   const int64_t ci = slot - (o0 / C + lo);
   const int64_t left = o1 - o0 - ci * C;
   if (ci < 0 || left <= 0 || o1 - o0 <= p.short_len) return false;

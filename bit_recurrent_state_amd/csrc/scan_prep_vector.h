@@ -18,43 +18,43 @@
 
 namespace qscan {
 
-// K^ and U0 from T, FP32 in LDS: a wave takes 16 channels (of K~^T, in its
+// V^T of 16 value columns: 8 tokens of a column, both halves of the chunk.
+__device__ __forceinline__ void load_columns(const Params& p, const Chunk& c, int h, int b,
+                                             uint32_t (&raw)[2][8]) {
+  const int lane = threadIdx.x & 63;
+  const int v = min(b * 16 + (lane & 15), p.dv - 1);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    int64_t at[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      at[e] = (c.row + min(s * 32 + (lane >> 4) * 8 + e, c.len - 1)) * p.vs + (int64_t)h * p.dv + v;
+    load_raw<8>(p.v, at, p.dtype, raw[s]);
+  }
+}
+
+// K^ and U0 from T's terms in LDS: a wave takes 16 channels (of K~^T, in its
 // registers) and 16 value columns at a time.  Results come with four channels or
 // columns of a token in a lane.
 template <int DK>
 __device__ __forceinline__ void solve(const Params& p, const Chunk& c, int64_t sh, int h,
-                                      const Square* T, const Frag<P> (&kt)[2]) {
+                                      const uint16_t* T, const Frag<P> (&kt)[2],
+                                      uint32_t (&raw)[2][8]) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int fr = lane & 15, fg = lane >> 4;
-  auto t_frag = [&](int rb, int s) {
-    float x[8];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const f32x4 v = *reinterpret_cast<const f32x4*>(&T[rb * 16 + fr][s * 32 + fg * 8 + 4 * q]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[4 * q + e] = v[e];
-    }
-    return split8<P>(x);
-  };
+  auto t_frag = [&](int rb, int s) { return tile_frag<P, C>(T, rb, s, C * C); };
   const int vb = p.dvp / 16;
   for (int b = wave; b < vb; b += 8) {
-    // V^T: 8 tokens of a column
-    const int v = min(b * 16 + fr, p.dv - 1);
     Frag<P> f[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      int64_t at[8];
-      uint32_t raw[8];
       float x[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        at[e] = (c.row + min(s * 32 + fg * 8 + e, c.len - 1)) * p.vs + (int64_t)h * p.dv + v;
-      load_raw<8>(p.v, at, p.dtype, raw);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        x[e] = s * 32 + fg * 8 + e < c.len && b * 16 + fr < p.dv ? from_raw(raw[e], p.dtype) : 0.0f;
+        x[e] = s * 32 + fg * 8 + e < c.len && b * 16 + fr < p.dv ? from_raw(raw[s][e], p.dtype) : 0.0f;
       f[s] = split8<P>(x);
     }
+    if (b + 8 < vb) load_columns(p, c, h, b + 8, raw);
 #pragma unroll
     for (int rb = 0; rb < 4; ++rb) {
       f32x4 acc = {0, 0, 0, 0};
@@ -98,6 +98,35 @@ __global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
   const int fr = lane & 15, fg = lane >> 4;
   const int hq = h / (p.heads / p.heads_qk);
   const bool qeven = p.qs % 4 == 0, keven = p.ks % 4 == 0;
+  // everything that comes from the caller's arrays is on its way before the first sum
+  const bool second = wave >= 4;
+  const int t = rb * 16 + fr;
+  uint32_t rk[2][8], rv[2][8];
+  float rx[KS][2][4];
+  if (wave < DK / 16) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      int64_t at[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        at[i] = (c.row + min(s * 32 + fg * 8 + i, c.len - 1)) * p.ks + (int64_t)hq * DK + wave * 16 + fr;
+      load_raw<8>(p.k, at, p.dtype, rk[s]);
+    }
+  }
+  if (!FAR) {
+    const int64_t row = c.row + min(t, c.len - 1);
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int64_t at = (int64_t)hq * DK + s * 32 + fg * 8 + 4 * q;
+        if (second)
+          load4(p.k, row * p.ks + at, p.dtype, keven, rx[s][q]);
+        else
+          load4(p.q, row * p.qs + at, p.dtype, qeven, rx[s][q]);
+      }
+  }
+  if (DELTA && wave < p.dvp / 16) load_columns(p, c, h, wave, rv);
   for (int u = threadIdx.x; u < DK * 4; u += 512) {
     const int ch = u % DK, t0 = u / DK * 16;
     float g[16], s = 0.0f;
@@ -136,11 +165,6 @@ __global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const int t0 = s * 32 + fg * 8, b = t0 >> 4;
-      int64_t at[8];
-      uint32_t raw[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) at[i] = (c.row + min(t0 + i, c.len - 1)) * p.ks + (int64_t)hq * DK + ch;
-      load_raw<8>(p.k, at, p.dtype, raw);
       float before = 0.0f, after = 0.0f;
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
@@ -168,7 +192,7 @@ __global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
       float ko[8], ke[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float k = t0 + i < c.len ? from_raw(raw[i], p.dtype) : 0.0f;
+        const float k = t0 + i < c.len ? from_raw(rk[s][i], p.dtype) : 0.0f;
         ko[i] = k * fast_exp(sfx[i] + after);
         if (DELTA) ke[i] = k * fast_exp(pre[t0 + i][ch] + before);
       }
@@ -183,26 +207,16 @@ __global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
   }
   if (FAR) {
     if (DELTA) {
+      const uint16_t* from = p.t + sh * P * C * C;
+      for (int u = threadIdx.x; u < P * C * C / 8; u += 512)
+        reinterpret_cast<u32x4*>(&Kn[0][0])[u] = reinterpret_cast<const u32x4*>(from)[u];
       __syncthreads();
-      const uint16_t* t = p.t + sh * P * C * C;
-      for (int u = threadIdx.x; u < C * C; u += 512) {
-        const int r = u / C, q = u % C;
-        float x = 0.0f;
-        if (r >= 32 || q < 32)
-#pragma unroll
-          for (int n = P - 1; n >= 0; --n) x += bf16_to_f(t[n * C * C + tiled<C>(r, q)]);
-        M[r][q] = x;
-      }
-      __syncthreads();
-      solve<DK>(p, c, sh, h, M, kt);
+      solve<DK>(p, c, sh, h, &Kn[0][0], kt, rv);
     }
     return;
   }
 
   // rows: block rb of q (waves 0..3) or k (4..7)
-  const bool second = wave >= 4;
-  const int t = rb * 16 + fr;
-  const int64_t row = c.row + min(t, c.len - 1);
   const float in = t < c.len ? 1.0f : 0.0f;
   Frag<P> own[KS];
 #pragma unroll
@@ -211,19 +225,19 @@ __global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
     float xe[8], xn[8];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      float x[4];
-      if (second)
-        load4(p.k, row * p.ks + (int64_t)hq * DK + ch + 4 * q, p.dtype, keven, x);
-      else
-        load4(p.q, row * p.qs + (int64_t)hq * DK + ch + 4 * q, p.dtype, qeven, x);
+      const float(&x)[4] = rx[s][q];
       f32x4 cs = *reinterpret_cast<const f32x4*>(&pre[t][ch + 4 * q]);
 #pragma unroll
       for (int m = 0; m < 3; ++m)
         if (m < rb) cs += *reinterpret_cast<const f32x4*>(&tot[m][ch + 4 * q]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        xe[4 * q + i] = in * x[i] * fast_exp(cs[i]);
-        xn[4 * q + i] = far ? 0.0f : in * x[i] * fast_exp(-cs[i]);
+        const float e = fast_exp(cs[i]);
+        xe[4 * q + i] = in * x[i] * e;
+        if (second) {  // 1 / e, refined once
+          const float r = __builtin_amdgcn_rcpf(e);
+          xn[4 * q + i] = far ? 0.0f : in * x[i] * fmaf(fmaf(-e, r, 1.0f), r, r);
+        }
       }
     }
     own[s] = split8<P>(xe);
@@ -269,7 +283,18 @@ __global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
   if (DELTA) {
     __syncthreads();
     invert<1>(M, M);
-    solve<DK>(p, c, sh, h, M, kt);
+    {  // T's terms over k e^-c, as tiles: 8 columns a thread
+      const int tile = threadIdx.x >> 6;
+      const f32x4* src = reinterpret_cast<const f32x4*>(&M[tile / 2 * 16 + fr][tile % 2 * 32 + fg * 8]);
+      const f32x4 a = src[0], b = src[1];
+      const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+      const Frag<P> f = split8<P>(x);
+#pragma unroll
+      for (int n = 0; n < P; ++n)
+        *reinterpret_cast<u32x4*>(&Kn[0][0] + n * C * C + threadIdx.x * 8) = f.t[n];
+    }
+    __syncthreads();
+    solve<DK>(p, c, sh, h, &Kn[0][0], kt, rv);
   }
 }
 
