@@ -164,35 +164,30 @@ __device__ __forceinline__ float fast_exp(float x) {
   return fmaf(e, r * 0.693147182f, e);
 }
 
-// Four neighbouring elements; `even`: they are aligned to four.
-__device__ __forceinline__ void load4(const void* p, int64_t at, int dtype, bool even,
-                                      float (&x)[4]) {
-  uint32_t w[4];
+// Four neighbouring elements as they lie in memory (16-bit ones two to a word),
+// and their values; `even`: they are aligned to four.  In two steps for the
+// same reason as load_raw.
+__device__ __forceinline__ u32x4 load4(const void* p, int64_t at, int dtype, bool even) {
   if (dtype == 0) {
     const uint32_t* s = static_cast<const uint32_t*>(p) + at;
-    if (even) {
-      const u32x4 v = *reinterpret_cast<const u32x4*>(s);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = v[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = s[i];
-    }
-  } else {
-    const uint16_t* s = static_cast<const uint16_t*>(p) + at;
-    if (even) {
-      const u32x2 v = *reinterpret_cast<const u32x2*>(s);
-      w[0] = v.x & 0xFFFFu;
-      w[1] = v.x >> 16;
-      w[2] = v.y & 0xFFFFu;
-      w[3] = v.y >> 16;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = s[i];
-    }
+    return even ? *reinterpret_cast<const u32x4*>(s) : u32x4{s[0], s[1], s[2], s[3]};
   }
+  const uint16_t* s = static_cast<const uint16_t*>(p) + at;
+  u32x2 w;
+  if (even)
+    w = *reinterpret_cast<const u32x2*>(s);
+  else
+    w = u32x2{s[0] | (uint32_t)s[1] << 16, s[2] | (uint32_t)s[3] << 16};
+  return u32x4{w.x, w.y, 0, 0};
+}
+
+__device__ __forceinline__ void widen4(const u32x4& w, int dtype, float (&x)[4]) {
+  const uint32_t words = dtype == 0 ? ~0u : 0u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = from_raw(w[i], dtype);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t half = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
+    x[i] = from_raw((w[i] & words) | (half & ~words), dtype);
+  }
 }
 
 // The same without a branch: places that are not `ok` go to the sink.  Loads

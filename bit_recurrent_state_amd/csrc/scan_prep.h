@@ -399,8 +399,8 @@ __global__ void __launch_bounds__(256) operands_vector_kernel(Params p) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       float x[4], y[4];
-      load4(p.q, row * p.qs + (int64_t)hq * DK + ch + 4 * q, p.dtype, qeven, x);
-      load4(p.k, row * p.ks + (int64_t)hq * DK + ch + 4 * q, p.dtype, keven, y);
+      widen4(load4(p.q, row * p.qs + (int64_t)hq * DK + ch + 4 * q, p.dtype, qeven), p.dtype, x);
+      widen4(load4(p.k, row * p.ks + (int64_t)hq * DK + ch + 4 * q, p.dtype, keven), p.dtype, y);
       f32x4 cs = *reinterpret_cast<const f32x4*>(&pre[t][ch + 4 * q]);
       f32x4 se = *reinterpret_cast<const f32x4*>(&suf[t][ch + 4 * q]);
 #pragma unroll

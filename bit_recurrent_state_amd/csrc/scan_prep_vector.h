@@ -97,12 +97,11 @@ __global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, rb = wave & 3;
   const int fr = lane & 15, fg = lane >> 4;
   const int hq = h / (p.heads / p.heads_qk);
-  const bool qeven = p.qs % 4 == 0, keven = p.ks % 4 == 0;
   // everything that comes from the caller's arrays is on its way before the first sum
-  const bool second = wave >= 4;
+  const bool second = wave >= 4, even = (second ? p.ks : p.qs) % 4 == 0;
   const int t = rb * 16 + fr;
   uint32_t rk[2][8], rv[2][8];
-  float rx[KS][2][4];
+  u32x4 rx[KS][2];
   if (wave < DK / 16) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -120,10 +119,7 @@ __global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const int64_t at = (int64_t)hq * DK + s * 32 + fg * 8 + 4 * q;
-        if (second)
-          load4(p.k, row * p.ks + at, p.dtype, keven, rx[s][q]);
-        else
-          load4(p.q, row * p.qs + at, p.dtype, qeven, rx[s][q]);
+        rx[s][q] = load4(second ? p.k : p.q, row * (second ? p.ks : p.qs) + at, p.dtype, even);
       }
   }
   if (DELTA && wave < p.dvp / 16) load_columns(p, c, h, wave, rv);
@@ -225,7 +221,8 @@ __global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
     float xe[8], xn[8];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const float(&x)[4] = rx[s][q];
+      float x[4];
+      widen4(rx[s][q], p.dtype, x);
       f32x4 cs = *reinterpret_cast<const f32x4*>(&pre[t][ch + 4 * q]);
 #pragma unroll
       for (int m = 0; m < 3; ++m)
@@ -255,18 +252,25 @@ __global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
   }
   __syncthreads();  // k e^-c is there, and the sums have been read
   if (far) return;
-  for (int b = 0; b < 4; ++b) {
-    f32x4 acc = {0, 0, 0, 0};
-    if (b <= rb && (DELTA || !second)) {
+  f32x4 all[4];
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const Frag<P> f = tile_frag<P, DK>(&Kn[0][0], b, s, C * DK);
-        if (second)
-          mma(acc, f, own[s]);
-        else
-          mma(acc, head<PO>(f), head<PO>(own[s]));
-      }
-    }
+  for (int b = 0; b < 4; ++b) all[b] = f32x4{0, 0, 0, 0};
+  if (DELTA || !second) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (b <= rb) {
+          const Frag<P> f = tile_frag<P, DK>(&Kn[0][0], b, s, C * DK);
+          if (second)
+            mma(all[b], f, own[s]);
+          else
+            mma(all[b], head<PO>(f), head<PO>(own[s]));
+        }
+  }
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const f32x4 acc = all[b];
     const int i = rb * 16 + fr, j0 = b * 16 + fg * 4;
     float x[4];
 #pragma unroll

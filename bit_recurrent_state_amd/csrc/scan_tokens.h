@@ -35,15 +35,16 @@ __global__ void __launch_bounds__(256) tokens_kernel(Params p) {
   for (int q = 0; q < Q; ++q)
     S[q] = p.s0 ? *reinterpret_cast<const f32x4*>(p.s0 + st + 32 * q) : f32x4{0, 0, 0, 0};
   // a token's inputs, loaded one token ahead
-  float k[Q][4], x[Q][4], ga = 0.0f, beta = 1.0f;
+  u32x4 k[Q], x[Q];
+  float ga = 0.0f, beta = 1.0f;
   f32x4 g[VEC ? Q : 1];
   uint32_t vr[1];
   auto load = [&](int i) {
     const int64_t row = o0 + i;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      load4(p.k, row * p.ks + (int64_t)hq * DK + 32 * q + 4 * l, p.dtype, keven, k[q]);
-      load4(p.q, row * p.qs + (int64_t)hq * DK + 32 * q + 4 * l, p.dtype, qeven, x[q]);
+      k[q] = load4(p.k, row * p.ks + (int64_t)hq * DK + 32 * q + 4 * l, p.dtype, keven);
+      x[q] = load4(p.q, row * p.qs + (int64_t)hq * DK + 32 * q + 4 * l, p.dtype, qeven);
       if (VEC)
         g[q] = *reinterpret_cast<const f32x4*>(p.g + (row * p.heads + h) * DK + 32 * q + 4 * l);
     }
@@ -58,13 +59,14 @@ __global__ void __launch_bounds__(256) tokens_kernel(Params p) {
     const float bc = beta;
     float w = from_raw(vr[0], p.dtype);
 #pragma unroll
-    for (int q = 0; q < Q; ++q)
+    for (int q = 0; q < Q; ++q) {
+      widen4(k[q], p.dtype, kc[q]);
+      widen4(x[q], p.dtype, xc[q]);
+      if (VEC) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        kc[q][e] = k[q][e];
-        xc[q][e] = x[q][e];
-        if (VEC) a[VEC ? q : 0][e] = fast_exp(gate(g[VEC ? q : 0][e]));
+        for (int e = 0; e < 4; ++e) a[VEC ? q : 0][e] = fast_exp(gate(g[VEC ? q : 0][e]));
       }
+    }
     if (!VEC) a[0][0] = fast_exp(gate(ga));
     if (i + 1 < len) load(i + 1);
     float u = 0.0f;
