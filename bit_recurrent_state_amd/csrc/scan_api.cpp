@@ -79,15 +79,15 @@ size_t layout(const qstate_scan_config* c, bool backward, void* workspace, Param
   p.nslots = (int)(c->tokens / kChunk + c->batch);
   p.dvp = (c->dv + 31) / 32 * 32;
   p.out_terms = vec ? (c->dtype == QSTATE_FP32 ? kTerms : 2) : (p.direct ? 2 : kTerms);
-  // Value columns of a chain workgroup.  Narrow blocks shorten the chain from
-  // chunk to chunk, wide ones share its fixed work: 16 while 32 would leave CUs
-  // (256) without a workgroup, 64 where that still leaves none without.  2900
-  // tokens of 6 x 32 heads, forward: 32 columns 299 us, 64 columns 244 us;
-  // 2048 tokens of 2 x 16 heads: 16 columns 103 us, 32 columns 164 us.  The
-  // backward chain's workgroups are twice as long, so that one and a quarter of
-  // them a CU (5 x 16 heads) still favour 16 (103 us against 164).
+  // Value columns of a chain workgroup, of which a CU (256) holds one at a time:
+  // the fewest rounds, each as long as its width makes it.  Narrow blocks
+  // shorten the chain from chunk to chunk, wide ones share its fixed work: 32
+  // columns take about 1.5 times as long as 16 forward and 1.6 times backward
+  // (256 blocks of 32, backward: 66 us, as 16: 78; 320: 164 and 102).  64, forward,
+  // pay where there are many (768 of 32: 299 us, as 64: 234; 2048: 136 and 124).
   const int64_t blocks = (int64_t)c->batch * c->heads * (p.dvp / 32);
-  p.vblock = blocks < (backward ? 512 : 256) ? 16 : 32;
+  const int64_t narrow = (2 * blocks + 255) / 256 * 10, wide = (blocks + 255) / 256 * (backward ? 16 : 15);
+  p.vblock = narrow < wide ? 16 : 32;
   if (!backward && blocks >= 512 && p.dvp % 64 == 0 && c->dk <= 128) p.vblock = 64;
   p.nvb = p.dvp / p.vblock;
   p.dop_terms = bf16 ? 1 : kTerms;

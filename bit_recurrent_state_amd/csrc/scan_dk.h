@@ -44,15 +44,13 @@ hipError_t forward_tail(const Params& p, hipStream_t s) {
 template <int DK, int NT, int NPQ, int NPO, bool VEC, bool DELTA>
 hipError_t backward_tail(const Params& p, hipStream_t s) {
   const dim3 slots(p.nslots, p.heads);
-  operands_kernel<DK><<<dim3(p.nslots, p.heads_qk), 256, 0, s>>>(p, 1);
-  {
-    if (VEC) {
-      operands_vector_kernel<DK, DELTA, true><<<slots, 256, 0, s>>>(p);
-      chunk_kernel<DK, P, true, DELTA, true><<<slots, 256, 0, s>>>(p);
-      chunk_vector_kernel<DK, DELTA, true><<<slots, 256, 0, s>>>(p);
-    } else {
-      chunk_kernel<DK, NPQ, false, DELTA, true><<<slots, 256, 0, s>>>(p);
-    }
+  if (VEC) {
+    operands_vector_kernel<DK, DELTA, true><<<slots, 256, 0, s>>>(p);
+    chunk_kernel<DK, P, true, DELTA, true><<<slots, 256, 0, s>>>(p);
+    chunk_vector_kernel<DK, DELTA, true><<<slots, 256, 0, s>>>(p);
+  } else {
+    operands_kernel<DK><<<dim3(p.nslots, p.heads_qk), 256, 0, s>>>(p, 1);
+    chunk_kernel<DK, NPQ, false, DELTA, true><<<slots, 256, 0, s>>>(p);
   }
   states_kernel<DK, NT, NPQ, P, VEC, DELTA, true, false><<<chain_grid(p), 256, 0, s>>>(p);
   state_grads_kernel<DK, NT, NPQ, NPO, VEC, DELTA><<<chain_grid(p), 512, 0, s>>>(p);

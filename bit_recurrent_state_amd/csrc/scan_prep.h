@@ -7,7 +7,7 @@
 
 namespace qscan {
 
-// ---- transposes and terms of q and k --------------------------------------------------------
+// ---- transposes and terms of q and k, one gate per token ------------------------------------
 // One workgroup per (slot, q/k head).  Threads run over channels, so the
 // caller's rows are read whole; each thread turns 8 tokens of its channel into
 // 16 bytes of the transposed planes.
@@ -16,15 +16,14 @@ __global__ void __launch_bounds__(256) operands_kernel(Params p, int backward) {
   const int slot = blockIdx.x, hq = blockIdx.y;
   Chunk c;
   if (!find_and_note(p, slot, hq == 0, c)) return;
-  const bool vec = p.mixer == GLA || p.mixer == KDA;
-  const int terms = vec ? (p.dtype == 1 ? 1 : P) : p.terms;
+  const int terms = p.terms;
   const int64_t sh = (int64_t)slot * p.heads_qk + hq;
   if (p.dtype == 1 && terms == 1) {
     // bfloat16 is moved as it is: 8 tokens of 2 channels per thread
     for (int which = 0; which <= backward; ++which) {
       const uint16_t* src = static_cast<const uint16_t*>(which ? p.q : p.k);
       const int64_t stride = which ? p.qs : p.ks;
-      uint16_t* tr = vec ? (which ? p.qt_raw : p.kt_raw) : (which ? p.qt : p.kt);
+      uint16_t* tr = which ? p.qt : p.kt;
       for (int u = threadIdx.x; u < DK / 2 * (C / 8); u += 256) {
         const int ch = u % (DK / 2) * 2, t0 = u / (DK / 2) * 8;
         uint32_t x[8];
@@ -59,7 +58,7 @@ __global__ void __launch_bounds__(256) operands_kernel(Params p, int backward) {
     if (which == 1 && !backward && p.direct) break;
     const void* src = which ? p.q : p.k;
     const int64_t stride = which ? p.qs : p.ks;
-    uint16_t* tr = vec ? (which ? p.qt_raw : p.kt_raw) : (which ? p.qt : p.kt);
+    uint16_t* tr = which ? p.qt : p.kt;
     uint16_t* rw = which ? p.qrow : p.krow;
     const bool transpose = which == 0 || backward;
     for (int u = threadIdx.x; u < DK * (C / 8); u += 256) {
@@ -79,7 +78,7 @@ __global__ void __launch_bounds__(256) operands_kernel(Params p, int backward) {
         *reinterpret_cast<u32x4*>(tr + (sh * terms + n) * DK * C + tiled<C>(ch, t0)) =
             n == 0 ? f.t[0] : n == 1 ? f.t[1] : f.t[2];
     }
-    if (p.direct || vec) continue;
+    if (p.direct) continue;
     for (int u = threadIdx.x; u < DK / 8 * C; u += 256) {  // rows: 8 channels of a token
       const int c0 = u % (DK / 8) * 8, tk = u / (DK / 8);
       float x[8];
@@ -351,9 +350,9 @@ __global__ void __launch_bounds__(256) operands_vector_kernel(Params p) {
   __shared__ __align__(16) float tot[4][DK];
   const int slot = blockIdx.x, h = blockIdx.y;
   Chunk c;
-  if (!(BWD ? noted_chunk(p, slot, c) : find_and_note(p, slot, h == 0, c))) return;
+  if (!find_and_note(p, slot, h == 0, c)) return;
   const int64_t sh = (int64_t)slot * p.heads + h;
-  const int hq = h / (p.heads / p.heads_qk);
+  const int group = p.heads / p.heads_qk, hq = h / group;
   const bool qeven = p.qs % 4 == 0, keven = p.ks % 4 == 0;
   for (int u = threadIdx.x; u < DK * 4; u += 256) {
     const int ch = u % DK, t0 = u / DK * 16;
@@ -448,6 +447,23 @@ __global__ void __launch_bounds__(256) operands_vector_kernel(Params p) {
     for (int m = 0; m < 4; ++m) {
       if (m < b) before += tot[m][ch];
       if (m > b) after += tot[m][ch];
+    }
+    if (BWD && h % group == 0) {  // q and k as they are, once for the heads that share them
+      const int terms = p.dtype == 1 ? 1 : P;
+      float xk[8], xq[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        xk[i] = t0 + i < c.len ? from_raw(rk[i], p.dtype) : 0.0f;
+        xq[i] = t0 + i < c.len ? from_raw(rq[i], p.dtype) : 0.0f;
+      }
+      const Frag<P> fk = split8<P>(xk), fq = split8<P>(xq);
+      const int64_t to = ((int64_t)slot * p.heads_qk + hq) * terms * C * DK + u * 8;
+#pragma unroll
+      for (int n = 0; n < P; ++n)
+        if (n < terms) {
+          *reinterpret_cast<u32x4*>(p.kt_raw + to + n * C * DK) = fk.t[n];
+          *reinterpret_cast<u32x4*>(p.qt_raw + to + n * C * DK) = fq.t[n];
+        }
     }
     float qe[8], ke[8], ko[8], kn[8], ps[8], ss[8];
 #pragma unroll
