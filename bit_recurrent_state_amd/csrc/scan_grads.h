@@ -719,6 +719,7 @@ __global__ void __launch_bounds__(256) grads_vector_kernel(Params p) {
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
+        asm volatile("" ::: "memory");  // else all rows' loads come first, and registers spill
 #pragma unroll
         for (int j = 0; j < i; ++j) kd[j] *= al[i];
         kd[i] = k[i];
@@ -730,7 +731,9 @@ __global__ void __launch_bounds__(256) grads_vector_kernel(Params p) {
         }
       }
 #pragma unroll
-      for (int i = 15; i >= 0; --i) {  // token i's decay is taken on as i is passed
+      for (int i = 15; i >= 0; --i) {
+        asm volatile("" ::: "memory");
+        // token i's decay is taken on as i is passed
         y[i] = fmaf(Ed[fg][i][i], q[i], y[i]);
 #pragma unroll
         for (int j = 0; j < i; ++j) {

@@ -14,7 +14,7 @@ namespace qscan {
 constexpr int kChunk = 64;  // tokens of a chunk
 constexpr int kTerms = 3;   // bfloat16 terms of an FP32 operand
 constexpr int kShort = 8;   // longest sequence that is taken token by token
-constexpr float kFarDecay = 8.0f;  // largest decay of a chunk, as a logarithm, that is divided out
+constexpr float kFarDecay = 24.0f;  // largest decay of a chunk, as a logarithm, that is divided out
 
 // Workspace operands are bfloat16 terms, a plane per term, in tiles of 16 rows
 // x 32 columns (scan_device.h); the sizes below are rows x columns.

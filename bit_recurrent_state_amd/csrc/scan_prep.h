@@ -249,8 +249,10 @@ __device__ __forceinline__ void store_dop(const Params& p, const Chunk& c, int64
 //
 // VEC: a gate per key channel, for chunks over which no channel decays by more
 // than e^kFarDecay: A = (q e^c)(k e^-c)^T and L = (k e^c)(k e^-c)^T are then
-// plain products.  Their exponents are rounded to 2^-24 of kFarDecay at most, so
-// the quotients they stand for hold to FP32.  Other chunks go to
+// plain products.  Their exponents, at most kFarDecay = 24, are rounded to 2^-24
+// of themselves, so that a quotient errs by at most 3e-6, and by 1e-7 at the
+// decays of a few per cent a token that most channels have.  (One channel's
+// values stay far inside FP32's range: e^24 = 3e10.)  Other chunks go to
 // chunk_vector_kernel.
 template <int DK, int NPQ, bool VEC, bool DELTA, bool BWD>
 __global__ void __launch_bounds__(256) chunk_kernel(Params p) {
@@ -534,6 +536,7 @@ __global__ void __launch_bounds__(256) chunk_vector_kernel(Params p) {
   for (int b = 0; b < 4; ++b) accA[b] = accL[b] = f32x4{0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < 16; ++i) dA[i] = dL[i] = 0.0f;
+#pragma unroll 1
   for (int c0 = 0; c0 < DK; c0 += SL) {
     __syncthreads();
     {
@@ -594,7 +597,7 @@ __global__ void __launch_bounds__(256) chunk_vector_kernel(Params p) {
     }
     // on the diagonal
     const int t0 = wave * 16;
-#pragma unroll
+#pragma unroll 1
     for (int part = 0; part < 2; ++part) {
       const int k0 = cg * 16 + part * 8;
       float kj[8], kd[8];
@@ -606,9 +609,10 @@ __global__ void __launch_bounds__(256) chunk_vector_kernel(Params p) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const bool first = i == fr;
+        asm volatile("" ::: "memory");  // else all tokens' loads come first, and registers spill
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          kd[e] = first ? kj[e] : kd[e] * al[t0 + i][k0 + e];
+          kd[e] = fmaf(kd[e], al[t0 + i][k0 + e], first ? kj[e] : 0.0f);
           dA[i] = fmaf(qs[t0 + i][k0 + e], kd[e], dA[i]);
           if (DELTA) dL[i] = fmaf(ks[t0 + i][k0 + e], kd[e], dL[i]);
         }
