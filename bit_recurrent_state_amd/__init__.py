@@ -11,4 +11,4 @@ from .qstate import (BDR, GDN, GLA, KDA, KEY_AXIS, RTN, SCALAR, SR, VALUE_AXIS, 
                      qstate_store_fp32)
 from .norm import (SIGMOID, SILU, NormConfig, block_norm, qstate_norm, qstate_norm_backward,  # noqa
                    qstate_norm_workspace)
-from .scan import ScanConfig, qstate_scan, qstate_scan_backward, qstate_scan_workspace, scan  # noqa
+from .sequence import ScanConfig, qstate_scan, qstate_scan_backward, qstate_scan_workspace, scan  # noqa

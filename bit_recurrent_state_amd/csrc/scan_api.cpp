@@ -38,9 +38,11 @@ int check_config(const qstate_scan_config* c) {
   const int64_t far = (int64_t)1 << 22;  // offsets inside a chunk take 32 bits
   if (c->q_stride > far || c->k_stride > far || c->v_stride > far || c->o_stride > far)
     return QSTATE_E_UNSUPPORTED;
-  // the grids: chunks of all sequences, and a workgroup per head and column block
-  if (c->tokens / kChunk + c->batch > 2147483647 ||
-      (int64_t)c->batch * c->heads * ((c->dv + 31) / 32) > 1000000000)
+  // the grids (chunks of all sequences; a workgroup per head and 16 columns) of
+  // up to 512 threads a workgroup stay below 2^32 threads
+  const int64_t most = 8388607;
+  if (c->tokens / kChunk + c->batch > most ||
+      ((int64_t)c->batch * c->heads + 8) * ((c->dv + 31) / 32 * 2) > most)
     return QSTATE_E_UNSUPPORTED;
   return QSTATE_OK;
 }

@@ -14,7 +14,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from ._lib import NormConfigC, check, lib
-from .scan import DTYPES, _array, _call, _on_device, _ptr, _stream, _workspace
+from .sequence import DTYPES, _array, _call, _on_device, _ptr, _stream, _workspace
 
 __all__ = ["SILU", "SIGMOID", "NormConfig", "qstate_norm", "qstate_norm_workspace",
            "qstate_norm_backward", "block_norm"]

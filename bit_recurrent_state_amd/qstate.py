@@ -16,7 +16,7 @@ import torch
 from ._lib import (BDR, GDN, GLA, KDA, KEY_AXIS, RTN, SCALAR, SR, VALUE_AXIS, QStateConfig, check,
                    lib)
 from .norm import SILU, NormConfig, qstate_norm
-from .scan import scan
+from .sequence import scan
 
 __all__ = [
     "GDN", "GLA", "SCALAR", "KDA", "RTN", "SR", "BDR", "VALUE_AXIS", "KEY_AXIS", "Config",
@@ -182,7 +182,7 @@ class ReadoutNorm:
     o * rsqrt(mean(o^2) + eps) * weight * act(gate), over each head's dv values."""
 
     weight: Optional[torch.Tensor] = None  # float32 [dv] or [heads, dv]
-    gate: Optional[torch.Tensor] = None    # as o
+    gate: Optional[torch.Tensor] = None    # as o, contiguous
     eps: float = 1e-6
     act: int = SILU
 
@@ -190,7 +190,7 @@ class ReadoutNorm:
         """In place on o [tokens, heads, dv]."""
         each = self.weight is not None and self.weight.dim() == 2
         cfg = NormConfig(o.shape[0], o.shape[1], o.shape[2], o.dtype, self.act, each, self.eps)
-        gate = None if self.gate is None else self.gate.reshape(o.shape)
+        gate = None if self.gate is None else self.gate.view(o.shape)
         qstate_norm(cfg, o, self.weight, gate, r=o, stream=stream)
 
 

@@ -79,8 +79,9 @@ typedef struct {
   int32_t mixer;    /* qstate_mixer                                           */
   int32_t dtype;    /* qstate_dtype of q, k, v, o and their gradients         */
   int32_t pad;      /* 0                                                      */
-  int64_t tokens;   /* rows in all, 0 .. 2^31 - 1; without offsets a multiple
-                       of batch                                               */
+  int64_t tokens;   /* rows in all; without offsets a multiple of batch.
+                       tokens / 64 + batch and (batch * heads + 8) * dv / 16
+                       (dv rounded up to 32) are at most 8388607              */
   int64_t q_stride, k_stride, v_stride, o_stride; /* elements; 0: packed      */
 } qstate_scan_config;
 

@@ -52,6 +52,8 @@ def _scan(**kw):
     (dict(tokens=-1), INVALID), (dict(q_stride=255), INVALID), (dict(v_stride=-1), INVALID),
     (dict(dk=96), UNSUPPORTED), (dict(dk=512), UNSUPPORTED), (dict(heads=300, heads_qk=1), UNSUPPORTED),
     (dict(dv=4097), UNSUPPORTED), (dict(tokens=1 << 31), UNSUPPORTED),
+    (dict(tokens=1 << 28), OK), (dict(tokens=1 << 29), UNSUPPORTED),
+    (dict(batch=500000, tokens=0, dv=32), OK), (dict(batch=1100000, tokens=0, dv=32), UNSUPPORTED),
     (dict(o_stride=(1 << 22) + 8), UNSUPPORTED),
 ])
 def test_scan_configs(L, kw, status):
