@@ -80,15 +80,21 @@ __device__ __forceinline__ void solve(const Params& p, const Chunk& c, int64_t s
 // FAR: only chunks that decay far, whose T chunk_vector_kernel has left in p.t;
 // otherwise everything, but for those chunks no A, L, T and what follows.
 template <int DK, int PO, bool DELTA, bool FAR>
-__global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
-  constexpr int LP = DK + 4, KS = DK / 32;
-  constexpr int kPre = C * LP > C * (C + 4) ? C * LP : C * (C + 4);
-  __shared__ __align__(16) float buf[kPre];  // sums of log decays in blocks of 16; then M and T
-  __shared__ __align__(16) uint16_t Kn[P][C * DK];
-  __shared__ __align__(16) float tot[4][DK];
-  __shared__ float bs[C];
-  float(*pre)[LP] = reinterpret_cast<float(*)[LP]>(buf);
-  Square* M = reinterpret_cast<Square*>(buf);
+__global__ void __launch_bounds__(512, DELTA ? 2 : 4) prep_vector_kernel(Params p) {
+  // 80 KB for dk = 128, so that without the delta rule a CU holds two workgroups
+  // and one computes while the other waits: 64 us with two, 96 us with one (123
+  // chunks of 16 heads, three terms).  With it T's steps need more than 128
+  // registers; held to that they spill: 218 us against 193 us with one workgroup
+  // (128 chunks of 16 heads, two terms).
+  constexpr int KS = DK / 32;
+  constexpr int kKn = P * C * DK, kTM = P * C * C + 2 * C * (C + 4);
+  __shared__ __align__(16) float buf[C * DK];  // sums of log decays in blocks of 16
+  __shared__ __align__(16) uint16_t Kn[kKn > kTM ? kKn : kTM];
+  // token t's sums, four channels together, turned by t against bank conflicts
+  auto pre = [&](int t, int ch) -> float& { return buf[t * DK + (ch ^ ((t & 7) << 2))]; };
+  auto tot = [&](int b, int ch) -> float& { return pre(b * 16 + 15, ch); };  // a block's
+  // T's terms, and M behind them, take the place of k e^-c
+  Square* const M = reinterpret_cast<Square*>(Kn + P * C * C);
   const int slot = blockIdx.x, h = blockIdx.y;
   Chunk c;
   if (!(FAR ? noted_chunk(p, slot, c) : find_and_note(p, slot, h == 0, c))) return;
@@ -97,12 +103,13 @@ __global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, rb = wave & 3;
   const int fr = lane & 15, fg = lane >> 4;
   const int hq = h / (p.heads / p.heads_qk);
-  // everything that comes from the caller's arrays is on its way before the first sum
+  // what comes from the caller's arrays is on its way before the first sum
   const bool second = wave >= 4, even = (second ? p.ks : p.qs) % 4 == 0;
   const int t = rb * 16 + fr;
   uint32_t rk[2][8], rv[2][8];
   u32x4 rx[KS][2];
-  if (wave < DK / 16) {
+  auto load_keys = [&]() {
+    if (wave >= DK / 16) return;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       int64_t at[8];
@@ -111,7 +118,8 @@ __global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
         at[i] = (c.row + min(s * 32 + fg * 8 + i, c.len - 1)) * p.ks + (int64_t)hq * DK + wave * 16 + fr;
       load_raw<8>(p.k, at, p.dtype, rk[s]);
     }
-  }
+  };
+  if (FAR || DELTA) load_keys();
   if (!FAR) {
     const int64_t row = c.row + min(t, c.len - 1);
 #pragma unroll
@@ -132,32 +140,40 @@ __global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       s += t0 + i < c.len ? gate(g[i]) : 0.0f;
-      pre[t0 + i][ch] = s;
+      pre(t0 + i, ch) = s;
     }
-    tot[u / DK][ch] = s;
   }
   if (threadIdx.x < C) {
     const int t = threadIdx.x;
-    const float b = t < c.len ? (p.beta ? p.beta[(c.row + t) * p.heads + h] : 1.0f) : 0.0f;
-    bs[t] = b;
-    rows_at(p, slot, h)[2 * C + t] = b;
+    rows_at(p, slot, h)[2 * C + t] =
+        t < c.len ? (p.beta ? p.beta[(c.row + t) * p.heads + h] : 1.0f) : 0.0f;
   }
   __syncthreads();
   bool over = false;
   if (!FAR && threadIdx.x < DK) {
     const int ch = threadIdx.x;
-    const float all = (tot[0][ch] + tot[1][ch]) + (tot[2][ch] + tot[3][ch]);
+    const float all = (tot(0, ch) + tot(1, ch)) + (tot(2, ch) + tot(3, ch));
     p.decay[sh * DK + ch] = fast_exp(all);
     over = !(all >= -kFarDecay);
   }
-  const bool far = FAR || __syncthreads_or(over);
-  if (!FAR && threadIdx.x == 0) p.far[sh] = far;
+  bool far = FAR;
+  if (!FAR) {
+    uint32_t* const flag = reinterpret_cast<uint32_t*>(Kn);
+    const uint64_t any = __ballot(over);
+    if (lane == 0) flag[wave] = any != 0;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) far = far || flag[w];
+    if (threadIdx.x == 0) p.far[sh] = far;
+    __syncthreads();
+  }
 
   // columns of k: a wave's 16 channels, both halves of the tokens
   Frag<P> kt[2];
-  if (wave < DK / 16) {
+  auto columns = [&]() {
+    if (wave >= DK / 16) return;
     const int ch = wave * 16 + fr;
-    const float t4[4] = {tot[0][ch], tot[1][ch], tot[2][ch], tot[3][ch]};
+    const float t4[4] = {tot(0, ch), tot(1, ch), tot(2, ch), tot(3, ch)};
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const int t0 = s * 32 + fg * 8, b = t0 >> 4;
@@ -183,14 +199,14 @@ __global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
       } else {
         const float block = b == 0 ? t4[0] : b == 1 ? t4[1] : b == 2 ? t4[2] : t4[3];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sfx[i] = block - pre[t0 + i][ch];
+        for (int i = 0; i < 8; ++i) sfx[i] = block - pre(t0 + i, ch);
       }
       float ko[8], ke[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float k = t0 + i < c.len ? from_raw(rk[s][i], p.dtype) : 0.0f;
         ko[i] = k * fast_exp(sfx[i] + after);
-        if (DELTA) ke[i] = k * fast_exp(pre[t0 + i][ch] + before);
+        if (DELTA) ke[i] = k * fast_exp(pre(t0 + i, ch) + before);
       }
       if (DELTA) kt[s] = split8<P>(ke);
       if (!FAR) {
@@ -200,14 +216,15 @@ __global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
           *reinterpret_cast<u32x4*>(p.kt + (sh * P + n) * C * DK + (wave * 2 + s) * 512 + lane * 8) = f.t[n];
       }
     }
-  }
+  };
   if (FAR) {
     if (DELTA) {
+      columns();
       const uint16_t* from = p.t + sh * P * C * C;
       for (int u = threadIdx.x; u < P * C * C / 8; u += 512)
-        reinterpret_cast<u32x4*>(&Kn[0][0])[u] = reinterpret_cast<const u32x4*>(from)[u];
+        reinterpret_cast<u32x4*>(Kn)[u] = reinterpret_cast<const u32x4*>(from)[u];
       __syncthreads();
-      solve<DK>(p, c, sh, h, &Kn[0][0], kt, rv);
+      solve<DK>(p, c, sh, h, Kn, kt, rv);
     }
     return;
   }
@@ -223,10 +240,10 @@ __global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
     for (int q = 0; q < 2; ++q) {
       float x[4];
       widen4(rx[s][q], p.dtype, x);
-      f32x4 cs = *reinterpret_cast<const f32x4*>(&pre[t][ch + 4 * q]);
+      f32x4 cs = *reinterpret_cast<const f32x4*>(&pre(t, ch + 4 * q));
 #pragma unroll
       for (int m = 0; m < 3; ++m)
-        if (m < rb) cs += *reinterpret_cast<const f32x4*>(&tot[m][ch + 4 * q]);
+        if (m < rb) cs += *reinterpret_cast<const f32x4*>(&tot(m, ch + 4 * q));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float e = fast_exp(cs[i]);
@@ -242,7 +259,7 @@ __global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
       const Frag<P> f = split8<P>(xn);
 #pragma unroll
       for (int n = 0; n < P; ++n)
-        *reinterpret_cast<u32x4*>(&Kn[n][(rb * KS + s) * 512 + lane * 8]) = f.t[n];
+        *reinterpret_cast<u32x4*>(Kn + n * C * DK + (rb * KS + s) * 512 + lane * 8) = f.t[n];
     } else {
 #pragma unroll
       for (int n = 0; n < PO; ++n)
@@ -250,33 +267,41 @@ __global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
             own[s].t[n];
     }
   }
-  __syncthreads();  // k e^-c is there, and the sums have been read
-  if (far) return;
+  if (!DELTA) load_keys();
+  __syncthreads();  // k e^-c is there
   f32x4 all[4];
 #pragma unroll
   for (int b = 0; b < 4; ++b) all[b] = f32x4{0, 0, 0, 0};
-  if (DELTA || !second) {
+  if (!far && (DELTA || !second)) {
 #pragma unroll
     for (int s = 0; s < KS; ++s)
 #pragma unroll
       for (int b = 0; b < 4; ++b)
         if (b <= rb) {
-          const Frag<P> f = tile_frag<P, DK>(&Kn[0][0], b, s, C * DK);
+          const Frag<P> f = tile_frag<P, DK>(Kn, b, s, C * DK);
           if (second)
             mma(all[b], f, own[s]);
           else
             mma(all[b], head<PO>(f), head<PO>(own[s]));
         }
   }
+  if (DELTA) __syncthreads();  // M goes where k e^-c was
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
+    if (far) break;
     const f32x4 acc = all[b];
     const int i = rb * 16 + fr, j0 = b * 16 + fg * 4;
+    f32x4 bj = {0, 0, 0, 0};
+    if (DELTA && second) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        bj[r] = j0 + r < c.len ? p.beta[(c.row + j0 + r) * p.heads + h] : 0.0f;
+    }
     float x[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int j = j0 + r;
-      x[r] = second ? (i > j ? acc[r] * bs[j] : 0.0f) : (i >= j ? acc[r] : 0.0f);
+      x[r] = second ? (i > j ? acc[r] * bj[r] : 0.0f) : (i >= j ? acc[r] : 0.0f);
     }
     if (second) {
       if (DELTA) *reinterpret_cast<f32x4*>(&M[i][j0]) = f32x4{x[0], x[1], x[2], x[3]};
@@ -284,6 +309,8 @@ __global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
       put4<PO>(p.a + sh * P * C * C + tiled<C>(i, j0), C * C, x);
     }
   }
+  columns();
+  if (far) return;
   if (DELTA) {
     __syncthreads();
     invert<1>(M, M);
@@ -295,10 +322,10 @@ __global__ void __launch_bounds__(512) prep_vector_kernel(Params p) {
       const Frag<P> f = split8<P>(x);
 #pragma unroll
       for (int n = 0; n < P; ++n)
-        *reinterpret_cast<u32x4*>(&Kn[0][0] + n * C * C + threadIdx.x * 8) = f.t[n];
+        *reinterpret_cast<u32x4*>(Kn + n * C * C + threadIdx.x * 8) = f.t[n];
     }
     __syncthreads();
-    solve<DK>(p, c, sh, h, &Kn[0][0], kt, rv);
+    solve<DK>(p, c, sh, h, Kn, kt, rv);
   }
 }
 
