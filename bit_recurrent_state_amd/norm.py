@@ -14,7 +14,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from ._lib import NormConfigC, check, lib
-from .sequence import DTYPES, _array, _call, _on_device, _ptr, _stream, _workspace
+from .sequence import DTYPES, _array, _bytes_on, _call, _on_device, _ptr, _stream, _workspace
 
 __all__ = ["SILU", "SIGMOID", "NormConfig", "qstate_norm", "qstate_norm_workspace",
            "qstate_norm_backward", "block_norm"]
@@ -105,11 +105,11 @@ def _workspace_bytes(c: NormConfigC) -> int:
     return n.value
 
 
-def _own_workspace(c, wanted, dev):
+def _own_workspace(c, wanted, dev, stream=None):
     """A workspace of this call where sums over rows are wanted: the tensor, (pointer, bytes)."""
     if not wanted:
         return None, (None, 0)
-    w = torch.empty(max(_workspace_bytes(c), 1), dtype=torch.uint8, device=dev)
+    w = _bytes_on(max(_workspace_bytes(c), 1), dev, stream)
     return w, (w.data_ptr(), w.numel())
 
 
@@ -131,7 +131,7 @@ def qstate_norm_backward(cfg: NormConfig, x, weight=None, gate=None, residual=No
         keep, w = None, _workspace(workspace, dev)
     else:
         keep, w = _own_workspace(c, any(t is not None for t in (dweight, dscale, dnext_weight)),
-                                 dev)
+                                 dev, stream)
     _launch_backward(c, dev, args, int(has_h), more, w, stream)
 
 
@@ -150,12 +150,26 @@ def _token_rows(t, groups, width):
     return r, 0 if r.shape[0] <= 1 or r.stride(0) == groups * width else r.stride(0)
 
 
+def _one_distance(t, width) -> bool:
+    if t is None or t.is_contiguous():
+        return True
+    try:
+        t.view(-1, width)
+        return True
+    except RuntimeError:
+        return False
+
+
 def _forward(x, weight, gate, residual, scale, next_weight, eps, act):
     """The checked call: r, h, and what backward needs."""
     width = x.shape[-1]
     each = weight is not None and weight.dim() == 2
-    # [tokens][groups]: a weight per group needs it, for the others it says how the rows lie
-    groups = x.shape[-2] if x.dim() > 2 or each else 1
+    # [tokens][groups]: a weight per group needs it; else it only says how the rows lie, and they
+    # mostly lie at one distance
+    groups = 1
+    if each or (x.dim() > 2 and x.shape[-2] <= 65535
+                and not all(_one_distance(t, width) for t in (x, gate, residual))):
+        groups = x.shape[-2]
     (x3, xs), (gate3, gs), (res3, rs) = (_token_rows(t, groups, width) for t in (x, gate, residual))
     weight, scale, next_weight = (None if t is None else t.contiguous()
                                   for t in (weight, scale, next_weight))

@@ -15,8 +15,8 @@ import torch
 
 from ._lib import (BDR, GDN, GLA, KDA, KEY_AXIS, RTN, SCALAR, SR, VALUE_AXIS, QStateConfig, check,
                    lib)
-from .norm import SILU, NormConfig, qstate_norm
-from .sequence import scan
+from .norm import SILU, NormConfig, qstate_norm, qstate_norm_workspace
+from .sequence import _array, scan
 
 __all__ = [
     "GDN", "GLA", "SCALAR", "KDA", "RTN", "SR", "BDR", "VALUE_AXIS", "KEY_AXIS", "Config",
@@ -186,10 +186,20 @@ class ReadoutNorm:
     eps: float = 1e-6
     act: int = SILU
 
+    def config(self, shape, dtype, device) -> NormConfig:
+        """The configuration for a readout of this shape, its tensors checked."""
+        tokens, heads, dv = shape
+        each = self.weight is not None and self.weight.dim() == 2
+        cfg = NormConfig(tokens, heads, dv, dtype, self.act, each, self.eps)
+        qstate_norm_workspace(cfg)  # the library's checks of it
+        _array(self.weight, "weight", torch.float32, dv * (heads if each else 1), device,
+               optional=True)
+        _array(self.gate, "gate", dtype, tokens * heads * dv, device, optional=True)
+        return cfg
+
     def apply_(self, o: torch.Tensor, stream=None) -> None:
         """In place on o [tokens, heads, dv]."""
-        each = self.weight is not None and self.weight.dim() == 2
-        cfg = NormConfig(o.shape[0], o.shape[1], o.shape[2], o.dtype, self.act, each, self.eps)
+        cfg = self.config(o.shape, o.dtype, o.device)
         gate = None if self.gate is None else self.gate.view(o.shape)
         qstate_norm(cfg, o, self.weight, gate, r=o, stream=stream)
 
@@ -214,15 +224,21 @@ class QState:
     def step(self, q, k, v, alpha, beta=None, o=None, stream=None, norm=None):
         """One token for every sequence; with `norm` (a ReadoutNorm), o is the normed and gated
         readout."""
+        if norm is not None:  # refused before the state changes
+            if o is None:
+                raise ValueError("norm: there is no readout without o")
+            shape = (self.cfg.batch, self.cfg.heads, self.cfg.dv)
+            norm.config(shape, torch.float32, o.device)
         qstate_step(self.handle, self.cfg, q, k, v, alpha, beta, o, stream)
-        if norm is not None and o is not None:
-            norm.apply_(o.view(self.cfg.batch, self.cfg.heads, self.cfg.dv), stream)
+        if norm is not None:
+            norm.apply_(o.view(shape), stream)
 
     def prefill(self, q, k, v, log_alpha, beta=None, offsets=None, norm=None):
         """A prompt's or a chunk's tokens at once, for sequences that decode on with `step`: the
         scan from the stored state, whose end is stored back (one quantization event for every
-        sequence, those without tokens too: the counter goes up by one, a window starts empty).  Arguments as `scan`'s, one sequence per batch
-        row, q and k with the handle's heads or a divisor of them; returns o."""
+        sequence, those without tokens too: the counter goes up by one, a window starts empty).
+        Arguments as `scan`'s, one sequence per batch row, q and k with the handle's heads or a
+        divisor of them; returns o."""
         c = self.cfg
         if offsets is not None and offsets.numel() != c.batch + 1:
             raise ValueError(f"offsets: expected {c.batch + 1} elements, got {offsets.numel()}")
@@ -230,6 +246,8 @@ class QState:
                 offsets is None and v.shape[0] != c.batch):
             raise ValueError(f"q {tuple(q.shape)}, v {tuple(v.shape)} do not go with the state "
                              f"[{c.batch}][{c.heads}][{c.dv}][{c.dk}]")
+        if norm is not None:
+            norm.config((v[..., 0, 0].numel(), c.heads, c.dv), v.dtype, v.device)
         with torch.no_grad(), torch.cuda.device(v.device):
             S = torch.empty((c.batch, c.heads, c.dv, c.dk), dtype=torch.float32, device=v.device)
             self.store_fp32(S)

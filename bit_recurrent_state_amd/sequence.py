@@ -127,9 +127,20 @@ def _launch_backward(c, dev, inputs, more, workspace, stream):
                                         *workspace, _stream(stream, dev)))
 
 
-def _own_workspace(c, backward, dev):
+def _bytes_on(n: int, dev, stream) -> torch.Tensor:
+    """n bytes that belong to the stream of the call: once freed they are used again only behind
+    its kernels, also where it is not the current one."""
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=dev)
+
+
+def _own_workspace(c, backward, dev, stream=None):
     """A workspace of this call: the tensor, and (pointer, bytes)."""
-    w = torch.empty(_workspace_bytes(c, backward), dtype=torch.uint8, device=dev)
+    w = _bytes_on(_workspace_bytes(c, backward), dev, stream)
     return w, (w.data_ptr(), w.numel())
 
 
@@ -168,7 +179,7 @@ def qstate_scan(cfg: ScanConfig, q, k, v, log_alpha, beta=None, offsets=None, in
                 cfg.batch * cfg.heads * cfg.dv * cfg.dk, dev, optional=True)
     c = cfg.to_c()
     keep, w = (None, _workspace(workspace, dev)) if workspace is not None else \
-        _own_workspace(c, False, dev)
+        _own_workspace(c, False, dev, stream)
     _launch_scan(c, dev, args, po, ps, w, stream)
 
 
@@ -194,20 +205,21 @@ def qstate_scan_backward(cfg: ScanConfig, q, k, v, log_alpha, beta, offsets, ini
     )
     c = cfg.to_c()
     keep, w = (None, _workspace(workspace, dev)) if workspace is not None else \
-        _own_workspace(c, True, dev)
+        _own_workspace(c, True, dev, stream)
     _launch_backward(c, dev, args, more, w, stream)
 
 
 def _token_rows(t: torch.Tensor) -> torch.Tensor:
     """[.., heads, d] with any leading dims as [tokens][heads][d]; a copy only where the heads are
-    not packed, the tokens do not lie at one distance, or rows start off a 16-byte boundary."""
+    not packed, the tokens do not lie at one distance (or 2^22 elements and more apart), or rows
+    start off a 16-byte boundary."""
     heads, d = t.shape[-2:]
     try:
         r = t.view(-1, heads, d)
     except RuntimeError:
         r = t.reshape(-1, heads, d)
     packed = (d == 1 or r.stride(2) == 1) and (heads == 1 or r.stride(1) == d)
-    apart = r.shape[0] <= 1 or r.stride(0) >= heads * d
+    apart = r.shape[0] <= 1 or heads * d <= r.stride(0) <= 1 << 22
     if not (packed and apart) or r.data_ptr() % 16:
         r = r.clone(memory_format=torch.contiguous_format)
     return r

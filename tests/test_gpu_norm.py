@@ -219,3 +219,13 @@ def test_refusals():
     from bit_recurrent_state_amd._lib import QStateError
     with pytest.raises(QStateError):
         block_norm(torch.zeros(2, 64, device="cuda"), eps=0.0)
+
+
+def test_many_rows_before_the_last_dimension():
+    """[1, rows, width] with more rows than a token may have, also as part of wider rows."""
+    x = make(70000, 0, 16, torch.float32, True, False, False, False, False)
+    want = run(x)[0]
+    wide = torch.cat([x["x"], x["gate"]], 1)[None]
+    for a, z in ((x["x"][None], x["gate"][None]), (wide[..., :16], wide[..., 16:])):
+        got = run({**x, "x": a, "gate": z})[0]
+        assert got.shape == a.shape and torch.equal(got[0], want)

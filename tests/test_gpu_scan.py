@@ -387,3 +387,89 @@ def test_training_chain():
                                [leaf[n] for n in NAMES] + e64)
     for i, (a, b) in enumerate(zip(got, want)):
         assert rel(a, b) <= 4 * tolerance(torch.float32, True), i
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_own_workspace_belongs_to_the_stream(handle):
+    """A call on a stream that is not the current one takes its workspace from that stream's
+    memory, so that later work of the current stream cannot be given it while the call runs."""
+    from bit_recurrent_state_amd import NormConfig, ScanConfig, qstate_norm_backward, qstate_scan
+    from bit_recurrent_state_amd import norm, sequence
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if handle else side
+    x = inputs(GDN, 2, [40, 9], 2, 2, 64, 32, torch.float32, "cuda")
+    o, want = torch.empty_like(x["v"]), call(x, GDN)[0]
+    g = torch.randn(30, 1, 64, device="cuda")
+    dw, r = torch.empty(64, device="cuda"), 1 / (g.double().pow(2).mean(-1, keepdim=True) + 1e-6).sqrt()
+    torch.cuda.synchronize()
+    made = []
+
+    def watch(module, name):
+        real = getattr(module, name)
+
+        def f(*args, **kw):
+            made.append(real(*args, **kw))
+            return made[-1]
+        return real, f
+
+    for module in (sequence, norm):
+        real, f = watch(module, "_own_workspace")
+        module._own_workspace = f
+        try:
+            if module is sequence:
+                c = ScanConfig(2, 2, 64, 32, 49)
+                qstate_scan(c, x["q"], x["k"], x["v"], x["log_alpha"], x["beta"], x["offsets"],
+                            x["initial_state"], o, stream=stream)
+            else:
+                qstate_norm_backward(NormConfig(30, 1, 64), g, dr=g, dweight=dw, stream=stream)
+        finally:
+            module._own_workspace = real
+    side.synchronize()
+    for _, (at, n) in made:
+        segments = [s for s in torch.cuda.memory_snapshot()
+                    if s["address"] <= at < s["address"] + s["total_size"]]
+        assert [s["stream"] for s in segments] == [side.cuda_stream]
+    assert len(made) == 2 and torch.equal(o, want)
+    assert rel(dw, (g.double() ** 2 * r).sum((0, 1))) <= 30 * 2 ** -22
+
+
+def test_rows_far_apart():
+    """Rows of q, k and v that lie farther apart than the kernels take are copied."""
+    x = inputs(GDN, 1, [3], 1, 1, 64, 16, torch.bfloat16, "cuda")
+    want = call(x, GDN)
+    far = (1 << 22) + 8
+    wide = torch.zeros(2 * far + 256, dtype=torch.bfloat16, device="cuda")
+    parts = {}
+    for i, n in enumerate(("q", "k", "v")):
+        w = x[n].shape[2]
+        parts[n] = wide.as_strided((3, 1, w), (far, w, 1), 80 * i)
+        parts[n].copy_(x[n])
+    got = call({**x, **parts}, GDN)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_readout_norm_refused_before_the_step():
+    """A readout norm that does not fit is refused before the state changes."""
+    from bit_recurrent_state_amd import Config, QState, ReadoutNorm
+    cfg = Config(batch=2, heads=2, dk=64, dv=32, group=32, mixer=GDN)
+    st = QState(cfg)
+    g = torch.Generator().manual_seed(3)
+    f32 = lambda *s: torch.randn(*s, generator=g).cuda()
+    st.load_fp32(f32(2, 2, 32, 64))
+    before = torch.empty(2, 2, 32, 64, device="cuda")
+    st.store_fp32(before)
+    q, k, v, o = f32(2, 2, 64), f32(2, 2, 64), f32(2, 2, 32), f32(2, 2, 32)
+    alpha, beta = torch.full((2, 2), 0.9, device="cuda"), torch.full((2, 2), 0.5, device="cuda")
+    bad = [ReadoutNorm(weight=f32(31)), ReadoutNorm(gate=f32(2, 2, 31)), ReadoutNorm(eps=0.0),
+           ReadoutNorm(act=7), ReadoutNorm(weight=f32(3, 32)), ReadoutNorm(gate=v.bfloat16())]
+    from bit_recurrent_state_amd._lib import QStateError
+    for norm in bad:
+        with pytest.raises((ValueError, TypeError, QStateError)):
+            st.step(q, k, v, alpha, beta, o, norm=norm)
+        with pytest.raises((ValueError, TypeError, QStateError)):
+            st.prefill(q[:, None], k[:, None], v[:, None], alpha[:, None].log(), beta[:, None], norm=norm)
+    with pytest.raises(ValueError):
+        st.step(q, k, v, alpha, beta, None, norm=ReadoutNorm())
+    after = torch.empty_like(before)
+    st.store_fp32(after)
+    assert torch.equal(before, after)
