@@ -11,7 +11,9 @@
 //                  + sum_{i>=t} (q_i dq_i + k_i dk+_i - k_i dk-_i (chunk part))
 // with the products taken per channel where the gate is.  The last line counts
 // each pair of tokens only where t lies between them, so terms that do not
-// depend on a gate are not added and taken off again.
+// depend on a gate are not added and taken off again; E's diagonal, which would
+// cancel there up to rounding, enters dq and dk beside the products (a single
+// token without a state then has a gate's gradient of exactly zero).
 //
 // Waves split the key channels: the states are then read once per workgroup.
 
@@ -130,6 +132,7 @@ __global__ void __launch_bounds__(DK >= 128 ? 512 : 256) grads_kernel(Params p) 
   __shared__ float red[2][NW][C], redb[NW][C];
   __shared__ __align__(16) float rows[5 * C];
   __shared__ float redx[NW];
+  __shared__ __align__(16) float diag[C];  // E's diagonal
   uint16_t* const Ol = lds;
   uint16_t* const Ul = lds + NPO * C * VP;
   uint16_t* const Yl = Ul + P * C * VP;
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(DK >= 128 ? 512 : 256) grads_kernel(Params p) 
 
   // E (then F) as planes in LDS
   const double* cs = reinterpret_cast<const double*>(rows + 3 * C);
-  auto put_square = [&](f32x4(&x)[NE], bool strict, float sign) {
+  auto put_square = [&](f32x4(&x)[NE], float sign) {
     __syncthreads();
 #pragma unroll
     for (int b = 0; b < NE; ++b) {
@@ -279,7 +282,8 @@ __global__ void __launch_bounds__(DK >= 128 ? 512 : 256) grads_kernel(Params p) 
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int i = i0 + r;
-        const bool in = strict ? i > j : i >= j;
+        const bool in = i > j;
+        if (sign > 0.0f && i == j) diag[i] = x[b][r] * beta;
         float g = beta;
         if (!VEC) g *= fast_exp(in ? (float)(cs[i] - cs[j]) : 0.0f);
         v[r] = in ? x[b][r] * g : 0.0f;
@@ -310,7 +314,7 @@ __global__ void __launch_bounds__(DK >= 128 ? 512 : 256) grads_kernel(Params p) 
       fk[ct][s] = tile_frag<NPQ, C>(kn, wave * CT + ct, s, DK * C);
       fq[ct][s] = tile_frag<NPQ, C>(qe, wave * CT + ct, s, DK * C);
     }
-  put_square(e, false, 1.0f);
+  put_square(e, 1.0f);
   f32x4 ai[CT][4];
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
@@ -371,7 +375,7 @@ __global__ void __launch_bounds__(DK >= 128 ? 512 : 256) grads_kernel(Params p) 
         rq[ct][m][n] = *reinterpret_cast<const u32x2*>(qr + at);
       }
   if (DELTA) {
-    put_square(f, true, -1.0f);
+    put_square(f, -1.0f);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
@@ -406,6 +410,7 @@ __global__ void __launch_bounds__(DK >= 128 ? 512 : 256) grads_kernel(Params p) 
       float k[4], q[4], dq[4], dk[4];
       sum4(rk[ct][m], k);
       sum4(rq[ct][m], q);
+      const f32x4 ed = *reinterpret_cast<const f32x4*>(diag + t0);
       f32x4 ec = {1, 1, 1, 1};
       if (VEC) ec = *reinterpret_cast<const f32x4*>(p.pfx + (sh * DK + ch) * C + t0);
 #pragma unroll
@@ -416,8 +421,8 @@ __global__ void __launch_bounds__(DK >= 128 ? 512 : 256) grads_kernel(Params p) 
           b *= ec[r];
           i /= ec[r];
         }
-        dq[r] = a;
-        dk[r] = b + am[ct][m][r] + i;
+        dq[r] = fmaf(ed[r], k[r], a);
+        dk[r] = fmaf(ed[r], q[r], b + am[ct][m][r] + i);
         const float s = k[r] * am[ct][m][r], d = q[r] * a + k[r] * (b - i);
         sS[m][r] = VEC || ct == 0 ? s : sS[m][r] + s;
         sD[m][r] = VEC || ct == 0 ? d : sD[m][r] + d;
@@ -725,16 +730,15 @@ __global__ void __launch_bounds__(256) grads_vector_kernel(Params p) {
         kd[i] = k[i];
         x[i] = z[i] = 0.0f;
 #pragma unroll
-        for (int j = 0; j <= i; ++j) {
+        for (int j = 0; j < i; ++j) {
           x[i] = fmaf(Ed[fg][i][j], kd[j], x[i]);
-          if (DELTA && j < i) z[i] = fmaf(Fd[fg][DELTA ? i : 0][j], kd[j], z[i]);
+          if (DELTA) z[i] = fmaf(Fd[fg][DELTA ? i : 0][j], kd[j], z[i]);
         }
       }
 #pragma unroll
       for (int i = 15; i >= 0; --i) {
         asm volatile("" ::: "memory");
         // token i's decay is taken on as i is passed
-        y[i] = fmaf(Ed[fg][i][i], q[i], y[i]);
 #pragma unroll
         for (int j = 0; j < i; ++j) {
           float s = fmaf(Ed[fg][i][j], q[i], y[j]);
@@ -777,8 +781,9 @@ __global__ void __launch_bounds__(256) grads_vector_kernel(Params p) {
         const float q = in ? load_elem(p.q, (c.row + t) * p.qs + (int64_t)hq * DK + ch, p.dtype) : 0.0f;
         const float k = in ? load_elem(p.k, (c.row + t) * p.ks + (int64_t)hq * DK + ch, p.dtype) : 0.0f;
         dc[m][r] = q * aq[m][r] + k * (ap[m][r] - ai[m][r]);
-        dq[r] = aq[m][r];
-        dk[r] = ap[m][r] + am[m][r] + ai[m][r];
+        const float ed = Ed[m][fg * 4 + r][fg * 4 + r];
+        dq[r] = fmaf(ed, k, aq[m][r]);
+        dk[r] = fmaf(ed, q, ap[m][r] + am[m][r] + ai[m][r]);
       }
       store_qk<DK>(p, c, sh, h, m * 16 + fg * 4, ch, dq, dk);
     }

@@ -473,3 +473,19 @@ def test_readout_norm_refused_before_the_step():
     after = torch.empty_like(before)
     st.store_fp32(after)
     assert torch.equal(before, after)
+
+
+@pytest.mark.parametrize("decay", [-0.05, -50.0])
+@pytest.mark.parametrize("mixer", MIXERS)
+def test_single_tokens_without_a_state(mixer, decay):
+    """No gate lies between a token and itself: without a state its gradient is exactly zero."""
+    m, lens = MIXERS[mixer], [1, 1, 0, 1]
+    x = inputs(m, 4, lens, 2, 1, 128, 40, torch.bfloat16, "cuda", state=False)
+    x["log_alpha"].fill_(decay)
+    g = torch.Generator().manual_seed(9)
+    do = torch.randn(x["v"].shape, generator=g).bfloat16().cuda()
+    dS = torch.randn(4, 2, 40, 128, generator=g).cuda()
+    _, _, got = gradients(x, m, do, dS)
+    assert not got["log_alpha"].any()
+    assert all(got[n].any() for n in ("q", "k", "v"))
+    check(x, m, 4)
