@@ -77,7 +77,6 @@ size_t layout(const qstate_scan_config* c, bool backward, void* workspace, Param
   p.os = c->o_stride ? c->o_stride : (int64_t)c->heads * c->dv;
   // bfloat16 rows enter the products as they are where 16-byte loads reach them
   p.direct = !vec && bf16 && p.qs % 8 == 0 && p.ks % 8 == 0;
-  p.terms = p.direct ? 1 : kTerms;
   p.nslots = (int)(c->tokens / kChunk + c->batch);
   p.dvp = (c->dv + 31) / 32 * 32;
   p.out_terms = vec ? (c->dtype == QSTATE_FP32 ? kTerms : 2) : (p.direct ? 2 : kTerms);
@@ -96,7 +95,7 @@ size_t layout(const qstate_scan_config* c, bool backward, void* workspace, Param
 
   Area w = {static_cast<char*>(workspace), 0};
   const uint64_t sh = (uint64_t)p.nslots * p.heads, sq = (uint64_t)p.nslots * p.heads_qk;
-  const uint64_t tile = (uint64_t)kChunk * p.dk, ops = (vec ? sh : sq) * p.terms * tile;
+  const uint64_t tile = (uint64_t)kChunk * p.dk, ops = (vec ? sh : sq) * (p.direct ? 1 : kTerms) * tile;
   const uint64_t square = sh * kTerms * kChunk * kChunk;
   w.take(p.chunks, p.nslots, true);
   w.take(p.sink, 64, true);

@@ -16,9 +16,8 @@ __global__ void __launch_bounds__(256) operands_kernel(Params p, int backward) {
   const int slot = blockIdx.x, hq = blockIdx.y;
   Chunk c;
   if (!find_and_note(p, slot, hq == 0, c)) return;
-  const int terms = p.terms;
   const int64_t sh = (int64_t)slot * p.heads_qk + hq;
-  if (p.dtype == 1 && terms == 1) {
+  if (p.direct) {
     // bfloat16 is moved as it is: 8 tokens of 2 channels per thread
     for (int which = 0; which <= backward; ++which) {
       const uint16_t* src = static_cast<const uint16_t*>(which ? p.q : p.k);
@@ -28,17 +27,9 @@ __global__ void __launch_bounds__(256) operands_kernel(Params p, int backward) {
         const int ch = u % (DK / 2) * 2, t0 = u / (DK / 2) * 8;
         uint32_t x[8];
         const uint16_t* at = src + (int64_t)hq * DK + ch;
-        if (stride % 2 == 0) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            x[i] = *reinterpret_cast<const uint32_t*>(at + (c.row + min(t0 + i, c.len - 1)) * stride);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint16_t* r = at + (c.row + min(t0 + i, c.len - 1)) * stride;
-            x[i] = r[0] | (uint32_t)r[1] << 16;
-          }
-        }
+        for (int i = 0; i < 8; ++i)
+          x[i] = *reinterpret_cast<const uint32_t*>(at + (c.row + min(t0 + i, c.len - 1)) * stride);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (t0 + i >= c.len) x[i] = 0;
@@ -55,13 +46,12 @@ __global__ void __launch_bounds__(256) operands_kernel(Params p, int backward) {
     return;
   }
   for (int which = 0; which < 2; ++which) {
-    if (which == 1 && !backward && p.direct) break;
     const void* src = which ? p.q : p.k;
     const int64_t stride = which ? p.qs : p.ks;
     uint16_t* tr = which ? p.qt : p.kt;
     uint16_t* rw = which ? p.qrow : p.krow;
     const bool transpose = which == 0 || backward;
-    for (int u = threadIdx.x; u < DK * (C / 8); u += 256) {
+    for (int u = threadIdx.x; transpose && u < DK * (C / 8); u += 256) {
       const int ch = u % DK, t0 = u / DK * 8;
       float x[8];
       int64_t at[8];
@@ -72,13 +62,11 @@ __global__ void __launch_bounds__(256) operands_kernel(Params p, int backward) {
       load_raw<8>(src, at, p.dtype, raw);
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = t0 + i < c.len ? from_raw(raw[i], p.dtype) : 0.0f;
-      if (!transpose) continue;
       const Frag<P> f = split8<P>(x);
-      for (int n = 0; n < terms; ++n)
-        *reinterpret_cast<u32x4*>(tr + (sh * terms + n) * DK * C + tiled<C>(ch, t0)) =
-            n == 0 ? f.t[0] : n == 1 ? f.t[1] : f.t[2];
+#pragma unroll
+      for (int n = 0; n < P; ++n)
+        *reinterpret_cast<u32x4*>(tr + (sh * P + n) * DK * C + tiled<C>(ch, t0)) = f.t[n];
     }
-    if (p.direct) continue;
     for (int u = threadIdx.x; u < DK / 8 * C; u += 256) {  // rows: 8 channels of a token
       const int c0 = u % (DK / 8) * 8, tk = u / (DK / 8);
       float x[8];
@@ -104,7 +92,8 @@ __global__ void __launch_bounds__(256) operands_kernel(Params p, int backward) {
 // 32 and 64 by X21 = -X22 (M21 X11) on FP32 matrix instructions.  One product's
 // result is the next one's right operand without leaving its registers: step r
 // of a product takes the columns k = 4 (lane >> 4) + r, as results hold rows.
-// 64 steps of substitution by one wave took 20 us a workgroup, this 2.
+// 64 steps of substitution by one wave took 20 us a workgroup, this 2 (read from
+// the clock inside the kernel).
 typedef float Square[C + 4];
 
 // D += A B for one 16 x 16 block: A from LDS rows, B given as four results.

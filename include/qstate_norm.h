@@ -13,7 +13,7 @@
  * Every part but the first norm is left out by a null pointer: gate (y = n),
  * residual (r = scale y), scale (1), next_weight (no h).  Everything between
  * the inputs and the outputs r and h is FP32, rounded once at the end (h is
- * taken from r before r is rounded).
+ * taken from r before r is rounded); squares of values beyond 1e19 overflow.
  *
  * Layout: rows are [tokens][groups]; a readout has groups = heads and
  * width = dv, a block's end groups = 1 and width the model's.
@@ -47,7 +47,7 @@ typedef enum { QSTATE_SILU = 0, QSTATE_SIGMOID = 1 } qstate_activation;
 
 typedef struct {
   int64_t tokens;        /* >= 0                                            */
-  int32_t groups;        /* rows of a token, 1..65536                       */
+  int32_t groups;        /* rows of a token, 1..65535                       */
   int32_t width;         /* 1..16384                                        */
   int32_t dtype;         /* qstate_dtype                                    */
   int32_t act;           /* qstate_activation of the gate                   */
