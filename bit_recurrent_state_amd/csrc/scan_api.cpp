@@ -38,11 +38,12 @@ int check_config(const qstate_scan_config* c) {
   const int64_t far = (int64_t)1 << 22;  // offsets inside a chunk take 32 bits
   if (c->q_stride > far || c->k_stride > far || c->v_stride > far || c->o_stride > far)
     return QSTATE_E_UNSUPPORTED;
-  // the grids (chunks of all sequences; a workgroup per head and 16 columns) of
-  // up to 512 threads a workgroup stay below 2^32 threads
-  const int64_t most = 8388607;
-  if (c->tokens / kChunk + c->batch > most ||
-      ((int64_t)c->batch * c->heads + 8) * ((c->dv + 31) / 32 * 2) > most)
+  // the grids stay below 2^32 threads: chunks of all sequences, or a workgroup per
+  // head and 16 columns, of up to 512 threads; a workgroup per chunk and q/k head
+  // and per head and 32 columns, of 256
+  const int64_t most = 8388607, chunks = c->tokens / kChunk + c->batch;
+  if (chunks > most || ((int64_t)c->batch * c->heads + 8) * ((c->dv + 31) / 32 * 2) > most ||
+      chunks * c->heads_qk > most / 2 * 3)
     return QSTATE_E_UNSUPPORTED;
   return QSTATE_OK;
 }

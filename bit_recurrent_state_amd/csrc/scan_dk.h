@@ -19,11 +19,10 @@ inline dim3 chain_grid(const Params& p) {
 template <int DK, int NT, int NPQ, int PO, bool VEC, bool DELTA>
 hipError_t forward_tail(const Params& p, hipStream_t s) {
   const dim3 slots(p.nslots, p.heads);
-  if (p.some_short) {
-    const dim3 rows((unsigned)((int64_t)p.batch * p.heads * ((p.dv + 31) / 32)));
-    tokens_kernel<DK, VEC, DELTA><<<rows, 256, 0, s>>>(p);
-    if (!p.some_long) return hipGetLastError();
-  }
+  const int64_t short_ones = token_blocks(p);
+  if (short_ones && (VEC || !p.some_long))
+    tokens_kernel<DK, VEC, DELTA><<<dim3((unsigned)short_ones), 256, 0, s>>>(p);
+  if (!p.some_long) return hipGetLastError();
   constexpr bool SOLVED = VEC && DELTA && DK <= 128;
   if constexpr (VEC && DK <= 128) {
     prep_vector_kernel<DK, PO, DELTA, false><<<slots, 512, 0, s>>>(p);
@@ -34,7 +33,8 @@ hipError_t forward_tail(const Params& p, hipStream_t s) {
     chunk_kernel<DK, P, true, DELTA, false><<<slots, 256, 0, s>>>(p);
     chunk_vector_kernel<DK, DELTA, false><<<slots, 256, 0, s>>>(p);
   } else {
-    operands_kernel<DK><<<dim3(p.nslots, p.heads_qk), 256, 0, s>>>(p, 0);
+    const dim3 blocks((unsigned)(short_ones + (int64_t)p.nslots * p.heads_qk));
+    tokens_operands_kernel<DK, DELTA><<<blocks, 256, 0, s>>>(p);
     chunk_kernel<DK, NPQ, false, DELTA, false><<<slots, 256, 0, s>>>(p);
   }
   states_kernel<DK, NT, NPQ, PO, VEC, DELTA, false, SOLVED><<<chain_grid(p), 512, 0, s>>>(p);
@@ -49,7 +49,7 @@ hipError_t backward_tail(const Params& p, hipStream_t s) {
     chunk_kernel<DK, P, true, DELTA, true><<<slots, 256, 0, s>>>(p);
     chunk_vector_kernel<DK, DELTA, true><<<slots, 256, 0, s>>>(p);
   } else {
-    operands_kernel<DK><<<dim3(p.nslots, p.heads_qk), 256, 0, s>>>(p, 1);
+    operands_kernel<DK><<<dim3(p.nslots, p.heads_qk), 256, 0, s>>>(p);
     chunk_kernel<DK, NPQ, false, DELTA, true><<<slots, 256, 0, s>>>(p);
   }
   states_kernel<DK, NT, NPQ, P, VEC, DELTA, true, false><<<chain_grid(p), 256, 0, s>>>(p);

@@ -11,15 +11,14 @@ namespace qscan {
 // One workgroup per (slot, q/k head).  Threads run over channels, so the
 // caller's rows are read whole; each thread turns 8 tokens of its channel into
 // 16 bytes of the transposed planes.
-template <int DK>
-__global__ void __launch_bounds__(256) operands_kernel(Params p, int backward) {
-  const int slot = blockIdx.x, hq = blockIdx.y;
+template <int DK, bool BWD>
+__device__ __forceinline__ void take_operands(const Params& p, int slot, int hq) {
   Chunk c;
   if (!find_and_note(p, slot, hq == 0, c)) return;
   const int64_t sh = (int64_t)slot * p.heads_qk + hq;
   if (p.direct) {
     // bfloat16 is moved as it is: 8 tokens of 2 channels per thread
-    for (int which = 0; which <= backward; ++which) {
+    for (int which = 0; which <= BWD; ++which) {
       const uint16_t* src = static_cast<const uint16_t*>(which ? p.q : p.k);
       const int64_t stride = which ? p.qs : p.ks;
       uint16_t* tr = which ? p.qt : p.kt;
@@ -50,7 +49,7 @@ __global__ void __launch_bounds__(256) operands_kernel(Params p, int backward) {
     const int64_t stride = which ? p.qs : p.ks;
     uint16_t* tr = which ? p.qt : p.kt;
     uint16_t* rw = which ? p.qrow : p.krow;
-    const bool transpose = which == 0 || backward;
+    const bool transpose = which == 0 || BWD;
     for (int u = threadIdx.x; transpose && u < DK * (C / 8); u += 256) {
       const int ch = u % DK, t0 = u / DK * 8;
       float x[8];
@@ -84,6 +83,11 @@ __global__ void __launch_bounds__(256) operands_kernel(Params p, int backward) {
         *reinterpret_cast<u32x4*>(rw + (sh * P + n) * DK * C + tiled<DK>(tk, c0)) = f.t[n];
     }
   }
+}
+
+template <int DK>
+__global__ void __launch_bounds__(256) operands_kernel(Params p) {
+  take_operands<DK, true>(p, blockIdx.x, blockIdx.y);
 }
 
 // ---- (I + M)^-1 of a strictly lower triangular M --------------------------------------------

@@ -9,15 +9,19 @@
 
 #pragma once
 
-#include "scan_device.h"
+#include "scan_prep.h"
 
 namespace qscan {
 
+// Workgroups of it: one per sequence, head and 32 value rows.
+__host__ __device__ inline int64_t token_blocks(const Params& p) {
+  return p.some_short ? (int64_t)p.batch * p.heads * ((p.dv + 31) / 32) : 0;
+}
+
 template <int DK, bool VEC, bool DELTA>
-__global__ void __launch_bounds__(256) tokens_kernel(Params p) {
+__device__ __forceinline__ void take_tokens(const Params& p, int64_t b) {
   constexpr int Q = DK / 32;  // groups of 4 channels: channel 32 q + 4 (lane & 7)
   const int nb = (p.dv + 31) / 32;
-  const int64_t b = blockIdx.x;
   const int64_t nh = b / nb;
   const int n = (int)(nh / p.heads), h = (int)(nh % p.heads);
   const int64_t o0 = offset_of(p, n), o1 = offset_of(p, n + 1);
@@ -94,6 +98,23 @@ __global__ void __launch_bounds__(256) tokens_kernel(Params p) {
 #pragma unroll
     for (int q = 0; q < Q; ++q) *reinterpret_cast<f32x4*>(p.s1 + st + 32 * q) = S[q];
   }
+}
+
+template <int DK, bool VEC, bool DELTA>
+__global__ void __launch_bounds__(256) tokens_kernel(Params p) {
+  take_tokens<DK, VEC, DELTA>(p, blockIdx.x);
+}
+
+// One gate per token: the operands of longer sequences' chunks are as
+// independent and come from the same launch.  One launch less takes 2 to 4 us
+// off a call: one token of 64 sequences, 16 heads of 128 x 128, 40.6 -> 39.0 us.
+template <int DK, bool DELTA>
+__global__ void __launch_bounds__(256) tokens_operands_kernel(Params p) {
+  const int64_t tb = token_blocks(p), b = blockIdx.x;
+  if (b < tb)
+    take_tokens<DK, false, DELTA>(p, b);
+  else
+    take_operands<DK, false>(p, (int)((b - tb) % p.nslots), (int)((b - tb) / p.nslots));
 }
 
 }  // namespace qscan

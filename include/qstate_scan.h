@@ -85,7 +85,8 @@ typedef struct {
   int32_t pad;      /* 0                                                      */
   int64_t tokens;   /* rows in all; without offsets a multiple of batch.
                        tokens / 64 + batch and (batch * heads + 8) * dv / 16
-                       (dv rounded up to 32) are at most 8388607              */
+                       (dv rounded up to 32) are at most 8388607, and
+                       (tokens / 64 + batch) * heads_qk at most 12582909      */
   int64_t q_stride, k_stride, v_stride, o_stride; /* elements; 0: packed      */
 } qstate_scan_config;
 

@@ -55,6 +55,7 @@ def _scan(**kw):
     (dict(tokens=1 << 28), OK), (dict(tokens=1 << 29), UNSUPPORTED),
     (dict(batch=500000, tokens=0, dv=32), OK), (dict(batch=1100000, tokens=0, dv=32), UNSUPPORTED),
     (dict(o_stride=(1 << 22) + 8), UNSUPPORTED),
+    (dict(tokens=1 << 28, heads_qk=4), UNSUPPORTED), (dict(tokens=1 << 26, heads_qk=4), OK),
 ])
 def test_scan_configs(L, kw, status):
     n = ctypes.c_size_t(7)
