@@ -16,6 +16,10 @@
 // token without a state then has a gate's gradient of exactly zero).
 //
 // Waves split the key channels: the states are then read once per workgroup.
+// 104 us for 1024 chunks and heads of 128 x 128 (GDN, bfloat16; 290 MB, 2.8 TB/s;
+// matrix instructions 19 % of the time), 115 us for 2048 of 128 x 64 without the
+// delta rule (350 MB, 3.1 TB/s): two workgroups a CU, each of which loads a slab,
+// splits it and multiplies in turn.
 
 #pragma once
 

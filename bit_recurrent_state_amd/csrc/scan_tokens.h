@@ -6,6 +6,8 @@
 // value rows, 8 lanes a row, and keeps them in registers over the tokens: FP32
 // throughout, one multiply and two fused multiply-adds per element and token,
 // dot products summed over the row's lanes.
+// 26 us for one token of 64 sequences, 16 heads of 128 x 128: 137 MB at 5.3 TB/s,
+// bound by memory.
 
 #pragma once
 
