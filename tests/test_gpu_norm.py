@@ -229,3 +229,37 @@ def test_many_rows_before_the_last_dimension():
     for a, z in ((x["x"][None], x["gate"][None]), (wide[..., :16], wide[..., 16:])):
         got = run({**x, "x": a, "gate": z})[0]
         assert got.shape == a.shape and torch.equal(got[0], want)
+
+
+def test_rows_beyond_32_bits():
+    """Rows behind 2^31 elements: the same bits as alone (about 35 GB)."""
+    from bit_recurrent_state_amd import NormConfig, qstate_norm, qstate_norm_backward
+    n, width = 70, 2048
+    before = (1 << 31) // width
+    x = make(n, 0, width, torch.bfloat16, True, True, True, False, True)
+    want = run(x)
+    dr, dh = (torch.randn(n, width, device="cuda").bfloat16() for _ in range(2))
+    small = NormConfig(n, 1, width, torch.bfloat16)
+    big = NormConfig(before + n, 1, width, torch.bfloat16)
+    vectors = [x[k] for k in ("weight", "scale", "next_weight")]
+
+    def go(c, xx, gate, res, dr, dh):
+        view = lambda t: t.view(c.tokens, 1, width)
+        r, h, dx, dz, dy = (torch.empty_like(view(xx)) for _ in range(5))
+        a = (view(xx), vectors[0], view(gate), view(res), vectors[1], vectors[2])
+        qstate_norm(c, *a, r, h)
+        qstate_norm_backward(c, *a, True, view(dr), view(dh), dx, dz, dy)
+        return [t.view(-1, width) for t in (r, h, dx, dz, dy)]
+
+    def behind(t):
+        b = torch.zeros(before + n, width, dtype=t.dtype, device="cuda")
+        b[before:] = t
+        return b
+
+    alone = go(small, x["x"], x["gate"], x["residual"], dr, dh)
+    assert torch.equal(alone[0], want[0]) and torch.equal(alone[1], want[1])
+    got = go(big, *(behind(t) for t in (x["x"], x["gate"], x["residual"], dr, dh)))
+    for a, b in zip(got, alone):
+        assert torch.equal(a[before:], b)
+    del got
+    torch.cuda.empty_cache()

@@ -489,3 +489,35 @@ def test_single_tokens_without_a_state(mixer, decay):
     assert not got["log_alpha"].any()
     assert all(got[n].any() for n in ("q", "k", "v"))
     check(x, m, 4)
+
+
+@pytest.mark.parametrize("mixer", MIXERS)
+def test_rows_beyond_32_bits(mixer):
+    """A sequence behind 2^31 elements of v: the same bits as alone (about 60 GB)."""
+    from bit_recurrent_state_amd import ScanConfig, qstate_scan, qstate_scan_backward
+    m, H, dk, dv, n = MIXERS[mixer], 16, 64, 2048, 100
+    before = -(-(1 << 31) // (H * dv)) // 64 * 64 + 64  # on a chunk's boundary, as alone
+    x = inputs(m, 1, [n], H, H, dk, dv, torch.bfloat16, "cuda")
+    g = torch.Generator().manual_seed(2)
+    do = torch.randn(x["v"].shape, generator=g).bfloat16().cuda()
+    dS = torch.randn(1, H, dv, dk, generator=g).cuda()
+    o, S, want = gradients(x, m, do, dS)
+    big = {}
+    for name in ("q", "k", "v", "log_alpha", "beta"):
+        if x[name] is not None:
+            big[name] = torch.empty((before + n,) + x[name].shape[1:], dtype=x[name].dtype, device="cuda")
+            big[name][before:] = x[name]
+    args = [big.get(k) for k in ("q", "k", "v", "log_alpha", "beta")]
+    args += [x["offsets"] + before, x["initial_state"]]
+    c = ScanConfig(1, H, dk, dv, before + n, mixer=m, dtype=torch.bfloat16)
+    o2, S2 = torch.empty_like(big["v"]), torch.empty_like(S)
+    qstate_scan(c, *args, o2, S2)
+    assert torch.equal(o2[before:], o) and torch.equal(S2, S)
+    o2[before:] = do
+    out = {k: torch.empty_like(v) for k, v in big.items()}
+    out["initial_state"] = torch.empty_like(S)
+    qstate_scan_backward(c, *args, o2, dS, *(out.get(k) for k in NAMES))
+    for k, t in out.items():
+        assert torch.equal(t if k == "initial_state" else t[before:], want[k]), k
+    del args, big, out, o2
+    torch.cuda.empty_cache()
