@@ -14,7 +14,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from ._lib import NormConfigC, check, lib
-from .sequence import DTYPES, _array, _bytes_on, _call, _on_device, _ptr, _stream, _workspace
+from .sequence import (DTYPES, _alive, _array, _bytes_on, _call, _on_device, _ptr, _refuse_capture,
+                       _stream, _workspace)
 
 __all__ = ["SILU", "SIGMOID", "NormConfig", "qstate_norm", "qstate_norm_workspace",
            "qstate_norm_backward", "block_norm"]
@@ -185,6 +186,7 @@ class _BlockNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, gate, residual, scale, next_weight, eps, act):
         r, h, ctx.cfg, saved = _forward(x, weight, gate, residual, scale, next_weight, eps, act)
+        _alive[ctx] = _stream(None, x.device)
         ctx.shape = x.shape
         ctx.save_for_backward(*saved)
         ctx.set_materialize_grads(False)
@@ -199,6 +201,7 @@ class _BlockNorm(torch.autograd.Function):
         x, weight, gate, residual, scale, next_weight = saved
         need = ctx.needs_input_grad
         dev = x.device
+        _refuse_capture(ctx, dev)
         dr, dh = (None if t is None else t.contiguous() for t in (dr, dh))
         dx, dgate, dres = (torch.empty(ctx.shape, dtype=x.dtype, device=dev) if need[i] else None
                            for i in (0, 2, 3))
@@ -220,7 +223,8 @@ def block_norm(x, *, weight=None, gate=None, residual=None, scale=None, next_wei
     Parts that are None are left out; returns r, or (r, h) with next_weight.  x, gate and residual
     have one shape [.., width] and one dtype (float32, bfloat16, float16); weight is float32
     [width], or [heads, width] for x [.., heads, width]; scale and next_weight float32 [width].
-    FP32 between inputs and outputs.  Differentiable once in every tensor."""
+    FP32 between inputs and outputs.  Differentiable once in every tensor (a backward pass is
+    captured into a graph only where no eager graph of the same leaves lives)."""
     _on_device(x, "x", None)
     if x.dtype not in DTYPES or x.dim() < 1:
         raise ValueError(f"x: one of float32, bfloat16, float16 [.., width], got {x.dtype} "

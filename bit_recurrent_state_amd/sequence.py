@@ -9,6 +9,7 @@ C ABI; every product runs in the library's kernels."""
 from __future__ import annotations
 
 import ctypes
+import weakref
 from dataclasses import dataclass
 from typing import Optional
 
@@ -257,11 +258,32 @@ def _forward(q, k, v, log_alpha, beta, initial_state, offsets, mixer, batch):
     return o, final, c, saved
 
 
+_alive = weakref.WeakKeyDictionary()  # differentiable calls whose graph lives: their stream
+
+
+def _leaves(node) -> set:
+    return {id(n.variable) for n, _ in node.next_functions if hasattr(n, "variable")}
+
+
+def _refuse_capture(ctx, device) -> None:
+    """Before a backward pass that is being captured: a leaf belongs to the stream of the graph
+    that it was first used in for as long as that lives.  PyTorch would have the capture wait for
+    another stream, which breaks it off and can end the process."""
+    if not torch.cuda.is_current_stream_capturing():
+        return
+    here, mine = _stream(None, device), _leaves(ctx)
+    for other, stream in list(_alive.items()):
+        if stream != here and mine & _leaves(other):
+            raise RuntimeError("a backward pass cannot be captured while a graph of the same "
+                               "leaves from another stream lives: drop the results of that call")
+
+
 class _Scan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, log_alpha, beta, initial_state, offsets, mixer, batch):
         o, final, ctx.cfg, saved = _forward(q, k, v, log_alpha, beta, initial_state, offsets,
                                             mixer, batch)
+        _alive[ctx] = _stream(None, v.device)
         ctx.shapes = q.shape, v.shape
         ctx.save_for_backward(*saved)
         ctx.set_materialize_grads(False)
@@ -272,6 +294,7 @@ class _Scan(torch.autograd.Function):
     def backward(ctx, d_o, d_final):
         q, k, v, g, b, s0, offsets = ctx.saved_tensors
         dev = v.device
+        _refuse_capture(ctx, dev)
         qk, vo = ctx.shapes
         new = torch.empty if offsets is None else torch.zeros
         d_o = torch.zeros(vo, dtype=v.dtype, device=dev) if d_o is None else _aligned(d_o)
@@ -298,7 +321,8 @@ def scan(q, k, v, log_alpha, beta=None, *, mixer: int = GDN, initial_state=None,
     [N, heads, dv, dk] float32 (zeros if None).  o has the shape and dtype of v, zero in rows of
     no sequence; final_state is float32 and can go to `QState.load_fp32` to decode on from there.
 
-    Differentiable once in every input but offsets; backward computes the states again."""
+    Differentiable once in every input but offsets; backward computes the states again.  A backward
+    pass is captured into a graph only where no eager graph of the same leaves lives."""
     for t, name in ((q, "q"), (k, "k"), (v, "v"), (log_alpha, "log_alpha")):
         _on_device(t, name, v.device if isinstance(v, torch.Tensor) else None)
     if mixer not in (GDN, GLA, SCALAR, KDA):

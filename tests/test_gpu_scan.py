@@ -521,3 +521,60 @@ def test_rows_beyond_32_bits(mixer):
         assert torch.equal(t if k == "initial_state" else t[before:], want[k]), k
     del args, big, out, o2
     torch.cuda.empty_cache()
+
+
+def test_training_step_in_a_graph():
+    """scan, block_norm and their gradients captured through autograd, over leaves that no eager
+    pass has used; replayed on new inputs with eager work between."""
+    from bit_recurrent_state_amd import block_norm
+    m, lens = KDA, [70, 0, 30]
+    xs = [inputs(m, 3, lens, 2, 1, 64, 32, torch.bfloat16, "cuda", seed=s) for s in range(3)]
+    weight, gate = torch.rand(2, 32, device="cuda"), torch.randn_like(xs[0]["v"])
+    dr, dS = torch.randn_like(xs[0]["v"]), torch.randn(3, 2, 32, 64, device="cuda")
+
+    def step(x, leaves):
+        o, S = call({**x, **leaves}, m)
+        r = block_norm(o, weight=leaves["weight"], gate=gate)
+        return [r, S, *torch.autograd.grad((r, S), list(leaves.values()), (dr, dS))]
+
+    def leaves_of(x):
+        leaves = {n: x[n].detach().clone().requires_grad_(True) for n in NAMES}
+        return {**leaves, "weight": weight.clone().requires_grad_(True)}
+
+    want = [[t.detach() for t in step(x, leaves_of(x))] for x in xs]
+    leaves = leaves_of(xs[0])
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = [t.detach() for t in step(xs[0], leaves)]
+    for i in (1, 0, 2, 1):
+        with torch.no_grad():
+            for n in NAMES:
+                leaves[n].copy_(xs[i][n])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want[i]))
+        again = step(xs[i], leaves_of(xs[i]))
+        assert all(torch.equal(a, b) for a, b in zip(again, want[i]))
+
+
+def test_captured_backward_beside_an_eager_graph_is_refused(monkeypatch):
+    """The same check in the operators, without a capture: it stands before any launch."""
+    from bit_recurrent_state_amd import block_norm
+    x = inputs(GDN, 1, [20], 1, 1, 64, 32, torch.float32, "cuda")
+    leaves = {n: x[n].detach().clone().requires_grad_(True) for n in NAMES}
+    w = torch.ones(32, device="cuda", requires_grad=True)
+    o, _ = call({**x, **leaves}, GDN)
+    eager = block_norm(o, weight=w)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        o2, _ = call({**x, **leaves}, GDN)
+        y = block_norm(o2.detach(), weight=w)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+        for out, leaf in ((o2, leaves["q"]), (y, w)):
+            with pytest.raises(RuntimeError, match="drop the results"):
+                torch.autograd.grad(out.sum(), leaf, retain_graph=True)
+        del eager, o
+        torch.autograd.grad(o2.sum(), leaves["q"])
+        torch.autograd.grad(y.sum(), w)
+    torch.cuda.synchronize()

@@ -196,3 +196,40 @@ def test_norm_reference_gradients_against_differences():
         up, down = ([a + s * 1e-6 * d if j == i else a for j, a in enumerate(args)] for s in (1, -1))
         diff = float(loss(up) - loss(down)) / 2e-6
         assert abs(diff - float((leaves[i].grad * d).sum())) <= 1e-7 * (1.0 + abs(diff)), i
+
+
+def test_captured_backward_beside_an_eager_graph_is_refused(monkeypatch):
+    """The rule itself, on the CPU: another stream's live graph of the same leaf, and only that."""
+    import gc
+
+    from bit_recurrent_state_amd import sequence
+
+    class Twice(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, stream):
+            sequence._alive[ctx] = stream
+            return 2 * x
+
+        @staticmethod
+        def backward(ctx, d):
+            sequence._refuse_capture(ctx, None)
+            return 2 * d, None
+
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    monkeypatch.setattr(sequence, "_stream", lambda stream, device: 7)
+    x, other = torch.ones(3, requires_grad=True), torch.ones(3, requires_grad=True)
+    capturing = False
+    eager, y = Twice.apply(x, 1), Twice.apply(x, 7)
+    far = Twice.apply(other, 1)
+    torch.autograd.grad(y.sum(), x, retain_graph=True)
+    capturing = True
+    with pytest.raises(RuntimeError, match="drop the results"):
+        torch.autograd.grad(y.sum(), x, retain_graph=True)
+    del eager
+    gc.collect()
+    (d,) = torch.autograd.grad(y.sum(), x)
+    assert torch.equal(d, torch.full((3,), 2.0)) and far.requires_grad
+    n = len(sequence._alive)
+    del y, far
+    gc.collect()
+    assert len(sequence._alive) == n - 2
