@@ -80,7 +80,6 @@ size_t layout(const qstate_scan_config* c, bool backward, void* workspace, Param
   p.direct = !vec && bf16 && p.qs % 8 == 0 && p.ks % 8 == 0;
   p.nslots = (int)(c->tokens / kChunk + c->batch);
   p.dvp = (c->dv + 31) / 32 * 32;
-  p.out_terms = vec ? (c->dtype == QSTATE_FP32 ? kTerms : 2) : (p.direct ? 2 : kTerms);
   // Value columns of a chain workgroup, of which a CU (256) holds one at a time:
   // the fewest rounds, each as long as its width makes it.  Narrow blocks
   // shorten the chain from chunk to chunk, wide ones share its fixed work: 32

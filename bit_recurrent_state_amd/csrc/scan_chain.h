@@ -38,22 +38,22 @@ __device__ __forceinline__ bool chain_block(const Params& p, int& n, int& h, int
 // 256 workgroups) to 2.8 us (KDA, 128); the matrix instructions are busy for
 // 8 to 13 % of it, LDS round trips between the barriers and 70 to 150 KB of
 // operands out of L2 for each chunk take the rest.
-// Outputs of 16 bits take PO = 2 terms of q, A, S and W, which hold them to
-// 2^-16; everything that reaches the state takes all three.
+// Outputs take every term, as the state does, whatever their type: with two terms
+// of q, A, S and W a 16-bit output that is small by cancellation would be off by
+// more than its own rounding.
 //
 // SOLVED: U0 = T V and K^ = T K~ are given (scan_prep_vector.h), and U = U0 - K^ S^T.
 //
 // SAVE (for the backward pass): four waves, no output; the states at the
 // chunks' starts and U are stored.
-template <int DK, int NT, int NPQ, int PO, bool VEC, bool DELTA, bool SAVE, bool SOLVED>
+template <int DK, int NT, int NPQ, bool VEC, bool DELTA, bool SAVE, bool SOLVED>
 __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
   constexpr int BV = 16 * NT, KS = DK / 32, MT = DK / 64, SP = DK + 8;
-  constexpr int NQ = NPQ < PO ? NPQ : PO;
   constexpr bool D = NPQ == 1;
   __shared__ __align__(16) uint16_t Sl[P][BV][SP];
   constexpr bool TR = DELTA && !SOLVED;  // U = T R is computed here
   __shared__ __align__(16) uint16_t Rt[TR ? P : 1][TR ? BV : 1][CP];
-  __shared__ __align__(16) uint16_t Wt[SAVE || VEC ? 1 : PO][SAVE || VEC ? 1 : BV][CP];
+  __shared__ __align__(16) uint16_t Wt[SAVE || VEC ? 1 : P][SAVE || VEC ? 1 : BV][CP];
   __shared__ __align__(16) uint16_t Wb[P][BV][CP];  // e^(c_end - c) W (one gate), else W
   int n, h, vb;
   if (!chain_block(p, n, h, vb)) return;
@@ -84,18 +84,18 @@ __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
   auto head_of = [&](int ci) { return (int64_t)(base + ci) * p.heads + h; };
 
   if (reader) {
-    Frag<NQ> fq[KS];
-    Frag<PO> fA[2];
+    Frag<NPQ> fq[KS];
+    Frag<P> fA[2];
     f32x4 ec = {1, 1, 1, 1};
     auto load_q = [&](int ci) {
       const auto q = rows_of<DK, D>(p, p.q, p.qrow, p.qs, VEC, base + ci, h, chunk(ci));
 #pragma unroll
-      for (int s = 0; s < KS; ++s) fq[s] = q.template frag<NQ>(wave, s);
+      for (int s = 0; s < KS; ++s) fq[s] = q.template frag<NPQ>(wave, s);
       if (!VEC) ec = *reinterpret_cast<const f32x4*>(rows_at(p, base + ci, h) + tok);
     };
     auto load_a = [&](int ci) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) fA[s] = tile_frag<PO, C>(p.a + head_of(ci) * P * C * C, wave, s, C * C);
+      for (int s = 0; s < 2; ++s) fA[s] = tile_frag<P, C>(p.a + head_of(ci) * P * C * C, wave, s, C * C);
     };
     if (nch > 0) {
       load_q(0);
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
       for (int s = 0; s < KS; ++s)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-          mma(Q[t], fq[s], load_frag<PO>(&Sl[0][t * 16 + fr][s * 32 + fg * 8], BV * SP));
+          mma(Q[t], fq[s], load_frag<P>(&Sl[0][t * 16 + fr][s * 32 + fg * 8], BV * SP));
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
 #pragma unroll
           for (int t = 0; t < NT; ++t)
             mma(O[t], fA[s],
-                load_frag<PO>(VEC ? &Wb[0][t * 16 + fr][s * 32 + fg * 8]
+                load_frag<P>(VEC ? &Wb[0][t * 16 + fr][s * 32 + fg * 8]
                                   : &Wt[0][t * 16 + fr][s * 32 + fg * 8], BV * CP));
       load_a(next);
       __syncthreads();
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(SAVE ? 256 : 512) states_kernel(Params p) {
         wb[r] = VEC ? w[r] : w[r] * eo[r];
       }
       put4<P>(&Wb[0][t * 16 + fr][tok], BV * CP, wb);
-      if (!SAVE && !VEC) put4<PO>(&Wt[0][t * 16 + fr][tok], BV * CP, w);
+      if (!SAVE && !VEC) put4<P>(&Wt[0][t * 16 + fr][tok], BV * CP, w);
     }
     load_v(next);
     __syncthreads();

@@ -304,15 +304,6 @@ __device__ __forceinline__ Frag<N> tile_frag(const uint16_t* p, int rb, int s, i
   return load_frag<N>(p + (rb * (COLS / 32) + s) * 512 + (threadIdx.x & 63) * 8, plane);
 }
 
-// The first N terms.
-template <int N, int M>
-__device__ __forceinline__ Frag<N> head(const Frag<M>& f) {
-  Frag<N> h;
-#pragma unroll
-  for (int n = 0; n < N; ++n) h.t[n] = f.t[n];
-  return h;
-}
-
 // q or k of a chunk as the left operand: the caller's bfloat16 rows, or tiles
 // in the workspace.  Rows behind the sequence's end repeat its last row: beta is
 // zero there, so what they compute reaches neither a state nor an output.

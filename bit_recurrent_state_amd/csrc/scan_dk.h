@@ -16,7 +16,7 @@ inline dim3 chain_grid(const Params& p) {
   return dim3((unsigned)(heads * p.nvb));
 }
 
-template <int DK, int NT, int NPQ, int PO, bool VEC, bool DELTA>
+template <int DK, int NT, int NPQ, bool VEC, bool DELTA>
 hipError_t forward_tail(const Params& p, hipStream_t s) {
   const dim3 slots(p.nslots, p.heads);
   const int64_t short_ones = token_blocks(p);
@@ -25,9 +25,9 @@ hipError_t forward_tail(const Params& p, hipStream_t s) {
   if (!p.some_long) return hipGetLastError();
   constexpr bool SOLVED = VEC && DELTA && DK <= 128;
   if constexpr (VEC && DK <= 128) {
-    prep_vector_kernel<DK, PO, DELTA, false><<<slots, 512, 0, s>>>(p);
+    prep_vector_kernel<DK, DELTA, false><<<slots, 512, 0, s>>>(p);
     chunk_vector_kernel<DK, DELTA, false><<<slots, 256, 0, s>>>(p);
-    if (DELTA) prep_vector_kernel<DK, PO, DELTA, true><<<slots, 512, 0, s>>>(p);
+    if (DELTA) prep_vector_kernel<DK, DELTA, true><<<slots, 512, 0, s>>>(p);
   } else if constexpr (VEC) {
     operands_vector_kernel<DK, DELTA, false><<<slots, 256, 0, s>>>(p);
     chunk_kernel<DK, P, true, DELTA, false><<<slots, 256, 0, s>>>(p);
@@ -37,7 +37,7 @@ hipError_t forward_tail(const Params& p, hipStream_t s) {
     tokens_operands_kernel<DK, DELTA><<<blocks, 256, 0, s>>>(p);
     chunk_kernel<DK, NPQ, false, DELTA, false><<<slots, 256, 0, s>>>(p);
   }
-  states_kernel<DK, NT, NPQ, PO, VEC, DELTA, false, SOLVED><<<chain_grid(p), 512, 0, s>>>(p);
+  states_kernel<DK, NT, NPQ, VEC, DELTA, false, SOLVED><<<chain_grid(p), 512, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -52,7 +52,7 @@ hipError_t backward_tail(const Params& p, hipStream_t s) {
     operands_kernel<DK><<<dim3(p.nslots, p.heads_qk), 256, 0, s>>>(p);
     chunk_kernel<DK, NPQ, false, DELTA, true><<<slots, 256, 0, s>>>(p);
   }
-  states_kernel<DK, NT, NPQ, P, VEC, DELTA, true, false><<<chain_grid(p), 256, 0, s>>>(p);
+  states_kernel<DK, NT, NPQ, VEC, DELTA, true, false><<<chain_grid(p), 256, 0, s>>>(p);
   state_grads_kernel<DK, NT, NPQ, NPO, VEC, DELTA><<<chain_grid(p), 512, 0, s>>>(p);
   grads_kernel<DK, NPQ, VEC ? NPO : NPQ, NPO, VEC, DELTA>
       <<<slots, DK >= 128 ? 512 : 256, 0, s>>>(p);
@@ -67,14 +67,12 @@ hipError_t backward_tail(const Params& p, hipStream_t s) {
 template <int DK, int NT>
 hipError_t forward(const Params& p, hipStream_t s) {
   switch (p.mixer) {
-    case GDN: return p.direct ? forward_tail<DK, NT, 1, 2, false, true>(p, s)
-                              : forward_tail<DK, NT, P, P, false, true>(p, s);
-    case SCALAR: return p.direct ? forward_tail<DK, NT, 1, 2, false, false>(p, s)
-                                 : forward_tail<DK, NT, P, P, false, false>(p, s);
-    case GLA: return p.dtype ? forward_tail<DK, NT, P, 2, true, false>(p, s)
-                             : forward_tail<DK, NT, P, P, true, false>(p, s);
-    case KDA: return p.dtype ? forward_tail<DK, NT, P, 2, true, true>(p, s)
-                             : forward_tail<DK, NT, P, P, true, true>(p, s);
+    case GDN: return p.direct ? forward_tail<DK, NT, 1, false, true>(p, s)
+                              : forward_tail<DK, NT, P, false, true>(p, s);
+    case SCALAR: return p.direct ? forward_tail<DK, NT, 1, false, false>(p, s)
+                                 : forward_tail<DK, NT, P, false, false>(p, s);
+    case GLA: return forward_tail<DK, NT, P, true, false>(p, s);
+    case KDA: return forward_tail<DK, NT, P, true, true>(p, s);
     default: return hipErrorInvalidValue;
   }
 }

@@ -29,7 +29,6 @@ struct Params {
   int direct;    // q and k enter the products as the caller's bfloat16 rows, one term
   int short_len; // sequences up to this length go to tokens_kernel (forward)
   int some_short, some_long;  // whether there may be sequences up to that length, and beyond
-  int out_terms; // terms of what only reaches an output (forward): 2 for 16-bit types
   int nslots;    // upper bound of the slots in use
   int nvb;       // blocks of dv columns of one head
   int vblock;    // dv columns of a block

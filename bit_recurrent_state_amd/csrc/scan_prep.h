@@ -319,12 +319,7 @@ __global__ void __launch_bounds__(256) chunk_kernel(Params p) {
     }
     // tiles of 32 columns beside the diagonal that hold only zeros are not read
     uint16_t* dst = (BWD ? p.at : p.a) + sh * P * C * C + tiled<C>(own, r0);
-    if (BWD ? (b >> 1) >= (wave >> 1) : (b >> 1) <= (wave >> 1)) {
-      if (BWD || p.out_terms == P)
-        put4<P>(dst, C * C, a);
-      else
-        put4<2>(dst, C * C, a);
-    }
+    if (BWD ? (b >> 1) >= (wave >> 1) : (b >> 1) <= (wave >> 1)) put4<P>(dst, C * C, a);
   }
   if (DELTA) store_inverses<BWD>(p, M, M2, sh);
 }

@@ -79,13 +79,13 @@ __device__ __forceinline__ void solve(const Params& p, const Chunk& c, int64_t s
 
 // FAR: only chunks that decay far, whose T chunk_vector_kernel has left in p.t;
 // otherwise everything, but for those chunks no A, L, T and what follows.
-template <int DK, int PO, bool DELTA, bool FAR>
+template <int DK, bool DELTA, bool FAR>
 __global__ void __launch_bounds__(512, DELTA ? 2 : 4) prep_vector_kernel(Params p) {
   // 80 KB for dk = 128, so that without the delta rule a CU holds two workgroups
   // and one computes while the other waits: 64 us with two, 96 us with one (123
   // chunks of 16 heads, three terms).  With it T's steps need more than 128
   // registers; held to that they spill: 218 us against 193 us with one workgroup
-  // (128 chunks of 16 heads, two terms).
+  // (128 chunks of 16 heads, with two terms of q and A).
   constexpr int KS = DK / 32;
   constexpr int kKn = P * C * DK, kTM = P * C * C + 2 * C * (C + 4);
   __shared__ __align__(16) float buf[C * DK];  // sums of log decays in blocks of 16
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(512, DELTA ? 2 : 4) prep_vector_kernel(Params 
         *reinterpret_cast<u32x4*>(Kn + n * C * DK + (rb * KS + s) * 512 + lane * 8) = f.t[n];
     } else {
 #pragma unroll
-      for (int n = 0; n < PO; ++n)
+      for (int n = 0; n < P; ++n)
         *reinterpret_cast<u32x4*>(p.qrow + (sh * P + n) * C * DK + (rb * KS + s) * 512 + lane * 8) =
             own[s].t[n];
     }
@@ -279,10 +279,7 @@ __global__ void __launch_bounds__(512, DELTA ? 2 : 4) prep_vector_kernel(Params 
       for (int b = 0; b < 4; ++b)
         if (b <= rb) {
           const Frag<P> f = tile_frag<P, DK>(Kn, b, s, C * DK);
-          if (second)
-            mma(all[b], f, own[s]);
-          else
-            mma(all[b], head<PO>(f), head<PO>(own[s]));
+          mma(all[b], f, own[s]);
         }
   }
   if (DELTA) __syncthreads();  // M goes where k e^-c was
@@ -306,7 +303,7 @@ __global__ void __launch_bounds__(512, DELTA ? 2 : 4) prep_vector_kernel(Params 
     if (second) {
       if (DELTA) *reinterpret_cast<f32x4*>(&M[i][j0]) = f32x4{x[0], x[1], x[2], x[3]};
     } else if ((b >> 1) <= (rb >> 1)) {
-      put4<PO>(p.a + sh * P * C * C + tiled<C>(i, j0), C * C, x);
+      put4<P>(p.a + sh * P * C * C + tiled<C>(i, j0), C * C, x);
     }
   }
   columns();
