@@ -38,7 +38,7 @@ def test_outputs_small_by_cancellation(mixer, dtype, dk):
 
     near = 1 - 2.0 ** -9 * torch.rand(H, dv, generator=g).cuda()
     gate = (T, H, dk) if m in (GLA, KDA) else (T, H)
-    x = {"q": _zero_rows(T, H, dk, dt), "k": _one_hot_rows(T, H, dk, dt),
+    x = {"q": _zero_rows(T, H, dk, dt), "k": _zero_rows(T, H, dk, dt),
          "v": _zero_rows(T, H, dv, dt), "log_alpha": torch.zeros(gate, device="cuda"),
          "beta": None if m == GLA else torch.full((T, H), 0.5, device="cuda"),
          "initial_state": torch.zeros(1, H, dv, dk, device="cuda"),
