@@ -77,17 +77,22 @@ hipError_t forward(const Params& p, hipStream_t s) {
   }
 }
 
+// d_o's terms (NPO) are those of the workspace's layout, whether or not q and k are split: bfloat16
+// rows off 16 bytes have split q and k and a d_o of one term.
 template <int DK, int NT>
 hipError_t backward(const Params& p, hipStream_t s) {
+  const bool one = p.dop_terms == 1;
   switch (p.mixer) {
     case GDN: return p.direct ? backward_tail<DK, NT, 1, 1, false, true>(p, s)
+                     : one    ? backward_tail<DK, NT, P, 1, false, true>(p, s)
                               : backward_tail<DK, NT, P, P, false, true>(p, s);
     case SCALAR: return p.direct ? backward_tail<DK, NT, 1, 1, false, false>(p, s)
+                        : one    ? backward_tail<DK, NT, P, 1, false, false>(p, s)
                                  : backward_tail<DK, NT, P, P, false, false>(p, s);
-    case GLA: return p.dtype == 1 ? backward_tail<DK, NT, P, 1, true, false>(p, s)
-                                  : backward_tail<DK, NT, P, P, true, false>(p, s);
-    case KDA: return p.dtype == 1 ? backward_tail<DK, NT, P, 1, true, true>(p, s)
-                                  : backward_tail<DK, NT, P, P, true, true>(p, s);
+    case GLA: return one ? backward_tail<DK, NT, P, 1, true, false>(p, s)
+                         : backward_tail<DK, NT, P, P, true, false>(p, s);
+    case KDA: return one ? backward_tail<DK, NT, P, 1, true, true>(p, s)
+                         : backward_tail<DK, NT, P, P, true, true>(p, s);
     default: return hipErrorInvalidValue;
   }
 }

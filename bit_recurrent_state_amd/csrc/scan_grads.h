@@ -27,7 +27,9 @@
 
 namespace qscan {
 
-struct ValueRows {  // [kChunk][dvp] rows of d_o
+// [kChunk][dvp] rows of d_o.  Its fragments have p.dop_terms terms: as many planes in the workspace,
+// or the caller's bfloat16 rows, which are one term and have no plane to go on to.
+struct ValueRows {
   const uint16_t* p;
   int64_t row, plane;
   int len;
@@ -49,7 +51,7 @@ __device__ __forceinline__ ValueRows dout_rows(const Params& p, int64_t sh, int 
   return r;
 }
 
-// Rows behind the end repeat the last one (of dO they are set to zero where that matters).
+// Zero behind the end: the caller's rows there are another sequence's.
 template <int N>
 __device__ __forceinline__ Frag<N> value_frag(const ValueRows& v, int row, int col) {
   Frag<N> f = load_frag<N>(v.p + min(row, v.len - 1) * v.row + col, v.plane);

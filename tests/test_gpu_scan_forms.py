@@ -75,3 +75,64 @@ def test_outputs_small_by_cancellation(mixer, dtype, dk):
     terms[2:] = 4 * 2 * q.double()[2:, :, None] * v.double()
     terms[:2] = 1e30  # the writing tokens read nothing of interest
     outputs(y, terms, 30)
+
+
+@pytest.mark.parametrize("mixer", MIXERS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dv", [32, 40])
+@pytest.mark.parametrize("pad", [8, 4, 3])
+def test_gradients_of_strided_rows(mixer, dtype, dv, pad):
+    """q, k and v cut from one projection, with its gradient: rows on 16 bytes (8), on 8 or 16 (4),
+    and on none (3); key heads shared and not."""
+    m, dt, N, lens, H, dk = MIXERS[mixer], TYPES[dtype], 2, [70, 30], 4, 64
+    for Hq in (4, 2):
+        x = inputs(m, N, lens, H, Hq, dk, dv, dt, "cuda", seed=pad)
+        T = sum(lens)
+        sizes = [Hq * dk, Hq * dk, H * dv, pad]
+        wide = torch.cat([x["q"].flatten(1), x["k"].flatten(1), x["v"].flatten(1),
+                          torch.zeros(T, pad, dtype=dt, device="cuda")], 1).requires_grad_(True)
+        q, k, v = (t.unflatten(1, (h, d)) for t, h, d in zip(wide.split(sizes, 1), (Hq, Hq, H), (dk, dk, dv)))
+        rest = {n: x[n].clone().requires_grad_(True) for n in ("log_alpha", "beta", "initial_state")
+                if x[n] is not None}
+        o, S = call({**x, **rest, "q": q, "k": k, "v": v}, m)
+        g = torch.Generator().manual_seed(1)
+        do, dS = torch.randn(o.shape, generator=g).to(dt).cuda(), torch.randn(S.shape, generator=g).cuda()
+        got = torch.autograd.grad((o, S), [wide, *rest.values()], (do, dS))
+        o64, S64, leaf = scan64(x, m, N, True)
+        names = [n for n in NAMES if x[n] is not None]
+        want = dict(zip(names, torch.autograd.grad((o64, S64), [leaf[n] for n in names],
+                                                   (do.double(), dS.double()))))
+        parts = dict(zip(("q", "k", "v"), (t.unflatten(1, (h, d)) for t, h, d in zip(
+            got[0].split(sizes, 1), (Hq, Hq, H), (dk, dk, dv)))))
+        parts.update(zip(rest, got[1:]))
+        assert rel(o, o64) <= tolerance(dt, False) and rel(S, S64) <= tolerance(torch.float32, False)
+        for n, t in parts.items():
+            assert rel(t, want[n]) <= tolerance(t.dtype, True), n
+
+
+@pytest.mark.parametrize("mixer", MIXERS)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_backward_with_row_strides_of_its_own(mixer, dtype):
+    """qstate_scan_backward with another odd stride for each of q, k and v: the bits of packed rows
+    in the same form (odd strides split every row), d_o and the gradients packed."""
+    from bit_recurrent_state_amd import ScanConfig, qstate_scan_backward
+    m, dt, H, Hq, dk, dv, lens = MIXERS[mixer], TYPES[dtype], 3, 1, 128, 33, [66, 9]
+    T = sum(lens)
+    x = inputs(m, 2, lens, H, Hq, dk, dv, dt, "cuda")
+    g = torch.Generator().manual_seed(4)
+    do, dS = torch.randn(T, H, dv, generator=g).to(dt).cuda(), torch.randn(2, H, dv, dk, generator=g).cuda()
+    rows, strides = {}, {}
+    for n, more in (("q", 3), ("k", 13), ("v", 1)):
+        h, d = x[n].shape[1:]
+        w = torch.zeros(T, h * d + more, dtype=dt, device="cuda")
+        w[:, :h * d] = x[n].flatten(1)
+        rows[n], strides[n] = w[:, :h * d].view(T, h, d), h * d + more
+    c = ScanConfig(2, H, dk, dv, T, Hq, m, dt, strides["q"], strides["k"], strides["v"], H * dv + 5)
+    out = {n: None if x[n] is None else torch.empty_like(x[n]) for n in NAMES}
+    qstate_scan_backward(c, rows["q"], rows["k"], rows["v"], x["log_alpha"], x["beta"], x["offsets"],
+                         x["initial_state"], do, dS, *(out[n] for n in NAMES))
+    o64, S64, leaf = scan64(x, m, 2, True)
+    names = [n for n in NAMES if x[n] is not None]
+    want = torch.autograd.grad((o64, S64), [leaf[n] for n in names], (do.double(), dS.double()))
+    for n, w in zip(names, want):
+        assert rel(out[n], w) <= tolerance(out[n].dtype, True), n
