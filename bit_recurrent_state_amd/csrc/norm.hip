@@ -179,8 +179,10 @@ __device__ __forceinline__ float activate(float z, int act, float& slope) {
   float s = __builtin_amdgcn_rcpf(d);
   s = fmaf(fmaf(-d, s, 1.0f), s, s);
   const float q = s * e;  // 1 - s without cancellation
-  slope = act == 0 ? s * fmaf(z, q, 1.0f) : s * q;
-  return act == 0 ? z * s : s;
+  // s and q stop at e^-87, so what multiplies them has to: z itself would bring z e^-87 instead of
+  // nothing where it is a masked gate's lowest value (or, in the slope, the largest)
+  slope = act == 0 ? s * fmaf(c, q, 1.0f) : s * q;
+  return act == 0 ? (z < c ? c : z) * s : s;
 }
 
 struct Place {

@@ -263,3 +263,39 @@ def test_rows_beyond_32_bits():
         assert torch.equal(a[before:], b)
     del got
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_silu_over_the_types_range(dtype):
+    """Gates from the type's lowest to its largest value, forward and backward, element by element:
+    far below zero SiLU and its slope are zero, far above the gate itself and one; at minus infinity
+    the limit.  Relative to each element: half a step of the type and 32 roundings, as for a row."""
+    dt = TYPES[dtype]
+    end = torch.finfo(dt).max
+    values = [-end, -end / 4, -1e4, -200.0, -100.0, -88.0, -80.0, 0.0, 80.0, 90.0, 200.0, 1e4, end / 4, end]
+    x = make(len(values), 0, 64, dt, True, False, False, False, False)
+    x["gate"] = torch.tensor(values).to(dt).cuda()[:, None].repeat(1, 64)
+    x["x"] = x["x"].abs().clamp(0.25, 0.5)  # products with the largest gates stay in the type's range
+    x["weight"].fill_(0.5)
+    leaves = {n: t.clone().requires_grad_(True) for n, t in x.items() if t is not None}
+    (out,) = run({**x, **leaves})
+    l64 = {n: t.double().requires_grad_(True) for n, t in x.items() if t is not None}
+    (want,) = norm64(*(l64.get(n) for n in NAMES), 1e-6, 0)
+    # seeds that keep the gradients of the largest gates in range
+    d = torch.where(x["gate"].abs() > 100, torch.finfo(dt).tiny * 16, 1.0).to(dt)
+    got = torch.autograd.grad(out, [leaves["x"], leaves["gate"]], d)
+    exact = torch.autograd.grad(want, [l64["x"], l64["gate"]], d.double())
+    step = torch.finfo(dt).eps / 2
+    for a, b in zip((out, got[1]), (want, exact[1])):
+        # results below the type's normal numbers are rounded to its smallest step
+        bound = (step + BASE) * b.abs() + torch.finfo(dt).tiny * (step * 2 + 2.0 ** -20) + 1e-34
+        assert ((a.double() - b).abs() <= bound).all(), (a[:, 0], b[:, 0])
+    # dx is a difference of terms; zero where the gate is far below zero
+    low = x["gate"][:, 0].float() < -99
+    assert got[0][low].abs().max() <= 1e-34
+    z = {**x, "gate": torch.full_like(x["gate"], -float("inf"))}
+    leaves = {n: t.clone().requires_grad_(True) for n, t in z.items() if t is not None}
+    (out,) = run({**z, **leaves})
+    grads = torch.autograd.grad(out, [leaves["x"], leaves["gate"]], torch.ones_like(out))
+    for t in (out, *grads):
+        assert t.abs().max() <= 1e-34
