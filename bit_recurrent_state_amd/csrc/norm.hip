@@ -317,11 +317,12 @@ __global__ void __launch_bounds__(BLOCK) backward_kernel(Params p) {
       }
       team_sum<WIDE>(ss, mr, team, lds);
       const float rs2 = 1.0f / sqrtf(ss * inv + p.eps);
-      const float k = rs2 * rs2 * rs2 * mr * inv;
+      const float k = rs2 * mr * inv;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        d[i] += m[i] * w2[i] * rs2 - k * y[i];
-        dw2[i] = fmaf(m[i], y[i] * rs2, dw2[i]);
+        const float n = y[i] * rs2;  // before rs2 a third time: its cube overflows with a tiny eps
+        d[i] += rs2 * (m[i] * w2[i] - k * n);
+        dw2[i] = fmaf(m[i], n, dw2[i]);
       }
     }
     if (p.dresidual) store_row<DT, V, VEC>(p.dresidual, out, t, team, width, d);

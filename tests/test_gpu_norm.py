@@ -299,3 +299,20 @@ def test_silu_over_the_types_range(dtype):
     grads = torch.autograd.grad(out, [leaves["x"], leaves["gate"]], torch.ones_like(out))
     for t in (out, *grads):
         assert t.abs().max() <= 1e-34
+
+
+def test_rows_of_zeros_with_a_tiny_eps():
+    """eps may be any positive number: a row of zeros has finite gradients where the formula's are."""
+    x = make(6, 0, 128, torch.float32, False, True, False, False, True)
+    x["x"][1] = 0
+    x["residual"][1] = 0
+    for eps in (1e-6, 1e-20, 1e-30):
+        leaves = {n: t.clone().requires_grad_(True) for n, t in x.items() if t is not None}
+        out = run({**x, **leaves}, eps=eps)
+        l64 = {n: t.double().requires_grad_(True) for n, t in x.items() if t is not None}
+        want = norm64(*(l64.get(n) for n in NAMES), eps, 0)
+        seeds = [torch.full_like(t, 1e-3) for t in out]
+        got = torch.autograd.grad(out, [leaves["residual"]], seeds)[0]
+        exact = torch.autograd.grad(want, [l64["residual"]], [s.double() for s in seeds])[0]
+        for i in range(6):
+            assert rel(got[i], exact[i]) <= tol(torch.float32), (eps, i)
