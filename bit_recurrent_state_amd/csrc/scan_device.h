@@ -6,11 +6,14 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "scan_launch.h"
 
 namespace qscan {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -162,6 +165,21 @@ __device__ __forceinline__ float fast_exp(float x) {
   const float r = fmaf(x, lo, fmaf(x, hi, -t));
   const float e = __builtin_amdgcn_exp2f(t);
   return fmaf(e, r * 0.693147182f, e);
+}
+
+// Sums of log decays in fixed point, as powers of two with 25 bits behind the
+// point: differences of sums are then exact, and a sum of a chunk that decays by
+// up to e^kFarDecay = 2^34.6 is as good at its end as at its start (in FP32 it
+// would be held to 2^-20 there).  `fixed` rounds a 64-bit sum to 2^-26 of an
+// octave, 1.1e-8; what does not fit wraps round and is not used.
+__device__ __forceinline__ int fixed(double s) {
+  const double scale = 1.4426950408889634 * 33554432.0, units = 6755399441055744.0;  // 1.5 * 2^52
+  return (int)(uint32_t)__double_as_longlong(fma(s, scale, units));
+}
+
+// 2^(x 2^-25) to an ulp or two.
+__device__ __forceinline__ float fixed_exp(int x) {
+  return ldexpf(__builtin_amdgcn_exp2f((float)(x & 0x1FFFFFF) * 0x1p-25f), x >> 25);
 }
 
 // Four neighbouring elements as they lie in memory (16-bit ones two to a word),

@@ -242,11 +242,11 @@ __device__ __forceinline__ void store_dop(const Params& p, const Chunk& c, int64
 //
 // VEC: a gate per key channel, for chunks over which no channel decays by more
 // than e^kFarDecay: A = (q e^c)(k e^-c)^T and L = (k e^c)(k e^-c)^T are then
-// plain products.  Their exponents, at most kFarDecay = 24, are rounded to 2^-24
-// of themselves, so that a quotient errs by at most 3e-6, and by 1e-7 at the
-// decays of a few per cent a token that most channels have.  (One channel's
-// values stay far inside FP32's range: e^24 = 3e10.)  Other chunks go to
-// chunk_vector_kernel.
+// plain products.  Sums of log decays are exact in fixed point but for a rounding
+// to 1.1e-8 of the token's and of each block's (scan_device.h), and what two tokens
+// have in common cancels exactly, so that a quotient holds to that and the two
+// exponentials' ulps at any c.  (One channel's values stay far inside FP32's range:
+// e^24 = 3e10.)  Other chunks go to chunk_vector_kernel.
 template <int DK, int NPQ, bool VEC, bool DELTA, bool BWD>
 __global__ void __launch_bounds__(256) chunk_kernel(Params p) {
   __shared__ double cs[C];
@@ -336,48 +336,74 @@ __global__ void __launch_bounds__(256) chunk_kernel(Params p) {
 template <int DK, bool DELTA, bool BWD>
 __global__ void __launch_bounds__(256) operands_vector_kernel(Params p) {
   constexpr int LP = DK + 4;
-  __shared__ __align__(16) float pre[C][LP], suf[C][LP];  // sums of log decays inside blocks of 16
+  // Sums of log decays inside blocks of 16: up to each token in fixed point; where the chunk decays
+  // far, in floats, and from each token to its block's end (the block's sum less the token's would
+  // cancel there).
+  __shared__ __align__(16) float pre[C][LP], suf[C][LP];
   __shared__ __align__(16) float tot[4][DK];
+  auto pre_fixed = [&](int t, int ch) -> int& { return reinterpret_cast<int&>(pre[t][ch]); };
+  auto tot_fixed = [&](int b, int ch) -> int& { return reinterpret_cast<int&>(tot[b][ch]); };
   const int slot = blockIdx.x, h = blockIdx.y;
   Chunk c;
   if (!find_and_note(p, slot, h == 0, c)) return;
   const int64_t sh = (int64_t)slot * p.heads + h;
   const int group = p.heads / p.heads_qk, hq = h / group;
   const bool qeven = p.qs % 4 == 0, keven = p.ks % 4 == 0;
-  for (int u = threadIdx.x; u < DK * 4; u += 256) {
-    const int ch = u % DK, t0 = u / DK * 16;
-    float g[16], s = 0.0f;
+  bool over = false;
+  auto sums = [&](auto exact) {  // true: fixed point
+    for (int u = threadIdx.x; u < DK * 4; u += 256) {
+      const int ch = u % DK, t0 = u / DK * 16;
+      float g[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      g[i] = p.g[((c.row + min(t0 + i, c.len - 1)) * p.heads + h) * DK + ch];
+      for (int i = 0; i < 16; ++i)
+        g[i] = p.g[((c.row + min(t0 + i, c.len - 1)) * p.heads + h) * DK + ch];
+      std::conditional_t<exact.value, double, float> s = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      g[i] = t0 + i < c.len ? gate(g[i]) : 0.0f;
-      s += g[i];
-      pre[t0 + i][ch] = s;
+      for (int i = 0; i < 16; ++i) {
+        g[i] = t0 + i < c.len ? gate(g[i]) : 0.0f;
+        s += g[i];
+        if constexpr (exact.value)
+          pre_fixed(t0 + i, ch) = fixed(s);
+        else
+          pre[t0 + i][ch] = s;
+      }
+      if constexpr (exact.value) {
+        tot_fixed(u / DK, ch) = fixed(s);
+        over = over || !(s >= -kFarDecay && s <= kFarDecay);
+      } else {
+        tot[u / DK][ch] = s;
+        s = 0.0f;
+#pragma unroll
+        for (int i = 15; i >= 0; --i) {
+          suf[t0 + i][ch] = s;
+          s += g[i];
+        }
+      }
     }
-    tot[u / DK][ch] = s;
-    s = 0.0f;
-#pragma unroll
-    for (int i = 15; i >= 0; --i) {
-      suf[t0 + i][ch] = s;
-      s += g[i];
-    }
-  }
+  };
+  sums(std::true_type());
   if (threadIdx.x < C) {
     const int t = threadIdx.x;
     rows_at(p, slot, h)[2 * C + t] = t < c.len ? (p.beta ? p.beta[(c.row + t) * p.heads + h] : 1.0f) : 0.0f;
   }
   __syncthreads();
-  bool over = false;
-  if (threadIdx.x < DK) {
+  if (threadIdx.x < DK) {  // no block alone is over, so none has wrapped round
     const int ch = threadIdx.x;
-    const float all = (tot[0][ch] + tot[1][ch]) + (tot[2][ch] + tot[3][ch]);
-    p.decay[sh * DK + ch] = fast_exp(all);
-    over = !(all >= -kFarDecay);
+    const int64_t all = (int64_t)tot_fixed(0, ch) + tot_fixed(1, ch) + tot_fixed(2, ch) + tot_fixed(3, ch);
+    over = over || all < fixed(-kFarDecay) || all > fixed(kFarDecay);
   }
   const bool far = __syncthreads_or(over);
   if (threadIdx.x == 0) p.far[sh] = far;
+  if (far) {
+    sums(std::false_type());
+    __syncthreads();
+  }
+  if (threadIdx.x < DK) {
+    const int ch = threadIdx.x;
+    p.decay[sh * DK + ch] =
+        far ? fast_exp((tot[0][ch] + tot[1][ch]) + (tot[2][ch] + tot[3][ch]))
+            : fixed_exp(tot_fixed(0, ch) + tot_fixed(1, ch) + tot_fixed(2, ch) + tot_fixed(3, ch));
+  }
 
   // rows: 8 channels of a token
   for (int u = threadIdx.x; u < C * DK / 8; u += 256) {
@@ -390,21 +416,44 @@ __global__ void __launch_bounds__(256) operands_vector_kernel(Params p) {
       float x[4], y[4];
       widen4(load4(p.q, row * p.qs + (int64_t)hq * DK + ch + 4 * q, p.dtype, qeven), p.dtype, x);
       widen4(load4(p.k, row * p.ks + (int64_t)hq * DK + ch + 4 * q, p.dtype, keven), p.dtype, y);
-      f32x4 cs = *reinterpret_cast<const f32x4*>(&pre[t][ch + 4 * q]);
-      f32x4 se = *reinterpret_cast<const f32x4*>(&suf[t][ch + 4 * q]);
+      float e[4], eo[4], en[4];
+      if (far) {
+        f32x4 cs = *reinterpret_cast<const f32x4*>(&pre[t][ch + 4 * q]);
+        f32x4 se = *reinterpret_cast<const f32x4*>(&suf[t][ch + 4 * q]);
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const f32x4 w = *reinterpret_cast<const f32x4*>(&tot[m][ch + 4 * q]);
-        if (m < b) cs += w;
-        if (m > b) se += w;
+        for (int m = 0; m < 4; ++m) {
+          const f32x4 w = *reinterpret_cast<const f32x4*>(&tot[m][ch + 4 * q]);
+          if (m < b) cs += w;
+          if (m > b) se += w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          e[i] = fast_exp(cs[i]);
+          eo[i] = fast_exp(se[i]);
+          en[i] = 0.0f;
+        }
+      } else {
+        i32x4 cs = *reinterpret_cast<const i32x4*>(&pre[t][ch + 4 * q]), end = {0, 0, 0, 0};
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const i32x4 w = *reinterpret_cast<const i32x4*>(&tot[m][ch + 4 * q]);
+          if (m < b) cs += w;
+          end += w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          e[i] = fixed_exp(cs[i]);
+          eo[i] = fixed_exp(end[i] - cs[i]);
+          en[i] = fixed_exp(-cs[i]);
+        }
       }
+      const float in = t < c.len ? 1.0f : 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float e = fast_exp(cs[i]), in = t < c.len ? 1.0f : 0.0f;
-        qe[4 * q + i] = in * x[i] * e;
-        ke[4 * q + i] = in * y[i] * e;
-        if (BWD) ko[4 * q + i] = in * y[i] * fast_exp(se[i]);
-        kn[4 * q + i] = far ? 0.0f : in * y[i] * fast_exp(-cs[i]);
+        qe[4 * q + i] = in * x[i] * e[i];
+        ke[4 * q + i] = in * y[i] * e[i];
+        if (BWD) ko[4 * q + i] = in * y[i] * eo[i];
+        kn[4 * q + i] = in * y[i] * en[i];
       }
     }
     const int64_t at = sh * P * C * DK + u * 8;
@@ -432,11 +481,40 @@ __global__ void __launch_bounds__(256) operands_vector_kernel(Params p) {
     }
     load_raw<8>(p.k, ak, p.dtype, rk);
     if (BWD) load_raw<8>(p.q, aq, p.dtype, rq);
-    float before = 0.0f, after = 0.0f;
+    // decays from the chunk's start to a token (es), from it to the chunk's end (eo), 1 / es (en); for
+    // the gradients the first two, or where the chunk decays far those of the token's block (bs, bo)
+    float es[8], eo[8], en[8], bs[8], bo[8];
+    if (far) {
+      float before = 0.0f, after = 0.0f;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      if (m < b) before += tot[m][ch];
-      if (m > b) after += tot[m][ch];
+      for (int m = 0; m < 4; ++m) {
+        if (m < b) before += tot[m][ch];
+        if (m > b) after += tot[m][ch];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float cs = pre[t0 + i][ch], se = suf[t0 + i][ch];
+        es[i] = fast_exp(cs + before);
+        eo[i] = fast_exp(se + after);
+        en[i] = 0.0f;
+        bs[i] = fast_exp(cs);
+        bo[i] = fast_exp(se);
+      }
+    } else {
+      int before = 0, end = 0;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int x = tot_fixed(m, ch);
+        if (m < b) before += x;
+        end += x;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int x = pre_fixed(t0 + i, ch) + before;
+        bs[i] = es[i] = fixed_exp(x);
+        bo[i] = eo[i] = fixed_exp(end - x);
+        en[i] = fixed_exp(-x);
+      }
     }
     if (BWD && h % group == 0) {  // q and k as they are, once for the heads that share them
       const int terms = p.dtype == 1 ? 1 : P;
@@ -455,20 +533,16 @@ __global__ void __launch_bounds__(256) operands_vector_kernel(Params p) {
           *reinterpret_cast<u32x4*>(p.qt_raw + to + n * C * DK) = fq.t[n];
         }
     }
-    float qe[8], ke[8], ko[8], kn[8], ps[8], ss[8];
+    float qe[8], ke[8], ko[8], kn[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float k = t0 + i < c.len ? from_raw(rk[i], p.dtype) : 0.0f;
-      const float se = suf[t0 + i][ch], eo = fast_exp(se + after);
-      ko[i] = k * eo;
+      ko[i] = k * eo[i];
       if (BWD) {
         const float q = t0 + i < c.len ? from_raw(rq[i], p.dtype) : 0.0f;
-        const float cs = pre[t0 + i][ch], e = fast_exp(cs + before);
-        qe[i] = q * e;
-        ke[i] = k * e;
-        kn[i] = far ? 0.0f : k * fast_exp(-(cs + before));
-        ps[i] = far ? fast_exp(cs) : e;
-        ss[i] = far ? fast_exp(se) : eo;
+        qe[i] = q * es[i];
+        ke[i] = k * es[i];
+        kn[i] = k * en[i];
       }
     }
     const int64_t at = sh * P * C * DK + u * 8;
@@ -486,8 +560,8 @@ __global__ void __launch_bounds__(256) operands_vector_kernel(Params p) {
       float* ds = p.sfx + (sh * DK + ch) * C + t0;
 #pragma unroll
       for (int i = 0; i < 8; i += 4) {
-        *reinterpret_cast<f32x4*>(dp + i) = f32x4{ps[i], ps[i + 1], ps[i + 2], ps[i + 3]};
-        *reinterpret_cast<f32x4*>(ds + i) = f32x4{ss[i], ss[i + 1], ss[i + 2], ss[i + 3]};
+        *reinterpret_cast<f32x4*>(dp + i) = f32x4{bs[i], bs[i + 1], bs[i + 2], bs[i + 3]};
+        *reinterpret_cast<f32x4*>(ds + i) = f32x4{bo[i], bo[i + 1], bo[i + 2], bo[i + 3]};
       }
     }
   }

@@ -88,11 +88,14 @@ __global__ void __launch_bounds__(512, DELTA ? 2 : 4) prep_vector_kernel(Params 
   // (128 chunks of 16 heads, with two terms of q and A).
   constexpr int KS = DK / 32;
   constexpr int kKn = P * C * DK, kTM = P * C * C + 2 * C * (C + 4);
-  __shared__ __align__(16) float buf[C * DK];  // sums of log decays in blocks of 16
+  // sums of log decays in blocks of 16: fixed point, floats in chunks that decay far
+  __shared__ __align__(16) float buf[C * DK];
   __shared__ __align__(16) uint16_t Kn[kKn > kTM ? kKn : kTM];
   // token t's sums, four channels together, turned by t against bank conflicts
   auto pre = [&](int t, int ch) -> float& { return buf[t * DK + (ch ^ ((t & 7) << 2))]; };
+  auto pre_fixed = [&](int t, int ch) -> int& { return reinterpret_cast<int&>(pre(t, ch)); };
   auto tot = [&](int b, int ch) -> float& { return pre(b * 16 + 15, ch); };  // a block's
+  auto tot_fixed = [&](int b, int ch) -> int& { return pre_fixed(b * 16 + 15, ch); };
   // T's terms, and M behind them, take the place of k e^-c
   Square* const M = reinterpret_cast<Square*>(Kn + P * C * C);
   const int slot = blockIdx.x, h = blockIdx.y;
@@ -131,30 +134,37 @@ __global__ void __launch_bounds__(512, DELTA ? 2 : 4) prep_vector_kernel(Params 
       }
   }
   if (DELTA && wave < p.dvp / 16) load_columns(p, c, h, wave, rv);
-  for (int u = threadIdx.x; u < DK * 4; u += 512) {
-    const int ch = u % DK, t0 = u / DK * 16;
-    float g[16], s = 0.0f;
+  bool over = false;
+  auto sums = [&](auto exact) {  // true: fixed point
+    for (int u = threadIdx.x; u < DK * 4; u += 512) {
+      const int ch = u % DK, t0 = u / DK * 16;
+      float g[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      g[i] = p.g[((c.row + min(t0 + i, c.len - 1)) * p.heads + h) * DK + ch];
+      for (int i = 0; i < 16; ++i)
+        g[i] = p.g[((c.row + min(t0 + i, c.len - 1)) * p.heads + h) * DK + ch];
+      std::conditional_t<exact.value, double, float> s = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      s += t0 + i < c.len ? gate(g[i]) : 0.0f;
-      pre(t0 + i, ch) = s;
+      for (int i = 0; i < 16; ++i) {
+        s += t0 + i < c.len ? gate(g[i]) : 0.0f;
+        if constexpr (exact.value)
+          pre_fixed(t0 + i, ch) = fixed(s);
+        else
+          pre(t0 + i, ch) = s;
+      }
+      over = over || !(s >= -kFarDecay && s <= kFarDecay);
     }
-  }
+  };
+  sums(std::bool_constant<!FAR>());
   if (threadIdx.x < C) {
     const int t = threadIdx.x;
     rows_at(p, slot, h)[2 * C + t] =
         t < c.len ? (p.beta ? p.beta[(c.row + t) * p.heads + h] : 1.0f) : 0.0f;
   }
   __syncthreads();
-  bool over = false;
-  if (!FAR && threadIdx.x < DK) {
+  if (!FAR && threadIdx.x < DK) {  // no block alone is over, so none has wrapped round
     const int ch = threadIdx.x;
-    const float all = (tot(0, ch) + tot(1, ch)) + (tot(2, ch) + tot(3, ch));
-    p.decay[sh * DK + ch] = fast_exp(all);
-    over = !(all >= -kFarDecay);
+    const int64_t all = (int64_t)tot_fixed(0, ch) + tot_fixed(1, ch) + tot_fixed(2, ch) + tot_fixed(3, ch);
+    over = over || all < fixed(-kFarDecay) || all > fixed(kFarDecay);
   }
   bool far = FAR;
   if (!FAR) {
@@ -166,6 +176,16 @@ __global__ void __launch_bounds__(512, DELTA ? 2 : 4) prep_vector_kernel(Params 
     for (int w = 0; w < 8; ++w) far = far || flag[w];
     if (threadIdx.x == 0) p.far[sh] = far;
     __syncthreads();
+    if (far) {
+      sums(std::false_type());
+      __syncthreads();
+    }
+    if (threadIdx.x < DK) {
+      const int ch = threadIdx.x;
+      p.decay[sh * DK + ch] =
+          far ? fast_exp((tot(0, ch) + tot(1, ch)) + (tot(2, ch) + tot(3, ch)))
+              : fixed_exp(tot_fixed(0, ch) + tot_fixed(1, ch) + tot_fixed(2, ch) + tot_fixed(3, ch));
+    }
   }
 
   // columns of k: a wave's 16 channels, both halves of the tokens
@@ -173,40 +193,50 @@ __global__ void __launch_bounds__(512, DELTA ? 2 : 4) prep_vector_kernel(Params 
   auto columns = [&]() {
     if (wave >= DK / 16) return;
     const int ch = wave * 16 + fr;
-    const float t4[4] = {tot(0, ch), tot(1, ch), tot(2, ch), tot(3, ch)};
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const int t0 = s * 32 + fg * 8, b = t0 >> 4;
-      float before = 0.0f, after = 0.0f;
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        if (m < b) before += t4[m];
-        if (m > b) after += t4[m];
-      }
-      // decays from a token to the end of its block: the block's less the token's, summed again
-      // from the gates where that would cancel
-      float sfx[8];
+      // decays from the chunk's start to a token, and from the token to the chunk's end
+      float ee[8], eo[8];
       if (far) {
-        const int e0 = b * 16 + 16;
-        float s2 = 0.0f;
-        for (int i = e0 - 1; i > t0 + 7; --i)
-          s2 += i < c.len ? gate(p.g[((c.row + i) * p.heads + h) * DK + ch]) : 0.0f;
+        float before = 0.0f, after = 0.0f;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          if (m < b) before += tot(m, ch);
+          if (m > b) after += tot(m, ch);
+        }
+        // to the end of the token's block: summed from there, the block's sum less the token's
+        // would cancel
+        float sfx = after;
+        for (int i = b * 16 + 15; i > t0 + 7; --i)
+          sfx += i < c.len ? gate(p.g[((c.row + i) * p.heads + h) * DK + ch]) : 0.0f;
 #pragma unroll
         for (int i = 7; i >= 0; --i) {
-          sfx[i] = s2;
-          s2 += t0 + i < c.len ? gate(p.g[((c.row + t0 + i) * p.heads + h) * DK + ch]) : 0.0f;
+          ee[i] = fast_exp(pre(t0 + i, ch) + before);
+          eo[i] = fast_exp(sfx);
+          sfx += t0 + i < c.len ? gate(p.g[((c.row + t0 + i) * p.heads + h) * DK + ch]) : 0.0f;
         }
       } else {
-        const float block = b == 0 ? t4[0] : b == 1 ? t4[1] : b == 2 ? t4[2] : t4[3];
+        int before = 0, end = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sfx[i] = block - pre(t0 + i, ch);
+        for (int m = 0; m < 4; ++m) {
+          const int x = tot_fixed(m, ch);
+          if (m < b) before += x;
+          end += x;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int x = pre_fixed(t0 + i, ch) + before;
+          if (DELTA) ee[i] = fixed_exp(x);
+          eo[i] = fixed_exp(end - x);
+        }
       }
       float ko[8], ke[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float k = t0 + i < c.len ? from_raw(rk[s][i], p.dtype) : 0.0f;
-        ko[i] = k * fast_exp(sfx[i] + after);
-        if (DELTA) ke[i] = k * fast_exp(pre(t0 + i, ch) + before);
+        ko[i] = k * eo[i];
+        if (DELTA) ke[i] = k * ee[i];
       }
       if (DELTA) kt[s] = split8<P>(ke);
       if (!FAR) {
@@ -240,13 +270,25 @@ __global__ void __launch_bounds__(512, DELTA ? 2 : 4) prep_vector_kernel(Params 
     for (int q = 0; q < 2; ++q) {
       float x[4];
       widen4(rx[s][q], p.dtype, x);
-      f32x4 cs = *reinterpret_cast<const f32x4*>(&pre(t, ch + 4 * q));
+      float ex[4];
+      if (far) {
+        f32x4 cs = *reinterpret_cast<const f32x4*>(&pre(t, ch + 4 * q));
 #pragma unroll
-      for (int m = 0; m < 3; ++m)
-        if (m < rb) cs += *reinterpret_cast<const f32x4*>(&tot(m, ch + 4 * q));
+        for (int m = 0; m < 3; ++m)
+          if (m < rb) cs += *reinterpret_cast<const f32x4*>(&tot(m, ch + 4 * q));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ex[i] = fast_exp(cs[i]);
+      } else {
+        i32x4 cs = *reinterpret_cast<const i32x4*>(&pre(t, ch + 4 * q));
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
+          if (m < rb) cs += *reinterpret_cast<const i32x4*>(&tot(m, ch + 4 * q));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ex[i] = fixed_exp(cs[i]);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float e = fast_exp(cs[i]);
+        const float e = ex[i];
         xe[4 * q + i] = in * x[i] * e;
         if (second) {  // 1 / e, refined once
           const float r = __builtin_amdgcn_rcpf(e);

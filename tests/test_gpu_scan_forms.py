@@ -136,3 +136,57 @@ def test_backward_with_row_strides_of_its_own(mixer, dtype):
     want = torch.autograd.grad((o64, S64), [leaf[n] for n in names], (do.double(), dS.double()))
     for n, w in zip(names, want):
         assert rel(out[n], w) <= tolerance(out[n].dtype, True), n
+
+
+@pytest.mark.parametrize("mixer", ["gla", "kda"])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dk,dv,H,Hq", [(64, 64, 2, 2), (128, 40, 4, 2), (256, 64, 2, 1)])
+def test_chunks_that_decay_far(mixer, dtype, dk, dv, H, Hq):
+    """Gates per channel: every chunk far; one head's middle chunk far between ordinary ones; one
+    channel of it; a state dropped inside a chunk."""
+    m = MIXERS[mixer]
+    lens = [150, 20]
+    for which in range(4):
+        x = inputs(m, 2, lens, H, Hq, dk, dv, TYPES[dtype], "cuda", seed=which)
+        if which == 0:
+            x["log_alpha"] *= 30.0
+        elif which == 1:
+            x["log_alpha"][64:128, 1] *= 30.0
+        elif which == 2:
+            x["log_alpha"][70:110, 0, dk - 1] = -2.0
+        else:
+            x["log_alpha"][100, 1] = -100.0
+        check(x, m, 2)
+
+
+@pytest.mark.parametrize("mixer", ["gla", "kda"])
+@pytest.mark.parametrize("dk", [64, 128, 256])
+@pytest.mark.parametrize("shape", ["even", "random", "early", "late"])
+def test_elements_just_below_a_far_decay(mixer, dk, shape):
+    """A chunk of 64 whose channels decay by e^-23.9, every factor e^(c_i - c_j) by itself: q and k
+    hold one channel, v writes token j's value into column j, so that o[i, j] = q_i k_j e^(c_i - c_j)
+    and the state's column is v_j k_j e^(c_end - c_j) (KDA: nearly so, with beta = 2^-20, against the
+    64-bit recurrence).  Relative to each element, in units of 2^-24: sums of log decays held to 2^-25
+    each (2), two exponentials to an ulp or two (2 * 4), the reciprocal (1), the splits of the operands
+    and the products left out (3), six sums (6): 20; what KDA's state takes off is 64 * 2^-20 of that
+    at most, so that its errors do not count, and rounds the sum: 24."""
+    m, H, dv, T = MIXERS[mixer], 2, 64, 64
+    g = torch.Generator().manual_seed(7)
+    w = {"even": torch.ones(T), "random": torch.rand(T, generator=g),
+         "early": (torch.arange(T) < 5).double() + 0.01, "late": (torch.arange(T) >= 59).double() + 0.01}[shape]
+    w = w.double()[:, None, None] * (0.5 + torch.rand(T, H, dk, generator=g).double())
+    la = (-23.9 * w / w.sum(0)).float().cuda()
+    ch = 11
+    q, k = (torch.zeros(T, H, dk, device="cuda") for _ in range(2))
+    q[:, :, ch], k[:, :, ch] = 1 + torch.rand(T, H, generator=g).cuda(), 1.0
+    x = {"q": q, "k": k, "v": torch.eye(T, device="cuda")[:, None].repeat(1, H, 1).contiguous(),
+         "log_alpha": la, "beta": None if m == GLA else torch.full((T, H), 2.0 ** -20, device="cuda"),
+         "initial_state": None, "offsets": torch.tensor([0, T], device="cuda")}
+    with torch.no_grad():
+        o, S = call(x, m)
+    o64, S64, _ = scan64(x, m, 1)
+    K = 20 if m == GLA else 24
+    for a, b in ((o, o64), (S, S64)):
+        err = ((a.double() - b).abs() / b.abs().clamp_min(1e-300))[b != 0]
+        assert err.numel() and float(err.max()) <= K * EPS, float(err.max()) / EPS
+        assert not a[b == 0].any()
