@@ -182,14 +182,23 @@ class ReadoutNorm:
     o * rsqrt(mean(o^2) + eps) * weight * act(gate), over each head's dv values."""
 
     weight: Optional[torch.Tensor] = None  # float32 [dv] or [heads, dv]
-    gate: Optional[torch.Tensor] = None    # as o, contiguous
+    gate: Optional[torch.Tensor] = None    # of o's type and shape (or its rows or values in a row)
     eps: float = 1e-6
     act: int = SILU
 
-    def config(self, shape, dtype, device) -> NormConfig:
-        """The configuration for a readout of this shape, its tensors checked."""
+    def config(self, shape, dtype, device, o_shape=None) -> NormConfig:
+        """The configuration for a readout of this shape, its tensors checked.  o_shape: the shape in
+        which the caller has it."""
         tokens, heads, dv = shape
         each = self.weight is not None and self.weight.dim() == 2
+        if self.weight is not None:
+            w = tuple(self.weight.shape)
+            if w[-1:] != (dv,) or each and w != (heads, dv):
+                raise ValueError(f"weight: expected [{dv}] or [{heads}, {dv}], got {w}")
+        if self.gate is not None:
+            g = tuple(self.gate.shape)
+            if g not in (tuple(shape), (tokens * heads * dv,), tuple(o_shape or shape)):
+                raise ValueError(f"gate: expected {tuple(o_shape or shape)}, got {g}")
         cfg = NormConfig(tokens, heads, dv, dtype, self.act, each, self.eps)
         qstate_norm_workspace(cfg)  # the library's checks of it
         _array(self.weight, "weight", torch.float32, dv * (heads if each else 1), device,
@@ -199,7 +208,10 @@ class ReadoutNorm:
 
     def apply_(self, o: torch.Tensor, stream=None) -> None:
         """In place on o [tokens, heads, dv]."""
-        cfg = self.config(o.shape, o.dtype, o.device)
+        self._run(self.config(o.shape, o.dtype, o.device), o, stream)
+
+    def _run(self, cfg: NormConfig, o: torch.Tensor, stream=None) -> None:
+        o = o.view(cfg.tokens, cfg.groups, cfg.width)
         gate = None if self.gate is None else self.gate.view(o.shape)
         qstate_norm(cfg, o, self.weight, gate, r=o, stream=stream)
 
@@ -228,10 +240,10 @@ class QState:
             if o is None:
                 raise ValueError("norm: there is no readout without o")
             shape = (self.cfg.batch, self.cfg.heads, self.cfg.dv)
-            norm.config(shape, torch.float32, o.device)
+            cfg = norm.config(shape, torch.float32, o.device, o.shape)
         qstate_step(self.handle, self.cfg, q, k, v, alpha, beta, o, stream)
         if norm is not None:
-            norm.apply_(o.view(shape), stream)
+            norm._run(cfg, o, stream)
 
     def prefill(self, q, k, v, log_alpha, beta=None, offsets=None, norm=None):
         """A prompt's or a chunk's tokens at once, for sequences that decode on with `step`: the
@@ -247,14 +259,14 @@ class QState:
             raise ValueError(f"q {tuple(q.shape)}, v {tuple(v.shape)} do not go with the state "
                              f"[{c.batch}][{c.heads}][{c.dv}][{c.dk}]")
         if norm is not None:
-            norm.config((v[..., 0, 0].numel(), c.heads, c.dv), v.dtype, v.device)
+            cfg = norm.config((v[..., 0, 0].numel(), c.heads, c.dv), v.dtype, v.device, v.shape)
         with torch.no_grad(), torch.cuda.device(v.device):
             S = torch.empty((c.batch, c.heads, c.dv, c.dk), dtype=torch.float32, device=v.device)
             self.store_fp32(S)
             o, S = scan(q, k, v, log_alpha, beta, mixer=c.mixer, initial_state=S, offsets=offsets)
             self.load_fp32(S)
             if norm is not None:
-                norm.apply_(o.view(-1, c.heads, c.dv))
+                norm._run(cfg, o)
         return o
 
     def readout(self, q, o, stream=None):

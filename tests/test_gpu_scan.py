@@ -578,3 +578,46 @@ def test_captured_backward_beside_an_eager_graph_is_refused(monkeypatch):
         torch.autograd.grad(o2.sum(), leaves["q"])
         torch.autograd.grad(y.sum(), w)
     torch.cuda.synchronize()
+
+
+def _prefill_case():
+    from bit_recurrent_state_amd import Config, QState
+    B, H, dk, dv, T = 3, 4, 64, 32, 5
+    st = QState(Config(B, H, dk, dv, 32, GDN, fp32_state=True))
+    x = inputs(GDN, B, [T] * B, H, H, dk, dv, torch.float32, "cuda", state=False)
+    p = [x[n].view((B, T) + x[n].shape[1:]) for n in ("q", "k", "v", "log_alpha", "beta")]
+    S = torch.randn(B, H, dv, dk, device="cuda")
+    st.load_fp32(S)
+    return st, p, S, torch.rand(H, dv, device="cuda"), torch.randn(B, T, H, dv, device="cuda")
+
+
+def test_readout_norm_shapes():
+    """A weight or a gate of the right size and another shape is refused before the state changes; a
+    gate may have o's shape or hold its values in a row."""
+    from bit_recurrent_state_amd import ReadoutNorm
+    st, p, S, w, G = _prefill_case()
+    one = [t[:, 0].contiguous() for t in p]
+    one[3] = one[3].exp()
+    o = torch.empty_like(one[2])
+    g = G[:, 0].contiguous()
+    for norm in (ReadoutNorm(w.t().contiguous()), ReadoutNorm(gate=g.transpose(0, 1).contiguous()),
+                 ReadoutNorm(gate=g.transpose(1, 2).contiguous())):
+        with pytest.raises(ValueError):
+            st.step(*one, o, norm=norm)
+    for norm in (ReadoutNorm(w.t().contiguous()), ReadoutNorm(gate=G.transpose(0, 1).contiguous()),
+                 ReadoutNorm(gate=G.transpose(1, 2).contiguous())):
+        with pytest.raises(ValueError):
+            st.prefill(*p, norm=norm)
+    back = torch.empty_like(S)
+    st.store_fp32(back)
+    assert torch.equal(back, S)
+    want = st.prefill(*p, norm=ReadoutNorm(w, G))
+    st.load_fp32(S)
+    assert torch.equal(st.prefill(*p, norm=ReadoutNorm(w, G.flatten(0, 1))), want)
+    st.load_fp32(S)
+    st.step(*one, o, norm=ReadoutNorm(w, g))
+    st.load_fp32(S)
+    o2 = torch.empty_like(o).view(-1)
+    st.step(*one, o2, norm=ReadoutNorm(w, g.view(-1)))
+    assert torch.equal(o2.view_as(o), o)
+    st.close()

@@ -233,3 +233,23 @@ def test_captured_backward_beside_an_eager_graph_is_refused(monkeypatch):
     del y, far
     gc.collect()
     assert len(sequence._alive) == n - 2
+
+
+def test_readout_norm_shapes(L):
+    """Right sizes in wrong shapes are refused, whatever the device."""
+    from bit_recurrent_state_amd import ReadoutNorm
+    shape, heads, dv = (6, 4, 32), 4, 32
+
+    def config(o_shape=None, **kw):
+        return ReadoutNorm(**kw).config(shape, torch.float32, torch.device("cpu"), o_shape)
+
+    for kw in (dict(weight=torch.ones(dv, heads)), dict(weight=torch.ones(heads * dv)),
+               dict(weight=torch.ones(dv + 1)), dict(weight=torch.tensor(1.0)),
+               dict(gate=torch.ones(4, 6, 32)), dict(gate=torch.ones(6, 32, 4)),
+               dict(gate=torch.ones(2, 3, 4, 32)), dict(gate=torch.ones(3, 2, 4, 32), o_shape=(2, 3, 4, 32))):
+        with pytest.raises(ValueError):
+            config(**kw)
+    for kw in (dict(weight=torch.ones(dv)), dict(weight=torch.ones(heads, dv)), dict(gate=torch.ones(shape)),
+               dict(gate=torch.ones(6 * 4 * 32)), dict(gate=torch.ones(2, 3, 4, 32), o_shape=(2, 3, 4, 32))):
+        with pytest.raises(TypeError, match="device tensor"):  # the next check: the shapes passed
+            config(**kw)
