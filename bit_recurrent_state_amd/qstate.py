@@ -16,7 +16,7 @@ import torch
 from ._lib import (BDR, GDN, GLA, KDA, KEY_AXIS, RTN, SCALAR, SR, VALUE_AXIS, QStateConfig, check,
                    lib)
 from .norm import SILU, NormConfig, qstate_norm, qstate_norm_workspace
-from .sequence import _array, scan
+from .sequence import _array, _on, scan
 
 __all__ = [
     "GDN", "GLA", "SCALAR", "KDA", "RTN", "SR", "BDR", "VALUE_AXIS", "KEY_AXIS", "Config",
@@ -245,12 +245,12 @@ class QState:
         if norm is not None:
             norm._run(cfg, o, stream)
 
-    def prefill(self, q, k, v, log_alpha, beta=None, offsets=None, norm=None):
+    def prefill(self, q, k, v, log_alpha, beta=None, offsets=None, norm=None, stream=None):
         """A prompt's or a chunk's tokens at once, for sequences that decode on with `step`: the
         scan from the stored state, whose end is stored back (one quantization event for every
         sequence, those without tokens too: the counter goes up by one, a window starts empty).
         Arguments as `scan`'s, one sequence per batch row, q and k with the handle's heads or a
-        divisor of them; returns o."""
+        divisor of them; returns o, which lies in the memory of the stream of the call."""
         c = self.cfg
         if offsets is not None and offsets.numel() != c.batch + 1:
             raise ValueError(f"offsets: expected {c.batch + 1} elements, got {offsets.numel()}")
@@ -260,7 +260,7 @@ class QState:
                              f"[{c.batch}][{c.heads}][{c.dv}][{c.dk}]")
         if norm is not None:
             cfg = norm.config((v[..., 0, 0].numel(), c.heads, c.dv), v.dtype, v.device, v.shape)
-        with torch.no_grad(), torch.cuda.device(v.device):
+        with torch.no_grad(), torch.cuda.device(v.device), _on(stream, v.device):
             S = torch.empty((c.batch, c.heads, c.dv, c.dk), dtype=torch.float32, device=v.device)
             self.store_fp32(S)
             o, S = scan(q, k, v, log_alpha, beta, mixer=c.mixer, initial_state=S, offsets=offsets)

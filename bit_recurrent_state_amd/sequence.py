@@ -59,6 +59,13 @@ def _stream(stream, device) -> int:
     return int(stream)
 
 
+def _on(stream, device):
+    """A context with `stream` as the current one (None: as it is)."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
 def _call(device, fn, *args):
     """fn(*args) with the tensors' device as the current one."""
     if torch.cuda.current_device() == device.index:
@@ -133,9 +140,7 @@ def _bytes_on(n: int, dev, stream) -> torch.Tensor:
     its kernels, also where it is not the current one."""
     if stream is None:
         return torch.empty(n, dtype=torch.uint8, device=dev)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    with torch.cuda.stream(stream):
+    with _on(stream, dev):
         return torch.empty(n, dtype=torch.uint8, device=dev)
 
 

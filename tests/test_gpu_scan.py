@@ -621,3 +621,28 @@ def test_readout_norm_shapes():
     st.step(*one, o2, norm=ReadoutNorm(w, g.view(-1)))
     assert torch.equal(o2.view_as(o), o)
     st.close()
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_prefill_on_another_stream(handle):
+    from bit_recurrent_state_amd import ReadoutNorm
+    st, p, S, w, G = _prefill_case()
+    want = st.prefill(*p, norm=ReadoutNorm(w, G))
+    end = torch.empty_like(S)
+    st.store_fp32(end)
+    st.load_fp32(S)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    seen = []
+    real = st.store_fp32
+    st.store_fp32 = lambda *a, **kw: (seen.append(torch.cuda.current_stream()), real(*a, **kw))
+    got = st.prefill(*p, norm=ReadoutNorm(w, G), stream=side.cuda_stream if handle else side)
+    side.synchronize()
+    back = torch.empty_like(S)
+    real(back)
+    assert torch.equal(got, want) and torch.equal(back, end)
+    assert [s.cuda_stream for s in seen] == [side.cuda_stream]
+    at = got.data_ptr()  # o lies in that stream's memory
+    assert [s["stream"] for s in torch.cuda.memory_snapshot()
+            if s["address"] <= at < s["address"] + s["total_size"]] == [side.cuda_stream]
+    st.close()
