@@ -14,8 +14,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from ._lib import NormConfigC, check, lib
-from .sequence import (DTYPES, _alive, _array, _bytes_on, _call, _on_device, _ptr, _refuse_capture,
-                       _stream, _workspace)
+from .sequence import (DTYPES, _array, _bytes_on, _call, _note_alive, _on_device, _ptr,
+                       _refuse_capture, _stream, _workspace)
 
 __all__ = ["SILU", "SIGMOID", "NormConfig", "qstate_norm", "qstate_norm_workspace",
            "qstate_norm_backward", "block_norm"]
@@ -186,7 +186,7 @@ class _BlockNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, gate, residual, scale, next_weight, eps, act):
         r, h, ctx.cfg, saved = _forward(x, weight, gate, residual, scale, next_weight, eps, act)
-        _alive[ctx] = _stream(None, x.device)
+        _note_alive(ctx, x.device)
         ctx.shape = x.shape
         ctx.save_for_backward(*saved)
         ctx.set_materialize_grads(False)

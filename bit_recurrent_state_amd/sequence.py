@@ -9,6 +9,7 @@ C ABI; every product runs in the library's kernels."""
 from __future__ import annotations
 
 import ctypes
+import threading
 import weakref
 from dataclasses import dataclass
 from typing import Optional
@@ -264,23 +265,47 @@ def _forward(q, k, v, log_alpha, beta, initial_state, offsets, mixer, batch):
 
 
 _alive = weakref.WeakKeyDictionary()  # differentiable calls whose graph lives: their stream
+_alive_lock = threading.Lock()  # a pass may be captured in one thread while another begins one
 
 
-def _leaves(node) -> set:
-    return {id(n.variable) for n, _ in node.next_functions if hasattr(n, "variable")}
+def _note_alive(ctx, device) -> None:
+    with _alive_lock:
+        _alive[ctx] = _stream(None, device)
+
+
+def _leaves(nodes) -> set:
+    """The leaves that the graph behind these nodes ends in."""
+    seen, todo, found = set(nodes), list(nodes), set()
+    while todo:
+        try:
+            behind = todo.pop().next_functions
+        except RuntimeError:  # of a call that is just made, or dropped, in another thread
+            continue
+        for n, _ in behind:
+            if n is None or n in seen:
+                continue
+            seen.add(n)
+            if hasattr(n, "variable"):
+                found.add(id(n.variable))
+            else:
+                todo.append(n)
+    return found
 
 
 def _refuse_capture(ctx, device) -> None:
     """Before a backward pass that is being captured: a leaf belongs to the stream of the graph
     that it was first used in for as long as that lives.  PyTorch would have the capture wait for
-    another stream, which breaks it off and can end the process."""
+    another stream, which breaks it off and can end the process.  Looked for are leaves behind this
+    call, passed directly or through other operations (a projection's weight), and behind live calls
+    of these operators from other streams; graphs without any of these operators are not known here."""
     if not torch.cuda.is_current_stream_capturing():
         return
-    here, mine = _stream(None, device), _leaves(ctx)
-    for other, stream in list(_alive.items()):
-        if stream != here and mine & _leaves(other):
-            raise RuntimeError("a backward pass cannot be captured while a graph of the same "
-                               "leaves from another stream lives: drop the results of that call")
+    here = _stream(None, device)
+    with _alive_lock:
+        others = [other for other, stream in _alive.items() if stream != here]
+    if others and _leaves([ctx]) & _leaves(others):
+        raise RuntimeError("a backward pass cannot be captured while a graph of the same "
+                           "leaves from another stream lives: drop the results of that call")
 
 
 class _Scan(torch.autograd.Function):
@@ -288,7 +313,7 @@ class _Scan(torch.autograd.Function):
     def forward(ctx, q, k, v, log_alpha, beta, initial_state, offsets, mixer, batch):
         o, final, ctx.cfg, saved = _forward(q, k, v, log_alpha, beta, initial_state, offsets,
                                             mixer, batch)
-        _alive[ctx] = _stream(None, v.device)
+        _note_alive(ctx, v.device)
         ctx.shapes = q.shape, v.shape
         ctx.save_for_backward(*saved)
         ctx.set_materialize_grads(False)

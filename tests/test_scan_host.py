@@ -253,3 +253,80 @@ def test_readout_norm_shapes(L):
                dict(gate=torch.ones(6 * 4 * 32)), dict(gate=torch.ones(2, 3, 4, 32), o_shape=(2, 3, 4, 32))):
         with pytest.raises(TypeError, match="device tensor"):  # the next check: the shapes passed
             config(**kw)
+
+
+def _noted(monkeypatch, capturing):
+    """A stand-in for the operators: noted and checked as they are, on the CPU."""
+    from bit_recurrent_state_amd import sequence
+
+    class Noted(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, stream):
+            with sequence._alive_lock:
+                sequence._alive[ctx] = stream
+            return 2 * x
+
+        @staticmethod
+        def backward(ctx, d):
+            sequence._refuse_capture(ctx, None)
+            return 2 * d, None
+
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    monkeypatch.setattr(sequence, "_stream", lambda stream, device: 7)
+    return Noted.apply
+
+
+@pytest.mark.parametrize("through", ["projection", "views", "both operators"])
+def test_captured_backward_sees_leaves_behind_other_operations(monkeypatch, through):
+    """The shared leaf is a weight whose product enters the operators, as in a layer."""
+    import gc
+    capturing = [False]
+    op = _noted(monkeypatch, capturing)
+    x, W = torch.ones(4, 3), torch.ones(3, 3, requires_grad=True)
+    W2 = torch.ones(3, 3, requires_grad=True)
+
+    def call(W, stream):
+        if through == "views":
+            return op(W.view(9)[1:].unflatten(0, (2, 4)).transpose(0, 1), stream)
+        y = op(torch.relu(x @ W), stream)
+        return op(y @ W2.detach(), stream) if through == "both operators" else y
+
+    eager, mine = call(W, 1), call(W, 7)
+    capturing[0] = True
+    with pytest.raises(RuntimeError, match="drop the results"):
+        torch.autograd.grad(mine.sum(), W, retain_graph=True)
+    other = call(W2, 1)  # another leaf's graph does not matter
+    del eager
+    gc.collect()
+    torch.autograd.grad(mine.sum(), W)
+    assert other.requires_grad
+
+
+def test_captured_backward_while_other_threads_begin_calls(monkeypatch):
+    """The list of live calls is read while other threads add to it and drop from it."""
+    import threading
+    capturing = [True]
+    op = _noted(monkeypatch, capturing)
+    x, other = torch.ones(3, requires_grad=True), torch.ones(3, requires_grad=True)
+    stop, failed = threading.Event(), []
+
+    def begin():
+        try:
+            kept = []
+            while not stop.is_set():
+                kept.append(op(other, 1))
+                del kept[:-50]
+        except Exception as e:  # noqa
+            failed.append(e)
+
+    threads = [threading.Thread(target=begin) for _ in range(3)]
+    for t in threads:
+        t.start()
+    try:
+        for _ in range(300):
+            torch.autograd.grad(op(x, 7).sum(), x)
+    finally:
+        stop.set()
+        for t in threads:
+            t.join()
+    assert not failed
