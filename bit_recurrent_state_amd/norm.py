@@ -15,7 +15,7 @@ from torch.autograd.function import once_differentiable
 
 from ._lib import NormConfigC, check, lib
 from .sequence import (DTYPES, _array, _bytes_on, _call, _note_alive, _on_device, _ptr,
-                       _refuse_capture, _stream, _workspace)
+                       _refuse_capture, _refuse_tracing, _stream, _through_autograd, _workspace)
 
 __all__ = ["SILU", "SIGMOID", "NormConfig", "qstate_norm", "qstate_norm_workspace",
            "qstate_norm_backward", "block_norm"]
@@ -224,7 +224,9 @@ def block_norm(x, *, weight=None, gate=None, residual=None, scale=None, next_wei
     have one shape [.., width] and one dtype (float32, bfloat16, float16); weight is float32
     [width], or [heads, width] for x [.., heads, width]; scale and next_weight float32 [width].
     FP32 between inputs and outputs.  Differentiable once in every tensor (a backward pass is
-    captured into a graph only where no eager graph of the same leaves lives)."""
+    captured into a graph only where no eager graph of the same leaves lives); forward-mode
+    derivatives and tracing (make_fx, torch.jit.trace) are refused."""
+    _refuse_tracing("block_norm")
     _on_device(x, "x", None)
     if x.dtype not in DTYPES or x.dim() < 1:
         raise ValueError(f"x: one of float32, bfloat16, float16 [.., width], got {x.dtype} "
@@ -246,8 +248,7 @@ def block_norm(x, *, weight=None, gate=None, residual=None, scale=None, next_wei
         want = (x.shape[-2] if x.dim() > 1 else -1, width) if each else (width,)
         if tuple(t.shape) != want or t.dtype != torch.float32:
             raise ValueError(f"{name}: expected float32 {want}, got {t.dtype} {tuple(t.shape)}")
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in
-                                       (x, weight, gate, residual, scale, next_weight)):
+    if _through_autograd((x, weight, gate, residual, scale, next_weight)):
         return _BlockNorm.apply(x, weight, gate, residual, scale, next_weight, eps, act)
     r, h = _forward(x, weight, gate, residual, scale, next_weight, eps, act)[:2]
     return r if h is None else (r, h)

@@ -15,6 +15,7 @@ from dataclasses import dataclass
 from typing import Optional
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from ._lib import GDN, GLA, KDA, SCALAR, ScanConfigC, check, lib
@@ -264,6 +265,22 @@ def _forward(q, k, v, log_alpha, beta, initial_state, offsets, mixer, batch):
     return o, final, c, saved
 
 
+def _refuse_tracing(name: str) -> None:
+    """A trace records PyTorch's own operations and not the launches: it would hold this call as
+    memory that nothing writes."""
+    if torch.jit.is_tracing() or torch._C._get_dispatch_mode(
+            torch._C._TorchDispatchModeKey.PROXY) is not None:
+        raise RuntimeError(f"{name} cannot be traced (make_fx, torch.jit.trace)")
+
+
+def _through_autograd(tensors) -> bool:
+    """Whether a call needs its autograd function: where a gradient is wanted, and inside forward-mode
+    differentiation, which has no rule here and is refused by it."""
+    if getattr(forward_ad, "_current_level", 0) >= 0:
+        return True
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
 _alive = weakref.WeakKeyDictionary()  # differentiable calls whose graph lives: their stream
 _alive_lock = threading.Lock()  # a pass may be captured in one thread while another begins one
 
@@ -352,7 +369,9 @@ def scan(q, k, v, log_alpha, beta=None, *, mixer: int = GDN, initial_state=None,
     no sequence; final_state is float32 and can go to `QState.load_fp32` to decode on from there.
 
     Differentiable once in every input but offsets; backward computes the states again.  A backward
-    pass is captured into a graph only where no eager graph of the same leaves lives."""
+    pass is captured into a graph only where no eager graph of the same leaves lives.  Forward-mode
+    derivatives and tracing (make_fx, torch.jit.trace) are refused."""
+    _refuse_tracing("scan")
     for t, name in ((q, "q"), (k, "k"), (v, "v"), (log_alpha, "log_alpha")):
         _on_device(t, name, v.device if isinstance(v, torch.Tensor) else None)
     if mixer not in (GDN, GLA, SCALAR, KDA):
@@ -396,7 +415,6 @@ def scan(q, k, v, log_alpha, beta=None, *, mixer: int = GDN, initial_state=None,
                 or initial_state.dtype != torch.float32):
             raise ValueError(f"initial_state: expected float32 {(batch, heads, dv, dk)}, got "
                              f"{initial_state.dtype} {tuple(initial_state.shape)}")
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in
-                                       (q, k, v, log_alpha, beta, initial_state)):
+    if _through_autograd((q, k, v, log_alpha, beta, initial_state)):
         return _Scan.apply(q, k, v, log_alpha, beta, initial_state, offsets, mixer, batch)
     return _forward(q, k, v, log_alpha, beta, initial_state, offsets, mixer, batch)[:2]

@@ -316,3 +316,33 @@ def test_rows_of_zeros_with_a_tiny_eps():
         exact = torch.autograd.grad(want, [l64["residual"]], [s.double() for s in seeds])[0]
         for i in range(6):
             assert rel(got[i], exact[i]) <= tol(torch.float32), (eps, i)
+
+
+def test_forward_mode_and_tracing_are_refused():
+    """Neither has a rule here: an error, and not a result without a tangent or an empty trace."""
+    from torch.autograd import forward_ad
+    from torch.fx.experimental.proxy_tensor import make_fx
+
+    from bit_recurrent_state_amd import block_norm, scan
+    from scan_reference import GDN, inputs
+    x = torch.randn(3, 64, device="cuda")
+    s = inputs(GDN, 1, [12], 1, 1, 64, 8, torch.float32, "cuda")
+
+    def go(x, v):
+        o, _ = scan(s["q"], s["k"], v, s["log_alpha"], s["beta"], mixer=GDN, offsets=s["offsets"])
+        return block_norm(x), o
+
+    want = go(x, s["v"])
+    with forward_ad.dual_level():
+        again = go(x, s["v"])  # no tangents: as ever
+        assert all(torch.equal(a, b) for a, b in zip(want, again))
+        with pytest.raises(NotImplementedError):
+            block_norm(forward_ad.make_dual(x, torch.ones_like(x)))
+        with pytest.raises(NotImplementedError):
+            go(x, forward_ad.make_dual(s["v"], torch.ones_like(s["v"])))
+    for f, a in ((lambda x: block_norm(x), x), (lambda v: go(x, v)[1], s["v"])):
+        with pytest.raises(RuntimeError, match="trac"):
+            make_fx(f)(a)
+        with pytest.raises(RuntimeError, match="trac"):
+            torch.jit.trace(f, a)
+    assert all(torch.equal(a, b) for a, b in zip(want, go(x, s["v"])))

@@ -330,3 +330,29 @@ def test_captured_backward_while_other_threads_begin_calls(monkeypatch):
         for t in threads:
             t.join()
     assert not failed
+
+
+def test_tracing_is_refused_and_forward_mode_goes_through_autograd():
+    from torch.autograd import forward_ad
+    from torch.fx.experimental.proxy_tensor import make_fx
+
+    from bit_recurrent_state_amd import block_norm, scan
+    from bit_recurrent_state_amd.sequence import _through_autograd
+    x, s = torch.randn(3, 8), inputs(GDN, 1, [3], 2, 2, 64, 8, torch.float32, "cpu")
+
+    def call(v):
+        return scan(s["q"], s["k"], v, s["log_alpha"], s["beta"], mixer=GDN, offsets=s["offsets"])[0]
+
+    for f, a in ((lambda x: block_norm(x), x), (call, s["v"])):
+        with pytest.raises(RuntimeError, match="traced"):
+            make_fx(f)(a)
+        with pytest.raises(RuntimeError, match="traced"):
+            torch.jit.trace(f, a)
+        with pytest.raises(TypeError, match="device tensor"):  # and no longer after it
+            f(a)
+    assert not _through_autograd((x, None))
+    with forward_ad.dual_level():
+        assert _through_autograd((x, None))
+        with torch.no_grad():
+            assert _through_autograd((forward_ad.make_dual(x, x),))
+    assert _through_autograd((x.clone().requires_grad_(True),)) and not _through_autograd((x,))
