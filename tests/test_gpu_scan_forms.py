@@ -138,6 +138,18 @@ def test_backward_with_row_strides_of_its_own(mixer, dtype):
         assert rel(out[n], w) <= tolerance(out[n].dtype, True), n
 
 
+@pytest.mark.parametrize("mixer", MIXERS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dk,N,dv", [(64, 2, 90), (128, 2, 90), (256, 2, 90), (64, 4, 121), (128, 4, 121),
+                                     (256, 4, 121)])
+def test_wide_column_blocks(mixer, dtype, dk, N, dv):
+    """As many heads and columns as make the chains take 32 columns a workgroup (32 heads, N = 2:
+    192 blocks of 32) and, forward up to dk = 128, 64 (N = 4: 512)."""
+    m = MIXERS[mixer]
+    lens = [70, 9, 0, 66][:N]
+    check(inputs(m, N, lens, 32, 16, dk, dv, TYPES[dtype], "cuda"), m, N)
+
+
 @pytest.mark.parametrize("mixer", ["gla", "kda"])
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("dk,dv,H,Hq", [(64, 64, 2, 2), (128, 40, 4, 2), (256, 64, 2, 1)])
