@@ -80,16 +80,27 @@ size_t layout(const qstate_scan_config* c, bool backward, void* workspace, Param
   p.direct = !vec && bf16 && p.qs % 8 == 0 && p.ks % 8 == 0;
   p.nslots = (int)(c->tokens / kChunk + c->batch);
   p.dvp = (c->dv + 31) / 32 * 32;
-  // Value columns of a chain workgroup, of which a CU (256) holds one at a time:
-  // the fewest rounds, each as long as its width makes it.  Narrow blocks
-  // shorten the chain from chunk to chunk, wide ones share its fixed work: 32
-  // columns take about 1.5 times as long as 16 forward and 1.6 times backward
-  // (256 blocks of 32, backward: 66 us, as 16: 78; 320: 164 and 102).  64, forward,
-  // pay where there are many (768 of 32: 299 us, as 64: 234; 2048: 136 and 124).
+  // Value columns of a chain workgroup.  Narrow blocks shorten the chain from chunk to chunk, wide
+  // ones share its operands, whose way out of L2 and through LDS bounds it: workgroups that share a CU
+  // take about as long as one after the other (GDN, 1024 tokens: 256 of 16 columns 64 us, 512 110 us),
+  // though registers and LDS hold two.  So 16 or 32 by the least sum over a CU's workgroups, at 10 for
+  // 16 columns and 15 forward, 16 backward for 32; and 64, forward, beyond 256 blocks of 32.  Whole
+  // calls in us, 1024 tokens a sequence (1536: 512), dk 128:
+  //   blocks of 32        128  256  384  512  768 1536
+  //   GDN, 16 columns      64  110  158  209  336  355   backward  167  334  500  660  980  987
+  //   32                   73   87  144  159  249  260             200  317  494  570  847  855
+  //   64                  103  115  129  145  260  231
+  // SCALAR, 16 / 32 / 64 columns: 63 / 59 / 84 at 256, 89 / 98 / 91 at 384, 110 / 107 / 99 at 512;
+  // GLA: 118 / 103 / 121, 186 / 175 / 161 and 260 / 211 / 192.  Equal lengths at 768 are the exception
+  // (SCALAR 166 with 32, 188 with 64); ragged ones are not (GDN, six prompts of up to 2900 tokens: 410
+  // with 32, 374 with 64).
+  // With the delta rule on split q and k a workgroup has no registers left for 64 columns forward and 32
+  // backward: KDA at 512 446 / 370 / 377 and 1123 / 1216, FP32 GDN 454 / 380 / 483 and 1039 / 1135.
   const int64_t blocks = (int64_t)c->batch * c->heads * (p.dvp / 32);
+  const bool heavy = delta && !p.direct;
   const int64_t narrow = (2 * blocks + 255) / 256 * 10, wide = (blocks + 255) / 256 * (backward ? 16 : 15);
-  p.vblock = narrow < wide ? 16 : 32;
-  if (!backward && blocks >= 512 && p.dvp % 64 == 0 && c->dk <= 128) p.vblock = 64;
+  p.vblock = narrow < wide || (backward && heavy) ? 16 : 32;
+  if (!backward && !heavy && blocks > 256 && p.dvp % 64 == 0 && c->dk <= 128) p.vblock = 64;
   p.nvb = p.dvp / p.vblock;
   p.dop_terms = bf16 ? 1 : kTerms;
 

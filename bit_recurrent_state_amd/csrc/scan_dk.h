@@ -62,37 +62,53 @@ hipError_t backward_tail(const Params& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Column blocks as the host's rule has them (scan_api.cpp).
+template <int DK, int NPQ, bool VEC, bool DELTA>
+hipError_t forward_width(const Params& p, hipStream_t s) {
+  if constexpr (DK <= 128 && !(DELTA && NPQ > 1))
+    if (p.vblock == 64) return forward_tail<DK, 4, NPQ, VEC, DELTA>(p, s);
+  return p.vblock == 16 ? forward_tail<DK, 1, NPQ, VEC, DELTA>(p, s)
+                        : forward_tail<DK, 2, NPQ, VEC, DELTA>(p, s);
+}
+
+template <int DK, int NPQ, int NPO, bool VEC, bool DELTA>
+hipError_t backward_width(const Params& p, hipStream_t s) {
+  if constexpr (!(DELTA && NPQ > 1))
+    if (p.vblock == 32) return backward_tail<DK, 2, NPQ, NPO, VEC, DELTA>(p, s);
+  return backward_tail<DK, 1, NPQ, NPO, VEC, DELTA>(p, s);
+}
+
 // Operand kinds: the caller's bfloat16 rows (one term); rows split into terms
 // (FP32, FP16, unaligned bfloat16); rows scaled per channel (always split).
-template <int DK, int NT>
+template <int DK>
 hipError_t forward(const Params& p, hipStream_t s) {
   switch (p.mixer) {
-    case GDN: return p.direct ? forward_tail<DK, NT, 1, false, true>(p, s)
-                              : forward_tail<DK, NT, P, false, true>(p, s);
-    case SCALAR: return p.direct ? forward_tail<DK, NT, 1, false, false>(p, s)
-                                 : forward_tail<DK, NT, P, false, false>(p, s);
-    case GLA: return forward_tail<DK, NT, P, true, false>(p, s);
-    case KDA: return forward_tail<DK, NT, P, true, true>(p, s);
+    case GDN: return p.direct ? forward_width<DK, 1, false, true>(p, s)
+                              : forward_width<DK, P, false, true>(p, s);
+    case SCALAR: return p.direct ? forward_width<DK, 1, false, false>(p, s)
+                                 : forward_width<DK, P, false, false>(p, s);
+    case GLA: return forward_width<DK, P, true, false>(p, s);
+    case KDA: return forward_width<DK, P, true, true>(p, s);
     default: return hipErrorInvalidValue;
   }
 }
 
 // d_o's terms (NPO) are those of the workspace's layout, whether or not q and k are split: bfloat16
 // rows off 16 bytes have split q and k and a d_o of one term.
-template <int DK, int NT>
+template <int DK>
 hipError_t backward(const Params& p, hipStream_t s) {
   const bool one = p.dop_terms == 1;
   switch (p.mixer) {
-    case GDN: return p.direct ? backward_tail<DK, NT, 1, 1, false, true>(p, s)
-                     : one    ? backward_tail<DK, NT, P, 1, false, true>(p, s)
-                              : backward_tail<DK, NT, P, P, false, true>(p, s);
-    case SCALAR: return p.direct ? backward_tail<DK, NT, 1, 1, false, false>(p, s)
-                        : one    ? backward_tail<DK, NT, P, 1, false, false>(p, s)
-                                 : backward_tail<DK, NT, P, P, false, false>(p, s);
-    case GLA: return one ? backward_tail<DK, NT, P, 1, true, false>(p, s)
-                         : backward_tail<DK, NT, P, P, true, false>(p, s);
-    case KDA: return one ? backward_tail<DK, NT, P, 1, true, true>(p, s)
-                         : backward_tail<DK, NT, P, P, true, true>(p, s);
+    case GDN: return p.direct ? backward_width<DK, 1, 1, false, true>(p, s)
+                     : one    ? backward_width<DK, P, 1, false, true>(p, s)
+                              : backward_width<DK, P, P, false, true>(p, s);
+    case SCALAR: return p.direct ? backward_width<DK, 1, 1, false, false>(p, s)
+                        : one    ? backward_width<DK, P, 1, false, false>(p, s)
+                                 : backward_width<DK, P, P, false, false>(p, s);
+    case GLA: return one ? backward_width<DK, P, 1, true, false>(p, s)
+                         : backward_width<DK, P, P, true, false>(p, s);
+    case KDA: return one ? backward_width<DK, P, 1, true, true>(p, s)
+                         : backward_width<DK, P, P, true, true>(p, s);
     default: return hipErrorInvalidValue;
   }
 }

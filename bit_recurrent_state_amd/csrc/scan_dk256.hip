@@ -4,11 +4,7 @@
 
 namespace qscan {
 
-hipError_t forward_dk256(const Params& p, hipStream_t s) { 
-  return p.vblock == 16 ? forward<256, 1>(p, s) : forward<256, 2>(p, s);
- }
-hipError_t backward_dk256(const Params& p, hipStream_t s) { 
-  return p.vblock == 16 ? backward<256, 1>(p, s) : backward<256, 2>(p, s);
- }
+hipError_t forward_dk256(const Params& p, hipStream_t s) { return forward<256>(p, s); }
+hipError_t backward_dk256(const Params& p, hipStream_t s) { return backward<256>(p, s); }
 
 }  // namespace qscan
