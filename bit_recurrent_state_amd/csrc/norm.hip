@@ -7,7 +7,7 @@
 // are loaded, and their gradients summed, once per team: rows up to 512 wide
 // take 1 .. 64 lanes of a wave (a readout's 128 values: 16 lanes), wider ones a
 // workgroup.  8191 rows of 4096 bfloat16 values with all parts take 74 us forward
-// (336 MB, 4.5 TB/s) and 128 us backward (550 MB, 4.3 TB/s); a copy of that size
+// (336 MB, 4.5 TB/s) and 131 us backward (550 MB, 4.2 TB/s); a copy of that size
 // runs at 4.6 TB/s.
 
 #include <hip/hip_runtime.h>

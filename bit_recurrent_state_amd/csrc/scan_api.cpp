@@ -80,12 +80,12 @@ size_t layout(const qstate_scan_config* c, bool backward, void* workspace, Param
   p.direct = !vec && bf16 && p.qs % 8 == 0 && p.ks % 8 == 0;
   p.nslots = (int)(c->tokens / kChunk + c->batch);
   p.dvp = (c->dv + 31) / 32 * 32;
-  // Value columns of a chain workgroup.  Narrow blocks shorten the chain from chunk to chunk, wide
-  // ones share its operands, whose way out of L2 and through LDS bounds it: workgroups that share a CU
-  // take about as long as one after the other (GDN, 1024 tokens: 256 of 16 columns 64 us, 512 110 us),
-  // though registers and LDS hold two.  So 16 or 32 by the least sum over a CU's workgroups, at 10 for
-  // 16 columns and 15 forward, 16 backward for 32; and 64, forward, beyond 256 blocks of 32.  Whole
-  // calls in us, 1024 tokens a sequence (1536: 512), dk 128:
+  // Value columns of a chain workgroup, of which a CU (256) holds one at a time: eight waves of 132 to
+  // 256 registers a lane (SCALAR's of 16 columns take 112, two of them share a CU and what it brings
+  // out of L2).  16 or 32 by the fewest rounds, each as long as its width makes it: narrow blocks
+  // shorten the chain from chunk to chunk, wide ones share its fixed work; 10 for 16 columns and 15
+  // forward, 16 backward for 32.  64, forward, beyond 256 blocks of 32.  Whole calls in us, 1024 tokens
+  // a sequence (1536: 512), dk 128:
   //   blocks of 32        128  256  384  512  768 1536
   //   GDN, 16 columns      64  110  158  209  336  355   backward  167  334  500  660  980  987
   //   32                   73   87  144  159  249  260             200  317  494  570  847  855

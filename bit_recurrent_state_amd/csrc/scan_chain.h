@@ -34,9 +34,9 @@ __device__ __forceinline__ bool chain_block(const Params& p, int& n, int& h, int
 // What bounds it is the chain from one state to the next, so it has waves of
 // its own: waves 0..3 compute R, U and S, waves 4..7 beside them O, which
 // nothing waits for.  (All in four waves a chunk took 6400 cycles, O's part of
-// them 1900.)  At dk = 128 and 16 columns a chunk takes 2.4 us (GDN, bfloat16,
-// 256 workgroups) to 2.8 us (KDA, 128); the matrix instructions are busy for
-// 8 to 13 % of it, LDS round trips between the barriers and 70 to 150 KB of
+// them 1900.)  At dk = 128 and 16 columns a chunk takes 2.6 us (GDN, bfloat16,
+// 256 workgroups) to 3.1 us (KDA, 128); the matrix instructions are busy for
+// 9 to 14 % of it, LDS round trips between the barriers and 100 to 170 KB of
 // operands out of L2 for each chunk take the rest.
 // Outputs take every term, as the state does, whatever their type: with two terms
 // of q, A, S and W a 16-bit output that is small by cancellation would be off by

@@ -15,7 +15,7 @@ constexpr int kChunk = 64;  // tokens of a chunk
 constexpr int kTerms = 3;   // bfloat16 terms of an FP32 operand
 // Longest sequence that is taken token by token.  A token costs its own steps
 // there, a chunk the same for 1 and for 64 tokens: 96 ragged sequences of up to
-// 33 tokens (GLA, 16 heads of 128 x 128, FP32) took 267 us with 8 and 361 us
+// 33 tokens (GLA, 16 heads of 128 x 128, FP32) take 232 us with 8 and 418 us
 // with 32.
 constexpr int kShort = 8;
 constexpr float kFarDecay = 24.0f;  // largest decay of a chunk, as a logarithm, that is divided out

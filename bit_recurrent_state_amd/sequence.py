@@ -194,7 +194,8 @@ def qstate_scan(cfg: ScanConfig, q, k, v, log_alpha, beta=None, offsets=None, in
 def qstate_scan_backward(cfg: ScanConfig, q, k, v, log_alpha, beta, offsets, initial_state, d_o,
                          d_final_state, dq, dk, dv, dlog_alpha, dbeta=None, d_initial_state=None,
                          workspace=None, stream=None) -> None:
-    """Gradients of the scan's inputs from those of `o` and `final_state`."""
+    """Gradients of the scan's inputs from those of `o` and `final_state`; `d_o` and the gradients are
+    packed."""
     args = _inputs(cfg, q, k, v, log_alpha, beta, offsets, initial_state)
     dev = q.device
     hq = cfg.heads_qk or cfg.heads

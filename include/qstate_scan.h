@@ -100,9 +100,9 @@ int qstate_scan(const qstate_scan_config* cfg, const void* q, const void* k, con
                 const float* initial_state, void* o, float* final_state, void* workspace,
                 size_t workspace_bytes, void* stream);
 
-/* Gradients of a scalar of o and final_state, from d_o (dtype, laid out as o)
- * and d_final_state (NULL: zeros).  The states are computed again from the
- * inputs.  Written, each packed without row strides:
+/* Gradients of a scalar of o and final_state, from d_o (dtype [tokens][heads][dv],
+ * packed: o_stride is not used here) and d_final_state (NULL: zeros).  The states
+ * are computed again from the inputs.  Written, each packed without row strides:
  *   dq, dk  dtype [tokens][heads_qk][dk], summed over the heads that share them
  *   dv      dtype [tokens][heads][dv]
  *   dlog_alpha  float, laid out as log_alpha;  dbeta  float (not for GLA)
