@@ -14,6 +14,7 @@
  * residual (r = scale y), scale (1), next_weight (no h).  Everything between
  * the inputs and the outputs r and h is FP32, rounded once at the end (h is
  * taken from r before r is rounded); squares of values beyond 1e19 overflow.
+ * silu goes to zero below (to 2e-36, at minus infinity too) and to the gate above.
  *
  * Layout: rows are [tokens][groups]; a readout has groups = heads and
  * width = dv, a block's end groups = 1 and width the model's.
