@@ -35,6 +35,9 @@ SCAN_EXPORTS = ("qstate_scan_workspace", "qstate_scan", "qstate_scan_backward")
 # include/qstate_norm.h: the norms around the mixer block and their gradients
 NORM_EXPORTS = ("qstate_norm", "qstate_norm_workspace", "qstate_norm_backward")
 
+# include/qstate_draft.h: drafted tokens over the stored state
+DRAFT_EXPORTS = ("qstate_verify", "qstate_accept")
+
 
 class QStateConfig(ctypes.Structure):
     _fields_ = [
@@ -61,6 +64,11 @@ class NormConfigC(ctypes.Structure):
                                                  "weight_groups")]
                 + [("eps", ctypes.c_float)]
                 + [(n, ctypes.c_int64) for n in ("x_stride", "gate_stride", "residual_stride")])
+
+
+class DraftConfigC(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("tokens", "heads_qk", "dtype", "pad")]
+                + [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")])
 
 
 _lib = None
@@ -102,6 +110,8 @@ def lib() -> ctypes.CDLL:
         "qstate_norm_backward": (c_int, [ctypes.POINTER(NormConfigC)] + [P] * 6 + [c_int]
                                  + [P] * 9 + [sz, P]),
         "qstate_scan_backward": (c_int, [ctypes.POINTER(ScanConfigC)] + [P] * 16 + [sz, P]),
+        "qstate_verify": (c_int, [cfgp, ctypes.POINTER(DraftConfigC)] + [P] * 11),
+        "qstate_accept": (c_int, [cfgp, ctypes.POINTER(DraftConfigC), ctypes.c_uint64] + [P] * 8),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(L, name)

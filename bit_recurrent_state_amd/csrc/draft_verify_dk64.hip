@@ -1,0 +1,8 @@
+// draft_verify_dk64.hip — the readout of drafted tokens for key dimension dk = 64
+// (see draft_verify.h).
+
+#include "draft_verify.h"
+
+namespace qdraft {
+hipError_t verify_dk64(const Params& p, hipStream_t s) { return verify<64>(p, s); }
+}  // namespace qdraft

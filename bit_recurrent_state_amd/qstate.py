@@ -15,8 +15,9 @@ import torch
 
 from ._lib import (BDR, GDN, GLA, KDA, KEY_AXIS, RTN, SCALAR, SR, VALUE_AXIS, QStateConfig, check,
                    lib)
+from .draft import Draft, _accept, _verify
 from .norm import SILU, NormConfig, qstate_norm, qstate_norm_workspace
-from .sequence import _array, _on, scan
+from .sequence import _array, _on, _on_device, scan
 
 __all__ = [
     "GDN", "GLA", "SCALAR", "KDA", "RTN", "SR", "BDR", "VALUE_AXIS", "KEY_AXIS", "Config",
@@ -268,6 +269,38 @@ class QState:
             if norm is not None:
                 norm._run(cfg, o)
         return o
+
+    def verify(self, q, k, v, log_alpha, beta=None, parents=None, norm=None, stream=None):
+        """The readouts of drafted tokens, for every sequence a tree of them over its stored state,
+        which stays as it is; returns (o, draft), `draft` for `accept`.
+
+        q, k [N, T, heads_qk, dk], v [N, T, heads, dv], one dtype (float32, bfloat16, float16), T up
+        to 64 (32 with dk = 256), heads_qk a divisor of the handle's heads; log_alpha [N, T, heads]
+        (GDN, SCALAR) or [N, T, heads, dk] (GLA, KDA) and beta [N, T, heads] (not for GLA) in float32.
+        parents [N, T] (int32, on the device): the earlier row of the sequence that a row hangs on, -1
+        for the stored state, anything else (-2) where the row is padding; None is a chain.  o, of v's
+        shape and dtype, is what `step` would read out behind each node's path, without the
+        quantization after every token; zero in rows of no node.  o and draft lie in the memory of the
+        stream of the call.  Not for key-axis groups and pair windows."""
+        dev = self.codes.device
+        if norm is not None:  # refused before any launch
+            _on_device(v, "v", dev)
+            rows = v.shape[0] * v.shape[1] if v.dim() == 4 else 0
+            cfg = norm.config((rows, self.cfg.heads, self.cfg.dv), v.dtype, dev, v.shape)
+        with torch.no_grad(), torch.cuda.device(dev), _on(stream, dev):
+            o, draft = _verify(self.cfg, self.codes, self.scales, q, k, v, log_alpha, beta, parents)
+            if norm is not None:
+                norm._run(cfg, o)
+        return o, draft
+
+    def accept(self, draft: Draft, last, stream=None):
+        """The path of drafted tokens that ends in row last[n] (int32 [N], on the device) enters the
+        stored state of sequence n, in one quantization event: the counter goes up by one.  A sequence
+        with last[n] = -1 accepts none and keeps its state bit for bit."""
+        dev = self.codes.device
+        with torch.no_grad(), torch.cuda.device(dev), _on(stream, dev):
+            _accept(self.cfg, self.codes, self.scales, self.step_counter, draft, last)
+        self.step_counter += 1
 
     def readout(self, q, o, stream=None):
         qstate_readout(self.handle, self.cfg, q, o, stream)
