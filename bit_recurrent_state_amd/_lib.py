@@ -38,6 +38,14 @@ NORM_EXPORTS = ("qstate_norm", "qstate_norm_workspace", "qstate_norm_backward")
 # include/qstate_draft.h: drafted tokens over the stored state
 DRAFT_EXPORTS = ("qstate_verify", "qstate_accept")
 
+# include/qstate_group_norm.h: the group norm of the readout and its gradients
+GROUP_NORM_EXPORTS = ("qstate_group_norm", "qstate_group_norm_workspace",
+                      "qstate_group_norm_backward")
+
+# include/qstate_linear.h: products with 4-bit weights
+LINEAR_EXPORTS = ("qstate_linear", "qstate_linear_bytes", "qstate_linear_pack",
+                  "qstate_linear_quantize")
+
 
 class QStateConfig(ctypes.Structure):
     _fields_ = [
@@ -69,6 +77,18 @@ class NormConfigC(ctypes.Structure):
 class DraftConfigC(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int32) for n in ("tokens", "heads_qk", "dtype", "pad")]
                 + [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")])
+
+
+class GroupNormConfigC(ctypes.Structure):
+    _fields_ = ([("tokens", ctypes.c_int64)]
+                + [(n, ctypes.c_int32) for n in ("groups", "width", "dtype", "act", "mode", "center")]
+                + [("eps", ctypes.c_float), ("shared", ctypes.c_int32)]
+                + [(n, ctypes.c_int64) for n in ("x_stride", "gate_stride")])
+
+
+class LinearConfigC(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("inputs", "outputs", "group", "dtype")]
+                + [(n, ctypes.c_int64) for n in ("rows", "x_stride")])
 
 
 _lib = None
@@ -110,6 +130,16 @@ def lib() -> ctypes.CDLL:
         "qstate_norm_backward": (c_int, [ctypes.POINTER(NormConfigC)] + [P] * 6 + [c_int]
                                  + [P] * 9 + [sz, P]),
         "qstate_scan_backward": (c_int, [ctypes.POINTER(ScanConfigC)] + [P] * 16 + [sz, P]),
+        "qstate_group_norm": (c_int, [ctypes.POINTER(GroupNormConfigC)] + [P] * 6),
+        "qstate_group_norm_workspace": (c_int, [ctypes.POINTER(GroupNormConfigC),
+                                                ctypes.POINTER(sz)]),
+        "qstate_group_norm_backward": (c_int, [ctypes.POINTER(GroupNormConfigC)] + [P] * 10
+                                       + [sz, P]),
+        "qstate_linear": (c_int, [ctypes.POINTER(LinearConfigC)] + [P] * 6),
+        "qstate_linear_bytes": (c_int, [ctypes.POINTER(LinearConfigC), ctypes.POINTER(sz),
+                                        ctypes.POINTER(sz)]),
+        "qstate_linear_pack": (c_int, [ctypes.POINTER(LinearConfigC)] + [P] * 5),
+        "qstate_linear_quantize": (c_int, [ctypes.POINTER(LinearConfigC)] + [P] * 4),
         "qstate_verify": (c_int, [cfgp, ctypes.POINTER(DraftConfigC)] + [P] * 11),
         "qstate_accept": (c_int, [cfgp, ctypes.POINTER(DraftConfigC), ctypes.c_uint64] + [P] * 8),
     }

@@ -26,18 +26,22 @@ SOURCES = ([os.path.join(CSRC, f"qstate_window_dk{dk}_w{w}.hip")
               for kind in ("verify", "accept") for dk in (256, 128, 64)]
            + [os.path.join(CSRC, "draft_api.cpp")]
            + [os.path.join(CSRC, "qstate_ceiling.hip"), os.path.join(CSRC, "scan_api.cpp"),
-              os.path.join(CSRC, "norm.hip"), os.path.join(CSRC, "norm_api.cpp")]
+              os.path.join(CSRC, "norm.hip"), os.path.join(CSRC, "norm_api.cpp"),
+              os.path.join(CSRC, "group_norm.hip"), os.path.join(CSRC, "group_norm_api.cpp"),
+              os.path.join(CSRC, "linear.hip"), os.path.join(CSRC, "linear_api.cpp")]
            + [os.path.join(CSRC, "qstate_dispatch.cpp"), os.path.join(CSRC, "qstate_api.cpp")])
 HEADERS = [os.path.join(ROOT, "include", h) for h in ("qstate.h", "qstate_ceiling.h",
                                                          "qstate_scan.h", "qstate_norm.h",
-                                                         "qstate_draft.h")] + [
+                                                         "qstate_draft.h",
+                                                         "qstate_group_norm.h", "qstate_linear.h")] + [
     os.path.join(CSRC, h) for h in ("qstate_launch.h", "qstate_device.h", "qstate_value.h",
                                     "qstate_key.h", "qstate_window.h",
                                     "qstate_persist.h", "scan_launch.h", "scan_device.h",
                                     "scan_prep.h", "scan_prep_vector.h",
                                     "scan_chain.h", "scan_grads.h", "scan_tokens.h",
                                     "scan_dk.h",
-                                    "norm_launch.h",
+                                    "norm_launch.h", "norm_device.h", "group_norm_launch.h",
+                                    "linear_launch.h",
                                     "draft_launch.h", "draft_device.h", "draft_verify.h",
                                     "draft_accept.h")]
 BUILD = os.path.join(ROOT, "_build")

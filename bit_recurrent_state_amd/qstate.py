@@ -16,6 +16,8 @@ import torch
 from ._lib import (BDR, GDN, GLA, KDA, KEY_AXIS, RTN, SCALAR, SR, VALUE_AXIS, QStateConfig, check,
                    lib)
 from .draft import Draft, _accept, _verify
+from .group_norm import (GATE, GATE_FIRST, PLAIN, GroupNormConfig, qstate_group_norm,
+                         qstate_group_norm_workspace)
 from .norm import SILU, NormConfig, qstate_norm, qstate_norm_workspace
 from .sequence import _array, _on, _on_device, scan
 
@@ -180,30 +182,48 @@ def qstate_bits_by_decay(retention, mode: int, thr_or_frac: float, lo_bits: int 
 @dataclass
 class ReadoutNorm:
     """What a layer does with the readout before its output projection:
-    o * rsqrt(mean(o^2) + eps) * weight * act(gate), over each head's dv values."""
+    o * rsqrt(mean(o^2) + eps) * weight * act(gate), over each head's dv values; with `center`, `bias`
+    or `gate_first` the forms of `group_norm` over heads (a retention layer's, a Mamba2 block's)."""
 
     weight: Optional[torch.Tensor] = None  # float32 [dv] or [heads, dv]
     gate: Optional[torch.Tensor] = None    # of o's type and shape (or its rows or values in a row)
     eps: float = 1e-6
     act: int = SILU
+    bias: Optional[torch.Tensor] = None    # as weight
+    center: bool = False                   # the mean is taken off before the variance
+    gate_first: bool = False               # the norm of o * act(gate)
 
-    def config(self, shape, dtype, device, o_shape=None) -> NormConfig:
+    @property
+    def grouped(self) -> bool:
+        return self.center or self.gate_first or self.bias is not None
+
+    def config(self, shape, dtype, device, o_shape=None):
         """The configuration for a readout of this shape, its tensors checked.  o_shape: the shape in
         which the caller has it."""
         tokens, heads, dv = shape
-        each = self.weight is not None and self.weight.dim() == 2
-        if self.weight is not None:
-            w = tuple(self.weight.shape)
-            if w[-1:] != (dv,) or each and w != (heads, dv):
-                raise ValueError(f"weight: expected [{dv}] or [{heads}, {dv}], got {w}")
+        each = any(t is not None and t.dim() == 2 for t in (self.weight, self.bias))
+        for t, name in ((self.weight, "weight"), (self.bias, "bias")):
+            if t is not None:
+                w = tuple(t.shape)
+                if w[-1:] != (dv,) or each and w != (heads, dv):
+                    raise ValueError(f"{name}: expected [{dv}] or [{heads}, {dv}], got {w}")
         if self.gate is not None:
             g = tuple(self.gate.shape)
             if g not in (tuple(shape), (tokens * heads * dv,), tuple(o_shape or shape)):
                 raise ValueError(f"gate: expected {tuple(o_shape or shape)}, got {g}")
-        cfg = NormConfig(tokens, heads, dv, dtype, self.act, each, self.eps)
-        qstate_norm_workspace(cfg)  # the library's checks of it
-        _array(self.weight, "weight", torch.float32, dv * (heads if each else 1), device,
-               optional=True)
+        if self.grouped:
+            if self.gate_first and self.gate is None:
+                raise ValueError("gate_first: there is no gate")
+            mode = PLAIN if self.gate is None else GATE_FIRST if self.gate_first else GATE
+            cfg = GroupNormConfig(tokens, heads, dv, dtype, self.act, mode, self.center, self.eps,
+                                  not each)
+            qstate_group_norm_workspace(cfg)  # the library's checks of it
+        else:
+            cfg = NormConfig(tokens, heads, dv, dtype, self.act, each, self.eps)
+            qstate_norm_workspace(cfg)
+        n = dv * (heads if each else 1)
+        _array(self.weight, "weight", torch.float32, n, device, optional=True)
+        _array(self.bias, "bias", torch.float32, n, device, optional=True)
         _array(self.gate, "gate", dtype, tokens * heads * dv, device, optional=True)
         return cfg
 
@@ -211,7 +231,12 @@ class ReadoutNorm:
         """In place on o [tokens, heads, dv]."""
         self._run(self.config(o.shape, o.dtype, o.device), o, stream)
 
-    def _run(self, cfg: NormConfig, o: torch.Tensor, stream=None) -> None:
+    def _run(self, cfg, o: torch.Tensor, stream=None) -> None:
+        if self.grouped:
+            o = o.view(cfg.tokens, cfg.groups * cfg.width)
+            gate = None if self.gate is None else self.gate.view(o.shape)
+            qstate_group_norm(cfg, o, self.weight, self.bias, gate, o, stream)
+            return
         o = o.view(cfg.tokens, cfg.groups, cfg.width)
         gate = None if self.gate is None else self.gate.view(o.shape)
         qstate_norm(cfg, o, self.weight, gate, r=o, stream=stream)
