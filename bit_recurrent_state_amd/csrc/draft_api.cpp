@@ -116,10 +116,9 @@ int qstate_verify(const qstate_config* state, const qstate_draft_config* draft,
   p.o = o;
   p.writes = writes;
   p.direct = !vector_gate(state->mixer) && draft->dtype == QSTATE_BF16;
-  p.pairs = state->dv % 2 == 0 && p.vs % 2 == 0 && aligned(v, 2 * e) && aligned(o, 2 * e);
-  const int columns = (state->dv + 31) / 32;
-  p.waves = columns < 4 ? columns : 4;
-  p.blocks = (columns + p.waves - 1) / p.waves;
+  p.pairs = state->dv % 2 == 0 && aligned(o, 2 * e);
+  p.columns = state->dv > 64 ? 128 : 64;
+  p.blocks = (state->dv + p.columns - 1) / p.columns;
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   switch (state->dk) {
     case 64: return status(qdraft::verify_dk64(p, s));

@@ -25,9 +25,10 @@ struct Params {
   const float* writes_in;
   float* writes;
   int direct;     // bfloat16 q and k enter the products as they are
-  int pairs;      // two neighbouring values of v, o and writes are one access
-  int waves;      // waves of a workgroup; verify: 32 value columns each
+  int pairs;      // two neighbouring values of o and writes are one access
+  int columns;    // verify: value columns of a workgroup, 64 or 128
   int blocks;     // workgroups of a head
+  int waves;      // accept: waves of a workgroup
   int rows;       // accept: value rows of a workgroup
 };
 
