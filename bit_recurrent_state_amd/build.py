@@ -23,7 +23,7 @@ SOURCES = ([os.path.join(CSRC, f"qstate_window_dk{dk}_w{w}.hip")
               for kind in ("value", "key") for dk in (64, 128, 256)]
            + [os.path.join(CSRC, f"scan_dk{dk}.hip") for dk in (256, 128, 64)]
            + [os.path.join(CSRC, f"draft_{kind}_dk{dk}.hip")
-              for kind in ("verify", "accept") for dk in (256, 128, 64)]
+              for kind in ("verify", "verify_channels", "accept") for dk in (256, 128, 64)]
            + [os.path.join(CSRC, "draft_api.cpp")]
            + [os.path.join(CSRC, "qstate_ceiling.hip"), os.path.join(CSRC, "scan_api.cpp"),
               os.path.join(CSRC, "norm.hip"), os.path.join(CSRC, "norm_api.cpp"),

@@ -115,9 +115,12 @@ int qstate_verify(const qstate_config* state, const qstate_draft_config* draft,
   p.parents = parents;
   p.o = o;
   p.writes = writes;
-  p.direct = !vector_gate(state->mixer) && draft->dtype == QSTATE_BF16;
+  p.direct = !vector_gate(state->mixer) && draft->dtype == QSTATE_BF16 && p.qs % 8 == 0 && p.ks % 8 == 0;
   p.pairs = state->dv % 2 == 0 && aligned(o, 2 * e);
-  p.columns = state->dv > 64 ? 128 : 64;
+  p.vpairs = state->dv % 2 == 0 && p.vs % 2 == 0 && aligned(v, 2 * e);
+  const bool narrow =
+      qdraft::narrow(state->dk, draft->tokens, !p.direct, vector_gate(state->mixer));
+  p.columns = state->dv > 64 && !narrow ? 128 : 64;
   p.blocks = (state->dv + p.columns - 1) / p.columns;
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   switch (state->dk) {
