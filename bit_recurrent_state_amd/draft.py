@@ -13,7 +13,7 @@ from typing import Optional
 import torch
 
 from ._lib import GLA, KDA, DraftConfigC, check, lib
-from .sequence import DTYPES, _array, _call, _on_device, _refuse_tracing, _stream
+from .sequence import DTYPES, _array, _call, _on_device, _ptr, _refuse_tracing, _stream
 
 __all__ = ["Draft", "DraftConfig", "qstate_verify", "qstate_accept"]
 
@@ -127,8 +127,12 @@ def qstate_accept(cfg, draft: DraftConfig, step: int, codes, scales, k, log_alph
 
 def _row_stride(t: torch.Tensor) -> int:
     """Elements between the rows [N][T] of t, or -1 where it takes a copy."""
+    if t.data_ptr() % 16:
+        return -1
+    if t.is_contiguous():
+        return 0
     N, T, heads, d = t.shape
-    if not ((d == 1 or t.stride(3) == 1) and (heads == 1 or t.stride(2) == d)) or t.data_ptr() % 16:
+    if not ((d == 1 or t.stride(3) == 1) and (heads == 1 or t.stride(2) == d)):
         return -1
     row = t.stride(1) if T > 1 else t.stride(0) if N > 1 else heads * d
     if not heads * d <= row <= 1 << 22 or (N > 1 and T > 1 and t.stride(0) != T * row):
@@ -141,13 +145,14 @@ def _token_rows(t: torch.Tensor):
     distance, or start off a 16-byte boundary."""
     stride = _row_stride(t)
     if stride < 0:
-        t, stride = t.clone(memory_format=torch.contiguous_format), 0
+        t, stride = t.detach().clone(memory_format=torch.contiguous_format), 0
     return t, stride
 
 
 def _aligned(t: torch.Tensor) -> torch.Tensor:
-    t = t.contiguous()
-    return t.clone() if t.data_ptr() % 16 else t
+    if not t.is_contiguous():
+        t = t.detach().contiguous()
+    return t.detach().clone() if t.data_ptr() % 16 else t
 
 
 def _check_parents(parents, N, T, device):
@@ -167,39 +172,45 @@ def _check_gate(t, name, shape, device):
     return _aligned(t)
 
 
-def _verify(cfg, codes, scales, q, k, v, log_alpha, beta, parents):
-    """The checked call of QState.verify on the current stream: o, the draft."""
+def _verify(cfg, c_cfg, codes, scales, q, k, v, log_alpha, beta, parents):
+    """The checked call of QState.verify on the current stream, c_cfg and the state its own: o, the
+    draft."""
     _refuse_tracing("verify")
     dev = codes.device
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         _on_device(t, name, dev)
-    if v.dtype not in DTYPES or q.dtype != v.dtype or k.dtype != v.dtype:
-        raise ValueError(f"q, k, v: one of float32, bfloat16, float16, got {q.dtype}, {k.dtype}, "
-                         f"{v.dtype}")
-    if v.dim() != 4 or v.shape[0] != cfg.batch or tuple(v.shape[2:]) != (cfg.heads, cfg.dv):
-        raise ValueError(f"v: expected [{cfg.batch}, T, {cfg.heads}, {cfg.dv}], got "
-                         f"{tuple(v.shape)}")
-    N, T = v.shape[:2]
-    if q.dim() != 4 or q.shape != k.shape or q.shape[:2] != v.shape[:2] or q.shape[3] != cfg.dk:
-        raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} do not go with v "
-                         f"{tuple(v.shape)} and dk = {cfg.dk}")
-    c = DraftConfig(T, q.shape[2], v.dtype)
-    (q, c.q_stride), (k, c.k_stride), (v, c.v_stride) = (_token_rows(t) for t in (q, k, v))
-    log_alpha = _check_gate(log_alpha, "log_alpha", _gate(cfg, c), dev)
+    dt = v.dtype
+    if dt not in DTYPES or q.dtype != dt or k.dtype != dt:
+        raise ValueError(f"q, k, v: one of float32, bfloat16, float16, got {q.dtype}, {k.dtype}, {dt}")
+    shape = v.shape
+    if v.dim() != 4 or shape[0] != cfg.batch or shape[2] != cfg.heads or shape[3] != cfg.dv:
+        raise ValueError(f"v: expected [{cfg.batch}, T, {cfg.heads}, {cfg.dv}], got {tuple(shape)}")
+    N, T = shape[:2]
+    qk = q.shape
+    if q.dim() != 4 or qk != k.shape or qk[:2] != shape[:2] or qk[3] != cfg.dk:
+        raise ValueError(f"q {tuple(qk)} and k {tuple(k.shape)} do not go with v {tuple(shape)} and "
+                         f"dk = {cfg.dk}")
+    (q, qs), (k, ks), (v, vs) = _token_rows(q), _token_rows(k), _token_rows(v)
+    gate = (N, T, cfg.heads) + ((cfg.dk,) if cfg.mixer in (GLA, KDA) else ())
+    log_alpha = _check_gate(log_alpha, "log_alpha", gate, dev)
     if cfg.mixer == GLA:
         if beta is not None:
             raise ValueError("GLA takes no beta")
     else:
         beta = _check_gate(beta, "beta", (N, T, cfg.heads), dev)
     parents = _check_parents(parents, N, T, dev)
-    o = torch.empty(v.shape, dtype=v.dtype, device=dev)
-    writes = torch.empty(v.shape, dtype=torch.float32, device=dev)
-    qstate_verify(cfg, c, codes, scales, q, k, v, log_alpha, beta, parents, o, writes)
+    o = torch.empty(shape, dtype=dt, device=dev)
+    writes = torch.empty(shape, dtype=torch.float32, device=dev)
+    c = DraftConfigC(T, qk[2], DTYPES[dt], 0, qs, ks, vs)
+    check("qstate_verify", _call(dev, lib().qstate_verify, c_cfg, c, codes.data_ptr(), _ptr(scales),
+                                 q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(),
+                                 _ptr(beta), _ptr(parents), o.data_ptr(), writes.data_ptr(),
+                                 _stream(None, dev)))
     return o, Draft(k, log_alpha, parents, writes)
 
 
-def _accept(cfg, codes, scales, step, draft, last):
-    """The checked call of QState.accept on the current stream."""
+def _accept(cfg, c_cfg, codes, scales, step, draft, last):
+    """The checked call of QState.accept on the current stream, c_cfg and the state its own."""
     _refuse_tracing("accept")
     dev = codes.device
     k, writes = draft.k, draft.writes
@@ -208,12 +219,16 @@ def _accept(cfg, codes, scales, step, draft, last):
     if k.dtype not in DTYPES or k.dim() != 4 or k.shape[0] != cfg.batch or k.shape[3] != cfg.dk:
         raise ValueError(f"k: expected [{cfg.batch}, T, heads_qk, {cfg.dk}], got {k.dtype} "
                          f"{tuple(k.shape)}")
-    c = DraftConfig(k.shape[1], k.shape[2], k.dtype)
-    k, c.k_stride = _token_rows(k)
-    log_alpha = _check_gate(draft.log_alpha, "log_alpha", _gate(cfg, c), dev)
-    parents = _check_parents(draft.parents, cfg.batch, c.tokens, dev)
-    writes = _check_gate(writes, "writes", (cfg.batch, c.tokens, cfg.heads, cfg.dv), dev)
-    if tuple(last.shape) != (cfg.batch,) or last.dtype != torch.int32:
-        raise ValueError(f"last: expected int32 {(cfg.batch,)}, got {last.dtype} "
-                         f"{tuple(last.shape)}")
-    qstate_accept(cfg, c, step, codes, scales, k, log_alpha, parents, writes, last.contiguous())
+    N, T, heads_qk = k.shape[:3]
+    k, ks = _token_rows(k)
+    gate = (N, T, cfg.heads) + ((cfg.dk,) if cfg.mixer in (GLA, KDA) else ())
+    log_alpha = _check_gate(draft.log_alpha, "log_alpha", gate, dev)
+    parents = _check_parents(draft.parents, N, T, dev)
+    writes = _check_gate(writes, "writes", (N, T, cfg.heads, cfg.dv), dev)
+    if tuple(last.shape) != (N,) or last.dtype != torch.int32:
+        raise ValueError(f"last: expected int32 {(N,)}, got {last.dtype} {tuple(last.shape)}")
+    last = last.contiguous()
+    c = DraftConfigC(T, heads_qk, DTYPES[k.dtype], 0, 0, ks, 0)
+    check("qstate_accept", _call(dev, lib().qstate_accept, c_cfg, c, step, codes.data_ptr(),
+                                 _ptr(scales), k.data_ptr(), log_alpha.data_ptr(), _ptr(parents),
+                                 writes.data_ptr(), last.data_ptr(), _stream(None, dev)))

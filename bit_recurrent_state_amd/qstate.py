@@ -7,6 +7,7 @@ checked here so that a wrong tensor fails before it reaches the C ABI."""
 from __future__ import annotations
 
 import ctypes
+from contextlib import nullcontext
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -247,6 +248,7 @@ class QState:
 
     def __init__(self, cfg: Config, device="cuda"):
         self.cfg = cfg
+        self._c, self._keep = cfg.to_c()  # what the calls that take a configuration get
         cb, sb = qstate_state_bytes(cfg)
         if cfg.fp32_state:
             self.codes = torch.zeros(cb // 4, dtype=torch.float32, device=device)
@@ -312,8 +314,9 @@ class QState:
             _on_device(v, "v", dev)
             rows = v.shape[0] * v.shape[1] if v.dim() == 4 else 0
             cfg = norm.config((rows, self.cfg.heads, self.cfg.dv), v.dtype, dev, v.shape)
-        with torch.no_grad(), torch.cuda.device(dev), _on(stream, dev):
-            o, draft = _verify(self.cfg, self.codes, self.scales, q, k, v, log_alpha, beta, parents)
+        with nullcontext() if stream is None else _on(stream, dev):
+            o, draft = _verify(self.cfg, self._c, self.codes, self.scales, q, k, v, log_alpha, beta,
+                               parents)
             if norm is not None:
                 norm._run(cfg, o)
         return o, draft
@@ -323,9 +326,10 @@ class QState:
         stored state of sequence n, in one quantization event: the counter goes up by one.  A sequence
         with last[n] = -1 accepts none and keeps its state bit for bit."""
         dev = self.codes.device
-        with torch.no_grad(), torch.cuda.device(dev), _on(stream, dev):
-            _accept(self.cfg, self.codes, self.scales, self.step_counter, draft, last)
-        self.step_counter += 1
+        step = self.step_counter
+        with nullcontext() if stream is None else _on(stream, dev):
+            _accept(self.cfg, self._c, self.codes, self.scales, step, draft, last)
+        self.step_counter = step + 1
 
     def readout(self, q, o, stream=None):
         qstate_readout(self.handle, self.cfg, q, o, stream)
