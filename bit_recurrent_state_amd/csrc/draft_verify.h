@@ -364,14 +364,15 @@ struct alignas(16) Lds {
   using State = StateRows<DK, F32, NTW>;
   static constexpr int T = MT * 16;
   static constexpr int LP = Operands<DK, TERMS>::LP;
-  static constexpr int OT = VEC ? 16 : T;      // rows of operands at a time
+  // with a gate per channel a tile of nodes is worked out at a time
+  static constexpr int OT = VEC ? 16 : T, OM = VEC ? 1 : MT;
   static constexpr int MP = T + 4;
   uint16_t kop[TERMS][OT][LP], qop[TERMS][OT][LP];
   uint8_t codes[4][State::CODES];              // of each wave
   float scales[4][State::SCALES];
-  float A[T][MP], L[DELTA ? T : 1][MP];        // A diag b, -L diag b
-  float lt[DELTA ? MT : 1][16][20];            // -L diag b of the tiles on the diagonal, transposed
-  float inv[DELTA ? MT : 1][16][20];           // (I + L diag b)^-1 of the same tiles
+  float A[OT][MP], L[DELTA ? OT : 1][MP];      // A diag b, -L diag b
+  float lt[DELTA ? OM : 1][16][20];            // -L diag b of the tiles on the diagonal, transposed
+  float inv[DELTA ? OM : 1][16][20];           // (I + L diag b)^-1 of the same tiles
   float ec[T], beta[T];
   float alpha[VEC ? T : 1][DK];
   double c[T];
@@ -576,13 +577,6 @@ __global__ void __launch_bounds__(kThreads, TERMS == 1 && MT == 1 ? 4 : 1) verif
   if constexpr (VEC) {
     copies_done();
     if (wave == 0) paths();
-    // the walks below fill in what is an ancestor
-    for (int i = threadIdx.x; i < D::T * MP; i += kThreads) {
-      (&lds.A[0][0])[i] = 0.0f;
-      if (DELTA) (&lds.L[0][0])[i] = 0.0f;
-    }
-    if (DELTA)
-      for (int i = threadIdx.x; i < MT * 320; i += kThreads) (&lds.lt[0][0][0])[i] = 0.0f;
     __syncthreads();
     nodes = lds.nodes;
   } else {
@@ -613,60 +607,84 @@ __global__ void __launch_bounds__(kThreads, TERMS == 1 && MT == 1 ? 4 : 1) verif
   for (int mt = 0; mt < MT; ++mt) {
     if (mt * 16 >= rows) break;
     if constexpr (VEC) {
+      if (mt > 0) __syncthreads();  // the last tile's A and L are done with
       // each of 16 nodes goes up its path, 16 lanes a node: q and k take the decays on the way
       const int i = threadIdx.x >> 4, t = mt * 16 + i, sub = threadIdx.x & 15;
-      float q[DK / 64][4], k[DK / 64][4];
+      constexpr int R = DK / 64;
+      u32x4 wq[R], wk[R];
 #pragma unroll
-      for (int r = 0; r < DK / 64; ++r) {
-        qscan::widen4(load_q(t, 64 * r + 4 * sub), dtype, q[r]);
-        qscan::widen4(load_k(t, 64 * r + 4 * sub), dtype, k[r]);
+      for (int r = 0; r < R; ++r) {
+        wq[r] = load_q(t, 64 * r + 4 * sub);
+        wk[r] = load_k(t, 64 * r + 4 * sub);
       }
-      if (lds.mask[t] != 0) {
-        int at = t;
-        float x[DK / 64][4];
+      // what is no ancestor is zero
+      for (int j = sub; j < MP; j += 16) {
+        lds.A[i][j] = 0.0f;
+        if (DELTA) lds.L[i][j] = 0.0f;
+      }
+      if (DELTA) lds.lt[0][sub][i] = 0.0f;
+      const bool on = lds.mask[t] != 0;
+      // nodes and keys of the next steps, fetched three ahead
+      int ahead[3];
+      u32x4 kw[3][R];
+      ahead[0] = on ? lds.parent[t] : -1;
 #pragma unroll
-        for (int r = 0; r < DK / 64; ++r)
+      for (int d = 1; d < 3; ++d) ahead[d] = ahead[d - 1] < 0 ? -1 : lds.parent[ahead[d - 1]];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[r][j] = k[r][j];
-        for (;;) {
-          const int next = lds.parent[at];
-          u32x4 w[DK / 64];  // the parent's key, on its way meanwhile
+      for (int d = 0; d < 3; ++d)
 #pragma unroll
-          for (int r = 0; r < DK / 64; ++r) w[r] = load_k(max(next, 0), 64 * r + 4 * sub);
+        for (int r = 0; r < R; ++r) kw[d][r] = load_k(max(ahead[d], 0), 64 * r + 4 * sub);
+      float q[R][4], k[R][4], x[R][4];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        qscan::widen4(wq[r], dtype, q[r]);
+        qscan::widen4(wk[r], dtype, k[r]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[r][j] = k[r][j];
+      }
+      int at = on ? t : -1;
+      while (at >= 0) {
+#pragma unroll
+        for (int d = 0; d < 3; ++d) {  // in turns, so that what was fetched is not moved
+          if (at < 0) break;
           float a = 0.0f, l = 0.0f;
 #pragma unroll
-          for (int r = 0; r < DK / 64; ++r) {
-            const f32x4 d = *reinterpret_cast<const f32x4*>(&lds.alpha[at][64 * r + 4 * sub]);
+          for (int r = 0; r < R; ++r) {
+            const f32x4 f = *reinterpret_cast<const f32x4*>(&lds.alpha[at][64 * r + 4 * sub]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               a = fmaf(q[r][j], x[r][j], a);
               if (DELTA) l = fmaf(k[r][j], x[r][j], l);
-              q[r][j] *= d[j];
-              if (DELTA) k[r][j] *= d[j];
+              q[r][j] *= f[j];
+              if (DELTA) k[r][j] *= f[j];
             }
           }
           a = qscan::sum16(a);
           if (DELTA) l = qscan::sum16(l);
           if (sub == 0) {
-            lds.A[t][at] = a * lds.beta[at];
+            const float b = lds.beta[at];
+            lds.A[i][at] = a * b;
             if (DELTA && at != t) {
-              lds.L[t][at] = -l * lds.beta[at];
-              if (at >= mt * 16) lds.lt[mt][at - mt * 16][i] = -l * lds.beta[at];
+              lds.L[i][at] = -l * b;
+              if (at >= mt * 16) lds.lt[0][at - mt * 16][i] = -l * b;
             }
           }
-          if (next < 0) break;
-          at = next;
+          at = ahead[d];
+          ahead[d] = ahead[(d + 2) % 3] < 0 ? -1 : lds.parent[ahead[(d + 2) % 3]];
 #pragma unroll
-          for (int r = 0; r < DK / 64; ++r) qscan::widen4(w[r], dtype, x[r]);
+          for (int r = 0; r < R; ++r) {
+            qscan::widen4(kw[d][r], dtype, x[r]);
+            kw[d][r] = load_k(max(ahead[d], 0), 64 * r + 4 * sub);
+          }
         }
       }
 #pragma unroll
-      for (int r = 0; r < DK / 64; ++r) {
+      for (int r = 0; r < R; ++r) {
         qscan::put4<TERMS>(&lds.qop[0][i][64 * r + 4 * sub], plane, q[r]);
         if (DELTA) qscan::put4<TERMS>(&lds.kop[0][i][64 * r + 4 * sub], plane, k[r]);
       }
       __syncthreads();
-      if (DELTA && wave == 0 && g == 0) invert(lds.lt, lds.inv, mt);
+      if (DELTA && wave == 0 && g == 0) invert(lds.lt, lds.inv, 0);
     }
     if (mt > 0) load_v(mt);
     if (VEC || mt > 0) products(mt);
@@ -691,14 +709,14 @@ __global__ void __launch_bounds__(kThreads, TERMS == 1 && MT == 1 ? 4 : 1) verif
       if constexpr (DELTA) {
 #pragma unroll
         for (int jt = 0; jt < mt; ++jt)
-          small_mma(x, &lds.L[mt * 16][jt * 16], MP, u[jt][ct]);
+          small_mma(x, &lds.L[VEC ? 0 : mt * 16][jt * 16], MP, u[jt][ct]);
         u[mt][ct] = f32x4{0, 0, 0, 0};
-        small_mma(u[mt][ct], &lds.inv[mt][0][0], 20, x);
+        small_mma(u[mt][ct], &lds.inv[VEC ? 0 : mt][0][0], 20, x);
       } else {
         u[mt][ct] = x;
       }
 #pragma unroll
-      for (int jt = 0; jt <= mt; ++jt) small_mma(xq[ct], &lds.A[mt * 16][jt * 16], MP, u[jt][ct]);
+      for (int jt = 0; jt <= mt; ++jt) small_mma(xq[ct], &lds.A[VEC ? 0 : mt * 16][jt * 16], MP, u[jt][ct]);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         out[r][ct] = node[r] ? xq[ct][r] : 0.0f;
