@@ -148,9 +148,11 @@ int qstate_accept(const qstate_config* state, const qstate_draft_config* draft, 
   p.parents = parents;
   p.writes_in = writes;
   p.last = last;
-  // slices of at most 128 rows, so that their writes lie in LDS
-  p.waves = 4;
+  // 128 value rows a workgroup (the most its LDS has writes for), fewer while there are not enough
+  // workgroups for the chip: 1024, four a CU
   p.rows = 128;
+  while (p.rows > 32 && (int64_t)state->batch * state->heads * ((state->dv + p.rows - 1) / p.rows) < 1024)
+    p.rows /= 2;
   p.blocks = (state->dv + p.rows - 1) / p.rows;
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   switch (state->dk) {

@@ -34,7 +34,6 @@ struct Params {
   int vpairs;     // and of v
   int columns;    // verify: value columns of a workgroup, 64 or 128
   int blocks;     // workgroups of a head
-  int waves;      // accept: waves of a workgroup
   int rows;       // accept: value rows of a workgroup
   qs::KParams s;  // the state: codes, scales, sizes, widths, random bits
 };
