@@ -21,9 +21,67 @@ __device__ __forceinline__ GroupPlace group_place(const GroupParams& p, int64_t 
   return {tok * p.xs + in, tok * p.gs + in};
 }
 
+// Sums over the team, by DPP inside 16 lanes: shuffles through LDS cost as much as a quarter of the
+// row's own arithmetic.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+
+template <bool WIDE>
+__device__ __forceinline__ void row_sums(float& a, float& b, int team, float (*lds)[2]) {
+  if (WIDE) {
+    team_sum<true>(a, b, team, lds);
+    return;
+  }
+  auto both = [&](auto step) {
+    a += step(a);
+    b += step(b);
+  };
+  if (team > 1) both([](float x) { return dpp<0xB1>(x); });    // quad_perm 1, 0, 3, 2
+  if (team > 2) both([](float x) { return dpp<0x4E>(x); });    // quad_perm 2, 3, 0, 1
+  if (team > 4) both([](float x) { return dpp<0x141>(x); });   // row_half_mirror
+  if (team > 8) both([](float x) { return dpp<0x140>(x); });   // row_mirror
+  if (team > 16) both([](float x) { return __shfl_xor(x, 16); });
+  if (team > 32) both([](float x) { return __shfl_xor(x, 32); });
+}
+
+// 1 / sqrt(v): the instruction's, one Newton step on; the library's where squares would leave the range.
+__device__ __forceinline__ float inverse_root(float v) {
+  float r = __builtin_amdgcn_rsqf(v);
+  const float e = fmaf(-v * r, r, 1.0f);
+  r = fmaf(0.5f * r, e, r);
+  if (!(v >= 0x1p-100f && v <= 0x1p100f)) r = 1.0f / sqrtf(v);
+  return r;
+}
+
+// act(z), for the gradient its slope.  What ends in 16 bits takes exp(-z) as 2^(-z log2 e) without the
+// product's rest (an error of |z| 2^-24 of it, half a step of those types being 2^-12 at least) and the
+// reciprocal as it is: 13 instead of 20 instructions' time a value, which is what bounds the kernels.
+template <int DT, bool SLOPE>
+__device__ __forceinline__ float act_of(float z, int act, float& slope) {
+  if (DT == 0) return activate(z, act, slope);
+  const float c = z < -87.0f ? -87.0f : z;  // NaN stays
+  const float e = __builtin_amdgcn_exp2f(c * -1.44269502f);
+  const float s = __builtin_amdgcn_rcpf(1.0f + e);
+  if (SLOPE) {
+    const float q = s * e;  // 1 - s without cancellation; with a gate of infinity, nothing of it
+    slope = act == 0 ? s * fmaf(c > 87.0f ? 87.0f : c, q, 1.0f) : s * q;
+  }
+  return act == 0 ? (z < c ? c : z) * s : s;
+}
+
+// A row's values by type, zeros behind its width.  FULL: every thread's are inside.
+template <int DT, int V, bool VEC, bool FULL>
+__device__ __forceinline__ void values(const Raw<DT, V>& r, int t, int team, int width,
+                                       float (&x)[V * 8]) {
+  // (a width that nothing lies behind: the comparisons fall away)
+  widen<DT, V, VEC>(r, FULL ? 0 : t, FULL ? 1 : team, FULL ? 1 << 30 : width, x);
+}
+
 // x becomes the normalised row (columns behind the width stay zero); returns
 // what it was multiplied by.
-template <int V, bool WIDE, bool VEC>
+template <int V, bool WIDE, bool VEC, bool FULL>
 __device__ __forceinline__ float normalise(const GroupParams& p, int t, int team,
                                            float (*lds)[2], float (&x)[V * 8]) {
   const float inv = 1.0f / (float)p.width;
@@ -31,17 +89,17 @@ __device__ __forceinline__ float normalise(const GroupParams& p, int t, int team
   if (p.center) {
 #pragma unroll
     for (int i = 0; i < V * 8; ++i) s += x[i];
-    team_sum<WIDE>(s, unused, team, lds);
+    row_sums<WIDE>(s, unused, team, lds);
     const float mean = s * inv;
 #pragma unroll
     for (int i = 0; i < V * 8; ++i)
-      x[i] = column<VEC>(i / 8, i % 8, t, team) < p.width ? x[i] - mean : 0.0f;
+      x[i] = FULL || column<VEC>(i / 8, i % 8, t, team) < p.width ? x[i] - mean : 0.0f;
     s = unused = 0.0f;
   }
 #pragma unroll
   for (int i = 0; i < V * 8; ++i) s = fmaf(x[i], x[i], s);
-  team_sum<WIDE>(s, unused, team, lds);
-  const float r = 1.0f / sqrtf(s * inv + p.eps);
+  row_sums<WIDE>(s, unused, team, lds);
+  const float r = inverse_root(s * inv + p.eps);
 #pragma unroll
   for (int i = 0; i < V * 8; ++i) x[i] *= r;
   return r;
@@ -59,7 +117,7 @@ __device__ __forceinline__ void load_affine(const GroupParams& p, int64_t first,
   }
 }
 
-template <int DT, int V, bool WIDE, bool VEC, int BLOCK>
+template <int DT, int V, bool WIDE, bool VEC, bool FULL, int BLOCK>
 __global__ void __launch_bounds__(BLOCK) group_forward_kernel(GroupParams p) {
   constexpr int N = V * 8;
   __shared__ float lds[BLOCK / 64][2];
@@ -80,29 +138,32 @@ __global__ void __launch_bounds__(BLOCK) group_forward_kernel(GroupParams p) {
   load(row);
   for (; row < p.rows; row += p.teams) {
     float x[N], a[N], slope;
-    widen<DT, V, VEC>(rx, t, team, width, x);
+    values<DT, V, VEC, FULL>(rx, t, team, width, x);
     if (p.gate) {
-      widen<DT, V, VEC>(rz, t, team, width, a);
+      values<DT, V, VEC, FULL>(rz, t, team, width, a);
 #pragma unroll
-      for (int i = 0; i < N; ++i) a[i] = activate(a[i], p.act, slope);
+      for (int i = 0; i < N; ++i) a[i] = act_of<DT, false>(a[i], p.act, slope);
     }
     if (row + p.teams < p.rows) load(row + p.teams);
     if (p.mode == GATE_FIRST) {
 #pragma unroll
       for (int i = 0; i < N; ++i) x[i] *= a[i];
     }
-    normalise<V, WIDE, VEC>(p, t, team, lds, x);
+    normalise<V, WIDE, VEC, FULL>(p, t, team, lds, x);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      x[i] = fmaf(x[i], w[i], b[i]);
-      if (p.mode == GATE) x[i] *= a[i];
-      if (p.mode == ACTIVATE) x[i] = activate(x[i], p.act, slope);
+    for (int i = 0; i < N; ++i) x[i] = fmaf(x[i], w[i], b[i]);
+    if (p.mode == GATE) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] *= a[i];
+    } else if (p.mode == ACTIVATE) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = act_of<DT, false>(x[i], p.act, slope);
     }
     store_row<DT, V, VEC>(p.y, row * width, t, team, width, x);
   }
 }
 
-template <int DT, int V, bool WIDE, bool VEC, int BLOCK>
+template <int DT, int V, bool WIDE, bool VEC, bool FULL, int BLOCK>
 __global__ void __launch_bounds__(BLOCK) group_backward_kernel(GroupParams p) {
   constexpr int N = V * 8;
   __shared__ float lds[BLOCK / 64][2];
@@ -126,17 +187,21 @@ __global__ void __launch_bounds__(BLOCK) group_backward_kernel(GroupParams p) {
   for (; row < p.rows; row += p.teams) {
     const int64_t out = row * width;
     float x[N], u[N], a[N], slope[N], d[N];
-    widen<DT, V, VEC>(rx, t, team, width, x);
+    values<DT, V, VEC, FULL>(rx, t, team, width, x);
     if (p.gate) {
-      widen<DT, V, VEC>(rz, t, team, width, a);
+      values<DT, V, VEC, FULL>(rz, t, team, width, a);
 #pragma unroll
-      for (int i = 0; i < N; ++i) a[i] = activate(a[i], p.act, slope[i]);
+      for (int i = 0; i < N; ++i) a[i] = act_of<DT, true>(a[i], p.act, slope[i]);
     }
-    widen<DT, V, VEC>(rd, t, team, width, d);
+    values<DT, V, VEC, FULL>(rd, t, team, width, d);
     if (row + p.teams < p.rows) load(row + p.teams);
 #pragma unroll
-    for (int i = 0; i < N; ++i) u[i] = p.mode == GATE_FIRST ? x[i] * a[i] : x[i];
-    const float r = normalise<V, WIDE, VEC>(p, t, team, lds, u);
+    for (int i = 0; i < N; ++i) u[i] = x[i];
+    if (p.mode == GATE_FIRST) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) u[i] *= a[i];
+    }
+    const float r = normalise<V, WIDE, VEC, FULL>(p, t, team, lds, u);
     if (p.mode == GATE) {
       float z[N];
 #pragma unroll
@@ -149,7 +214,7 @@ __global__ void __launch_bounds__(BLOCK) group_backward_kernel(GroupParams p) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         float sl;
-        activate(fmaf(u[i], w[i], b[i]), p.act, sl);
+        act_of<DT, true>(fmaf(u[i], w[i], b[i]), p.act, sl);
         d[i] *= sl;
       }
     }
@@ -163,13 +228,14 @@ __global__ void __launch_bounds__(BLOCK) group_backward_kernel(GroupParams p) {
       mh = fmaf(d[i], u[i], mh);
     }
     if (!p.dx && !(p.dgate && p.mode == GATE_FIRST)) continue;
-    team_sum<WIDE>(m, mh, team, lds);
+    row_sums<WIDE>(m, mh, team, lds);
     m = p.center ? m * inv : 0.0f;
     mh *= inv;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      d[i] = r * (d[i] - m - u[i] * mh);
-      if (p.mode == GATE_FIRST) {
+    for (int i = 0; i < N; ++i) d[i] = r * (d[i] - fmaf(u[i], mh, m));
+    if (p.mode == GATE_FIRST) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
         u[i] = d[i] * x[i] * slope[i];
         d[i] *= a[i];
       }
@@ -223,22 +289,22 @@ __global__ void __launch_bounds__(256) group_parts_kernel(GroupParams p) {
   }
 }
 
-template <int DT, int V, bool WIDE, int BLOCK>
-static hipError_t run(const GroupParams& p, bool back, hipStream_t s) {
+template <int DT, int V, bool WIDE, bool VEC, bool FULL, int BLOCK>
+static hipError_t launch(const GroupParams& p, bool back, hipStream_t s) {
   const int64_t per = BLOCK / p.team;
   const dim3 grid((unsigned)((p.teams + per - 1) / per));
-  if (back) {
-    if (p.aligned)
-      group_backward_kernel<DT, V, WIDE, true, BLOCK><<<grid, BLOCK, 0, s>>>(p);
-    else
-      group_backward_kernel<DT, V, WIDE, false, BLOCK><<<grid, BLOCK, 0, s>>>(p);
-  } else {
-    if (p.aligned)
-      group_forward_kernel<DT, V, WIDE, true, BLOCK><<<grid, BLOCK, 0, s>>>(p);
-    else
-      group_forward_kernel<DT, V, WIDE, false, BLOCK><<<grid, BLOCK, 0, s>>>(p);
-  }
+  if (back)
+    group_backward_kernel<DT, V, WIDE, VEC, FULL, BLOCK><<<grid, BLOCK, 0, s>>>(p);
+  else
+    group_forward_kernel<DT, V, WIDE, VEC, FULL, BLOCK><<<grid, BLOCK, 0, s>>>(p);
   return hipGetLastError();
+}
+
+template <int DT, int V, bool WIDE, int BLOCK>
+static hipError_t run(const GroupParams& p, bool back, hipStream_t s) {
+  if (!p.aligned) return launch<DT, V, WIDE, false, false, BLOCK>(p, back, s);
+  return p.width == V * 8 * p.team ? launch<DT, V, WIDE, true, true, BLOCK>(p, back, s)
+                                   : launch<DT, V, WIDE, true, false, BLOCK>(p, back, s);
 }
 
 template <int DT>
