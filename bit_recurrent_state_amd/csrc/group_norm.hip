@@ -12,14 +12,23 @@
 
 namespace qnorm {
 
+// Where a team's row lies in x and the gate.  The teams' number is a multiple of the groups: a team
+// stays in its group and goes `step` tokens on at a time.
 struct GroupPlace {
-  int64_t x, gate;
+  int64_t x, gate, xstep, gstep;
+  __device__ __forceinline__ GroupPlace(const GroupParams& p, int64_t first) {
+    const int64_t tok = first / p.groups, in = (first - tok * p.groups) * p.width;
+    const int64_t step = p.teams / p.groups;
+    x = tok * p.xs + in;
+    gate = tok * p.gs + in;
+    xstep = step * p.xs;
+    gstep = step * p.gs;
+  }
+  __device__ __forceinline__ void next() {
+    x += xstep;
+    gate += gstep;
+  }
 };
-
-__device__ __forceinline__ GroupPlace group_place(const GroupParams& p, int64_t row) {
-  const int64_t tok = row / p.groups, in = (row - tok * p.groups) * p.width;
-  return {tok * p.xs + in, tok * p.gs + in};
-}
 
 // Sums over the team, by DPP inside 16 lanes: shuffles through LDS cost as much as a quarter of the
 // row's own arithmetic.
@@ -130,12 +139,13 @@ __global__ void __launch_bounds__(BLOCK) group_forward_kernel(GroupParams p) {
   int64_t row = first < p.teams ? first : p.rows;
   if (row >= p.rows) return;
   Raw<DT, V> rx, rz;
-  auto load = [&](int64_t r) {
-    const GroupPlace at = group_place(p, r);
+  GroupPlace at(p, row);
+  auto load = [&]() {
     load_raw<DT, V, VEC>(p.x, at.x, t, team, width, rx);
     if (p.gate) load_raw<DT, V, VEC>(p.gate, at.gate, t, team, width, rz);
+    at.next();
   };
-  load(row);
+  load();
   for (; row < p.rows; row += p.teams) {
     float x[N], a[N], slope;
     values<DT, V, VEC, FULL>(rx, t, team, width, x);
@@ -144,7 +154,7 @@ __global__ void __launch_bounds__(BLOCK) group_forward_kernel(GroupParams p) {
 #pragma unroll
       for (int i = 0; i < N; ++i) a[i] = act_of<DT, false>(a[i], p.act, slope);
     }
-    if (row + p.teams < p.rows) load(row + p.teams);
+    if (row + p.teams < p.rows) load();
     if (p.mode == GATE_FIRST) {
 #pragma unroll
       for (int i = 0; i < N; ++i) x[i] *= a[i];
@@ -176,13 +186,14 @@ __global__ void __launch_bounds__(BLOCK) group_backward_kernel(GroupParams p) {
 #pragma unroll
   for (int i = 0; i < N; ++i) dw[i] = db[i] = 0.0f;
   Raw<DT, V> rx, rz, rd;
+  int64_t row = first < p.teams ? first : p.rows;
+  GroupPlace at(p, row);
   auto load = [&](int64_t r) {
-    const GroupPlace at = group_place(p, r);
     load_raw<DT, V, VEC>(p.x, at.x, t, team, width, rx);
     if (p.gate) load_raw<DT, V, VEC>(p.gate, at.gate, t, team, width, rz);
     load_raw<DT, V, VEC>(p.dy, r * width, t, team, width, rd);
+    at.next();
   };
-  int64_t row = first < p.teams ? first : p.rows;
   if (row < p.rows) load(row);
   for (; row < p.rows; row += p.teams) {
     const int64_t out = row * width;

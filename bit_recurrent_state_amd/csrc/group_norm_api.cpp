@@ -45,8 +45,7 @@ bool gated(const qstate_group_norm_config* c) {
 // Teams: rows of up to 512 values take 1 .. 64 lanes of a wave, 8 values a lane;
 // wider ones a workgroup, 8 values a thread (16 above 8192).  As many teams as
 // fill the card (256 CUs, 16 waves each forward, 8 backward), or one per row if
-// there are fewer rows.  With a weight for each group their number is a multiple of
-// the groups, so that a team meets one group only.
+// there are fewer rows; a multiple of the groups, so that a team meets one group.
 void plan(const qstate_group_norm_config* c, bool backward, GroupParams& p) {
   std::memset(&p, 0, sizeof(p));
   p.rows = c->tokens * c->groups;
@@ -73,7 +72,7 @@ void plan(const qstate_group_norm_config* c, bool backward, GroupParams& p) {
   }
   int64_t teams = (int64_t)256 * (backward ? 512 : 1024) / p.team;
   if (teams > p.rows) teams = p.rows;
-  p.teams = p.shared ? teams : (teams + p.groups - 1) / p.groups * p.groups;
+  p.teams = (teams + p.groups - 1) / p.groups * p.groups;
   // parts of the weights' gradients: a team's, or a wave's where its teams share the weight
   const int64_t per = p.block / p.team;
   p.partials = !p.shared || p.wide ? p.teams : (p.teams + per - 1) / per * (p.block / 64);

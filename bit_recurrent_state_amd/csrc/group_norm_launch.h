@@ -25,7 +25,7 @@ struct GroupParams {
   int vectors;    // blocks of 8 values per thread
   int wide;       // rows take whole workgroups
   int aligned;    // 16-byte accesses reach every row
-  int64_t teams;  // a multiple of groups where weights differ by group
+  int64_t teams;  // a multiple of groups
   float* part;    // [2][partials][width]: dweight, dbias
   int64_t partials;
 };
