@@ -69,81 +69,79 @@ __device__ __forceinline__ void product(f32x4& acc, const RawX<DT>& x, const u32
   }
 }
 
-// MT tiles of 16 rows, NT of 16 outputs, W waves.
-template <int DT, int G, int MT, int NT, int W>
-__global__ void __launch_bounds__(W * 64) linear_kernel(Params p) {
+constexpr int kWaves = 8, kAhead = 2;  // of a workgroup; of a wave's tiles of inputs in flight
+
+// 16 rows of x, NT tiles of 16 outputs.
+template <int DT, int G, int NT>
+__global__ void __launch_bounds__(kWaves * 64) linear_kernel(Params p) {
   constexpr int S = kIn / G;  // groups of a tile
-  __shared__ float sums[W][MT * NT][256];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-  const int64_t row0 = (int64_t)blockIdx.y * (MT * 16);
+  __shared__ float sums[kWaves][NT][256];
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row0 = (int64_t)blockIdx.y * 16;
   const int ot0 = blockIdx.x * NT;
-  const char* x[MT];
+  // rows behind the last repeat it: a row of y depends on its own only
+  const char* x = static_cast<const char*>(p.x) +
+                  ((row0 + c < p.rows ? row0 + c : p.rows - 1) * p.xs + g * 8) * (DT == 0 ? 4 : 2);
+  f32x4 acc[NT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {  // rows behind the last repeat it: a row of y depends on its own only
-    const int64_t row = row0 + m * 16 + c;
-    x[m] = static_cast<const char*>(p.x) + (row < p.rows ? row : p.rows - 1) * p.xs * (DT == 0 ? 4 : 2);
-  }
-  f32x4 acc[MT][NT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[m][n] = f32x4{0, 0, 0, 0};
-  for (int kt = wave; kt < p.in_tiles; kt += W) {
-    u32x4 w[NT];
-    float s[NT][S];
+  for (int n = 0; n < NT; ++n) acc[n] = f32x4{0, 0, 0, 0};
+  u32x4 w[kAhead][NT];
+  float s[kAhead][NT][S];
+  RawX<DT> xr[kAhead][4];
+  auto load = [&](int d, int kt) {
+    if (kt >= p.in_tiles) return;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int64_t tile = (int64_t)min(ot0 + n, p.out_tiles - 1) * p.in_tiles + kt;
-      w[n] = reinterpret_cast<const u32x4*>(p.packed)[tile * 64 + lane];
+      w[d][n] = reinterpret_cast<const u32x4*>(p.packed)[tile * 64 + lane];
 #pragma unroll
-      for (int j = 0; j < S; ++j) s[n][j] = p.scales[(tile * 16 + c) * S + j];
+      for (int j = 0; j < S; ++j) s[d][n][j] = p.scales[(tile * 16 + c) * S + j];
     }
-    RawX<DT> xr[MT][4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int i = 0; i < 4; ++i) {
+      const int col = kt * kIn + i * 32;  // inputs behind the last count as zeros
+      const u32x4* at = reinterpret_cast<const u32x4*>(x + (col < p.inputs ? col : 0) * (DT == 0 ? 4 : 2));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int col = kt * kIn + i * 32;  // inputs behind the last count as zeros
-        const u32x4* at = reinterpret_cast<const u32x4*>(
-            x[m] + (int64_t)(col < p.inputs ? col + g * 8 : 0) * (DT == 0 ? 4 : 2));
+      for (int h = 0; h < (DT == 0 ? 2 : 1); ++h)
+        xr[d][i].w[h] = col < p.inputs ? at[h] : u32x4{0, 0, 0, 0};
+    }
+  };
 #pragma unroll
-        for (int h = 0; h < (DT == 0 ? 2 : 1); ++h)
-          xr[m][i].w[h] = col < p.inputs ? at[h] : u32x4{0, 0, 0, 0};
-      }
+  for (int d = 0; d < kAhead; ++d) load(d, wave + d * kWaves);
+  for (int kt = wave; kt < p.in_tiles; kt += kAhead * kWaves) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      f32x4 part[MT];
+    for (int d = 0; d < kAhead; ++d) {
+      if (kt + d * kWaves >= p.in_tiles) break;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const u32x4 b = widen<DT == 2>(w[n][i]);
+      for (int n = 0; n < NT; ++n) {
+        f32x4 part;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          if (i * 32 % G == 0) part[m] = f32x4{0, 0, 0, 0};
-          product<DT>(part[m], xr[m][i], b);
+        for (int i = 0; i < 4; ++i) {
+          if (i * 32 % G == 0) part = f32x4{0, 0, 0, 0};
+          product<DT>(part, xr[d][i], widen<DT == 2>(w[d][n][i]));
           if ((i + 1) * 32 % G == 0) {
-            const float f = s[n][i * 32 / G];
+            const float f = s[d][n][i * 32 / G];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[m][n][r] = fmaf(f, part[m][r], acc[m][n][r]);
+            for (int r = 0; r < 4; ++r) acc[n][r] = fmaf(f, part[r], acc[n][r]);
           }
         }
       }
+      load(d, kt + (d + kAhead) * kWaves);
     }
   }
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      *reinterpret_cast<f32x4*>(&sums[wave][m * NT + n][lane * 4]) = acc[m][n];
+  for (int n = 0; n < NT; ++n) *reinterpret_cast<f32x4*>(&sums[wave][n][lane * 4]) = acc[n];
   __syncthreads();
-  for (int e = threadIdx.x; e < MT * NT * 256; e += W * 64) {
+  for (int e = threadIdx.x; e < NT * 256; e += kWaves * 64) {
     // element e: row (e / 16) % 16 of its tile, output e % 16, in the lane that holds them
     const int tile = e >> 8, r = (e >> 4) & 15, o = e & 15;
     const int at = ((r >> 2) * 16 + o) * 4 + (r & 3);
     float y = 0.0f;
 #pragma unroll
-    for (int i = 0; i < W; ++i) y += sums[i][tile][at];
-    const int64_t row = row0 + tile / NT * 16 + r;
-    const int out = (ot0 + tile % NT) * 16 + o;
+    for (int i = 0; i < kWaves; ++i) y += sums[i][tile][at];
+    const int64_t row = row0 + r;
+    const int out = (ot0 + tile) * 16 + o;
     if (row >= p.rows || out >= p.outputs) continue;
     if (p.bias) y += p.bias[out];
     qscan::store_elem(p.y, row * p.outputs + out, DT, y);
@@ -219,26 +217,48 @@ __global__ void __launch_bounds__(64) quantize_kernel(Params p) {
   }
 }
 
-template <int DT, int G, int MT, int NT, int W>
+template <int DT, int G, int NT>
 static hipError_t run(const Params& p, hipStream_t s) {
-  const dim3 grid((unsigned)((p.out_tiles + NT - 1) / NT), (unsigned)((p.rows + MT * 16 - 1) / (MT * 16)));
-  linear_kernel<DT, G, MT, NT, W><<<grid, W * 64, 0, s>>>(p);
+  const dim3 grid((unsigned)((p.out_tiles + NT - 1) / NT), (unsigned)((p.rows + 15) / 16));
+  linear_kernel<DT, G, NT><<<grid, kWaves * 64, 0, s>>>(p);
   return hipGetLastError();
 }
 
+// How many tiles of outputs a workgroup takes.  Each of them reads the 16 rows of x once, which costs
+// its CU what four tiles of weights do; workgroups are shared out to 256 CUs.  Bfloat16, 16 rows of
+// 4096, us with 1 / 2 / 3 / 4 tiles: 4096 outputs 6.3 / 7.5 / 8.3 / 9.2, 6144 10.2 / 7.3 / 8.4 / 9.3,
+// 12288 14.2 / 10.9 / 8.2 / 8.9, 32768 36 / 23 / 22 / 21; 64 rows, 12288 outputs 48 / 27 / 22 / 19 (with
+// more rows a workgroup instead, 32 and 64: 21 at best).
+static int tiles_of(const Params& p) {
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int n = 1; n <= 4; ++n) {
+    const int64_t groups = (int64_t)((p.out_tiles + n - 1) / n) * ((p.rows + 15) / 16);
+    const int64_t cost = (groups + 255) / 256 * (4 + n);
+    if (cost < least) {
+      least = cost;
+      best = n;
+    }
+  }
+  return best;
+}
+
 template <int DT, int G>
-static hipError_t by_rows(const Params& p, hipStream_t s) {
-  if (p.rows <= 16) return run<DT, G, 1, 1, 8>(p, s);
-  if (p.rows <= 32) return run<DT, G, 2, 1, 8>(p, s);
-  return run<DT, G, 4, 1, 8>(p, s);
+static hipError_t by_tiles(const Params& p, hipStream_t s) {
+  switch (tiles_of(p)) {
+    case 1: return run<DT, G, 1>(p, s);
+    case 2: return run<DT, G, 2>(p, s);
+    case 3: return run<DT, G, 3>(p, s);
+    default: return run<DT, G, 4>(p, s);
+  }
 }
 
 template <int DT>
 static hipError_t by_group(const Params& p, hipStream_t s) {
   switch (p.group) {
-    case 32: return by_rows<DT, 32>(p, s);
-    case 64: return by_rows<DT, 64>(p, s);
-    case 128: return by_rows<DT, 128>(p, s);
+    case 32: return by_tiles<DT, 32>(p, s);
+    case 64: return by_tiles<DT, 64>(p, s);
+    case 128: return by_tiles<DT, 128>(p, s);
     default: return hipErrorInvalidValue;
   }
 }

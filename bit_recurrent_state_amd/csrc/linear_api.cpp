@@ -24,7 +24,7 @@ int check_config(const qstate_linear_config* c) {
   if (c->x_stride && c->x_stride < c->inputs) return QSTATE_E_INVALID;
   const int64_t most = (int64_t)1 << 20, far = (int64_t)1 << 40;
   if ((c->group != 32 && c->group != 64 && c->group != 128) || c->inputs > most ||
-      c->outputs > most || c->rows > most || c->x_stride > far)
+      c->outputs > most || c->rows > most / 2 || c->x_stride > far)
     return QSTATE_E_UNSUPPORTED;
   // grids of 256 threads a tile, and of 64 a group of 16 outputs, stay below 2^32 threads
   const int64_t tiles = ((int64_t)c->outputs + 15) / 16 * ((c->inputs + 127) / 128);

@@ -151,7 +151,7 @@ def linear4(x, weight: Weight4, bias=None):
     """x [.., inputs] times weights in four bits, [.., outputs]: x W^T + bias.
 
     x float32, bfloat16 or float16, bias float32 [outputs]; FP32 sums, rounded once to x's type.
-    Meant for few rows (64 read the weights once).  Not differentiable: inputs that want a gradient
+    Meant for few rows (every 16 of them read the weights).  Not differentiable: inputs that want a gradient
     are refused, and so is tracing (make_fx, torch.jit.trace)."""
     _refuse_tracing("linear4")
     _on_device(x, "x", weight.packed.device)

@@ -43,8 +43,8 @@ typedef struct {
   int32_t outputs;  /* 1 .. 2^20                                               */
   int32_t group;    /* 32, 64 or 128                                           */
   int32_t dtype;    /* qstate_dtype of x and y                                 */
-  int64_t rows;     /* of x; >= 0, at most 2^20.  Meant for up to 64: beyond,
-                       every 64 rows read the weights again                    */
+  int64_t rows;     /* of x; >= 0, at most 2^19.  Meant for few: every 16 rows read
+                       the weights again, from the caches as far as they hold  */
   int64_t x_stride; /* elements; 0: packed                                     */
 } qstate_linear_config;
 

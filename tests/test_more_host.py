@@ -94,12 +94,12 @@ def _linear(**kw):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(), OK), (dict(rows=0), OK), (dict(outputs=1), OK), (dict(inputs=1 << 20, outputs=1), OK),
-    (dict(outputs=1 << 20, inputs=128), OK), (dict(x_stride=256), OK), (dict(rows=1 << 20), OK),
+    (dict(outputs=1 << 20, inputs=128), OK), (dict(x_stride=256), OK), (dict(rows=1 << 19), OK),
     (dict(inputs=0), INVALID), (dict(outputs=0), INVALID), (dict(rows=-1), INVALID),
     (dict(group=0), INVALID), (dict(inputs=96, group=64), INVALID), (dict(dtype=3), INVALID),
     (dict(x_stride=255), INVALID), (dict(x_stride=-1), INVALID), (dict(group=16), UNSUPPORTED),
     (dict(group=256), UNSUPPORTED), (dict(inputs=1 << 21), UNSUPPORTED),
-    (dict(outputs=(1 << 20) + 1), UNSUPPORTED), (dict(rows=(1 << 20) + 1), UNSUPPORTED),
+    (dict(outputs=(1 << 20) + 1), UNSUPPORTED), (dict(rows=(1 << 19) + 1), UNSUPPORTED),
     (dict(inputs=1 << 20, outputs=1 << 15), UNSUPPORTED),
 ])
 def test_linear_configs(L, kw, status):
