@@ -208,7 +208,7 @@ struct Operands {
 // (rows of q, k) S^T for nodes row0 .. + 15 of the operands and tile t of value rows.
 template <int DK, int TERMS, bool DELTA, bool F32, int N>
 __device__ __forceinline__ void state_products(const StateRows<DK, F32, N>& S, int t,
-                                               const uint16_t* kop, const uint16_t* qop, int row0,
+                                               const Frag<1> (&b)[DK / 32], const uint16_t* kop, const uint16_t* qop, int row0,
                                                int plane, f32x4& xk, f32x4& xq) {
   using Op = Operands<DK, TERMS>;
   const int g = (threadIdx.x & 63) >> 4, row = row0 + (threadIdx.x & 15);
@@ -228,8 +228,6 @@ __device__ __forceinline__ void state_products(const StateRows<DK, F32, N>& S, i
 #pragma unroll
       for (int r = 0; r < 4; ++r) acc[r] = fmaf(scale, part[r], acc[r]);
     };
-    Frag<1> b[DK / 32];
-    S.operands(t, b);
     if (S.G >= 32) {
 #pragma unroll
       for (int s = 0; s < DK / 32; ++s) {
@@ -505,11 +503,15 @@ __global__ void __launch_bounds__(kThreads, TERMS == 1 && MT == 1 ? 4 : 1) verif
   }
 
   f32x4 xk[NTW], xq[NTW];
+  // the state's codes as operands: kept where several tiles of nodes use them and registers are left
+  constexpr bool hold = MT > 1 && !VEC && !F32 && DK <= 128 && (NTW == 1 || !DELTA);
+  Frag<1> codes[hold ? NTW : 1][DK / 32];
   auto products = [&](int mt) {
     if (idle) return;
 #pragma unroll
     for (int ct = 0; ct < NTW; ++ct) {
-      state_products<DK, TERMS, DELTA, F32, NTW>(S, ct, &lds.kop[0][0][0], &lds.qop[0][0][0],
+      if (!F32 && (!hold || mt == 0)) S.operands(ct, codes[hold ? ct : 0]);
+      state_products<DK, TERMS, DELTA, F32, NTW>(S, ct, codes[hold ? ct : 0], &lds.kop[0][0][0], &lds.qop[0][0][0],
                                                  VEC ? 0 : mt * 16, plane, xk[ct], xq[ct]);
       asm volatile("" ::: "memory");  // one tile's operands in registers at a time
     }

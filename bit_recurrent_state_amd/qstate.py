@@ -19,6 +19,7 @@ from ._lib import (BDR, GDN, GLA, KDA, KEY_AXIS, RTN, SCALAR, SR, VALUE_AXIS, QS
 from .draft import Draft, _accept, _verify
 from .group_norm import (GATE, GATE_FIRST, PLAIN, GroupNormConfig, qstate_group_norm,
                          qstate_group_norm_workspace)
+from .linear import Weight4, linear4
 from .norm import SILU, NormConfig, qstate_norm, qstate_norm_workspace
 from .sequence import _array, _on, _on_device, scan
 
@@ -243,6 +244,16 @@ class ReadoutNorm:
         qstate_norm(cfg, o, self.weight, gate, r=o, stream=stream)
 
 
+def _check_projection(project, cfg: Config, device) -> None:
+    """A projection of the readout [.., heads, dv], refused before any launch."""
+    if not isinstance(project, Weight4):
+        raise TypeError(f"project: expected a Weight4, got {type(project).__name__}")
+    if project.inputs != cfg.heads * cfg.dv:
+        raise ValueError(f"project: {project.inputs} inputs for a readout of {cfg.heads} x {cfg.dv}")
+    if project.packed.device != device:
+        raise ValueError(f"project is on {project.packed.device}, the state on {device}")
+
+
 class QState:
     """A handle plus the torch device buffers it works on (caller-owned memory)."""
 
@@ -261,9 +272,14 @@ class QState:
     def load_fp32(self, S, stream=None):
         qstate_load_fp32(self.handle, S, self.cfg, stream)
 
-    def step(self, q, k, v, alpha, beta=None, o=None, stream=None, norm=None):
+    def step(self, q, k, v, alpha, beta=None, o=None, stream=None, norm=None, project=None):
         """One token for every sequence; with `norm` (a ReadoutNorm), o is the normed and gated
-        readout."""
+        readout; with `project` (a Weight4 of heads * dv inputs), o's projection [N, outputs] is
+        returned, in the memory of the stream of the call."""
+        if project is not None:
+            if o is None:
+                raise ValueError("project: there is no readout without o")
+            _check_projection(project, self.cfg, self.codes.device)
         if norm is not None:  # refused before the state changes
             if o is None:
                 raise ValueError("norm: there is no readout without o")
@@ -272,14 +288,22 @@ class QState:
         qstate_step(self.handle, self.cfg, q, k, v, alpha, beta, o, stream)
         if norm is not None:
             norm._run(cfg, o, stream)
+        if project is None:
+            return None
+        with torch.no_grad(), nullcontext() if stream is None else _on(stream, o.device):
+            return linear4(o.view(self.cfg.batch, -1), project)
 
-    def prefill(self, q, k, v, log_alpha, beta=None, offsets=None, norm=None, stream=None):
+    def prefill(self, q, k, v, log_alpha, beta=None, offsets=None, norm=None, stream=None,
+                project=None):
         """A prompt's or a chunk's tokens at once, for sequences that decode on with `step`: the
         scan from the stored state, whose end is stored back (one quantization event for every
         sequence, those without tokens too: the counter goes up by one, a window starts empty).
         Arguments as `scan`'s, one sequence per batch row, q and k with the handle's heads or a
-        divisor of them; returns o, which lies in the memory of the stream of the call."""
+        divisor of them; returns o (with `project`, its projection [.., outputs]), which lies in the
+        memory of the stream of the call."""
         c = self.cfg
+        if project is not None:
+            _check_projection(project, c, self.codes.device)
         if offsets is not None and offsets.numel() != c.batch + 1:
             raise ValueError(f"offsets: expected {c.batch + 1} elements, got {offsets.numel()}")
         if v.shape[-2:] != (c.heads, c.dv) or q.shape[-1] != c.dk or (
@@ -295,9 +319,12 @@ class QState:
             self.load_fp32(S)
             if norm is not None:
                 norm._run(cfg, o)
+            if project is not None:
+                o = linear4(o.flatten(-2), project)
         return o
 
-    def verify(self, q, k, v, log_alpha, beta=None, parents=None, norm=None, stream=None):
+    def verify(self, q, k, v, log_alpha, beta=None, parents=None, norm=None, stream=None,
+               project=None):
         """The readouts of drafted tokens, for every sequence a tree of them over its stored state,
         which stays as it is; returns (o, draft), `draft` for `accept`.
 
@@ -307,18 +334,23 @@ class QState:
         parents [N, T] (int32, on the device): the earlier row of the sequence that a row hangs on, -1
         for the stored state, anything else (-2) where the row is padding; None is a chain.  o, of v's
         shape and dtype, is what `step` would read out behind each node's path, without the
-        quantization after every token; zero in rows of no node.  o and draft lie in the memory of the
+        quantization after every token; zero in rows of no node.  With `norm` it is normed and gated as
+        in `step`, with `project` its projection [N, T, outputs] is returned.  o and draft lie in the memory of the
         stream of the call.  Not for key-axis groups and pair windows."""
         dev = self.codes.device
         if norm is not None:  # refused before any launch
             _on_device(v, "v", dev)
             rows = v.shape[0] * v.shape[1] if v.dim() == 4 else 0
             cfg = norm.config((rows, self.cfg.heads, self.cfg.dv), v.dtype, dev, v.shape)
+        if project is not None:
+            _check_projection(project, self.cfg, dev)
         with nullcontext() if stream is None else _on(stream, dev):
             o, draft = _verify(self.cfg, self._c, self.codes, self.scales, q, k, v, log_alpha, beta,
                                parents)
             if norm is not None:
                 norm._run(cfg, o)
+            if project is not None:
+                o = linear4(o.flatten(-2), project)
         return o, draft
 
     def accept(self, draft: Draft, last, stream=None):

@@ -163,6 +163,69 @@ def test_streams_and_graphs():
         assert torch.equal(y, linear4(x, w))
 
 
+def _layer():
+    from bit_recurrent_state_amd import GDN, Config, QState, ReadoutNorm, Weight4
+    from draft_reference import inputs
+    x, S = inputs(GDN, 3, 5, "tree", 4, 2, 64, 32, torch.bfloat16, "cuda")
+    st = QState(Config(3, 4, 64, 32, 32, GDN, head_bits=[8, 4, 4, 4]))
+    st.load_fp32(S)
+    W = torch.randn(96, 128, device="cuda") / 11
+    g = torch.randn(3, 5, 4, 32, device="cuda").bfloat16()
+    return st, x, S, Weight4.quantize(W, 64), ReadoutNorm(gate=g, center=True)
+
+
+def test_a_layer_of_drafted_tokens():
+    """Readout, group norm with its gate and output projection in one call give what the operators give
+    one by one; the accepted path and the next token after it."""
+    from bit_recurrent_state_amd import ReadoutNorm, group_norm, linear4
+    st, x, S, w, norm = _layer()
+    args = (x["q"], x["k"], x["v"], x["log_alpha"], x["beta"])
+    y, draft = st.verify(*args, parents=x["parents"], norm=norm, project=w)
+    o, _ = st.verify(*args, parents=x["parents"])
+    by_hand = group_norm(o.flatten(-2), 4, gate=norm.gate.flatten(-2), eps=norm.eps)
+    assert y.shape == (3, 5, 96) and torch.equal(y, linear4(by_hand, w))
+    st.accept(draft, torch.tensor([4, 1, 2], dtype=torch.int32, device="cuda"))
+    codes, scales, counter = st.codes.clone(), st.scales.clone(), st.step_counter
+    f32 = torch.float32
+    one = [torch.randn(3, 4, d, device="cuda") for d in (64, 64, 32)]
+    gates = torch.rand(3, 4, device="cuda"), torch.rand(3, 4, device="cuda")
+    a, b = torch.empty(3, 4, 32, device="cuda"), torch.empty(3, 4, 32, device="cuda")
+    gate = ReadoutNorm(gate=norm.gate[:, 0].to(f32).contiguous())
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = st.step(*one, *gates, a, norm=gate, project=w, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    st.codes.copy_(codes)
+    st.scales.copy_(scales)
+    st.step_counter = counter
+    st.step(*one, *gates, b, norm=gate)
+    assert torch.equal(a, b) and torch.equal(got, linear4(b.view(3, 128), w))
+    st.load_fp32(S)
+    p = st.prefill(*args, norm=norm, project=w)
+    st.load_fp32(S)
+    assert torch.equal(p, linear4(st.prefill(*args, norm=norm).flatten(-2), w))
+
+
+def test_projections_that_do_not_fit_leave_the_state():
+    from bit_recurrent_state_amd import Weight4
+    st, x, S, w, _ = _layer()
+    codes, counter = st.codes.clone(), st.step_counter
+    args = (x["q"], x["k"], x["v"], x["log_alpha"], x["beta"])
+    other = Weight4.quantize(torch.randn(8, 64, device="cuda"))
+    one = [t[:, 0].float().repeat_interleave(2, 1).contiguous() for t in (x["q"], x["k"])]
+    one += [x["v"][:, 0].float().contiguous(), x["log_alpha"][:, 0].contiguous(), x["beta"][:, 0].contiguous()]
+    for bad, err in ((other, ValueError), (torch.zeros(96, 128, device="cuda"), TypeError)):
+        with pytest.raises(err):
+            st.verify(*args, project=bad)
+        with pytest.raises(err):
+            st.prefill(*args, project=bad)
+        with pytest.raises(err):
+            st.step(*one, torch.empty(3, 4, 32, device="cuda"), project=bad)
+    with pytest.raises(ValueError):
+        st.step(*one, project=w)
+    assert torch.equal(st.codes, codes) and st.step_counter == counter
+
+
 def test_refusals():
     from bit_recurrent_state_amd import Weight4, linear4
     from bit_recurrent_state_amd._lib import QStateError
