@@ -43,10 +43,11 @@ bool gated(const qstate_group_norm_config* c) {
 }
 
 // Teams: rows of up to 512 values take 1 .. 64 lanes of a wave, 8 values a lane;
-// wider ones a workgroup, 8 values a thread (16 above 8192).  As many teams as
-// fill the card (256 CUs, 16 waves each forward, 8 backward), or one per row if
-// there are fewer rows; a multiple of the groups, so that a team meets one group.
-void plan(const qstate_group_norm_config* c, bool backward, GroupParams& p) {
+// wider ones a workgroup, 8 values a thread (16 above 8192).  As many teams as fill
+// the card (256 CUs, 16 waves each; 8 waves in the backward pass left it at 64
+// instead of 56 us), or one per row if there are fewer rows; a multiple of the
+// groups, so that a team meets one group.
+void plan(const qstate_group_norm_config* c, GroupParams& p) {
   std::memset(&p, 0, sizeof(p));
   p.rows = c->tokens * c->groups;
   p.groups = c->groups;
@@ -70,7 +71,7 @@ void plan(const qstate_group_norm_config* c, bool backward, GroupParams& p) {
     p.team = 1;
     while (p.team * 8 < c->width) p.team *= 2;
   }
-  int64_t teams = (int64_t)256 * (backward ? 512 : 1024) / p.team;
+  int64_t teams = (int64_t)256 * 1024 / p.team;
   if (teams > p.rows) teams = p.rows;
   p.teams = (teams + p.groups - 1) / p.groups * p.groups;
   // parts of the weights' gradients: a team's, or a wave's where its teams share the weight
@@ -100,7 +101,7 @@ int qstate_group_norm(const qstate_group_norm_config* cfg, const void* x, const 
   if (cfg->tokens == 0) return QSTATE_OK;
   if (!x || !y || (gated(cfg) && !gate)) return QSTATE_E_INVALID;
   GroupParams p;
-  plan(cfg, false, p);
+  plan(cfg, p);
   p.x = x;
   p.weight = weight;
   p.bias = bias;
@@ -116,7 +117,7 @@ int qstate_group_norm_workspace(const qstate_group_norm_config* cfg, size_t* byt
   if (rc != QSTATE_OK) return rc;
   if (!bytes) return QSTATE_E_INVALID;
   GroupParams p;
-  plan(cfg, true, p);
+  plan(cfg, p);
   *bytes = (size_t)p.partials * p.width * 2 * sizeof(float);
   return QSTATE_OK;
 }
@@ -142,7 +143,7 @@ int qstate_group_norm_backward(const qstate_group_norm_config* cfg, const void* 
   if (sums && need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
     return QSTATE_E_INVALID;
   GroupParams p;
-  plan(cfg, true, p);
+  plan(cfg, p);
   if (!sums && p.rows == 0) return QSTATE_OK;
   p.x = x;
   p.weight = weight;

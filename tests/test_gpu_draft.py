@@ -407,8 +407,10 @@ def test_refusals():
         with pytest.raises((TypeError, ValueError)):
             verify(st, dict(x, **bad))
     y, _ = inputs(GDN, 2, 65, "tree", 2, 2, 64, 32, torch.float32, "cuda")
-    with pytest.raises(QStateError):
-        verify(st, y)
+    none = {n: None if t is None else t[:, :0] for n, t in x.items()}
+    for T in (y, none):  # one to 64 rows
+        with pytest.raises(QStateError):
+            verify(st, T)
     _, draft = verify(st, x)
     last = torch.zeros(2, dtype=torch.int32, device="cuda")
     step = st.step_counter
