@@ -365,7 +365,8 @@ struct alignas(16) Lds {
   // with a gate per channel a tile of nodes is worked out at a time
   static constexpr int OT = VEC ? 16 : T, OM = VEC ? 1 : MT;
   static constexpr int MP = T + 4;
-  uint16_t kop[TERMS][OT][LP], qop[TERMS][OT][LP];
+  // (without the delta rule and with a gate per channel no product takes k)
+  uint16_t kop[VEC && !DELTA ? 1 : TERMS][VEC && !DELTA ? 1 : OT][LP], qop[TERMS][OT][LP];
   uint8_t codes[4][State::CODES];              // of each wave
   float scales[4][State::SCALES];
   float A[OT][MP], L[DELTA ? OT : 1][MP];      // A diag b, -L diag b
@@ -405,7 +406,7 @@ __device__ __forceinline__ void invert(const float (*lt)[16][20], float (*inv)[1
 
 // A workgroup of four waves takes 64 NTW value columns, a wave NTW tiles of 16.
 template <int DK, int MT, int TERMS, bool VEC, bool DELTA, bool F32, int NTW>
-__global__ void __launch_bounds__(kThreads, TERMS == 1 && MT == 1 ? 4 : 1) verify_kernel(Params p) {
+__global__ void __launch_bounds__(kThreads, TERMS == 1 && MT == 1 && DK <= 128 ? 4 : 1) verify_kernel(Params p) {
   using D = Lds<DK, MT, TERMS, VEC, DELTA, F32, NTW>;
   using Op = Operands<DK, TERMS>;
   constexpr int LP = D::LP, MP = D::MP, plane = D::OT * LP;
@@ -439,8 +440,6 @@ __global__ void __launch_bounds__(kThreads, TERMS == 1 && MT == 1 ? 4 : 1) verif
   const Rows vrows(p.v, row_of(p, n, 0) * p.vs + (int64_t)h * dv, (int)p.vs, dtype);
   auto load_q = [&](int t, int e) { return qrows.four(min(t, T - 1), e, qfour); };
   auto load_k = [&](int t, int e) { return krows.four(min(t, T - 1), e, kfour); };
-  const int t0 = threadIdx.x / (DK / 4), e0 = threadIdx.x % (DK / 4) * 4;
-  constexpr int TS = kThreads / (DK / 4);  // rows between a thread's groups
   constexpr int VW = TERMS == 1 ? 1 : NTW;
   uint32_t raw[4][VW];  // of a tile's v
   auto load_v = [&](int mt) {
@@ -464,9 +463,9 @@ __global__ void __launch_bounds__(kThreads, TERMS == 1 && MT == 1 ? 4 : 1) verif
     S.fetch(p, n, h, first, lds.codes[wave], lds.scales[wave]);
     load_v(0);
   } else {
-    constexpr int IT = D::T * DK / 4 / kThreads;  // a thread's groups of four columns of all rows
+    // a thread's groups of four columns of all rows, from row t0 on, TS rows apart
+    constexpr int IT = D::T * DK / 4 / kThreads, TS = kThreads / (DK / 4);
     const int t0 = threadIdx.x / (DK / 4), e0 = threadIdx.x % (DK / 4) * 4;
-    constexpr int TS = kThreads / (DK / 4);  // rows between a thread's groups
     if constexpr (VEC) {
       f32x4 a[IT];
 #pragma unroll
