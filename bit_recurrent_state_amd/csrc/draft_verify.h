@@ -26,6 +26,10 @@
 // differences of 64-bit sums.  A gate per channel: each node goes up its path and
 // multiplies the decays into its q and k on the way, exact at any decay.
 //
+// A product over nodes keeps a NaN where its other factor is a zero, the mark of no ancestor.  So each
+// tile of U is looked through; if something is not finite, zeros take its place in the products, and
+// what hangs on it is made NaN along the paths: a broken branch changes no bit of another (1 to 3 %).
+//
 // Bound by latency, then by memory: what a workgroup reads is asked for before
 // anything is waited for, codes, scales and bfloat16 rows by copies to LDS that
 // take no registers, so that four workgroups share a CU.  256 sequences with 16 nodes,
@@ -280,6 +284,22 @@ __device__ __forceinline__ void small_mma(f32x4& acc, const float* a, int stride
   for (int r = 0; r < 4; ++r) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[r], b[r], acc, 0, 0, 0);
 }
 
+// Products with zeros keep a NaN, so what is not finite would spoil nodes that do not hang on it.
+__device__ __forceinline__ bool broken(float x) { return __builtin_amdgcn_classf(x, 0x207); }
+
+// Zeros in the place of a tile's values that are not finite; their rows, in the lane's column.
+__device__ __forceinline__ uint32_t take_out(f32x4& x) {
+  uint32_t rows = 0;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    rows |= (uint32_t)broken(x[r]) << r;
+    x[r] = broken(x[r]) ? 0.0f : x[r];
+  }
+  rows <<= (threadIdx.x & 63) >> 4 << 2;
+  rows |= __shfl_xor(rows, 16);
+  return rows | __shfl_xor(rows, 32);
+}
+
 // Rows of a sequence, from a base address that is the same for the workgroup.
 struct Rows {
   const char* base;
@@ -421,9 +441,15 @@ __device__ __forceinline__ void invert(const float (*lt)[16][20], float (*inv)[1
   for (int i = 0; i < 16; ++i) inv[tile][i][col] = x[i];
 }
 
+// Workgroups of a CU that the registers have to leave room for: with a gate per channel two where the
+// LDS holds two (64 sequences of up to 33 nodes, KDA: 57 us, 84 with six registers more).
+template <int DK, int MT, int TERMS, bool VEC, bool DELTA, bool F32, int NTW>
+constexpr int kResident = TERMS == 1 && MT == 1 && DK <= 128 ? 4
+                          : VEC && sizeof(Lds<DK, MT, TERMS, VEC, DELTA, F32, NTW>) <= 80 << 10 ? 2 : 1;
+
 // A workgroup of four waves takes 64 NTW value columns, a wave NTW tiles of 16.
 template <int DK, int MT, int TERMS, bool VEC, bool DELTA, bool F32, int NTW>
-__global__ void __launch_bounds__(kThreads, TERMS == 1 && MT == 1 && DK <= 128 ? 4 : 1)
+__global__ void __launch_bounds__(kThreads, (kResident<DK, MT, TERMS, VEC, DELTA, F32, NTW>))
 verify_kernel(Params p) {
   using D = Lds<DK, MT, TERMS, VEC, DELTA, F32, NTW>;
   using Op = Operands<DK, TERMS>;
@@ -588,7 +614,15 @@ verify_kernel(Params p) {
         x[r] = on ? a[r] * f : 0.0f;
         (is_l ? lds.L : lds.A)[row][col] = x[r];
       }
-      if (is_l && it == jt) *reinterpret_cast<f32x4*>(&lds.lt[it][lane & 15][4 * g]) = x;
+      if (is_l && it == jt) {
+        // not into the inverse: the node's U is spoilt by its e^c instead
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if (broken(x[r])) lds.ec[it * 16 + 4 * g + r] = NAN;
+          x[r] = broken(x[r]) ? 0.0f : x[r];
+        }
+        *reinterpret_cast<f32x4*>(&lds.lt[it][lane & 15][4 * g]) = x;
+      }
     }
   };
 
@@ -622,6 +656,7 @@ verify_kernel(Params p) {
 
   const Columns<NTW> to(p, n, h, col0, dtype);
   f32x4 u[MT][NTW];
+  bool spoilt = false;  // something in the wave's part of U is not finite
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     if (mt * 16 >= rows) break;
@@ -685,7 +720,8 @@ verify_kernel(Params p) {
             lds.A[i][at] = a * b;
             if (DELTA && at != t) {
               lds.L[i][at] = -l * b;
-              if (at >= mt * 16) lds.lt[0][at - mt * 16][i] = -l * b;
+              if (at >= mt * 16) lds.lt[0][at - mt * 16][i] = broken(l * b) ? 0.0f : -l * b;
+              if (broken(l * b)) lds.ec[t] = NAN;  // not into the inverse
             }
           }
           at = ahead[d];
@@ -714,34 +750,84 @@ verify_kernel(Params p) {
     bool node[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) node[r] = (uint32_t)(nodes >> (mt * 16)) & (1u << (4 * g + r));
-    float out[4][NTW], wr[4][NTW];
+    // earlier tile jt as the right operand of a product
+    auto finite = [&](int jt, int ct) {
+      f32x4 y = u[jt][ct];
+      if (spoilt) take_out(y);
+      return y;
+    };
+    f32x4 x[NTW];
+    bool bad = false;
 #pragma unroll
     for (int ct = 0; ct < NTW; ++ct) {
-      f32x4 x;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float v = VW < NTW ? __uint_as_float(ct ? raw[r][0] & 0xFFFF0000u : raw[r][0] << 16)
                                  : qscan::from_raw(raw[r][VW == 1 ? 0 : ct], dtype);
-        x[r] = node[r] ? (DELTA ? fmaf(-ec[r], xk[ct][r], v) : v) : 0.0f;
+        x[ct][r] = node[r] ? (DELTA ? fmaf(-ec[r], xk[ct][r], v) : v) : 0.0f;
         xq[ct][r] *= ec[r];
       }
       if constexpr (DELTA) {
 #pragma unroll
         for (int jt = 0; jt < mt; ++jt)
-          small_mma(x, &lds.L[VEC ? 0 : mt * 16][jt * 16], MP, u[jt][ct]);
+          small_mma(x[ct], &lds.L[VEC ? 0 : mt * 16][jt * 16], MP, finite(jt, ct));
         u[mt][ct] = f32x4{0, 0, 0, 0};
-        small_mma(u[mt][ct], &lds.inv[VEC ? 0 : mt][0][0], 20, x);
+        small_mma(u[mt][ct], &lds.inv[VEC ? 0 : mt][0][0], 20, x[ct]);
       } else {
-        u[mt][ct] = x;
+        u[mt][ct] = x[ct];
       }
 #pragma unroll
-      for (int jt = 0; jt <= mt; ++jt) small_mma(xq[ct], &lds.A[VEC ? 0 : mt * 16][jt * 16], MP, u[jt][ct]);
+      for (int r = 0; r < 4; ++r) bad |= broken(u[mt][ct][r]);
+    }
+    spoilt |= __ballot(bad) != 0;
+    unsigned long long gone[NTW] = {};  // nodes whose U is not finite
+    if (spoilt) {
+#pragma unroll
+      for (int ct = 0; ct < NTW; ++ct) {
+#pragma unroll
+        for (int jt = 0; jt < mt; ++jt) {
+          f32x4 y = u[jt][ct];
+          gone[ct] |= (unsigned long long)take_out(y) << (jt * 16);
+        }
+        gone[ct] |= (unsigned long long)take_out(x[ct]) << (mt * 16);
+        if (DELTA) {
+          f32x4 below;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) below[r] = lds.mask[mt * 16 + 4 * g + r] & gone[ct] ? NAN : 0.0f;
+          gone[ct] |= (unsigned long long)take_out(below) << (mt * 16);
+          u[mt][ct] = f32x4{0, 0, 0, 0};
+          small_mma(u[mt][ct], &lds.inv[VEC ? 0 : mt][0][0], 20, x[ct]);
+        } else {
+          u[mt][ct] = x[ct];
+        }
+        gone[ct] |= (unsigned long long)take_out(u[mt][ct]) << (mt * 16);
+      }
+    }
+#pragma unroll
+    for (int ct = 0; ct < NTW; ++ct) {
+#pragma unroll
+      for (int jt = 0; jt < mt; ++jt)
+        small_mma(xq[ct], &lds.A[VEC ? 0 : mt * 16][jt * 16], MP, finite(jt, ct));
+      small_mma(xq[ct], &lds.A[VEC ? 0 : mt * 16][mt * 16], MP, u[mt][ct]);
+    }
+    if (spoilt) {
+#pragma unroll
+      for (int ct = 0; ct < NTW; ++ct)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = mt * 16 + 4 * g + r;
+          if (lds.mask[row] & gone[ct]) xq[ct][r] = NAN;
+          if (gone[ct] >> row & 1) u[mt][ct][r] = NAN;
+        }
+    }
+    float out[4][NTW], wr[4][NTW];
+#pragma unroll
+    for (int ct = 0; ct < NTW; ++ct)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         out[r][ct] = node[r] ? xq[ct][r] : 0.0f;
         wr[r][ct] = node[r] ? u[mt][ct][r] * bt[r] : 0.0f;
       }
-    }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = mt * 16 + 4 * g + r;

@@ -176,6 +176,50 @@ def test_nan_stays_in_its_head(mixer):
     assert torch.equal(bad[0], good[0]) and torch.equal(bad[2], good[2]) and torch.equal(bad[1, 0], good[1, 0])
 
 
+def below(parents, n, t):
+    """bool [N][T]: node t of sequence n and what hangs on it."""
+    hit = torch.zeros(parents.shape, dtype=torch.bool)
+    hit[n, t] = True
+    for i, p in enumerate(parents[n].tolist()):
+        if 0 <= p < i and hit[n, p]:
+            hit[n, i] = True
+    return hit
+
+
+@pytest.mark.parametrize("mixer", MIXERS)
+@pytest.mark.parametrize("name", ["q", "k", "v", "log_alpha", "beta"])
+@pytest.mark.parametrize("dtype,T,dk,dv,store", [("bf16", 14, 128, 128, "int4"), ("bf16", 64, 128, 72, "mix"),
+                                                 ("f32", 40, 64, 48, "f32"), ("f16", 31, 256, 128, "int8")])
+def test_broken_branch(mixer, name, dtype, T, dk, dv, store):
+    """NaN and infinities in a node change no bit of the nodes that do not hang on it."""
+    m = MIXERS[mixer]
+    x, S = inputs(m, 2, T, "tree", 2, 2, dk, dv, TYPES[dtype], "cuda", seed=T)
+    if x[name] is None:
+        return
+    st, _ = handle(m, S, store)
+    o, d = verify(st, x)
+    for value in (float("nan"), float("inf")):
+        for t in (0, T // 3, T - 2):
+            y = {n: None if a is None else a.clone() for n, a in x.items()}
+            y[name][1, t, 1].view(-1)[-1] = value
+            o2, d2 = verify(st, y)
+            hit = below(x["parents"].cpu(), 1, t).cuda()
+            for a, b in ((o, o2), (d.writes, d2.writes)):
+                assert torch.equal(a[~hit], b[~hit]) and torch.equal(a[:, :, 0], b[:, :, 0])
+            assert not o2[1, t, 1].isfinite().all()
+            if name == "v":  # its column alone
+                assert torch.equal(o2[..., :-1], o[..., :-1])
+                assert not o2[hit][:, 1, -1].isfinite().any()
+            # a path beside it enters the state as if it were not there
+            ways = [i for i in range(T) if not hit[1, i]]
+            last = torch.tensor([T - 1, ways[-1] if ways else -1], dtype=torch.int32, device="cuda")
+            a, _ = handle(m, S, store)
+            b, _ = handle(m, S, store)
+            a.accept(d, last)
+            b.accept(d2, last)
+            assert torch.equal(a.codes, b.codes) and (store == "f32" or torch.equal(a.scales, b.scales))
+
+
 @pytest.mark.parametrize("last", [-1, -5, 9, 1 << 30, 3])
 def test_last_that_is_no_node(last):
     x, S = inputs(GDN, 2, 9, "tree", 2, 2, 64, 32, torch.float32, "cuda")
