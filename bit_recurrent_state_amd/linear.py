@@ -18,6 +18,8 @@ from .sequence import (DTYPES, _array, _call, _on_device, _refuse_tracing, _stre
 __all__ = ["LinearConfig", "Weight4", "qstate_linear", "qstate_linear_bytes", "qstate_linear_pack",
            "qstate_linear_quantize", "linear4"]
 
+_ROWS = 1 << 19  # of x in a call of the library
+
 
 @dataclass
 class LinearConfig:
@@ -171,11 +173,17 @@ def linear4(x, weight: Weight4, bias=None):
     if ((weight.inputs > 1 and r.stride(1) != 1) or stride < weight.inputs
             or stride * r.element_size() % 16 or r.data_ptr() % 16):
         r, stride = r.clone(memory_format=torch.contiguous_format), weight.inputs
-    c = LinearConfigC(weight.inputs, weight.outputs, weight.group, DTYPES[x.dtype], r.shape[0],
-                      stride)
     dev = x.device
     y = torch.empty(x.shape[:-1] + (weight.outputs,), dtype=x.dtype, device=dev)
-    check("qstate_linear", _call(dev, lib().qstate_linear, c, r.data_ptr(), weight.packed.data_ptr(),
-                                 weight.scales.data_ptr(), None if bias is None else bias.data_ptr(),
-                                 y.data_ptr(), _stream(None, dev)))
-    return y
+    size, start = r.element_size(), 0
+    while True:
+        rows = min(r.shape[0] - start, _ROWS)
+        c = LinearConfigC(weight.inputs, weight.outputs, weight.group, DTYPES[x.dtype], rows, stride)
+        check("qstate_linear", _call(
+            dev, lib().qstate_linear, c, r.data_ptr() + start * stride * size,
+            weight.packed.data_ptr(), weight.scales.data_ptr(),
+            None if bias is None else bias.data_ptr(),
+            y.data_ptr() + start * weight.outputs * size, _stream(None, dev)))
+        start += rows
+        if start >= r.shape[0]:
+            return y

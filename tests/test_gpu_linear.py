@@ -253,3 +253,15 @@ def test_refusals():
         linear4(x.clone().requires_grad_(True), w)
     with pytest.raises(RuntimeError):
         torch.jit.trace(lambda t: linear4(t, w), (x,), check_trace=False)
+
+
+def test_more_rows_than_a_call_takes():
+    """Rows of a long prompt: the last ones as by themselves."""
+    from bit_recurrent_state_amd import Weight4, linear4
+    g = torch.Generator().manual_seed(5)
+    w = Weight4.quantize(torch.randn(17, 64, generator=g).cuda(), 32)
+    x = torch.randn(1, 64, generator=g).bfloat16().cuda().repeat((1 << 19) + 21, 1)
+    x[-30:] = torch.randn(30, 64, generator=g).bfloat16().cuda()
+    y = linear4(x, w)
+    assert torch.equal(y[-30:], linear4(x[-30:], w))
+    assert torch.equal(y[:-30], linear4(x[:1], w).expand(y.shape[0] - 30, -1))
