@@ -334,9 +334,10 @@ class QState:
         parents [N, T] (int32, on the device): the earlier row of the sequence that a row hangs on, -1
         for the stored state, anything else (-2) where the row is padding; None is a chain.  o, of v's
         shape and dtype, is what `step` would read out behind each node's path, without the
-        quantization after every token; zero in rows of no node.  With `norm` it is normed and gated as
-        in `step`, with `project` its projection [N, T, outputs] is returned.  o and draft lie in the memory of the
-        stream of the call.  Not for key-axis groups and pair windows."""
+        quantization after every token; zero in rows of no node.  A node that is not finite spoils
+        those that hang on it and no other.  With `norm` o is normed and gated as in `step`, with
+        `project` its projection [N, T, outputs] is returned.  o and draft lie in the memory of the
+        stream of the call.  Not differentiable; not for key-axis groups and pair windows."""
         dev = self.codes.device
         if norm is not None:  # refused before any launch
             _on_device(v, "v", dev)
@@ -356,7 +357,8 @@ class QState:
     def accept(self, draft: Draft, last, stream=None):
         """The path of drafted tokens that ends in row last[n] (int32 [N], on the device) enters the
         stored state of sequence n, in one quantization event: the counter goes up by one.  A sequence
-        with last[n] = -1 accepts none and keeps its state bit for bit."""
+        with last[n] = -1 accepts none and keeps its state bit for bit.  In a captured graph every
+        replay is the event of the capture: the counter stays, and SR's random bits repeat."""
         dev = self.codes.device
         step = self.step_counter
         with nullcontext() if stream is None else _on(stream, dev):
