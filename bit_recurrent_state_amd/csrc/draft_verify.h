@@ -33,9 +33,9 @@
 // Bound by latency, then by memory: what a workgroup reads is asked for before
 // anything is waited for, codes, scales and bfloat16 rows by copies to LDS that
 // take no registers, so that four workgroups share a CU.  256 sequences with 16 nodes,
-// 32 heads of 128 x 128, GDN, INT4 (a quarter INT8), bfloat16: 71 us, 300 MB at
-// 4.2 TB/s (192 us with loads where they are used, 106 with the codes gathered
-// into registers).  64 sequences of up to 33 nodes, 16 heads, KDA, INT8: 57 us for
+// 32 heads of 128 x 128, GDN, INT4 (a quarter INT8), bfloat16: 73 us, 300 MB at
+// 4.1 TB/s (192 us with loads where they are used, 106 with the codes gathered
+// into registers).  64 sequences of up to 33 nodes, 16 heads, KDA, INT8: 58 us for
 // 53 MB; its workgroups take 80 KB of LDS and 11 of their 30 thousand cycles
 // for the walks.  32 sequences of 64 nodes, SCALAR, 32 heads of 64 x 128, INT4: 23 us
 // for 40 MB.
@@ -414,6 +414,7 @@ struct alignas(16) Lds {
   double c[T];
   unsigned long long mask[T];                  // node and ancestors; 0: no node
   unsigned long long nodes, pad;               // which rows are nodes
+  unsigned long long gone[4][NTW][16];         // of a wave's columns: the nodes whose U is not finite
   int parent[T];
 };
 
@@ -442,7 +443,7 @@ __device__ __forceinline__ void invert(const float (*lt)[16][20], float (*inv)[1
 }
 
 // Workgroups of a CU that the registers have to leave room for: with a gate per channel two where the
-// LDS holds two (64 sequences of up to 33 nodes, KDA: 57 us, 84 with six registers more).
+// LDS holds two (64 sequences of up to 33 nodes, KDA: 58 us; 84 with one workgroup, six registers more).
 template <int DK, int MT, int TERMS, bool VEC, bool DELTA, bool F32, int NTW>
 constexpr int kResident = TERMS == 1 && MT == 1 && DK <= 128 ? 4
                           : VEC && sizeof(Lds<DK, MT, TERMS, VEC, DELTA, F32, NTW>) <= 80 << 10 ? 2 : 1;
@@ -656,7 +657,10 @@ verify_kernel(Params p) {
 
   const Columns<NTW> to(p, n, h, col0, dtype);
   f32x4 u[MT][NTW];
-  bool spoilt = false;  // something in the wave's part of U is not finite
+  bool spoilt = false;  // something in the wave's part of U is not finite: zeros stand in its place
+  if (lane < 16)
+#pragma unroll
+    for (int ct = 0; ct < NTW; ++ct) lds.gone[wave][ct][lane] = 0;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     if (mt * 16 >= rows) break;
@@ -750,12 +754,6 @@ verify_kernel(Params p) {
     bool node[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) node[r] = (uint32_t)(nodes >> (mt * 16)) & (1u << (4 * g + r));
-    // earlier tile jt as the right operand of a product
-    auto finite = [&](int jt, int ct) {
-      f32x4 y = u[jt][ct];
-      if (spoilt) take_out(y);
-      return y;
-    };
     f32x4 x[NTW];
     bool bad = false;
 #pragma unroll
@@ -770,7 +768,7 @@ verify_kernel(Params p) {
       if constexpr (DELTA) {
 #pragma unroll
         for (int jt = 0; jt < mt; ++jt)
-          small_mma(x[ct], &lds.L[VEC ? 0 : mt * 16][jt * 16], MP, finite(jt, ct));
+          small_mma(x[ct], &lds.L[VEC ? 0 : mt * 16][jt * 16], MP, u[jt][ct]);
         u[mt][ct] = f32x4{0, 0, 0, 0};
         small_mma(u[mt][ct], &lds.inv[VEC ? 0 : mt][0][0], 20, x[ct]);
       } else {
@@ -780,45 +778,30 @@ verify_kernel(Params p) {
       for (int r = 0; r < 4; ++r) bad |= broken(u[mt][ct][r]);
     }
     spoilt |= __ballot(bad) != 0;
-    unsigned long long gone[NTW] = {};  // nodes whose U is not finite
     if (spoilt) {
 #pragma unroll
       for (int ct = 0; ct < NTW; ++ct) {
-#pragma unroll
-        for (int jt = 0; jt < mt; ++jt) {
-          f32x4 y = u[jt][ct];
-          gone[ct] |= (unsigned long long)take_out(y) << (jt * 16);
-        }
-        gone[ct] |= (unsigned long long)take_out(x[ct]) << (mt * 16);
+        unsigned long long gone = lds.gone[wave][ct][lane & 15];
+        gone |= (unsigned long long)take_out(x[ct]) << (mt * 16);
         if (DELTA) {
           f32x4 below;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) below[r] = lds.mask[mt * 16 + 4 * g + r] & gone[ct] ? NAN : 0.0f;
-          gone[ct] |= (unsigned long long)take_out(below) << (mt * 16);
+          for (int r = 0; r < 4; ++r) below[r] = lds.mask[mt * 16 + 4 * g + r] & gone ? NAN : 0.0f;
+          gone |= (unsigned long long)take_out(below) << (mt * 16);
           u[mt][ct] = f32x4{0, 0, 0, 0};
           small_mma(u[mt][ct], &lds.inv[VEC ? 0 : mt][0][0], 20, x[ct]);
         } else {
           u[mt][ct] = x[ct];
         }
-        gone[ct] |= (unsigned long long)take_out(u[mt][ct]) << (mt * 16);
+        gone |= (unsigned long long)take_out(u[mt][ct]) << (mt * 16);
+        lds.gone[wave][ct][lane & 15] = gone;  // the four lanes of a column have the same
       }
     }
 #pragma unroll
     for (int ct = 0; ct < NTW; ++ct) {
 #pragma unroll
-      for (int jt = 0; jt < mt; ++jt)
-        small_mma(xq[ct], &lds.A[VEC ? 0 : mt * 16][jt * 16], MP, finite(jt, ct));
-      small_mma(xq[ct], &lds.A[VEC ? 0 : mt * 16][mt * 16], MP, u[mt][ct]);
-    }
-    if (spoilt) {
-#pragma unroll
-      for (int ct = 0; ct < NTW; ++ct)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = mt * 16 + 4 * g + r;
-          if (lds.mask[row] & gone[ct]) xq[ct][r] = NAN;
-          if (gone[ct] >> row & 1) u[mt][ct][r] = NAN;
-        }
+      for (int jt = 0; jt <= mt; ++jt)
+        small_mma(xq[ct], &lds.A[VEC ? 0 : mt * 16][jt * 16], MP, u[jt][ct]);
     }
     float out[4][NTW], wr[4][NTW];
 #pragma unroll
@@ -828,6 +811,18 @@ verify_kernel(Params p) {
         out[r][ct] = node[r] ? xq[ct][r] : 0.0f;
         wr[r][ct] = node[r] ? u[mt][ct][r] * bt[r] : 0.0f;
       }
+    if (spoilt) {
+#pragma unroll
+      for (int ct = 0; ct < NTW; ++ct) {
+        const unsigned long long gone = lds.gone[wave][ct][lane & 15];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = mt * 16 + 4 * g + r;
+          if (lds.mask[row] & gone) out[r][ct] = NAN;
+          if (gone >> row & 1) wr[r][ct] = NAN;
+        }
+      }
+    }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = mt * 16 + 4 * g + r;
