@@ -27,8 +27,9 @@
 // multiplies the decays into its q and k on the way, exact at any decay.
 //
 // A product over nodes keeps a NaN where its other factor is a zero, the mark of no ancestor.  So each
-// tile of U is looked through; if something is not finite, zeros take its place in the products, and
-// what hangs on it is made NaN along the paths: a broken branch changes no bit of another (1 to 3 %).
+// tile of U is looked through, and of the inverse; if something is not finite, zeros take its place in
+// the products, and what hangs on it is made NaN along the paths: a broken branch changes no bit of
+// another (1 to 3 %).
 //
 // Bound by latency, then by memory: what a workgroup reads is asked for before
 // anything is waited for, codes, scales and bfloat16 rows by copies to LDS that
@@ -420,7 +421,10 @@ struct alignas(16) Lds {
 
 // The inverse of the unit triangular tile `tile`, a column a lane: each row that is
 // done is taken off all rows below at once, so that nothing waits but for the row before.
-__device__ __forceinline__ void invert(const float (*lt)[16][20], float (*inv)[16][20], int tile) {
+// Finite factors may still have a product beyond the range, which a zero, the mark of no ancestor, would
+// hand to rows beside the branch: such a column is done again without the products of zeros, and its
+// infinite rows, zeros in the inverse, are spoilt by their e^c (of the tile's rows).
+__device__ __forceinline__ void invert(const float (*lt)[16][20], float (*inv)[16][20], int tile, float* ec) {
   const int col = threadIdx.x & 15;
   float x[16];
 #pragma unroll
@@ -438,8 +442,25 @@ __device__ __forceinline__ void invert(const float (*lt)[16][20], float (*inv)[1
         if (4 * b + i > j) x[4 * b + i] = fmaf(f[i], x[j], x[4 * b + i]);
     }
   }
+  float none = 0.0f;  // NaN once something is not finite
 #pragma unroll
-  for (int i = 0; i < 16; ++i) inv[tile][i][col] = x[i];
+  for (int i = 0; i < 16; ++i) {
+    inv[tile][i][col] = x[i];
+    none = fmaf(x[i], 0.0f, none);
+  }
+  if (none == 0.0f) return;
+  // (rolled: unrolled, what hardly ever runs cost every call of KDA 9 %)
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i) {
+    float y = i == col ? 1.0f : 0.0f;
+#pragma unroll 1
+    for (int j = 0; j < i; ++j) {
+      const float f = lt[tile][j][i];
+      if (f != 0.0f) y = fmaf(f, inv[tile][j][col], y);
+    }
+    if (broken(y)) ec[i] = NAN;
+    inv[tile][i][col] = broken(y) ? 0.0f : y;
+  }
 }
 
 // Workgroups of a CU that the registers have to leave room for: with a gate per channel two where the
@@ -650,7 +671,7 @@ verify_kernel(Params p) {
       between(nodes ? 64 - __clzll(nodes) : 0);
     if (DELTA) {
       if (MT > 1) __syncthreads();  // with one tile the second wave has all of L
-      if (wave == 1 && g < MT) invert(lds.lt, lds.inv, g);
+      if (wave == 1 && g < MT) invert(lds.lt, lds.inv, g, &lds.ec[g * 16]);
     }
   }
   const int rows = nodes ? 64 - __clzll(nodes) : 0;  // up to the last node
@@ -743,7 +764,7 @@ verify_kernel(Params p) {
         if (DELTA) qscan::put4<TERMS>(&lds.kop[0][i][64 * r + 4 * sub], plane, k[r]);
       }
       __syncthreads();
-      if (DELTA && wave == 0 && g == 0) invert(lds.lt, lds.inv, 0);
+      if (DELTA && wave == 0 && g == 0) invert(lds.lt, lds.inv, 0, &lds.ec[mt * 16]);
     }
     if (mt > 0) load_v(mt);
     if (VEC || mt > 0) products(mt);

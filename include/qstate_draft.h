@@ -23,10 +23,10 @@
  * instructions with every FP32 operand split into three bfloat16 terms (codes,
  * and bfloat16 q and k with one gate a token, need one), so that results hold
  * to FP32; o is rounded once.  Log decays are at most 0; anything below -87
- * counts as -87.  A NaN or an infinity in a node's inputs spoils what depends
- * on it, in that node and the nodes that hang on it, and changes no bit of the
- * others; what rows of no node hold is of no matter.  The same call gives the
- * same bits.
+ * counts as -87.  A NaN or an infinity in a node's inputs, or products of them
+ * that leave FP32's range, spoil what depends on it, in that node and the nodes
+ * that hang on it, and change no bit of the others; what rows of no node hold is
+ * of no matter.  The same call gives the same bits.
  *
  * Layout (device memory, caller-owned); rows are [batch][T]:
  *   q, k       dtype [batch][T][heads_qk][dk], rows q_stride / k_stride

@@ -220,6 +220,46 @@ def test_broken_branch(mixer, name, dtype, T, dk, dv, store):
             assert torch.equal(a.codes, b.codes) and (store == "f32" or torch.equal(a.scales, b.scales))
 
 
+def overflowing(m, T, branch, dtype, dk, dv, store):
+    """A tree with a path of nodes `branch` whose keys are finite but so long that products of two of
+    them, 1e24, have squares beyond FP32: with and without, and the nodes that hang on the path."""
+    x, S = inputs(m, 2, T, "chain", 2, 2, dk, dv, TYPES[dtype], "cuda", seed=T)
+    parents, other = [], -1
+    for t in range(T):
+        if t in branch:
+            parents.append(([-1] + branch)[branch.index(t)])
+            continue
+        on = branch[-1] if t % 5 == 4 and branch[-1] < t else other if t % 3 else -1
+        parents.append(on)
+        other = t if on != branch[-1] else other
+    x["parents"][:] = torch.tensor(parents, dtype=torch.int32, device="cuda")
+    y = {n: None if t is None else t.clone() for n, t in x.items()}
+    y["k"][1, branch] = (1e12 * x["k"][1, branch[0]].float()).to(TYPES[dtype])
+    return x, y, S, below(x["parents"].cpu(), 1, branch[0])
+
+
+@pytest.mark.parametrize("mixer", MIXERS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,branch,dk,dv,store", [(6, [0, 1, 2], 128, 128, "int4"), (20, [4, 13, 15], 64, 72, "f32"),
+                                                  (40, [1, 17, 20], 128, 48, "mix"), (31, [16, 17, 18, 19], 256, 32, "int8")])
+def test_products_beyond_the_range(mixer, dtype, T, branch, dk, dv, store):
+    """Keys whose products overflow change no bit of the nodes that do not hang on them."""
+    m = MIXERS[mixer]
+    x, y, S, hit = overflowing(m, T, branch, dtype, dk, dv, store)
+    st, _ = handle(m, S, store)
+    o, d = verify(st, x)
+    o2, d2 = verify(st, y)
+    assert bool(o[~hit.cuda()].isfinite().all()) and bool(o2[1, branch[0]].isfinite().all())
+    for a, b in ((o, o2), (d.writes, d2.writes)):
+        assert torch.equal(a[~hit.cuda()], b[~hit.cuda()])
+    last = torch.tensor([T - 1, [i for i in range(T) if not hit[1, i]][-1]], dtype=torch.int32, device="cuda")
+    a, _ = handle(m, S, store)
+    b, _ = handle(m, S, store)
+    a.accept(d, last)
+    b.accept(d2, last)
+    assert torch.equal(a.codes, b.codes) and (store == "f32" or torch.equal(a.scales, b.scales))
+
+
 @pytest.mark.parametrize("last", [-1, -5, 9, 1 << 30, 3])
 def test_last_that_is_no_node(last):
     x, S = inputs(GDN, 2, 9, "tree", 2, 2, 64, 32, torch.float32, "cuda")
