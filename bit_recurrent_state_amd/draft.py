@@ -13,7 +13,8 @@ from typing import Optional
 import torch
 
 from ._lib import GLA, KDA, DraftConfigC, check, lib
-from .sequence import DTYPES, _array, _call, _on_device, _ptr, _refuse_tracing, _stream
+from .sequence import (DTYPES, _array, _call, _on_device, _ptr, _refuse_tracing, _stream,
+                       _through_autograd)
 
 __all__ = ["Draft", "DraftConfig", "qstate_verify", "qstate_accept"]
 
@@ -172,10 +173,16 @@ def _check_gate(t, name, shape, device):
     return _aligned(t)
 
 
+def _refuse_gradients(name, tensors):
+    _refuse_tracing(name)
+    if _through_autograd([t for t in tensors if isinstance(t, torch.Tensor)]):
+        raise RuntimeError(f"{name} is not differentiable: call it under torch.no_grad()")
+
+
 def _verify(cfg, c_cfg, codes, scales, q, k, v, log_alpha, beta, parents):
     """The checked call of QState.verify on the current stream, c_cfg and the state its own: o, the
     draft."""
-    _refuse_tracing("verify")
+    _refuse_gradients("verify", (q, k, v, log_alpha, beta))
     dev = codes.device
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         _on_device(t, name, dev)
@@ -211,7 +218,7 @@ def _verify(cfg, c_cfg, codes, scales, q, k, v, log_alpha, beta, parents):
 
 def _accept(cfg, c_cfg, codes, scales, step, draft, last):
     """The checked call of QState.accept on the current stream, c_cfg and the state its own."""
-    _refuse_tracing("accept")
+    _refuse_gradients("accept", (draft.k, draft.log_alpha, draft.writes))
     dev = codes.device
     k, writes = draft.k, draft.writes
     for t, name in ((k, "k"), (writes, "writes"), (last, "last")):

@@ -16,7 +16,7 @@ import torch
 
 from ._lib import (BDR, GDN, GLA, KDA, KEY_AXIS, RTN, SCALAR, SR, VALUE_AXIS, QStateConfig, check,
                    lib)
-from .draft import Draft, _accept, _verify
+from .draft import Draft, _accept, _refuse_gradients, _verify
 from .group_norm import (GATE, GATE_FIRST, PLAIN, GroupNormConfig, qstate_group_norm,
                          qstate_group_norm_workspace)
 from .linear import Weight4, linear4
@@ -337,9 +337,12 @@ class QState:
         quantization after every token; zero in rows of no node.  A node that is not finite spoils
         those that hang on it and no other.  With `norm` o is normed and gated as in `step`, with
         `project` its projection [N, T, outputs] is returned.  o and draft lie in the memory of the
-        stream of the call.  Not differentiable; not for key-axis groups and pair windows."""
+        stream of the call.  Not differentiable: inputs that want a gradient are refused, and so are
+        forward-mode derivatives and tracing (make_fx, torch.jit.trace).  Not for key-axis groups and
+        pair windows."""
         dev = self.codes.device
         if norm is not None:  # refused before any launch
+            _refuse_gradients("verify", (norm.weight, norm.gate, norm.bias))
             _on_device(v, "v", dev)
             rows = v.shape[0] * v.shape[1] if v.dim() == 4 else 0
             cfg = norm.config((rows, self.cfg.heads, self.cfg.dv), v.dtype, dev, v.shape)
@@ -358,7 +361,8 @@ class QState:
         """The path of drafted tokens that ends in row last[n] (int32 [N], on the device) enters the
         stored state of sequence n, in one quantization event: the counter goes up by one.  A sequence
         with last[n] = -1 accepts none and keeps its state bit for bit.  In a captured graph every
-        replay is the event of the capture: the counter stays, and SR's random bits repeat."""
+        replay is the event of the capture: the counter stays, and SR's random bits repeat.  Not
+        differentiable, as `verify`."""
         dev = self.codes.device
         step = self.step_counter
         with nullcontext() if stream is None else _on(stream, dev):

@@ -453,6 +453,48 @@ def test_a_round_of_decoding():
         assert rel(got, S) <= (r + 1) * (ACCEPT + VERIFY)
 
 
+@pytest.mark.parametrize("name", ["q", "k", "v", "log_alpha", "beta", "weight", "gate", "bias"])
+def test_gradients_are_refused(name):
+    """Not differentiable: where a gradient or a tangent is wanted, nothing is launched."""
+    from torch.autograd import forward_ad as fwd
+
+    from bit_recurrent_state_amd import Draft, ReadoutNorm
+    x, S = inputs(GDN, 2, 5, "tree", 2, 2, 64, 32, torch.float32, "cuda")
+    st, _ = handle(GDN, S)
+    extra = {"weight": torch.ones(32, device="cuda"), "bias": torch.zeros(32, device="cuda"),
+             "gate": torch.randn(x["v"].shape, device="cuda")}
+    _, draft = verify(st, x)
+    last = torch.zeros(2, dtype=torch.int32, device="cuda")
+    before, step = st.codes.clone(), st.step_counter
+
+    def go(change):
+        y = {n: change(t) if n == name else t for n, t in {**x, **extra}.items()}
+        return verify(st, y, norm=ReadoutNorm(y["weight"], y["gate"], bias=y["bias"]))
+
+    def leaf(t):
+        return t.clone().requires_grad_(True)
+
+    with pytest.raises(RuntimeError):
+        go(leaf)
+    with fwd.dual_level(), pytest.raises(RuntimeError):
+        go(lambda t: fwd.make_dual(t, torch.ones_like(t)))
+    with torch.no_grad():
+        got = go(leaf)[0]
+    assert torch.equal(got, go(lambda t: t)[0])
+    if name in ("k", "log_alpha"):
+        d = Draft(leaf(draft.k) if name == "k" else draft.k,
+                  leaf(draft.log_alpha) if name == "log_alpha" else draft.log_alpha,
+                  draft.parents, draft.writes)
+        with pytest.raises(RuntimeError):
+            st.accept(d, last)
+        with fwd.dual_level(), pytest.raises(RuntimeError):
+            st.accept(draft, last)
+        assert torch.equal(st.codes, before) and st.step_counter == step
+        with torch.no_grad():
+            st.accept(d, last)
+        assert st.step_counter == step + 1
+
+
 def test_behind_2_to_the_31_elements():
     """Sequences whose FP32 state lies behind 2^31 elements give what they give alone."""
     from bit_recurrent_state_amd import Config, QState
