@@ -246,6 +246,7 @@ class ReadoutNorm:
 
 def _check_projection(project, cfg: Config, device) -> None:
     """A projection of the readout [.., heads, dv], refused before any launch."""
+    _refuse_gradients("project", ())
     if not isinstance(project, Weight4):
         raise TypeError(f"project: expected a Weight4, got {type(project).__name__}")
     if project.inputs != cfg.heads * cfg.dv:

@@ -226,6 +226,37 @@ def test_projections_that_do_not_fit_leave_the_state():
     assert torch.equal(st.codes, codes) and st.step_counter == counter
 
 
+def test_projections_in_forward_mode_leave_the_state():
+    """Inside forward-mode differentiation and under a trace linear4 is refused: before the state changes."""
+    from torch.autograd import forward_ad as fwd
+
+    from bit_recurrent_state_amd import Config, QState, Weight4
+    st = QState(Config(2, 2, 64, 16, mixer=1, fp32_state=True))
+    st.load_fp32(torch.randn(2, 2, 16, 64, device="cuda"))
+    before, step = st.codes.clone(), st.step_counter
+    w = Weight4.quantize(torch.randn(20, 32, device="cuda"), 32)
+    q, k, v, o = (torch.randn(2, 2, d, device="cuda") for d in (64, 64, 16, 16))
+    a = torch.full_like(q, 0.9)
+    kept = o.clone()
+
+    def calls(q, o):
+        yield lambda: st.step(q, k, v, a, None, o, project=w)
+        yield lambda: st.prefill(q[:, None], k[:, None], v[:, None], a.log()[:, None], project=w)
+        yield lambda: st.verify(q[:, None], k[:, None], v[:, None], a.log()[:, None], project=w)
+
+    with fwd.dual_level():
+        for go in calls(q, o):
+            with pytest.raises(RuntimeError):
+                go()
+    for i in range(3):
+        with pytest.raises(RuntimeError):
+            torch.jit.trace(lambda q: list(calls(q, o))[i]() or q, (q,), check_trace=False)
+    assert torch.equal(st.codes, before) and st.step_counter == step and torch.equal(o, kept)
+    st.step(q, k, v, a, None, o, project=w)
+    assert st.step_counter == step + 1
+
+
+
 def test_refusals():
     from bit_recurrent_state_amd import Weight4, linear4
     from bit_recurrent_state_amd._lib import QStateError
