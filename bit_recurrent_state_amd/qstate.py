@@ -6,6 +6,7 @@ checked here so that a wrong tensor fails before it reaches the C ABI."""
 
 from __future__ import annotations
 
+import copy
 import ctypes
 from contextlib import nullcontext
 from dataclasses import dataclass
@@ -259,7 +260,9 @@ class QState:
     """A handle plus the torch device buffers it works on (caller-owned memory)."""
 
     def __init__(self, cfg: Config, device="cuda"):
-        self.cfg = cfg
+        # the handle's own: the caller may change its configuration for the next handle, and every call's
+        # checks go by the sizes of this one's memory
+        self.cfg = cfg = copy.deepcopy(cfg)
         self._c, self._keep = cfg.to_c()  # what the calls that take a configuration get
         cb, sb = qstate_state_bytes(cfg)
         if cfg.fp32_state:

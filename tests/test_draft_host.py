@@ -139,3 +139,34 @@ def test_reference_of_branches():
     assert torch.equal(o[:, [0, 2]], o2) and torch.equal(w[:, [0, 2]], w2)
     assert not o[:, 3].any() and not w[:, 3].any()
     assert GLA != KDA
+
+
+def test_a_handle_keeps_its_configuration(monkeypatch):
+    """A configuration that is changed for the next handle: the first one's calls still go by the sizes
+    of its memory, and refuse others before the library is reached."""
+    from bit_recurrent_state_amd import Config, Draft, QState, draft, qstate
+    calls = []
+    monkeypatch.setattr(qstate, "qstate_create", lambda *a: None)
+    monkeypatch.setattr(qstate, "qstate_get_step", lambda h: 0)
+    monkeypatch.setattr(qstate, "qstate_set_step", lambda h, s: None)
+    monkeypatch.setattr(draft, "_on_device", lambda *a: None)
+    monkeypatch.setattr(draft, "_stream", lambda *a: None)
+    monkeypatch.setattr(draft, "_call", lambda *a: calls.append(a) or 0)
+    bits = [8, 4]
+    cfg = Config(4, 2, 64, 16, mixer=GDN, head_bits=bits)
+    st = QState(cfg, device="cpu")
+    cfg.batch, cfg.heads, cfg.dv = 2, 1, 8
+    bits[0] = 4
+    few, _ = inputs(GDN, 2, 3, "chain", 1, 1, 64, 8, torch.float32, "cpu")
+    names = ("q", "k", "v", "log_alpha", "beta")
+    with pytest.raises(ValueError):
+        st.verify(*(few[n] for n in names))
+    last = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        st.accept(Draft(few["k"], few["log_alpha"], None, few["v"]), last)
+    assert not calls
+    x, _ = inputs(GDN, 4, 3, "chain", 2, 2, 64, 16, torch.float32, "cpu")
+    _, d = st.verify(*(x[n] for n in names))
+    st.accept(d, torch.zeros(4, dtype=torch.int32))
+    assert len(calls) == 2
+    assert st.cfg.bits().tolist() == [[8] * 4, [4] * 4]
