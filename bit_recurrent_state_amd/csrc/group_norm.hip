@@ -68,18 +68,28 @@ __device__ __forceinline__ float inverse_root(float v) {
   return r;
 }
 
-// act(z), for the gradient its slope.  What ends in 16 bits takes exp(-z) as 2^(-z log2 e) without the
-// product's rest (an error of |z| 2^-24 of it, half a step of those types being 2^-12 at least) and the
-// reciprocal as it is: 11 instead of 20 instructions' time a value, which is what bounds the kernels.
+// act(z), for the gradient its slope.  What only ends in 16 bits, the forward pass of those types, takes
+// exp(-z) as 2^(-z log2 e) without the product's rest (an error of |z| 2^-24 of it, half a step of the
+// types being 2^-12 at least).  The backward pass also sums into FP32 gradients of the weights: t = -z
+// log2 e rounded is off by -z - t ln 2, a fused multiply-add and exact but for the rest of ln 2 (|z|
+// 2.8e-9), and e takes it on, one more.  The reciprocal is the instruction's, to an ulp.  11 and 13
+// instead of 20 instructions' time a value, which is what bounds the kernels.
 template <int DT, bool SLOPE>
 __device__ __forceinline__ float act_of(float z, int act, float& slope) {
   if (DT == 0) return activate(z, act, slope);
   const float c = __builtin_elementwise_maximum(z, -87.0f);  // NaN stays
-  const float e = __builtin_amdgcn_exp2f(c * -1.44269502f);
-  const float s = __builtin_amdgcn_rcpf(1.0f + e);
+  float e, s;
   if (SLOPE) {
+    const float d = __builtin_elementwise_minimum(c, 87.0f);
+    const float t = d * -1.44269502f;
+    e = __builtin_amdgcn_exp2f(t);
+    e = fmaf(e, fmaf(t, -0.693147182f, -d), e);
+    s = __builtin_amdgcn_rcpf(1.0f + e);
     const float q = s * e;  // 1 - s without cancellation; with a gate of infinity, nothing of it
-    slope = act == 0 ? s * fmaf(__builtin_elementwise_minimum(c, 87.0f), q, 1.0f) : s * q;
+    slope = act == 0 ? s * fmaf(d, q, 1.0f) : s * q;
+  } else {
+    e = __builtin_amdgcn_exp2f(c * -1.44269502f);
+    s = __builtin_amdgcn_rcpf(1.0f + e);
   }
   return act == 0 ? c * s : s;
 }

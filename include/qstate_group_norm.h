@@ -15,7 +15,9 @@
  *
  * which is the readout of a retention layer (centered, a gate after), of a
  * Mamba2 block (not centered, the gate before), and a norm with its activation.
- * Everything between x, gate and y is FP32, rounded once at the end; the
+ * Everything between x, gate and y is FP32, rounded once at the end (an
+ * activation at z that goes into a 16-bit y is off by up to |z| 2^-23 of its
+ * value before that); dweight and dbias hold to FP32 whatever x's type; the
  * variance is taken from the centered values.  Squares of values beyond 1e19
  * overflow.  silu goes to zero below (to 2e-36, at minus infinity too) and to its
  * argument above.  A NaN or an infinity spoils its group of its token (and the sums of

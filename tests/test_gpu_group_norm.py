@@ -127,6 +127,37 @@ def test_large_mean():
     assert rel(call(x, 2, "plain"), want) <= 4096 * 10 * 2.0 ** -24 + BASE
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("act", [0, 1])
+@pytest.mark.parametrize("mode", ["gate", "activate"])
+def test_weights_gradients_hold_to_fp32(dtype, act, mode):
+    """dweight and dbias are FP32 whatever x's type is, also where the activation is small.
+
+    One token, so that a value is one term, and x of 1 and -1, so that normalised values are off by the
+    root's 3 roundings.  sigmoid: the exponential's ulp (2 roundings), what its argument is off by (4 at
+    -86), its product, the sum, the reciprocal's ulp (2): 10.  silu's slope: 1 - s off by 4, which adding 1
+    makes 6 where |z| is 4 or more, and two products; the term's product: 22 * 2^-24 in all."""
+    g = torch.Generator().manual_seed(4)
+    C = 256
+    x = torch.where(torch.rand(1, C, generator=g) < 0.5, -1.0, 1.0)
+    z = torch.empty(1, C).uniform_(-86.0, -4.0, generator=g)
+    dt = TYPES[dtype]
+    leaves = {"x": x.to(dt), "weight": torch.ones(C) if mode == "gate" else torch.zeros(C),
+              "bias": torch.zeros(C) if mode == "gate" else z[0].clone(),
+              "gate": z.to(dt) if mode == "gate" else None}
+    leaves = {n: None if t is None else t.cuda() for n, t in leaves.items()}
+    own = {n: None if t is None else t.clone().requires_grad_(True) for n, t in leaves.items()}
+    l64 = {n: None if t is None else t.double().requires_grad_(True) for n, t in leaves.items()}
+    y = call(own, 2, mode, False, 1e-12, act)
+    want = norm64(l64["x"], 2, l64["weight"], l64["bias"], l64["gate"], mode, False, 1e-12, act)
+    sums = ("weight", "bias")
+    got = torch.autograd.grad(y, [own[n] for n in sums], torch.ones_like(y))
+    exact = torch.autograd.grad(want, [l64[n] for n in sums], torch.ones_like(want))
+    for n, a, b in zip(sums, got, exact):
+        off = ((a.double() - b) / b).abs()
+        assert bool((off <= 22 * 2.0 ** -24).all()), (n, float(off.max()))
+
+
 def test_equal_values_and_zeros():
     """Rows without variance: the bias alone, finite gradients."""
     x = make(6, 2, 64, torch.float32, "plain")
