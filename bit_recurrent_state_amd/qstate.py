@@ -340,7 +340,8 @@ class QState:
         shape and dtype, is what `step` would read out behind each node's path, without the
         quantization after every token; zero in rows of no node.  A node that is not finite spoils
         those that hang on it and no other.  With `norm` o is normed and gated as in `step`, with
-        `project` its projection [N, T, outputs] is returned.  o and draft lie in the memory of the
+        `project` its projection [N, T, outputs] is returned; both take rows of no node as rows of
+        zeros, which a norm's bias (and gate) makes others.  o and draft lie in the memory of the
         stream of the call.  Not differentiable: inputs that want a gradient are refused, and so are
         forward-mode derivatives and tracing (make_fx, torch.jit.trace).  Not for key-axis groups and
         pair windows."""

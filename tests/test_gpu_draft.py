@@ -453,6 +453,35 @@ def test_a_round_of_decoding():
         assert rel(got, S) <= (r + 1) * (ACCEPT + VERIFY)
 
 
+@pytest.mark.parametrize("mixer", ["gdn", "kda"])
+@pytest.mark.parametrize("gate_first", [False, True])
+def test_norm_of_rows_of_no_node(mixer, gate_first):
+    """The norm and the projection take padding as rows of zeros: what is in it reaches no node, and it
+    comes out as the projection of bias (and gate)."""
+    from bit_recurrent_state_amd import ReadoutNorm, Weight4
+    m = MIXERS[mixer]
+    x, S = inputs(m, 3, 13, "ragged", 2, 2, 64, 32, torch.bfloat16, "cuda", seed=5)
+    x["parents"][0, 4] = -2
+    none = ~node_mask(x["parents"]).to("cuda")
+    assert none.any() and not none.all()
+    st, _ = handle(m, S, "int4")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w, b = (torch.randn(2, 32, device="cuda", generator=g) for _ in range(2))
+    z = torch.randn(x["v"].shape, device="cuda", generator=g).bfloat16()
+    z2 = torch.where(none[..., None, None], torch.full_like(z, float("nan")), z)
+    project = Weight4.quantize(torch.randn(48, 64, device="cuda", generator=g), 32)
+    for p in (None, project):
+        o, _ = verify(st, x, norm=ReadoutNorm(w, z, bias=b, gate_first=gate_first), project=p)
+        o2, _ = verify(st, x, norm=ReadoutNorm(w, z2, bias=b, gate_first=gate_first), project=p)
+        assert torch.equal(o[~none], o2[~none]) and o2[none].isnan().all()
+        if p is None:
+            want = b.expand_as(z)[none]
+            if not gate_first:
+                want = want.double() * torch.nn.functional.silu(z[none].double())
+            # a rounding of the product, of its activation (as exp, sum, quotient, product) and to bfloat16
+            assert bool(((o[none] - want).abs() <= (2.0 ** -8 + 2.0 ** -18) * want.abs()).all())
+
+
 @pytest.mark.parametrize("name", ["q", "k", "v", "log_alpha", "beta", "weight", "gate", "bias"])
 def test_gradients_are_refused(name):
     """Not differentiable: where a gradient or a tangent is wanted, nothing is launched."""
