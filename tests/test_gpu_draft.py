@@ -104,6 +104,18 @@ def test_stored_forms(mixer, store, dk, group):
 
 
 @pytest.mark.parametrize("mixer", MIXERS)
+@pytest.mark.parametrize("store", ["int8", "int4", "mix", "channels"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_stored_forms_of_16_bit_rows(mixer, store, dtype):
+    """16-bit rows over quantized states, one to four tiles of nodes, one and two tiles of value columns."""
+    for N, T, shape, Hq, dk, dv, group in ((3, 16, "tree", 1, 128, 128, 32), (2, 17, "ragged", 2, 64, 128, 16),
+                                           (2, 33, "tree", 1, 128, 72, 64), (2, 64, "tree", 4, 64, 128, 32),
+                                           (2, 64, "chain", 2, 128, 64, 128), (3, 48, "ragged", 1, 128, 40, 16),
+                                           (2, 32, "tree", 2, 256, 72, 64), (2, 9, "tree", 1, 256, 128, 16)):
+        check(MIXERS[mixer], N, T, shape, 4, Hq, dk, dv, TYPES[dtype], store, group)
+
+
+@pytest.mark.parametrize("mixer", MIXERS)
 @pytest.mark.parametrize("gate", [0.0, 20.0, 300.0, 5000.0])
 def test_gates(mixer, gate):
     """No decay at all, and decays that leave nothing of what was before."""
