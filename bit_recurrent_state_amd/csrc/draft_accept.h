@@ -9,7 +9,8 @@
 // The first rows are asked for before the path is looked up.
 // Bound by memory and the quantizer's instructions: 128 sequences, 16 heads of 128 x 128, INT8,
 // paths of 4 nodes 23 us (78 MB, 3.4 TB/s; 33 us with loads behind the path's); 16 sequences
-// of FP32 states, a gate per channel, 10.6 us (34 MB).
+// of FP32 states, a gate per channel, 10.6 us (34 MB).  256 sequences, 32 heads of INT4, a quarter INT8,
+// paths of about 7 nodes 84 to 89 us (245 MB, 2.8 TB/s), with widths per channel 87.
 
 #pragma once
 

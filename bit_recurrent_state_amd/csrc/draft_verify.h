@@ -1,5 +1,5 @@
 // draft_verify.h — the readout of a tree of drafted tokens over the stored
-// state, which it reads once and leaves alone.
+// state, which it reads once (FP32 states: for every 16 nodes) and leaves alone.
 //
 // With M the nodes' ancestors, c the sums of log decays along the paths and
 // G_ij = e^(c_i - c_j) for j in M(i) or j = i, the recurrence along all paths is
@@ -34,12 +34,13 @@
 // Bound by latency, then by memory: what a workgroup reads is asked for before
 // anything is waited for, codes, scales and bfloat16 rows by copies to LDS that
 // take no registers, so that four workgroups share a CU.  256 sequences with 16 nodes,
-// 32 heads of 128 x 128, GDN, INT4 (a quarter INT8), bfloat16: 73 us, 300 MB at
-// 4.1 TB/s (192 us with loads where they are used, 106 with the codes gathered
+// 32 heads of 128 x 128, GDN, INT4 (a quarter INT8), bfloat16: 75 us, 300 MB at
+// 4.0 TB/s (192 us with loads where they are used, 106 with the codes gathered
 // into registers).  64 sequences of up to 33 nodes, 16 heads, KDA, INT8: 58 us for
 // 53 MB; its workgroups take 80 KB of LDS and 11 of their 30 thousand cycles
-// for the walks.  32 sequences of 64 nodes, SCALAR, 32 heads of 64 x 128, INT4: 23 us
-// for 40 MB.
+// for the walks.  32 sequences of 64 nodes, SCALAR, 32 heads of 64 x 128, INT4: 24 us
+// for 40 MB.  The first batch with float16 rows (three terms) takes 110 us, with FP32 rows 125, over
+// states with widths per channel, whose codes lanes gather for themselves, 100.
 
 #pragma once
 
@@ -47,11 +48,12 @@
 
 namespace qdraft {
 
-// Codes of 8 neighbouring columns as an operand.
+// The upper halves of two floats: two bfloat16 numbers where the lower halves are zeros.
 __device__ __forceinline__ uint32_t top_halves(float a, float b) {
   return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
 }
 
+// Codes of 8 neighbouring columns as an operand.
 __device__ __forceinline__ Frag<1> from_int8(uint32_t lo, uint32_t hi) {
   Frag<1> f;
 #pragma unroll
@@ -162,7 +164,9 @@ struct StateRows {
 
   __device__ __forceinline__ int row(int t) const { return min(row0 + N * ((int)threadIdx.x & 15) + t, dv - 1); }
 
-  // FP32: columns 32 s .. of tile t as an operand
+  // FP32: columns 32 s .. of tile t as an operand.  Loaded and split again for every tile of nodes: three
+  // terms of all columns would take 3 DK / 8 registers more a tile of value rows (64 sequences, 32 heads of
+  // 128 x 128: 34 us with 16 nodes, 139 with 64)
   __device__ __forceinline__ Frag<3> values(int t, int s) const {
     const f32x4* x = reinterpret_cast<const f32x4*>(head + (int64_t)row(t) * DK * 4) + s * 8 +
                      ((threadIdx.x & 63) >> 4) * 2;
@@ -414,7 +418,7 @@ struct alignas(16) Lds {
   float alpha[VEC ? T : 1][DK];
   double c[T];
   unsigned long long mask[T];                  // node and ancestors; 0: no node
-  unsigned long long nodes, pad;               // which rows are nodes
+  unsigned long long nodes;                    // which rows are nodes
   unsigned long long gone[4][NTW][16];         // of a wave's columns: the nodes whose U is not finite
   int parent[T];
 };

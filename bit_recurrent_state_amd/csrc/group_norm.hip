@@ -6,7 +6,7 @@
 // normalised values again instead of reading them.  Teams stay in their group: its
 // weights are loaded, and their gradients summed, once per team.  8191 rows of 8 groups
 // of 512 bfloat16 values with a gate in front take 42 us (201 MB, 4.8 TB/s: memory);
-// 8192 x 32 x 128 activated 35 us forward (134 MB, 3.8 TB/s) and 56 backward (201 MB, 3.6
+// 8192 x 32 x 128 activated 35 us forward (134 MB, 3.8 TB/s) and 57 backward (201 MB, 3.5
 // TB/s), where the activation's instructions take as long as the memory.
 
 #include <hip/hip_runtime.h>

@@ -153,8 +153,10 @@ def linear4(x, weight: Weight4, bias=None):
     """x [.., inputs] times weights in four bits, [.., outputs]: x W^T + bias.
 
     x float32, bfloat16 or float16, bias float32 [outputs]; FP32 sums, rounded once to x's type.
-    Meant for few rows (every 16 of them read the weights).  Not differentiable: inputs that want a gradient
-    are refused, and so is tracing (make_fx, torch.jit.trace)."""
+    Meant for few rows: every 16 of them read the weights.  A call takes less time than a bfloat16 product's
+    up to about 128 rows with 4096 x 4096 weights, 64 with 12288 x 4096; with 4096 rows it takes five times as
+    long.  Not differentiable: inputs that want a gradient are refused, and so is tracing (make_fx,
+    torch.jit.trace)."""
     _refuse_tracing("linear4")
     _on_device(x, "x", weight.packed.device)
     if x.dtype not in DTYPES or x.dim() < 1 or x.shape[-1] != weight.inputs:

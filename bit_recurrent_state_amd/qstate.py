@@ -279,7 +279,8 @@ class QState:
     def step(self, q, k, v, alpha, beta=None, o=None, stream=None, norm=None, project=None):
         """One token for every sequence; with `norm` (a ReadoutNorm), o is the normed and gated
         readout; with `project` (a Weight4 of heads * dv inputs), o's projection [N, outputs] is
-        returned, in the memory of the stream of the call."""
+        returned, in the memory of the stream of the call (`linear4`: beyond about a hundred sequences
+        a product with 16-bit weights is the faster one)."""
         if project is not None:
             if o is None:
                 raise ValueError("project: there is no readout without o")
@@ -303,8 +304,9 @@ class QState:
         scan from the stored state, whose end is stored back (one quantization event for every
         sequence, those without tokens too: the counter goes up by one, a window starts empty).
         Arguments as `scan`'s, one sequence per batch row, q and k with the handle's heads or a
-        divisor of them; returns o (with `project`, its projection [.., outputs]), which lies in the
-        memory of the stream of the call."""
+        divisor of them; returns o (with `project`, its projection [.., outputs], by `linear4`, which is
+        meant for chunks of up to about a hundred tokens in all), in the memory of the stream of the
+        call."""
         c = self.cfg
         if project is not None:
             _check_projection(project, c, self.codes.device)
@@ -341,8 +343,9 @@ class QState:
         quantization after every token; zero in rows of no node.  A node that is not finite spoils
         those that hang on it and no other.  With `norm` o is normed and gated as in `step`, with
         `project` its projection [N, T, outputs] is returned; both take rows of no node as rows of
-        zeros, which a norm's bias (and gate) makes others.  o and draft lie in the memory of the
-        stream of the call.  Not differentiable: inputs that want a gradient are refused, and so are
+        zeros, which a norm's bias (and gate) makes others.  (The projection is `linear4`'s: beyond about
+        a hundred rows N T a product with 16-bit weights is the faster one.)  o and draft lie in the
+        memory of the stream of the call.  Not differentiable: inputs that want a gradient are refused, and so are
         forward-mode derivatives and tracing (make_fx, torch.jit.trace).  Not for key-axis groups and
         pair windows."""
         dev = self.codes.device
