@@ -272,6 +272,25 @@ def test_products_beyond_the_range(mixer, dtype, T, branch, dk, dv, store):
     assert torch.equal(a.codes, b.codes) and (store == "f32" or torch.equal(a.scales, b.scales))
 
 
+@pytest.mark.parametrize("mixer", MIXERS)
+@pytest.mark.parametrize("dtype,dk,dv,store", [("f32", 64, 40, "f32"), ("bf16", 128, 128, "int8")])
+def test_products_beyond_the_range_behind_a_common_node(mixer, dtype, dk, dv, store):
+    """Node 0 has a long key, which its children 1 and 3 live with; what overflows behind 1 changes no bit
+    of 3 and the nodes behind it."""
+    m = MIXERS[mixer]
+    x, S = inputs(m, 2, 20, "chain", 2, 1, dk, dv, TYPES[dtype], "cuda", seed=2)
+    x["parents"][:] = torch.tensor([-1, 0, 1, 0, 3, 2] + list(range(4, 18)), dtype=torch.int32, device="cuda")
+    x["k"][:, 0] = (1e12 * x["k"][:, 0].float()).to(TYPES[dtype])
+    y = dict(x, k=x["k"].clone())
+    y["k"][:, 1:3] = x["k"][:, :1]
+    hit = (below(x["parents"].cpu(), 0, 1) | below(x["parents"].cpu(), 1, 1)).cuda()
+    st, _ = handle(m, S, store)
+    (o, d), (o2, d2) = verify(st, x), verify(st, y)
+    assert not hit.all() and not hit[:, [0, 3, 4]].any()
+    for a, b in ((o, o2), (d.writes, d2.writes)):
+        assert torch.equal(a[~hit], b[~hit]) and bool(a[~hit].isfinite().all())
+
+
 @pytest.mark.parametrize("last", [-1, -5, 9, 1 << 30, 3])
 def test_last_that_is_no_node(last):
     x, S = inputs(GDN, 2, 9, "tree", 2, 2, 64, 32, torch.float32, "cuda")
